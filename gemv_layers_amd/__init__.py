@@ -38,6 +38,8 @@ EXPORTS = (
     "gemm_peak_empty_launch", "gemm_fill_launch",
     "gemm_mx_packed_sizes", "gemm_mx_pack_weight", "gemm_mx_quantize_act", "gemm_mx_decode",
     "gemm_mx_decode_bf16", "gemm_pack_weight_bf16", "gemm_bf16_packed",
+    "gemm_i8_quantize", "gemm_i8", "gemm_i8_swiglu", "gemm_i8_work_bytes", "gemm_i8_bf16",
+    "gemm_i8_swiglu_bf16", "gemm_bf16_bwd", "gemm_bf16_swiglu_train", "gemm_bf16_swiglu_bwd",
 )
 
 
@@ -107,6 +109,18 @@ def lib() -> ctypes.CDLL:
     L.gemm_pack_weight_bf16.restype = i32
     L.gemm_bf16_packed.argtypes = [i64, i64, i64, p, i64, p, p, i64, p]
     L.gemm_bf16_packed.restype = i32
+    L.gemm_i8_quantize.argtypes = [i64, i64, p, i64, p, i64, p, p]
+    L.gemm_i8_work_bytes.argtypes = [i64, i64, ctypes.POINTER(ctypes.c_int64)]
+    for name in ("gemm_i8", "gemm_i8_swiglu"):
+        getattr(L, name).argtypes = [i64, i64, i64, p, i64, p, p, i64, p, p, i64, p]
+    for name in ("gemm_i8_bf16", "gemm_i8_swiglu_bf16"):
+        getattr(L, name).argtypes = [i64, i64, i64, p, i64, p, i64, p, p, i64, p, i64, p]
+    L.gemm_bf16_bwd.argtypes = [i64, i64, i64, p, i64, p, i64, p, i64, p, i64, p, i64, p]
+    L.gemm_bf16_swiglu_train.argtypes = [i64, i64, i64, p, i64, p, i64, p, i64, p, i64, p]
+    L.gemm_bf16_swiglu_bwd.argtypes = [i64, i64, i64, p, i64, p, i64, p, i64, p, i64, p, i64, p, i64, p, i64, p]
+    for name in ("gemm_i8_quantize", "gemm_i8_work_bytes", "gemm_i8", "gemm_i8_swiglu", "gemm_i8_bf16",
+                 "gemm_i8_swiglu_bf16", "gemm_bf16_bwd", "gemm_bf16_swiglu_train", "gemm_bf16_swiglu_bwd"):
+        getattr(L, name).restype = i32
     _lib = L
     return L
 
@@ -197,6 +211,50 @@ def gemm_pack_weight_bf16(K, N, B, ldb, Bp, stream=None) -> None:
 
 def gemm_bf16_packed(M, N, K, A, lda, Bp, C, ldc, stream=None) -> None:
     _check("gemm_bf16_packed", lib().gemm_bf16_packed(M, N, K, A, lda, Bp, C, ldc, stream))
+
+
+def gemm_i8_quantize(R, K, X, ldx, Q, ldq, S, stream=None) -> None:
+    _check("gemm_i8_quantize", lib().gemm_i8_quantize(R, K, X, ldx, Q, ldq, S, stream))
+
+
+def gemm_i8(M, N, K, Aq, ldaq, Sa, Wq, ldwq, Sw, C, ldc, stream=None) -> None:
+    _check("gemm_i8", lib().gemm_i8(M, N, K, Aq, ldaq, Sa, Wq, ldwq, Sw, C, ldc, stream))
+
+
+def gemm_i8_swiglu(M, N, K, Aq, ldaq, Sa, Wq, ldwq, Sw, C, ldc, stream=None) -> None:
+    _check("gemm_i8_swiglu", lib().gemm_i8_swiglu(M, N, K, Aq, ldaq, Sa, Wq, ldwq, Sw, C, ldc, stream))
+
+
+def gemm_i8_work_bytes(M: int, K: int) -> int:
+    """Bytes of the work buffer of gemm_i8_bf16 and gemm_i8_swiglu_bf16."""
+    n = ctypes.c_int64()
+    _check("gemm_i8_work_bytes", lib().gemm_i8_work_bytes(M, K, ctypes.byref(n)))
+    return n.value
+
+
+def gemm_i8_bf16(M, N, K, A, lda, Wq, ldwq, Sw, C, ldc, work, work_bytes, stream=None) -> None:
+    _check("gemm_i8_bf16", lib().gemm_i8_bf16(M, N, K, A, lda, Wq, ldwq, Sw, C, ldc, work, work_bytes, stream))
+
+
+def gemm_i8_swiglu_bf16(M, N, K, A, lda, Wq, ldwq, Sw, C, ldc, work, work_bytes, stream=None) -> None:
+    _check("gemm_i8_swiglu_bf16",
+           lib().gemm_i8_swiglu_bf16(M, N, K, A, lda, Wq, ldwq, Sw, C, ldc, work, work_bytes, stream))
+
+
+def gemm_bf16_bwd(M, N, K, dC, lddc, A, lda, B, ldb, dA, ldda, dB, lddb, stream=None) -> None:
+    _check("gemm_bf16_bwd", lib().gemm_bf16_bwd(M, N, K, dC, lddc, A, lda, B, ldb, dA, ldda, dB, lddb, stream))
+
+
+def gemm_bf16_swiglu_train(M, N, K, A, lda, B, ldb, GU, ldgu, C, ldc, stream=None) -> None:
+    _check("gemm_bf16_swiglu_train",
+           lib().gemm_bf16_swiglu_train(M, N, K, A, lda, B, ldb, GU, ldgu, C, ldc, stream))
+
+
+def gemm_bf16_swiglu_bwd(M, N, K, dC, lddc, GU, ldgu, A, lda, B, ldb, dGU, lddgu, dA, ldda, dB, lddb,
+                         stream=None) -> None:
+    _check("gemm_bf16_swiglu_bwd",
+           lib().gemm_bf16_swiglu_bwd(M, N, K, dC, lddc, GU, ldgu, A, lda, B, ldb, dGU, lddgu, dA, ldda, dB, lddb,
+                                      stream))
 
 
 def gemm_wave_efficiency(ctas: int, slots: int):
@@ -303,3 +361,191 @@ def swiglu_matmul(A, B, out=None, stream=None):
           ctypes.c_void_p(B.data_ptr()), max(B.stride(0), 2 * N), ctypes.c_void_p(out.data_ptr()),
           max(out.stride(0), N), st)
     return out
+
+
+# ---- 8-bit products and training: PyTorch marshalling ----------------------------------------
+
+
+def _rows(t, name, dtype, cols=None):
+    """Checks a 2-D device tensor of `dtype` with unit column stride and non-overlapping rows;
+    returns its leading dimension."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}")
+    if t.dim() != 2 or (cols is not None and t.shape[1] != cols):
+        raise ValueError(f"{name} must have {'two dimensions' if cols is None else f'{cols} columns'}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    r, c = t.shape
+    sr, sc = t.stride()
+    if sc != 1 and c > 1 and r > 0:
+        raise ValueError(f"{name} needs unit column stride")
+    if r <= 1 or sr >= c:
+        return sr if sr > c else c
+    raise ValueError(f"{name} has overlapping rows")
+
+
+def _scales(t, name, n):
+    import torch
+
+    if t.dtype != torch.float32 or t.dim() != 1 or t.shape[0] != n or not t.is_cuda:
+        raise ValueError(f"{name} must be a device vector of {n} float32 values")
+    if n > 1 and t.stride(0) != 1:
+        raise ValueError(f"{name} needs unit stride")
+    return t.data_ptr()
+
+
+def _same_device(*ts):
+    d = ts[0].device
+    for t in ts:
+        if t is not None and t.device != d:
+            raise ValueError("all tensors must be on one device")
+
+
+def _out(out, shape, device):
+    import torch
+
+    if out is None:
+        return torch.empty(shape, dtype=torch.bfloat16, device=device)
+    if tuple(out.shape) != shape:
+        raise ValueError(f"the output must have shape {shape}")
+    return out
+
+
+def i8_quantize(X, stream=None):
+    """8-bit codes and scales of each row of a bf16 matrix: (Q int8 of X's shape, S float32).
+    Q's rows are padded to 16 bytes in memory, as the matrix kernels want them. For an nn.Linear
+    weight the rows are output channels; for activations they are tokens."""
+    import torch
+
+    ldx = _rows(X, "X", torch.bfloat16)
+    R, K = X.shape
+    ldq = -(-K // 16) * 16
+    Q = torch.empty((R, ldq), dtype=torch.int8, device=X.device)[:, :K]
+    S = torch.empty((R,), dtype=torch.float32, device=X.device)
+    gemm_i8_quantize(R, K, X.data_ptr(), ldx, Q.data_ptr(), ldq, S.data_ptr(),
+                     stream if stream is not None else current_stream_handle())
+    return Q, S
+
+
+def _i8_codes(name, Aq, Sa, Wq, Sw, out, stream, glu):
+    import torch
+
+    lda, ldw = _rows(Aq, "Aq", torch.int8), _rows(Wq, "Wq", torch.int8, Aq.shape[1])
+    M, K = Aq.shape
+    N = Wq.shape[0]
+    if glu:
+        if N % 2:
+            raise ValueError("Wq must have 2N rows, gate then up")
+        N //= 2
+    sa, sw = _scales(Sa, "Sa", M), _scales(Sw, "Sw", Wq.shape[0])
+    out = _out(out, (M, N), Aq.device)
+    ldc = _rows(out, "out", torch.bfloat16)
+    _same_device(Aq, Sa, Wq, Sw, out)
+    st = getattr(lib(), name)(M, N, K, Aq.data_ptr(), lda, sa, Wq.data_ptr(), ldw, sw, out.data_ptr(), ldc,
+                              stream if stream is not None else current_stream_handle())
+    _check(name, st)
+    return out
+
+
+def i8_matmul(Aq, Sa, Wq, Sw, out=None, stream=None):
+    """(Aq @ Wq.T) * Sa[:, None] * Sw as bf16: int8 codes Aq (M x K) and Wq (N x K), float32 scales."""
+    return _i8_codes("gemm_i8", Aq, Sa, Wq, Sw, out, stream, False)
+
+
+def i8_swiglu_matmul(Aq, Sa, Wq, Sw, out=None, stream=None):
+    """silu(g) * u of the 8-bit product with a 2N x K gate/up weight (gate rows first); M x N bf16."""
+    return _i8_codes("gemm_i8_swiglu", Aq, Sa, Wq, Sw, out, stream, True)
+
+
+def _i8_dynamic(name, A, Wq, Sw, out, work, stream, glu):
+    import torch
+
+    lda, ldw = _rows(A, "A", torch.bfloat16), _rows(Wq, "Wq", torch.int8, A.shape[1])
+    M, K = A.shape
+    N = Wq.shape[0]
+    if glu:
+        if N % 2:
+            raise ValueError("Wq must have 2N rows, gate then up")
+        N //= 2
+    sw = _scales(Sw, "Sw", Wq.shape[0])
+    out = _out(out, (M, N), A.device)
+    ldc = _rows(out, "out", torch.bfloat16)
+    if work is None:
+        work = torch.empty((max(gemm_i8_work_bytes(M, K), 16),), dtype=torch.uint8, device=A.device)
+    elif work.dtype != torch.uint8 or not work.is_contiguous():
+        raise ValueError("work must be a contiguous uint8 tensor")
+    _same_device(A, Wq, Sw, out, work)
+    st = getattr(lib(), name)(M, N, K, A.data_ptr(), lda, Wq.data_ptr(), ldw, sw, out.data_ptr(), ldc,
+                              work.data_ptr(), work.numel(),
+                              stream if stream is not None else current_stream_handle())
+    _check(name, st)
+    return out
+
+
+def i8_linear(A, Wq, Sw, out=None, work=None, stream=None):
+    """The 8-bit product of bf16 activations A (M x K), quantised row by row in the call, with an
+    8-bit weight (N x K codes, N scales); M x N bf16. `work`: a uint8 tensor of
+    gemm_i8_work_bytes(M, K) bytes to reuse, else one is allocated on the current stream."""
+    return _i8_dynamic("gemm_i8_bf16", A, Wq, Sw, out, work, stream, False)
+
+
+def i8_swiglu_linear(A, Wq, Sw, out=None, work=None, stream=None):
+    """silu(g) * u of the 8-bit product of bf16 activations with a 2N x K gate/up weight."""
+    return _i8_dynamic("gemm_i8_swiglu_bf16", A, Wq, Sw, out, work, stream, True)
+
+
+def matmul_backward(dC, A, B, need_dA=True, need_dB=True, stream=None):
+    """(dA, dB) = (dC @ B.T, A.T @ dC), the gradients of matmul(A, B); None for one not needed."""
+    import torch
+
+    bf16 = torch.bfloat16
+    lda, ldb = _rows(A, "A", bf16), _rows(B, "B", bf16)
+    (M, K), N = A.shape, B.shape[1]
+    lddc = _rows(dC, "dC", bf16, N)
+    if B.shape[0] != K or dC.shape[0] != M:
+        raise ValueError("shapes do not form the gradient of a matrix product")
+    _same_device(dC, A, B)
+    dA = torch.empty((M, K), dtype=bf16, device=A.device) if need_dA else None
+    dB = torch.empty((K, N), dtype=bf16, device=A.device) if need_dB else None
+    gemm_bf16_bwd(M, N, K, dC.data_ptr(), lddc, A.data_ptr(), lda, B.data_ptr(), ldb,
+                  dA.data_ptr() if need_dA else None, K, dB.data_ptr() if need_dB else None, N,
+                  stream if stream is not None else current_stream_handle())
+    return dA, dB
+
+
+def swiglu_forward(A, B, stream=None):
+    """(C, GU) of the gated block for training: GU = A @ B (M x 2N, gate then up), C = silu(g) * u."""
+    import torch
+
+    bf16 = torch.bfloat16
+    lda, ldb = _rows(A, "A", bf16), _rows(B, "B", bf16)
+    (M, K), N = A.shape, B.shape[1] // 2
+    if B.shape[0] != K or B.shape[1] % 2:
+        raise ValueError("B must be K x 2N for A of shape M x K")
+    _same_device(A, B)
+    C = torch.empty((M, N), dtype=bf16, device=A.device)
+    GU = torch.empty((M, 2 * N), dtype=bf16, device=A.device)
+    gemm_bf16_swiglu_train(M, N, K, A.data_ptr(), lda, B.data_ptr(), ldb, GU.data_ptr(), 2 * N, C.data_ptr(), N,
+                           stream if stream is not None else current_stream_handle())
+    return C, GU
+
+
+def swiglu_backward(dC, GU, A, B, need_dA=True, need_dB=True, inplace=False, stream=None):
+    """(dA, dB, dGU): the gradients of swiglu_forward's C. With `inplace`, dGU takes GU's memory."""
+    import torch
+
+    bf16 = torch.bfloat16
+    lda, ldb = _rows(A, "A", bf16), _rows(B, "B", bf16)
+    (M, K), N = A.shape, B.shape[1] // 2
+    lddc, ldgu = _rows(dC, "dC", bf16, N), _rows(GU, "GU", bf16, 2 * N)
+    if B.shape[0] != K or B.shape[1] % 2 or dC.shape[0] != M or GU.shape[0] != M:
+        raise ValueError("shapes do not form the gradient of the gated block")
+    _same_device(dC, GU, A, B)
+    dGU = GU if inplace else torch.empty((M, 2 * N), dtype=bf16, device=A.device)
+    dA = torch.empty((M, K), dtype=bf16, device=A.device) if need_dA else None
+    dB = torch.empty((K, 2 * N), dtype=bf16, device=A.device) if need_dB else None
+    gemm_bf16_swiglu_bwd(M, N, K, dC.data_ptr(), lddc, GU.data_ptr(), ldgu, A.data_ptr(), lda, B.data_ptr(), ldb,
+                         dGU.data_ptr(), ldgu if inplace else 2 * N, dA.data_ptr() if need_dA else None, K,
+                         dB.data_ptr() if need_dB else None, 2 * N,
+                         stream if stream is not None else current_stream_handle())
+    return dA, dB, dGU

@@ -11,8 +11,10 @@
 #include <mutex>
 #include <string>
 
+#include "abi.h"
 #include "gemm_bf16.h"
 #include "kernels.h"
+#include "ops.h"
 #include "plan.h"
 
 namespace {
@@ -64,6 +66,21 @@ std::mutex g_mu;
 DeviceState g_dev[kMaxDevices];
 std::atomic<int> g_ready_count{0};
 std::string g_last_plan = "{}";
+// The 8-bit and training calls keep their plan as it is, with the operator's name, and
+// gemm_last_plan writes it out when asked (the text costs more than the rest of a small call's
+// host work). `op` null: g_last_plan is the newest.
+struct LastOp {
+    const char* op = nullptr;
+    glk::Plan plan;
+    int64_t M = 0, N = 0, K = 0;
+};
+LastOp g_last_op;
+
+// (with g_mu held)
+void set_last_text(std::string s) {
+    g_last_plan = std::move(s);
+    g_last_op.op = nullptr;
+}
 
 // The workspace region of `stream` on the device of `ds` (the current device), made on the
 // stream's first call that needs one. Split partials and counters of concurrent calls on
@@ -250,7 +267,7 @@ int run(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const void*
     if (e != hipSuccess) return GEMM_ERR_HIP;
     {
         std::lock_guard<std::mutex> lk(g_mu);
-        g_last_plan = glk::plan_json(p, M, N, K);
+        set_last_text(glk::plan_json(p, M, N, K));
     }
     return GEMM_OK;
 }
@@ -371,7 +388,7 @@ int mx_decode(int64_t M, int64_t N, int64_t K, const void* Aq, int64_t ldaq, con
     }
     if (e != hipSuccess) return GEMM_ERR_HIP;
     std::lock_guard<std::mutex> lk(g_mu);
-    g_last_plan = glk::plan_json(p, M, N, K);
+    set_last_text(glk::plan_json(p, M, N, K));
     return GEMM_OK;
 }
 
@@ -418,11 +435,43 @@ int packed_decode(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, c
     }
     if (e != hipSuccess) return GEMM_ERR_HIP;
     std::lock_guard<std::mutex> lk(g_mu);
-    g_last_plan = glk::plan_json(p, M, N, K);
+    set_last_text(glk::plan_json(p, M, N, K));
     return GEMM_OK;
 }
 
 }  // namespace
+
+// ---- shared with the other entry points' files (abi.h) --------------------------------------------
+
+namespace glk {
+
+const DeviceInfo* current_device(int* status) {
+    DeviceState* ds = current_state(status);
+    return ds ? &ds->info : nullptr;
+}
+
+int stream_workspace(hipStream_t stream, Workspace* out) {
+    int st = GEMM_OK;
+    DeviceState* ds = current_state(&st);
+    if (!ds) return st;
+    Region* rg = nullptr;
+    st = region_for(*ds, stream, &rg);
+    if (st != GEMM_OK) return st;
+    out->ws = rg->ws;
+    out->counters = rg->counters;
+    return GEMM_OK;
+}
+
+void set_last_plan(const Plan& p, int64_t M, int64_t N, int64_t K, const char* op) {
+    std::lock_guard<std::mutex> lk(g_mu);
+    g_last_op.op = op;
+    g_last_op.plan = p;
+    g_last_op.M = M;
+    g_last_op.N = N;
+    g_last_op.K = K;
+}
+
+}  // namespace glk
 
 extern "C" {
 
@@ -546,7 +595,14 @@ int gemm_wave_efficiency(int64_t ctas, int64_t slots, double* efficiency, int64_
 
 int gemm_last_plan(char* buf, int len) {
     std::lock_guard<std::mutex> lk(g_mu);
-    return copy_out(g_last_plan, buf, len);
+    if (!g_last_op.op) return copy_out(g_last_plan, buf, len);
+    std::string s = glk::plan_json(g_last_op.plan, g_last_op.M, g_last_op.N, g_last_op.K);
+    const std::string key = "\"op\": \"";
+    for (size_t at = s.find(key); at != std::string::npos; at = s.find(key, at)) {
+        at += key.size();
+        s.replace(at, s.find('"', at) - at, g_last_op.op);
+    }
+    return copy_out(s, buf, len);
 }
 
 const char* gemm_status_string(int status) {

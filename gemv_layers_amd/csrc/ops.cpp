@@ -1,0 +1,211 @@
+// Entry points of the 8-bit and training products (declared in include/gemm_bf16.h): argument
+// checks on the host before any HIP call, planning, and dispatch onto the caller's stream.
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "abi.h"
+#include "gemm_bf16.h"
+#include "kernels.h"
+#include "ops.h"
+
+namespace {
+
+using glk::OpArgs;
+
+constexpr int64_t kMaxCodesK = 131071;  // 128 * 128 * K < 2^31
+constexpr int64_t kMaxRows = (int64_t(1) << 24) - 1;  // one workgroup of 256 per row, 32-bit grids
+
+bool misaligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }
+
+hipStream_t hip_stream(gemm_stream_t s) { return reinterpret_cast<hipStream_t>(s); }
+
+const char* op_name(int mode, bool glu) {
+    switch (mode) {
+        case glk::kOpI8: return glu ? "i8_swiglu" : "i8";
+        case glk::kOpAbt: return "grad_a";
+        case glk::kOpAtb: return "grad_b";
+        default: return "swiglu_train";
+    }
+}
+
+// One product on the current device: M, N > 0, operands checked.
+int run_op(int mode, bool glu, const OpArgs& a, hipStream_t stream) {
+    int st = GEMM_OK;
+    const glk::DeviceInfo* dev = glk::current_device(&st);
+    if (!dev) return st;
+    glk::Plan p;
+    hipError_t e = hipSuccess;
+    if (a.K == 0) {
+        p = glk::make_plan(a.M, a.N, 0, *dev, false, 2, glu);
+        e = glk::launch_zero_c(a.C, a.M, a.N, a.ldc, stream);
+        if (e == hipSuccess && mode == glk::kOpTrain) e = glk::launch_zero_c(a.GU, a.M, 2 * a.N, a.ldgu, stream);
+    } else {
+        p = glk::make_plan(a.M, a.N, a.K, *dev, false, 2, glu);
+        e = glk::launch_op_generic(mode, glu, a, stream);
+    }
+    if (e != hipSuccess) return GEMM_ERR_HIP;
+    glk::set_last_plan(p, a.M, a.N, a.K, op_name(mode, glu));
+    return GEMM_OK;
+}
+
+// checks shared by the 8-bit products; `rows` of Wq are N or 2N
+int check_i8(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const void* Wq, int64_t ldwq,
+             const float* Sw, const void* C, int64_t ldc, bool glu) {
+    if (M < 0 || N < 0 || K < 0 || (glu && N > INT64_MAX / 2)) return GEMM_ERR_INVALID_ARG;
+    if (lda < K || ldwq < K || ldc < N) return GEMM_ERR_INVALID_ARG;
+    if (M > 0 && K > 0 && !A) return GEMM_ERR_INVALID_ARG;
+    if (N > 0 && ((K > 0 && !Wq) || !Sw || misaligned(Sw, 4))) return GEMM_ERR_INVALID_ARG;
+    if (M > 0 && N > 0 && (!C || misaligned(C, 2))) return GEMM_ERR_INVALID_ARG;
+    if (K > kMaxCodesK) return GEMM_ERR_UNSUPPORTED;
+    return GEMM_OK;
+}
+
+int i8_product(int64_t M, int64_t N, int64_t K, const void* Aq, int64_t ldaq, const float* Sa, const void* Wq,
+               int64_t ldwq, const float* Sw, void* C, int64_t ldc, bool glu, hipStream_t stream) {
+    const int st = check_i8(M, N, K, Aq, ldaq, Wq, ldwq, Sw, C, ldc, glu);
+    if (st != GEMM_OK) return st;
+    if (M > 0 && (!Sa || misaligned(Sa, 4))) return GEMM_ERR_INVALID_ARG;
+    if (M == 0 || N == 0) return GEMM_OK;
+    const OpArgs a{Aq, Wq, static_cast<uint16_t*>(C), nullptr, Sa, Sw, M, N, K, ldaq, ldwq, ldc, 0};
+    return run_op(glk::kOpI8, glu, a, stream);
+}
+
+int quantize(int64_t R, int64_t K, const void* X, int64_t ldx, void* Q, int64_t ldq, float* S, hipStream_t stream) {
+    if (R < 0 || K < 0 || ldx < K || ldq < K) return GEMM_ERR_INVALID_ARG;
+    if (R > 0 && (!S || misaligned(S, 4) || misaligned(X, 2))) return GEMM_ERR_INVALID_ARG;
+    if (R > 0 && K > 0 && (!X || !Q)) return GEMM_ERR_INVALID_ARG;
+    if (R > kMaxRows) return GEMM_ERR_UNSUPPORTED;
+    if (R == 0) return GEMM_OK;
+    int st = GEMM_OK;
+    if (!glk::current_device(&st)) return st;
+    return glk::launch_i8_quantize(static_cast<const uint16_t*>(X), R, K, ldx, static_cast<int8_t*>(Q), ldq, S,
+                                   stream) == hipSuccess
+               ? GEMM_OK
+               : GEMM_ERR_HIP;
+}
+
+// M x K codes with rows padded to 16 bytes, then M scales
+int64_t padded_codes(int64_t K) { return (K + 15) / 16 * 16; }
+int64_t work_bytes_of(int64_t M, int64_t K) { return M * padded_codes(K) + 4 * M; }
+
+int i8_product_bf16(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const void* Wq, int64_t ldwq,
+                    const float* Sw, void* C, int64_t ldc, void* work, int64_t work_bytes, bool glu,
+                    hipStream_t stream) {
+    int st = check_i8(M, N, K, A, lda, Wq, ldwq, Sw, C, ldc, glu);
+    if (st != GEMM_OK) return st;
+    if (M > 0 && misaligned(A, 2)) return GEMM_ERR_INVALID_ARG;
+    if (M > kMaxRows) return GEMM_ERR_UNSUPPORTED;
+    if (M == 0 || N == 0) return GEMM_OK;
+    if (!work || misaligned(work, 16) || work_bytes < work_bytes_of(M, K)) return GEMM_ERR_INVALID_ARG;
+    const int64_t ldq = padded_codes(K);
+    float* sa = reinterpret_cast<float*>(static_cast<char*>(work) + M * ldq);
+    st = quantize(M, K, A, lda, work, ldq, sa, stream);
+    if (st != GEMM_OK) return st;
+    return i8_product(M, N, K, work, ldq, sa, Wq, ldwq, Sw, C, ldc, glu, stream);
+}
+
+// dA = D B^T and dB = A^T D for D (M x W), either skipped when null
+int gradients(int64_t M, int64_t W, int64_t K, const void* D, int64_t ldd, const void* A, int64_t lda,
+              const void* B, int64_t ldb, void* dA, int64_t ldda, void* dB, int64_t lddb, hipStream_t stream) {
+    if (dA && M > 0 && K > 0) {
+        const OpArgs a{D, B, static_cast<uint16_t*>(dA), nullptr, nullptr, nullptr, M, K, W, ldd, ldb, ldda, 0};
+        const int st = run_op(glk::kOpAbt, false, a, stream);
+        if (st != GEMM_OK) return st;
+    }
+    if (dB && K > 0 && W > 0) {
+        const OpArgs a{A, D, static_cast<uint16_t*>(dB), nullptr, nullptr, nullptr, K, W, M, lda, ldd, lddb, 0};
+        return run_op(glk::kOpAtb, false, a, stream);
+    }
+    return GEMM_OK;
+}
+
+// checks of the operands of `gradients`; W columns of D
+int check_gradients(int64_t M, int64_t W, int64_t K, const void* A, int64_t lda, const void* B, int64_t ldb,
+                    const void* dA, int64_t ldda, const void* dB, int64_t lddb) {
+    if (dA && (ldb < W || ldda < K || (K > 0 && W > 0 && !B))) return GEMM_ERR_INVALID_ARG;
+    if (dB && (lda < K || lddb < W || (M > 0 && K > 0 && !A))) return GEMM_ERR_INVALID_ARG;
+    if ((dA && (misaligned(dA, 2) || misaligned(B, 2))) || (dB && (misaligned(dB, 2) || misaligned(A, 2))))
+        return GEMM_ERR_INVALID_ARG;
+    return GEMM_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int gemm_i8_quantize(int64_t R, int64_t K, const void* X, int64_t ldx, void* Q, int64_t ldq, float* S,
+                     gemm_stream_t stream) {
+    return quantize(R, K, X, ldx, Q, ldq, S, hip_stream(stream));
+}
+
+int gemm_i8(int64_t M, int64_t N, int64_t K, const void* Aq, int64_t ldaq, const float* Sa, const void* Wq,
+            int64_t ldwq, const float* Sw, void* C, int64_t ldc, gemm_stream_t stream) {
+    return i8_product(M, N, K, Aq, ldaq, Sa, Wq, ldwq, Sw, C, ldc, false, hip_stream(stream));
+}
+
+int gemm_i8_swiglu(int64_t M, int64_t N, int64_t K, const void* Aq, int64_t ldaq, const float* Sa, const void* Wq,
+                   int64_t ldwq, const float* Sw, void* C, int64_t ldc, gemm_stream_t stream) {
+    return i8_product(M, N, K, Aq, ldaq, Sa, Wq, ldwq, Sw, C, ldc, true, hip_stream(stream));
+}
+
+int gemm_i8_work_bytes(int64_t M, int64_t K, int64_t* bytes) {
+    if (M < 0 || K < 0 || !bytes) return GEMM_ERR_INVALID_ARG;
+    if (M > kMaxRows || K > kMaxCodesK) return GEMM_ERR_UNSUPPORTED;
+    *bytes = work_bytes_of(M, K);
+    return GEMM_OK;
+}
+
+int gemm_i8_bf16(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const void* Wq, int64_t ldwq,
+                 const float* Sw, void* C, int64_t ldc, void* work, int64_t work_bytes, gemm_stream_t stream) {
+    return i8_product_bf16(M, N, K, A, lda, Wq, ldwq, Sw, C, ldc, work, work_bytes, false, hip_stream(stream));
+}
+
+int gemm_i8_swiglu_bf16(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const void* Wq, int64_t ldwq,
+                        const float* Sw, void* C, int64_t ldc, void* work, int64_t work_bytes,
+                        gemm_stream_t stream) {
+    return i8_product_bf16(M, N, K, A, lda, Wq, ldwq, Sw, C, ldc, work, work_bytes, true, hip_stream(stream));
+}
+
+int gemm_bf16_bwd(int64_t M, int64_t N, int64_t K, const void* dC, int64_t lddc, const void* A, int64_t lda,
+                  const void* B, int64_t ldb, void* dA, int64_t ldda, void* dB, int64_t lddb,
+                  gemm_stream_t stream) {
+    if (M < 0 || N < 0 || K < 0 || lddc < N || misaligned(dC, 2)) return GEMM_ERR_INVALID_ARG;
+    if ((dA || dB) && M > 0 && N > 0 && K > 0 && !dC) return GEMM_ERR_INVALID_ARG;
+    const int st = check_gradients(M, N, K, A, lda, B, ldb, dA, ldda, dB, lddb);
+    if (st != GEMM_OK) return st;
+    return gradients(M, N, K, dC, lddc, A, lda, B, ldb, dA, ldda, dB, lddb, hip_stream(stream));
+}
+
+int gemm_bf16_swiglu_train(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const void* B, int64_t ldb,
+                           void* GU, int64_t ldgu, void* C, int64_t ldc, gemm_stream_t stream) {
+    if (M < 0 || N < 0 || K < 0 || N > INT64_MAX / 2) return GEMM_ERR_INVALID_ARG;
+    if (lda < K || ldb < 2 * N || ldgu < 2 * N || ldc < N) return GEMM_ERR_INVALID_ARG;
+    if ((M > 0 && K > 0 && !A) || (K > 0 && N > 0 && !B) || (M > 0 && N > 0 && (!GU || !C)))
+        return GEMM_ERR_INVALID_ARG;
+    if (misaligned(A, 2) || misaligned(B, 2) || misaligned(GU, 2) || misaligned(C, 2)) return GEMM_ERR_INVALID_ARG;
+    if (M == 0 || N == 0) return GEMM_OK;
+    const OpArgs a{A, B, static_cast<uint16_t*>(C), static_cast<uint16_t*>(GU), nullptr, nullptr,
+                   M, N, K, lda, ldb, ldc, ldgu};
+    return run_op(glk::kOpTrain, true, a, hip_stream(stream));
+}
+
+int gemm_bf16_swiglu_bwd(int64_t M, int64_t N, int64_t K, const void* dC, int64_t lddc, const void* GU,
+                         int64_t ldgu, const void* A, int64_t lda, const void* B, int64_t ldb, void* dGU,
+                         int64_t lddgu, void* dA, int64_t ldda, void* dB, int64_t lddb, gemm_stream_t stream) {
+    if (M < 0 || N < 0 || K < 0 || N > INT64_MAX / 2) return GEMM_ERR_INVALID_ARG;
+    if (lddc < N || ldgu < 2 * N || lddgu < 2 * N) return GEMM_ERR_INVALID_ARG;
+    if (M > 0 && N > 0 && (!dC || !GU || !dGU)) return GEMM_ERR_INVALID_ARG;
+    if (misaligned(dC, 2) || misaligned(GU, 2) || misaligned(dGU, 2)) return GEMM_ERR_INVALID_ARG;
+    int st = check_gradients(M, 2 * N, K, A, lda, B, ldb, dA, ldda, dB, lddb);
+    if (st != GEMM_OK) return st;
+    if (M > 0 && N > 0) {
+        if (!glk::current_device(&st)) return st;
+        if (glk::launch_swiglu_grad(static_cast<const uint16_t*>(dC), lddc, static_cast<const uint16_t*>(GU), ldgu,
+                                    static_cast<uint16_t*>(dGU), lddgu, M, N, hip_stream(stream)) != hipSuccess)
+            return GEMM_ERR_HIP;
+    }
+    return gradients(M, 2 * N, K, dGU, lddgu, A, lda, B, ldb, dA, ldda, dB, lddb, hip_stream(stream));
+}
+
+}  // extern "C"

@@ -1,0 +1,41 @@
+// Launch interfaces of the 8-bit and training kernels (internal header).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace glk {
+
+// Which product a kernel computes. "Contiguous" operands hold the summed index contiguous in
+// memory, "strided" ones hold it as their row index.
+enum OpMode : int {
+    kOpI8 = 0,     // C = (A W^T) sa sw: 8-bit codes, both operands contiguous (W is N x K)
+    kOpAbt = 1,    // C = A B^T: bf16, both operands contiguous (B is N x K)
+    kOpAtb = 2,    // C = A^T B: bf16, both operands strided (A is K x M, B is K x N)
+    kOpTrain = 3,  // GU = A B, C = silu(g) u: bf16, A contiguous, B (K x 2N) strided; gated
+};
+
+// One product: an M x N output summed over K. Sizes and leading dimensions are in elements.
+struct OpArgs {
+    const void* A;
+    const void* B;
+    uint16_t* C;
+    uint16_t* GU;     // kOpTrain: M x 2N
+    const float* sa;  // kOpI8: M
+    const float* sb;  // kOpI8: N, or 2N gated
+    int64_t M, N, K;
+    int64_t lda, ldb, ldc, ldgu;
+};
+
+// ---- general kernel (any alignment, leading dimension or size) -------------------------------
+hipError_t launch_op_generic(int mode, bool glu, const OpArgs& a, hipStream_t s);
+
+// ---- row kernels --------------------------------------------------------------------------------
+// symmetric 8-bit codes of each row: see gemm_i8_quantize
+hipError_t launch_i8_quantize(const uint16_t* X, int64_t R, int64_t K, int64_t ldx, int8_t* Q, int64_t ldq,
+                              float* S, hipStream_t s);
+// dGU from dC and GU: see gemm_bf16_swiglu_bwd
+hipError_t launch_swiglu_grad(const uint16_t* dC, int64_t lddc, const uint16_t* GU, int64_t ldgu, uint16_t* dGU,
+                              int64_t lddgu, int64_t M, int64_t N, hipStream_t s);
+
+}  // namespace glk

@@ -1,0 +1,217 @@
+// Row kernels of the 8-bit and training operators: one pass over memory each.
+//
+// Quantisation, s = max|x| / 127 in float32 and q = round(x / s) for each row. A row stays in the
+// registers of its workgroup between the maximum and the codes, so that memory is read once (2
+// bytes an element) and written once (1 byte). The maximum is an integer one over the magnitude
+// bits of bf16, whose order is that of the values, infinities and NaN last: no value is lost to a
+// comparison with NaN. The codes are those of the correctly rounded float32 quotient x / s, from
+// one multiplication by 127 / max|x|: with bf16 x, 127 x / max|x| = k + 1/2 means 254 x = (2 k + 1)
+// max|x|, so 127 divides 2 k + 1 (then |x| = max|x| / 2, whose code is divided out once a row) or the
+// mantissa of max|x| (then s and the factor are powers of two and nothing rounds). Any other x is
+// off half-way by 1 / (254 * 255) of its size at least, 100 times the float32 roundings of either way.
+
+// The gated block's gradient, element by element: reads dC, g and u, writes dg and du, 10 bytes an
+// element.
+
+#include "common.h"
+#include "ops.h"
+
+namespace glk {
+
+struct CodeScale {
+    float s, inv;     // the row's scale, and 127 / max|x|
+    float half, qh;   // max|x| / 2, and the magnitude of its code
+    bool divide;      // a row so small that the scale may be subnormal: every code by division
+    bool none;        // a row of zeros, or with an infinity or NaN: codes 0
+};
+__device__ __forceinline__ CodeScale code_scale(uint32_t amax_bits) {
+    const float amax = __builtin_bit_cast(float, amax_bits << 16);
+    CodeScale c;
+    c.none = amax_bits == 0 || amax_bits >= 0x7F80u;
+    c.s = amax_bits >= 0x7F80u ? __builtin_nanf("") : amax / 127.0f;
+    c.divide = amax < 0x1p-60f;
+    c.inv = 127.0f / amax;
+    c.half = 0.5f * amax;
+    c.qh = rintf(c.half / c.s);
+    return c;
+}
+__device__ __forceinline__ int code_of(float x, const CodeScale& c) {
+    if (c.none) return 0;
+    if (c.divide) return (int)rintf(x / c.s);
+    const float q = rintf(x * c.inv);
+    return (int)(fabsf(x) == c.half ? copysignf(c.qh, x) : q);
+}
+
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) v = max(v, (uint32_t)__shfl_xor((int)v, o));
+    return v;
+}
+
+// one row per workgroup of NW waves, NC 16-byte chunks per thread in registers
+template <int NW, int NC>
+__global__ void __launch_bounds__(64 * NW) i8_quantize_kernel(const uint16_t* __restrict__ X, int K, int64_t ldx,
+                                                              int8_t* __restrict__ Q, int64_t ldq,
+                                                              float* __restrict__ S) {
+    __shared__ uint32_t part[NW];
+    const int tid = threadIdx.x;
+    const int64_t r = blockIdx.x;
+    const uint16_t* x = X + r * ldx;
+    u32x4 v[NC];
+    uint32_t amax = 0;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+        const int k = 8 * (c * 64 * NW + tid);
+        v[c] = u32x4{0, 0, 0, 0};
+        if (k + 8 <= K) {
+            v[c] = *reinterpret_cast<const u32x4*>(x + k);
+        } else if (k < K) {
+            uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+            for (int j = 0; j < 7; ++j)
+                if (k + j < K) w[j >> 1] |= (uint32_t)x[k + j] << (16 * (j & 1));
+            v[c] = u32x4{w[0], w[1], w[2], w[3]};
+        }
+    }
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) amax = max(amax, max(v[c][j] & 0x7FFFu, (v[c][j] >> 16) & 0x7FFFu));
+    amax = wave_max(amax);
+    if constexpr (NW > 1) {
+        if ((tid & 63) == 0) part[tid >> 6] = amax;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < NW; ++w) amax = max(amax, part[w]);
+    }
+    const CodeScale cs = code_scale(amax);
+    if (tid == 0) S[r] = cs.s;
+    int8_t* q = Q + r * ldq;
+    const int64_t padded = min(ldq, (int64_t)(K + 15) / 16 * 16);
+    const bool wide = ((reinterpret_cast<uintptr_t>(Q) | (uintptr_t)ldq) & 7) == 0;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+        const int64_t k = 8 * ((int64_t)c * 64 * NW + tid);
+        if (k >= padded) continue;
+        uint32_t w[2] = {0, 0};  // (elements past K are zero in v)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float e = (j & 1) ? bf16_hi(v[c][j >> 1]) : bf16_lo(v[c][j >> 1]);
+            w[j >> 2] |= ((uint32_t)code_of(e, cs) & 0xFFu) << (8 * (j & 3));
+        }
+        if (wide && k + 8 <= padded) {
+            *reinterpret_cast<u32x2*>(q + k) = u32x2{w[0], w[1]};
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (k + j < padded) q[k + j] = (int8_t)(w[j >> 2] >> (8 * (j & 3)));
+        }
+    }
+}
+
+// any alignment and length: two passes over the row, element by element
+__global__ void __launch_bounds__(256) i8_quantize_any_kernel(const uint16_t* __restrict__ X, int64_t K, int64_t ldx,
+                                                              int8_t* __restrict__ Q, int64_t ldq,
+                                                              float* __restrict__ S) {
+    __shared__ uint32_t part[4];
+    const int tid = threadIdx.x;
+    const int64_t r = blockIdx.x;
+    const uint16_t* x = X + r * ldx;
+    uint32_t amax = 0;
+    for (int64_t k = tid; k < K; k += 256) amax = max(amax, (uint32_t)x[k] & 0x7FFFu);
+    amax = wave_max(amax);
+    if ((tid & 63) == 0) part[tid >> 6] = amax;
+    __syncthreads();
+    amax = max(max(part[0], part[1]), max(part[2], part[3]));
+    const CodeScale cs = code_scale(amax);
+    if (tid == 0) S[r] = cs.s;
+    int8_t* q = Q + r * ldq;
+    const int64_t padded = min(ldq, (K + 15) / 16 * 16);
+    for (int64_t k = tid; k < padded; k += 256)
+        q[k] = k < K ? (int8_t)code_of(__builtin_bit_cast(float, (uint32_t)x[k] << 16), cs) : (int8_t)0;
+}
+
+hipError_t launch_i8_quantize(const uint16_t* X, int64_t R, int64_t K, int64_t ldx, int8_t* Q, int64_t ldq,
+                              float* S, hipStream_t s) {
+    if (R > 0xFFFFFF) return hipErrorInvalidValue;
+    const unsigned grid = (unsigned)R;
+    const bool aligned = ((reinterpret_cast<uintptr_t>(X) & 15) == 0) && (ldx % 8 == 0);
+    // chunks of 8 elements, a padded row's among them
+    const int64_t chunks = (K + 15) / 16 * 2;
+    if (!aligned || chunks > 256 * 8)
+        i8_quantize_any_kernel<<<grid, 256, 0, s>>>(X, K, ldx, Q, ldq, S);
+    else if (chunks <= 64)
+        i8_quantize_kernel<1, 1><<<grid, 64, 0, s>>>(X, (int)K, ldx, Q, ldq, S);
+    else if (chunks <= 256)
+        i8_quantize_kernel<4, 1><<<grid, 256, 0, s>>>(X, (int)K, ldx, Q, ldq, S);
+    else if (chunks <= 512)
+        i8_quantize_kernel<4, 2><<<grid, 256, 0, s>>>(X, (int)K, ldx, Q, ldq, S);
+    else if (chunks <= 1024)
+        i8_quantize_kernel<4, 4><<<grid, 256, 0, s>>>(X, (int)K, ldx, Q, ldq, S);
+    else
+        i8_quantize_kernel<4, 8><<<grid, 256, 0, s>>>(X, (int)K, ldx, Q, ldq, S);
+    return hipGetLastError();
+}
+
+// ---- the gated block's gradient -------------------------------------------------------------------
+
+// du = d silu(g), dg = d u s (1 + g (1 - s)) with s = sigmoid(g), in float32
+__device__ __forceinline__ void swiglu_grad1(float d, float g, float u, float& dg, float& du) {
+    const float sig = 1.0f / (1.0f + expf(-g));
+    du = d * (g * sig);
+    dg = d * u * (sig * (1.0f + g * (1.0f - sig)));
+}
+
+// dGU may be GU itself: every element is read by the thread that writes it, before it does
+__global__ void __launch_bounds__(256) swiglu_grad_kernel(const uint16_t* __restrict__ dC, int64_t lddc,
+                                                          const uint16_t* GU, int64_t ldgu, uint16_t* dGU,
+                                                          int64_t lddgu, int64_t M, int64_t N) {
+    const int64_t per_row = N / 8, total = M * per_row;
+    const int64_t step = (int64_t)gridDim.x * 256;
+    for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < total; e += step) {
+        const int64_t m = e / per_row, n = 8 * (e - m * per_row);
+        const u32x4 d = *reinterpret_cast<const u32x4*>(dC + m * lddc + n);
+        const u32x4 g = *reinterpret_cast<const u32x4*>(GU + m * ldgu + n);
+        const u32x4 u = *reinterpret_cast<const u32x4*>(GU + m * ldgu + N + n);
+        u32x4 og, ou;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            float g0, g1, u0, u1;
+            swiglu_grad1(bf16_lo(d[j]), bf16_lo(g[j]), bf16_lo(u[j]), g0, u0);
+            swiglu_grad1(bf16_hi(d[j]), bf16_hi(g[j]), bf16_hi(u[j]), g1, u1);
+            og[j] = pack_bf16x2(g0, g1);
+            ou[j] = pack_bf16x2(u0, u1);
+        }
+        *reinterpret_cast<u32x4*>(dGU + m * lddgu + n) = og;
+        *reinterpret_cast<u32x4*>(dGU + m * lddgu + N + n) = ou;
+    }
+}
+
+__global__ void __launch_bounds__(256) swiglu_grad_any_kernel(const uint16_t* __restrict__ dC, int64_t lddc,
+                                                              const uint16_t* GU, int64_t ldgu, uint16_t* dGU,
+                                                              int64_t lddgu, int64_t M, int64_t N) {
+    const int64_t total = M * N, step = (int64_t)gridDim.x * 256;
+    auto wide = [](uint16_t h) { return __builtin_bit_cast(float, (uint32_t)h << 16); };
+    for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < total; e += step) {
+        const int64_t m = e / N, n = e - m * N;
+        float dg, du;
+        swiglu_grad1(wide(dC[m * lddc + n]), wide(GU[m * ldgu + n]), wide(GU[m * ldgu + N + n]), dg, du);
+        dGU[m * lddgu + n] = __builtin_bit_cast(uint16_t, (__bf16)dg);
+        dGU[m * lddgu + N + n] = __builtin_bit_cast(uint16_t, (__bf16)du);
+    }
+}
+
+hipError_t launch_swiglu_grad(const uint16_t* dC, int64_t lddc, const uint16_t* GU, int64_t ldgu, uint16_t* dGU,
+                              int64_t lddgu, int64_t M, int64_t N, hipStream_t s) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(dC) | reinterpret_cast<uintptr_t>(GU) | reinterpret_cast<uintptr_t>(dGU);
+    const bool vec = (at & 15) == 0 && ((N | lddc | ldgu | lddgu) & 7) == 0;
+    int64_t blocks = ((vec ? M * (N / 8) : M * N) + 255) / 256;
+    if (blocks > (1 << 20)) blocks = 1 << 20;
+    if (vec)
+        swiglu_grad_kernel<<<(unsigned)blocks, 256, 0, s>>>(dC, lddc, GU, ldgu, dGU, lddgu, M, N);
+    else
+        swiglu_grad_any_kernel<<<(unsigned)blocks, 256, 0, s>>>(dC, lddc, GU, ldgu, dGU, lddgu, M, N);
+    return hipGetLastError();
+}
+
+}  // namespace glk

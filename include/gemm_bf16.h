@@ -246,6 +246,130 @@ int gemm_pack_weight_bf16(int64_t K, int64_t N, const void *B, int64_t ldb, void
 int gemm_bf16_packed(int64_t M, int64_t N, int64_t K, const void *A, int64_t lda, const void *Bp,
                      void *C, int64_t ldc, gemm_stream_t stream);
 
+/* ------------------------------------------------------------------------------------------
+ * 8-bit integer products: C = (Aq * Wq^T) scaled by one float32 factor for each row of A (token)
+ * and one for each row of W (output channel). Codes are signed 8-bit integers, the sums are exact
+ * 32-bit integers, and each output is rounded once to bf16 (round to nearest even):
+ *   C[m][n] = bf16( Sa[m] * Sw[n] * sum_k Aq[m][k] Wq[n][k] ).
+ * Weights use the nn.Linear layout of the block-scaled calls above: row n of W holds the K inputs
+ * of output n. Both operands are row-major bytes with K contiguous.
+ * ------------------------------------------------------------------------------------------ */
+
+/*
+ * gemm_i8_quantize: symmetric 8-bit codes of each row of a bf16 matrix X (R x K, ldx >= K): the
+ * rows of activations are tokens, the rows of an nn.Linear weight are output channels.
+ *   S[r] = max_k |X[r][k]| / 127 (float32),  Q[r][k] = round(X[r][k] / S[r]), ties to even,
+ * which lies in [-127, 127]. A row of zeros gets S = 0 and codes 0. A row that holds an infinity
+ * or a NaN gets S = NaN and codes 0, so that every output made from it is NaN. Q is R x K bytes
+ * (ldq >= K); bytes K .. min(ldq, K rounded up to 16) - 1 of each row are written as zeros. S is R
+ * float32 values, 4-byte aligned. X needs 2-byte alignment only; 16-byte alignment with ldx % 8
+ * == 0 is faster.
+ * R == 0: nothing. K == 0: S = 0. GEMM_ERR_INVALID_ARG for negative sizes, ldx < K, ldq < K, a
+ * null pointer with a non-empty extent, or a misaligned X or S; GEMM_ERR_UNSUPPORTED for R >= 2^24.
+ * Deterministic, one launch.
+ */
+int gemm_i8_quantize(int64_t R, int64_t K, const void *X, int64_t ldx, void *Q, int64_t ldq,
+                     float *S, gemm_stream_t stream);
+
+/*
+ * gemm_i8: the scaled product above. Aq is M x K codes (ldaq >= K), Sa M float32, Wq N x K codes
+ * (ldwq >= K), Sw N float32, C M x N bf16 (ldc >= N, fully overwritten, no overlap with the
+ * inputs). Any code from -128 to 127 is taken. Aq and Wq with 16-byte aligned pointers and
+ * leading dimensions (what gemm_i8_quantize writes with ldq a multiple of 16) run the matrix
+ * kernels for any M, N and K; other operands run a general kernel with the same result, bit for
+ * bit. Bytes between K and the leading dimension may hold anything.
+ * M == 0 or N == 0: nothing. K == 0: C = 0. GEMM_ERR_INVALID_ARG for negative sizes, a leading
+ * dimension that is too small, a null pointer with a non-empty extent, a C that is not 2-byte or
+ * a scale that is not 4-byte aligned; GEMM_ERR_UNSUPPORTED for K > 131071, beyond which 32-bit
+ * sums could overflow. Deterministic, enqueued without synchronising, and using the stream's
+ * workspace region like gemm_bf16.
+ */
+int gemm_i8(int64_t M, int64_t N, int64_t K, const void *Aq, int64_t ldaq, const float *Sa,
+            const void *Wq, int64_t ldwq, const float *Sw, void *C, int64_t ldc,
+            gemm_stream_t stream);
+
+/*
+ * gemm_i8_swiglu: the gate and up projections of gemm_bf16_swiglu in 8 bits:
+ *   C = silu(g) .* u,  g = scaled product with rows 0 .. N-1 of Wq, u with rows N .. 2N-1.
+ * Wq is 2N x K codes and Sw 2N float32; g and u stay in registers (float32) and only C (M x N) is
+ * rounded. Otherwise as gemm_i8.
+ */
+int gemm_i8_swiglu(int64_t M, int64_t N, int64_t K, const void *Aq, int64_t ldaq, const float *Sa,
+                   const void *Wq, int64_t ldwq, const float *Sw, void *C, int64_t ldc,
+                   gemm_stream_t stream);
+
+/*
+ * gemm_i8_work_bytes: host-only. Bytes of the buffer `work` that gemm_i8_bf16 and
+ * gemm_i8_swiglu_bf16 need for M x K activations (codes with rows padded to 16 bytes, then scales).
+ * GEMM_ERR_INVALID_ARG for negative sizes or a null result pointer; GEMM_ERR_UNSUPPORTED when M
+ * reaches 2^24 or K exceeds 131071.
+ */
+int gemm_i8_work_bytes(int64_t M, int64_t K, int64_t *bytes);
+
+/*
+ * gemm_i8_bf16: gemm_i8_quantize of the bf16 activations A (M x K, lda >= K) into `work`, then
+ * gemm_i8: the 8-bit product with dynamic activation scales in one call, the same bits as the two.
+ * `work` is device memory of at least gemm_i8_work_bytes(M, K) bytes, 16-byte aligned, that the
+ * caller owns and may reuse once the call's work on the stream is done; `work_bytes` is its size
+ * (GEMM_ERR_INVALID_ARG when it is too small or misaligned).
+ */
+int gemm_i8_bf16(int64_t M, int64_t N, int64_t K, const void *A, int64_t lda, const void *Wq,
+                 int64_t ldwq, const float *Sw, void *C, int64_t ldc, void *work,
+                 int64_t work_bytes, gemm_stream_t stream);
+
+/* gemm_i8_swiglu_bf16: gemm_i8_quantize of A into `work`, then gemm_i8_swiglu; as gemm_i8_bf16. */
+int gemm_i8_swiglu_bf16(int64_t M, int64_t N, int64_t K, const void *A, int64_t lda, const void *Wq,
+                        int64_t ldwq, const float *Sw, void *C, int64_t ldc, void *work,
+                        int64_t work_bytes, gemm_stream_t stream);
+
+/* ------------------------------------------------------------------------------------------
+ * Training: the backward pass of gemm_bf16, and the gated block's forward and backward pass.
+ * bf16 operands row-major as in gemm_bf16, float32 accumulation, each output rounded once to bf16
+ * (round to nearest even). Operands whose pointers are not 16-byte aligned, or whose widths or
+ * leading dimensions are not multiples of 8, run a general kernel with the same contract; the
+ * number of tokens M is free. Deterministic (sums in a fixed order, no atomics on data), enqueued
+ * on `stream` without synchronising, using the stream's workspace region like gemm_bf16.
+ * ------------------------------------------------------------------------------------------ */
+
+/*
+ * gemm_bf16_bwd: the gradients of C = A * B (A M x K, B K x N) from dC (M x N, lddc >= N):
+ *   dA = dC * B^T (M x K, ldda >= K),   dB = A^T * dC (K x N, lddb >= N).
+ * A null dA or dB is not computed; then B or A respectively is not read and may be null. An empty
+ * sum (N == 0 for dA, M == 0 for dB) writes zeros. Both are overwritten, not accumulated into.
+ * GEMM_ERR_INVALID_ARG for negative sizes, a leading dimension that is too small, or a null operand
+ * that is needed.
+ */
+int gemm_bf16_bwd(int64_t M, int64_t N, int64_t K, const void *dC, int64_t lddc, const void *A,
+                  int64_t lda, const void *B, int64_t ldb, void *dA, int64_t ldda, void *dB,
+                  int64_t lddb, gemm_stream_t stream);
+
+/*
+ * gemm_bf16_swiglu_train: gemm_bf16_swiglu that also keeps what the backward pass needs:
+ *   GU = A * B (M x 2N bf16, ldgu >= 2N: g, then u),   C = silu(g) .* u (M x N bf16).
+ * C is made from the float32 g and u, so it is gemm_bf16_swiglu's C within float32 rounding.
+ * M == 0 or N == 0: nothing. K == 0: GU = 0 and C = 0. Errors as gemm_bf16_swiglu, and
+ * GEMM_ERR_INVALID_ARG for ldgu < 2N or a null GU.
+ */
+int gemm_bf16_swiglu_train(int64_t M, int64_t N, int64_t K, const void *A, int64_t lda,
+                           const void *B, int64_t ldb, void *GU, int64_t ldgu, void *C, int64_t ldc,
+                           gemm_stream_t stream);
+
+/*
+ * gemm_bf16_swiglu_bwd: the gradients of C = silu(g) .* u, (g | u) = A * B, from dC (M x N) and the
+ * bf16 GU that the forward pass kept (M x 2N):
+ *   du = dC .* silu(g),   dg = dC .* u .* s (1 + g (1 - s)),   s = 1 / (1 + e^-g),
+ *   dGU = (dg | du) (M x 2N bf16, lddgu >= 2N),
+ *   dA = dGU * B^T (M x K),   dB = A^T * dGU (K x 2N, lddb >= 2N).
+ * dg and du are computed in float32 and rounded once to bf16, the operand type of the two products.
+ * dGU is always written; it may be GU itself (the same pointer and leading dimension), which is then
+ * overwritten. A null dA or dB is not computed, and then B or A is not read. Empty sums write
+ * zeros. Errors as gemm_bf16_bwd.
+ */
+int gemm_bf16_swiglu_bwd(int64_t M, int64_t N, int64_t K, const void *dC, int64_t lddc,
+                         const void *GU, int64_t ldgu, const void *A, int64_t lda, const void *B,
+                         int64_t ldb, void *dGU, int64_t lddgu, void *dA, int64_t ldda, void *dB,
+                         int64_t lddb, gemm_stream_t stream);
+
 /* Flags of gemm_plan_describe. */
 #define GEMM_PLAN_SKINNY 1 /* the plan of gemm_bf16_skinny */
 #define GEMM_PLAN_SWIGLU 2 /* the plan of gemm_bf16_swiglu (with GEMM_PLAN_SKINNY: its skinny form) */

@@ -1,0 +1,371 @@
+"""The 8-bit products on the GPU against integer sums and float64.
+
+gemm_i8's result is pinned bit for bit: the 32-bit sum is exact, and its float32 conversion and two
+multiplications by the scales are single IEEE operations that numpy repeats. The gated form is held
+to a bound: g and u carry three float32 roundings each (3 * 2^-24, taken as 2^-22), which the slope of
+silu (at most 1.1) passes on; evaluating silu and the product adds 2^-20 of the result, and the
+rounding to bf16 2^-8 (as in the float product's check). Codes of gemm_i8_quantize are compared with
+the definition's two float32 divisions, bit for bit.
+"""
+
+import ctypes
+
+import numpy as np
+import pytest
+
+from oracle import bf16_to_f64
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+import gemv_layers_amd as g  # noqa: E402
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _device():
+    assert torch.cuda.is_available(), "GPU tests need a ROCm device"
+    torch.cuda.set_device(0)
+    g.gemm_init(0)
+    yield
+
+
+def bits(t):
+    return t.cpu().view(torch.int16).numpy().view(np.uint16)
+
+
+def codes(rows, k, ld, seed, full=False):
+    """Random codes (with -128 when `full`), the padding between k and ld filled with them too."""
+    rng = np.random.default_rng(seed)
+    return rng.integers(-128 if full else -127, 128, (rows, max(ld, 1)), dtype=np.int8)[:, :ld]
+
+
+def bf16_of(x32):
+    """float32 -> bf16 bits, to nearest even (finite values)."""
+    u = np.ascontiguousarray(x32, np.float32).view(np.uint32)
+    return ((u + 0x7FFF + ((u >> 16) & 1)) >> 16).astype(np.uint16)
+
+
+def widen(h):
+    """bf16 bits -> float64."""
+    return bf16_to_f64(np.ascontiguousarray(h))
+
+
+def place(a, offset=0):
+    """A host array on the device, `offset` elements past the start of its allocation."""
+    flat = np.concatenate([np.zeros(offset, a.dtype), a.ravel()])
+    return torch.from_numpy(flat).cuda(), offset * a.dtype.itemsize
+
+
+def poisoned(n):
+    return torch.full((max(n, 1),), float("nan"), dtype=torch.bfloat16, device="cuda")
+
+
+def product(M, N, K, lda=None, ldw=None, ldc=None, offset=0, c_offset=0, seed=0, full=False, glu=False, sa=None):
+    """Runs gemm_i8 (or its gated form) and returns (C bits, exact sums, sa, sw, plan)."""
+    lda = -(-K // 16) * 16 if lda is None else lda
+    ldw = -(-K // 16) * 16 if ldw is None else ldw
+    ldc = N if ldc is None else ldc
+    rows = 2 * N if glu else N
+    A, W = codes(M, K, lda, seed + 1, full), codes(rows, K, ldw, seed + 2, full)
+    rng = np.random.default_rng(seed + 3)
+    sa = rng.uniform(0.5, 2, M).astype(np.float32) / 127 if sa is None else sa
+    sw = (rng.uniform(0.5, 2, rows) * 0.02 / 127 / max(K, 1) ** 0.5 * 30).astype(np.float32)
+    (dA, oa), (dW, ow) = place(A, offset), place(W, offset)
+    (dsa, _), (dsw, _) = place(sa), place(sw)
+    C = poisoned(M * ldc + c_offset)
+    fn = g.gemm_i8_swiglu if glu else g.gemm_i8
+    fn(M, N, K, dA.data_ptr() + oa, lda, dsa.data_ptr(), dW.data_ptr() + ow, ldw, dsw.data_ptr(),
+       C.data_ptr() + 2 * c_offset, ldc, g.current_stream_handle())
+    torch.cuda.synchronize()
+    out = bits(C)
+    assert (out[:c_offset] == 0x7FC0).all() or c_offset == 0
+    out = out[c_offset: c_offset + M * ldc].reshape(M, ldc)
+    # columns past N keep the poison
+    assert not (out[:, N:] != bits(poisoned(1))[0]).any(), "wrote past N"
+    acc = A[:, :K].astype(np.float64) @ W[:, :K].astype(np.float64).T
+    return out[:, :N], acc, sa, sw, g.gemm_last_plan()
+
+
+def expect(acc, sa, sw):
+    with np.errstate(invalid="ignore"):
+        return bf16_of(acc.astype(np.float32) * sa[:, None] * sw[None, :])
+
+
+# single tokens, decode batches, ragged widths, lengths of one, k-steps cut anywhere, both tile
+# sizes, K split, and products cut in two
+SHAPES = [(1, 1, 1), (1, 16, 64), (1, 520, 328), (2, 1000, 1000), (3, 17, 15), (5, 129, 4097), (16, 64, 2048),
+          (17, 257, 33), (33, 2056, 520), (64, 1000, 200), (64, 4096, 1024), (65, 520, 328), (127, 129, 65),
+          (128, 128, 64), (129, 127, 63), (256, 256, 256), (300, 1000, 1000), (509, 2501, 1003), (1000, 1000, 1000),
+          (513, 1032, 2056), (128, 256, 11008), (1031, 4099, 129), (4097, 4104, 192), (4096, 4352, 256)]
+
+
+@pytest.mark.parametrize("M,N,K", SHAPES)
+def test_i8_bits(M, N, K):
+    C, acc, sa, sw, plan = product(M, N, K, seed=M + N + K)
+    want = expect(acc, sa, sw)
+    bad = np.argwhere(C != want)
+    assert bad.size == 0, f"{M}x{N}x{K} {plan}: {len(bad)} differ, first {bad[0].tolist()}"
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 11008, 4096), (16, 4096, 11008), (64, 11008, 4096), (64, 4096, 11008)])
+def test_i8_decode_full(M, N, K):
+    C, acc, sa, sw, plan = product(M, N, K, seed=7)
+    assert np.array_equal(C, expect(acc, sa, sw)), plan
+
+
+@pytest.mark.parametrize("M,N,K,lda,ldw,ldc,off,coff", [
+    (5, 13, 7, 7, 7, 13, 1, 1),              # nothing aligned
+    (70, 100, 30, 30, 31, 101, 0, 0),        # leading dimensions of no multiple
+    (70, 100, 30, 48, 64, 104, 0, 0),        # padded rows
+    (300, 264, 160, 176, 192, 264, 0, 3),    # C off 16-byte alignment
+    (300, 264, 160, 176, 192, 265, 0, 0),    # an odd ldc
+    (3, 264, 160, 176, 192, 272, 0, 1),
+    (300, 264, 160, 176, 192, 264, 8, 0),    # codes off 16-byte alignment
+    (64, 72, 1000, 1008, 1024, 80, 0, 0)])
+def test_i8_layouts(M, N, K, lda, ldw, ldc, off, coff):
+    for glu in (False, True):
+        C, acc, sa, sw, plan = product(M, N, K, lda, ldw, ldc, off, coff, seed=3, full=True, glu=glu)
+        if glu:
+            check_glu(C, acc, sa, sw, plan)
+        else:
+            assert np.array_equal(C, expect(acc, sa, sw)), plan
+
+
+def check_glu(C, acc, sa, sw, what):
+    N = C.shape[1]
+    y = acc * sa[:, None].astype(np.float64) * sw[None, :].astype(np.float64)
+    gate, up = y[:, :N], y[:, N:]
+    with np.errstate(over="ignore"):
+        silu = gate / (1 + np.exp(-gate))
+    h = silu * up
+    e = 2.0**-22
+    slack = 1.1 * e * np.abs(gate) * np.abs(up) + e * np.abs(h) + 2.0**-20 * np.abs(h) + 2.0**-8 * np.abs(h) + 1e-38
+    off = np.abs(widen(C) - h) - slack
+    assert np.isfinite(widen(C)).all() and (off <= 0).all(), f"{what}: {(off > 0).sum()} outside the bound"
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 1, 1), (1, 520, 328), (3, 17, 15), (16, 4096, 4096), (33, 2056, 520),
+                                   (64, 1000, 200), (65, 520, 328), (129, 127, 63), (300, 1000, 1000),
+                                   (509, 1251, 1003), (128, 256, 4096), (1031, 2056, 129), (4096, 2176, 256)])
+def test_i8_swiglu(M, N, K):
+    C, acc, sa, sw, plan = product(M, N, K, seed=M + K, glu=True)
+    check_glu(C, acc, sa, sw, plan)
+
+
+def test_largest_sums_do_not_overflow():
+    # 128 * 128 * 131071 is the largest sum that is taken
+    M, N, K = 3, 24, 131071
+    A = torch.full((M, K + 1), -128, dtype=torch.int8, device="cuda")
+    one = torch.ones(32, device="cuda")
+    C = poisoned(M * N)
+    g.gemm_i8(M, N, K, A.data_ptr(), K + 1, one.data_ptr(), torch.full((N, K + 1), -128, dtype=torch.int8,
+              device="cuda").data_ptr(), K + 1, one.data_ptr(), C.data_ptr(), N, g.current_stream_handle())
+    torch.cuda.synchronize()
+    assert (bits(C) == bf16_of(np.float32([128 * 128 * K]))[0]).all()
+
+
+def test_empty_and_k_zero():
+    one = torch.ones(16, device="cuda")
+    C = poisoned(12)
+    s = g.current_stream_handle()
+    for fn in (g.gemm_i8, g.gemm_i8_swiglu):
+        fn(0, 4, 16, None, 16, None, C.data_ptr(), 16, one.data_ptr(), None, 4, s)
+        fn(3, 0, 16, C.data_ptr(), 16, one.data_ptr(), None, 16, None, None, 0, s)
+        torch.cuda.synchronize()
+        assert (bits(C) == 0x7FC0).all()
+    nan = torch.full((16,), float("nan"), device="cuda")
+    for fn in (g.gemm_i8, g.gemm_i8_swiglu):
+        C = poisoned(12)
+        fn(3, 4, 0, None, 0, nan.data_ptr(), None, 0, nan.data_ptr(), C.data_ptr(), 4, s)
+        torch.cuda.synchronize()
+        assert (bits(C) == 0).all()
+
+
+@pytest.mark.parametrize("M,N,K", [(2, 40, 64), (300, 264, 160)])
+def test_scales_of_zero_inf_and_nan(M, N, K):
+    sa = np.ones(M, np.float32)
+    sa[0], sa[-1] = 0.0, np.nan
+    C, acc, sa, sw, plan = product(M, N, K, seed=5, sa=sa)
+    assert (widen(C[0]) == 0).all() and np.isnan(widen(C[-1])).all()
+    assert np.array_equal(C[1:-1], expect(acc, sa, sw)[1:-1])
+
+
+# ---- quantisation --------------------------------------------------------------------------------
+
+
+def want_codes(x):
+    """Codes and scales by the definition: s = max / 127 and round(x / s), each a float32 division."""
+    x = x.astype(np.float32)
+    amax = np.abs(x).max(1)
+    s = amax / np.float32(127)
+    with np.errstate(invalid="ignore", divide="ignore"):
+        q = np.where(amax[:, None] > 0, np.rint(x / s[:, None]), 0)
+    bad = ~np.isfinite(amax)
+    return np.where(bad[:, None], 0, q).astype(np.int8), np.where(bad, np.float32(np.nan), s)
+
+
+def quantize(xbits, K, ldx, ldq, offset=0):
+    R = len(xbits)
+    dX, o = place(xbits, offset)
+    Qd = torch.full((max(R * ldq, 1),), 99, dtype=torch.int8, device="cuda")
+    S = torch.full((R,), -1.0, device="cuda")
+    g.gemm_i8_quantize(R, K, dX.data_ptr() + o, ldx, Qd.data_ptr(), ldq, S.data_ptr(), g.current_stream_handle())
+    torch.cuda.synchronize()
+    return Qd.cpu().numpy()[: R * ldq].reshape(R, ldq), S.cpu().numpy()
+
+
+@pytest.mark.parametrize("R,K,ldx,ldq,offset", [
+    (1, 1, 1, 1, 0), (1, 1, 8, 16, 0), (3, 7, 8, 16, 0), (4, 64, 64, 64, 0), (5, 505, 512, 512, 0),
+    (2, 1000, 1000, 1003, 0), (3, 2048, 2048, 2048, 0), (2, 4096, 4096, 4096, 0), (3, 11008, 11008, 11008, 0),
+    (2, 16384, 16384, 16384, 0), (2, 16392, 16392, 16400, 0), (3, 1000, 1001, 1008, 1), (2, 40000, 40000, 40064, 0),
+    (700, 200, 208, 256, 0)])
+def test_quantize_codes(R, K, ldx, ldq, offset):
+    rng = np.random.default_rng(R + K)
+    x = rng.normal(size=(R, ldx)).astype(np.float32)
+    x[:, K:] = np.nan                                   # padding is not read
+    x[0, :K] *= 2.0**100
+    if R > 1:
+        x[1, :K] *= np.float32(2.0**-125)               # bf16 subnormals among them
+    xb = bf16_of(x)
+    xb[:, K:] = 0x7FC0
+    q, s = quantize(xb, K, ldx, ldq, offset)
+    wq, ws = want_codes(widen(xb[:, :K]))
+    assert np.array_equal(q[:, :K], wq) and np.array_equal(s, ws)
+    padded = min(ldq, -(-K // 16) * 16)
+    assert (q[:, K:padded] == 0).all() and (q[:, padded:] == 99).all()
+
+
+def test_quantize_ties_go_to_even():
+    # max 127 * 2^e: the scale is a power of two and half codes are exact
+    v = np.concatenate([[127.0], np.arange(-126.5, 127, 1)]).astype(np.float32)
+    for e in (-20, 0, 30):
+        xb = bf16_of((v * np.float32(2.0**e))[None])
+        keep = widen(xb)[0] == v * np.float32(2.0**e)   # halves above 64 need more than bf16's 8 bits
+        xb = np.ascontiguousarray(xb[:, keep])
+        q, s = quantize(xb, xb.shape[1], xb.shape[1], xb.shape[1])
+        assert s[0] == np.float32(2.0**e) and np.array_equal(q[0], np.rint(v[keep]).astype(np.int8))
+
+
+def test_quantize_every_mantissa_and_halves():
+    """Every bf16 mantissa as the row's maximum, against every mantissa at six exponents, half the
+    maximum among them."""
+    m = np.arange(128, 256, dtype=np.float64)
+    x = np.concatenate([m * 2.0**-e for e in range(1, 7)] + [-m / 2])
+    x = np.concatenate([m[:, None], np.broadcast_to(x, (128, len(x)))], 1)
+    x = np.where(np.abs(x) <= m[:, None], x, 0)
+    xb = bf16_of(x)
+    assert (widen(xb) == x).all()
+    q, s = quantize(xb, x.shape[1], x.shape[1], x.shape[1])
+    wq, ws = want_codes(x)
+    assert np.array_equal(q, wq) and np.array_equal(s, ws)
+
+
+def test_quantize_zero_inf_nan_rows():
+    x = np.zeros((6, 40), np.float32)
+    x[1] = 1.0
+    x[2, 3], x[2, 4] = np.inf, 1.0
+    x[3, 3], x[3, 4] = -np.inf, 1.0
+    x[4, 39] = np.nan
+    x[5, 0] = -0.0
+    q, s = quantize(bf16_of(x) | (np.isnan(x) * 0x7FC0).astype(np.uint16), 40, 40, 48)
+    assert (q[[0, 2, 3, 4, 5], :] == 0).all() and (q[1, :40] == 127).all()
+    assert s[0] == 0 and s[5] == 0 and np.isnan(s[[2, 3, 4]]).all() and s[1] == np.float32(1) / np.float32(127)
+
+
+def test_quantize_empty():
+    S = torch.full((3,), -1.0, device="cuda")
+    g.gemm_i8_quantize(3, 0, None, 0, None, 0, S.data_ptr(), g.current_stream_handle())
+    torch.cuda.synchronize()
+    assert (S == 0).all()
+
+
+# ---- products from bf16 activations ----------------------------------------------------------------
+
+
+def act(M, K, seed, ld=None):
+    gen = torch.Generator().manual_seed(seed)
+    x = torch.randn(M, ld or K, generator=gen)
+    x[:, ::61] *= 20
+    return x.bfloat16().cuda()[:, :K]
+
+
+@pytest.mark.parametrize("M,N,K,ld", [(1, 520, 328, None), (2, 11008, 4096, None), (3, 40, 33, None), (5, 24, 1000, 1001),
+                                      (16, 4096, 4096, None), (17, 264, 20000, None), (64, 1000, 4104, None),
+                                      (300, 1000, 1000, 1008), (1100, 520, 328, None)])
+def test_dynamic_equals_quantize_then_product(M, N, K, ld):
+    A = act(M, K, M + K, ld)
+    W = (torch.randn(2 * N, K, generator=torch.Generator().manual_seed(N)) * 0.02).bfloat16().cuda()
+    Wq, Sw = g.i8_quantize(W)
+    Aq, Sa = g.i8_quantize(A)
+    for dyn, stat, w, s in ((g.i8_linear, g.i8_matmul, Wq[:N], Sw[:N]),
+                            (g.i8_swiglu_linear, g.i8_swiglu_matmul, Wq, Sw)):
+        want = stat(Aq, Sa, w, s)
+        work = torch.full((g.gemm_i8_work_bytes(M, K) + 48,), 77, dtype=torch.uint8, device="cuda")
+        for got in (dyn(A, w, s), dyn(A, w, s, work=work)):
+            assert torch.equal(got.view(torch.int16), want.view(torch.int16))
+        assert (work[g.gemm_i8_work_bytes(M, K):] == 77).all()
+    acc = Aq.cpu().numpy().astype(np.float64) @ Wq[:N].cpu().numpy().astype(np.float64).T
+    got = g.i8_linear(A, Wq[:N], Sw[:N])
+    assert np.array_equal(bits(got), expect(acc, Sa.cpu().numpy(), Sw[:N].cpu().numpy()))
+
+
+def test_non_finite_token_gives_nan_outputs_only_in_its_row():
+    for M in (3, 200):
+        A = act(M, 264, 1)
+        A[1, 7] = float("inf")
+        W = (torch.randn(40, 264, generator=torch.Generator().manual_seed(2)) * 0.02).bfloat16().cuda()
+        Wq, Sw = g.i8_quantize(W)
+        y = g.i8_linear(A, Wq, Sw)
+        assert torch.isnan(y[1]).all() and torch.isfinite(y[0]).all() and torch.isfinite(y[2:]).all()
+
+
+def test_streams_graphs_and_repeats():
+    """A side stream, two streams at once, and a replayed graph give the bits of an eager call."""
+    cases = []
+    for M, N, K in ((3, 4096, 4096), (64, 1000, 2056), (300, 520, 4096)):
+        A = act(M, K, K)
+        Wq, Sw = g.i8_quantize((torch.randn(2 * N, K, generator=torch.Generator().manual_seed(N)) * 0.02).bfloat16().cuda())
+        out, work = torch.empty(M, N, dtype=torch.bfloat16, device="cuda"), torch.empty(
+            g.gemm_i8_work_bytes(M, K), dtype=torch.uint8, device="cuda")
+        cases.append((A, Wq, Sw, out, work, g.i8_swiglu_linear(A, Wq, Sw).clone()))
+    torch.cuda.synchronize()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(3):
+        outs = []
+        for A, Wq, Sw, _, _, _ in cases:
+            for s in (s1, s2):
+                with torch.cuda.stream(s):
+                    outs.append(g.i8_swiglu_linear(A, Wq, Sw))
+        torch.cuda.synchronize()
+        for i, y in enumerate(outs):
+            assert torch.equal(y.view(torch.int16), cases[i // 2][5].view(torch.int16))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for A, Wq, Sw, out, work, _ in cases:
+            g.i8_swiglu_linear(A, Wq, Sw, out=out, work=work)
+    for _ in range(4):
+        for c in cases:
+            c[3].fill_(float("nan"))
+        g.i8_linear(cases[0][0], cases[0][1], cases[0][2])
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for c in cases:
+            assert torch.equal(c[3].view(torch.int16), c[5].view(torch.int16))
+
+
+def test_refusals_on_the_device():
+    A = act(4, 64, 1)
+    Wq, Sw = g.i8_quantize(act(24, 64, 2))
+    with pytest.raises(ValueError):
+        g.i8_linear(A[:, :32], Wq, Sw)
+    with pytest.raises(ValueError):
+        g.i8_linear(A, Wq, Sw[:23])
+    with pytest.raises(ValueError):
+        g.i8_swiglu_linear(A, Wq[:23], Sw[:23])
+    with pytest.raises(ValueError):
+        g.i8_linear(A.t(), Wq, Sw)
+    with pytest.raises(ValueError):
+        g.i8_linear(A, Wq, Sw, out=torch.empty(4, 23, dtype=torch.bfloat16, device="cuda"))
+    with pytest.raises(g.GemmError):
+        g.i8_linear(A, Wq, Sw, work=torch.empty(16, dtype=torch.uint8, device="cuda"))

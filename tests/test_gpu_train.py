@@ -1,0 +1,286 @@
+"""The training entry points on the GPU: gemm_bf16_bwd, gemm_bf16_swiglu_train and
+gemm_bf16_swiglu_bwd against float64.
+
+Tolerances. Products: the product check's |c - ref| <= 2^-8 |ref| + 2^-16 sum |a b|. The forward's C:
+the oracle's bound for the fused gated product. dGU, element by element from bf16 inputs in float32:
+sigmoid and 1 + g (1 - s) carry a few float32 roundings of terms of size 1 and |g|, so dg is within
+2^-19 |d u| s (1 + |g|) and du within 2^-19 |d g| s of the exact value, before the rounding to bf16
+(2^-8 of the result); a sigmoid below float32's normal range (g < -87) may come out as zero, which
+the same sizes without s times 2^-126 cover. dA and dB are products of the dGU that the call wrote, and held to the product
+check on those bits.
+"""
+
+import numpy as np
+import pytest
+
+import oracle
+from oracle import bf16_to_f64
+from oracle import swiglu as osw
+from synth import matrix
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+import gemv_layers_amd as g  # noqa: E402
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _device():
+    assert torch.cuda.is_available(), "GPU tests need a ROCm device"
+    torch.cuda.set_device(0)
+    g.gemm_init(0)
+    yield
+
+
+class Buf:
+    """A bf16 matrix in device memory: `ld` columns a row, `offset` elements into its allocation."""
+
+    def __init__(self, rows, cols, data=None, ld=None, offset=0):
+        self.rows, self.cols, self.ld, self.offset = rows, cols, max(ld or cols, cols), offset
+        host = np.full(max(offset + rows * self.ld, 1), 0x7FC0, np.uint16)  # NaN outside the matrix
+        if data is not None:
+            host[offset: offset + rows * self.ld].reshape(rows, self.ld)[:, :cols] = data
+        self.t = torch.from_numpy(host.view(np.int16)).cuda()
+
+    def ptr(self):
+        return self.t.data_ptr() + 2 * self.offset
+
+    def bits(self):
+        h = self.t.cpu().numpy().view(np.uint16)
+        body = h[self.offset: self.offset + self.rows * self.ld].reshape(self.rows, self.ld)
+        assert (h[: self.offset] == 0x7FC0).all() and (body[:, self.cols:] == 0x7FC0).all(), "wrote outside"
+        return np.ascontiguousarray(body[:, : self.cols])
+
+
+def rows_of(M, n=48):
+    return np.arange(M) if M <= n else np.unique(np.linspace(0, M - 1, n).astype(int))
+
+
+def check_product(C, A, B, what):
+    """C against A B (bf16 bits), on sampled rows when it is large."""
+    r = rows_of(len(A), 4096 if A.shape[0] * A.shape[1] * B.shape[1] < 1 << 31 else 48)
+    ref, sabs = oracle.gemm(np.ascontiguousarray(A[r]), np.ascontiguousarray(B), M=len(r), N=B.shape[1], K=A.shape[1])
+    res = oracle.check(np.ascontiguousarray(C[r]), ref, sabs)
+    assert res.ok, f"{what}: {res.summary()}"
+
+
+# tokens x width out x width in: toy blocks, odd numbers of tokens, one token, both tile sizes, K split,
+# products cut in two, a sum over fewer tokens than one k-step
+SHAPES = [(1, 8, 8), (2, 16, 64), (31, 40, 24), (33, 520, 328), (64, 1000, 200), (65, 264, 136), (128, 128, 128),
+          (257, 256, 512), (300, 520, 328), (509, 1376, 512), (1000, 1000, 1000), (4097, 520, 264),
+          (200, 2048, 4096), (200, 4096, 2048), (640, 4352, 4096)]
+LOOSE = [(3, 5, 7, 0, 0), (70, 100, 30, 0, 0), (65, 72, 40, 3, 0), (65, 72, 40, 0, 1), (130, 200, 96, 5, 1)]
+PADDED = [(65, 264, 136, 8, 8), (300, 520, 328, 24, 16)]
+
+
+@pytest.mark.parametrize("M,N,K,pad,offset", [(*s, 0, 0) for s in SHAPES] + LOOSE + PADDED)
+def test_linear_backward(M, N, K, pad, offset):
+    A, B = matrix("normal", M, K, seed=M + 1), matrix("normal", K, N, seed=N + 2, sigma=0.05)
+    D = matrix("normal", M, N, seed=K + 3, sigma=0.01)
+    D[rows_of(M)[::7]] = 0                                # tokens without a gradient
+    bA, bB, bD = (Buf(*x.shape, x, x.shape[1] + pad, offset) for x in (A, B, D))
+    dA, dB = Buf(M, K, ld=K + pad, offset=offset), Buf(K, N, ld=N + pad, offset=offset)
+    s = g.current_stream_handle()
+    g.gemm_bf16_bwd(M, N, K, bD.ptr(), bD.ld, bA.ptr(), bA.ld, bB.ptr(), bB.ld, dA.ptr(), dA.ld, dB.ptr(), dB.ld, s)
+    torch.cuda.synchronize()
+    plan = g.gemm_last_plan()
+    assert plan["op"] == "grad_b" and (plan["M"], plan["N"], plan["K"]) == (K, N, M)
+    check_product(dA.bits(), D, B.T, f"dA {M}x{N}x{K}")
+    check_product(dB.bits(), np.ascontiguousarray(A.T), D, f"dB {M}x{N}x{K}")
+    # either gradient alone: the same bits, the other's operand not read
+    for need in ("A", "B"):
+        d1 = Buf(M, K, ld=K + pad, offset=offset) if need == "A" else Buf(K, N, ld=N + pad, offset=offset)
+        if need == "A":
+            g.gemm_bf16_bwd(M, N, K, bD.ptr(), bD.ld, None, 0, bB.ptr(), bB.ld, d1.ptr(), d1.ld, None, 0, s)
+        else:
+            g.gemm_bf16_bwd(M, N, K, bD.ptr(), bD.ld, bA.ptr(), bA.ld, None, 0, None, 0, d1.ptr(), d1.ld, s)
+        torch.cuda.synchronize()
+        assert np.array_equal(d1.bits(), (dA if need == "A" else dB).bits())
+
+
+def test_empty_sums_write_zeros():
+    s = g.current_stream_handle()
+    dA, dB = Buf(5, 8), Buf(8, 16)
+    some = Buf(32, 32, np.ones((32, 32), np.uint16))
+    g.gemm_bf16_bwd(5, 0, 8, None, 0, some.ptr(), 8, None, 0, dA.ptr(), 8, None, 0, s)   # N = 0
+    g.gemm_bf16_bwd(0, 16, 8, None, 16, None, 8, some.ptr(), 16, dA.ptr(), 8, dB.ptr(), 16, s)  # M = 0
+    torch.cuda.synchronize()
+    assert (dA.bits() == 0).all() and (dB.bits() == 0).all()
+    dA, dB = Buf(5, 8), Buf(8, 32)
+    g.gemm_bf16_swiglu_bwd(5, 0, 8, None, 0, None, 0, some.ptr(), 8, None, 0, None, 0, dA.ptr(), 8, None, 0, s)
+    g.gemm_bf16_swiglu_bwd(0, 16, 8, None, 16, None, 32, None, 8, some.ptr(), 32, None, 32, None, 8, dB.ptr(), 32, s)
+    GU, C = Buf(5, 32), Buf(5, 16)
+    g.gemm_bf16_swiglu_train(5, 16, 0, None, 0, None, 32, GU.ptr(), 32, C.ptr(), 16, s)
+    torch.cuda.synchronize()
+    for b in (dA, dB, GU, C):
+        assert (b.bits() == 0).all()
+
+
+@pytest.mark.parametrize("M,N,K,pad,offset", [(*s, 0, 0) for s in SHAPES] + LOOSE + PADDED)
+def test_gated_forward(M, N, K, pad, offset):
+    A, B = matrix("normal", M, K, seed=M + 11), matrix("normal", K, 2 * N, seed=N + 12, sigma=0.05)
+    bA, bB = Buf(M, K, A, K + pad, offset), Buf(K, 2 * N, B, 2 * N + pad, offset)
+    GU, C = Buf(M, 2 * N, ld=2 * N + pad, offset=offset), Buf(M, N, ld=N + pad, offset=offset)
+    g.gemm_bf16_swiglu_train(M, N, K, bA.ptr(), bA.ld, bB.ptr(), bB.ld, GU.ptr(), GU.ld, C.ptr(), C.ld,
+                             g.current_stream_handle())
+    torch.cuda.synchronize()
+    plan = g.gemm_last_plan()
+    assert plan["op"] == "swiglu_train"
+    check_product(GU.bits(), A, B, f"GU {M}x{N}x{K} {plan['reason']}")
+    r = rows_of(M, 4096 if M * N * K < 1 << 30 else 48)
+    h, slack = osw.swiglu(np.ascontiguousarray(A[r]), B, len(r), N, K)
+    res = osw.check(np.ascontiguousarray(C.bits()[r]), h, slack)
+    assert res.ok, f"C {M}x{N}x{K}: {res.summary()}"
+
+
+def grad_formula(d, gate, up):
+    """(dg, du, and the two bounds' sizes) in float64."""
+    with np.errstate(over="ignore"):
+        sig = 1 / (1 + np.exp(-gate))
+    dg, du = d * up * sig * (1 + gate * (1 - sig)), d * gate * sig
+    bare_g, bare_u = np.abs(d * up) * (1 + np.abs(gate)), np.abs(d * gate)
+    return dg, du, bare_g * (sig + 2.0**-107), bare_u * (sig + 2.0**-107)
+
+
+def check_dgu(got, D, GU, what):
+    d, gu = bf16_to_f64(D), bf16_to_f64(GU)
+    N = D.shape[1]
+    dg, du, sg, su = grad_formula(d, gu[:, :N], gu[:, N:])
+    ref, size = np.concatenate([dg, du], 1), np.concatenate([sg, su], 1)
+    off = np.abs(bf16_to_f64(got) - ref) - (2.0**-8 * np.abs(ref) + (1 + 2.0**-8) * 2.0**-19 * size + 2.0**-126)
+    assert (off <= 0).all(), f"{what}: {(off > 0).sum()} outside, worst {off.max()}"
+
+
+@pytest.mark.parametrize("M,N,K,pad,offset", [(*s, 0, 0) for s in SHAPES] + LOOSE + PADDED)
+def test_gated_backward(M, N, K, pad, offset):
+    A, B = matrix("normal", M, K, seed=M + 21), matrix("normal", K, 2 * N, seed=N + 22, sigma=0.05)
+    D, GU = matrix("normal", M, N, seed=K + 23, sigma=0.01), matrix("normal", M, 2 * N, seed=M + 24, sigma=3.0)
+    D[rows_of(M)[::7]] = 0
+    bA, bB = Buf(M, K, A, K + pad, offset), Buf(K, 2 * N, B, 2 * N + pad, offset)
+    bD, bG = Buf(M, N, D, N + pad, offset), Buf(M, 2 * N, GU, 2 * N + pad, offset)
+    out = []
+    for inplace in (False, True):
+        dG = bG if inplace else Buf(M, 2 * N, ld=2 * N + pad, offset=offset)
+        dA, dB = Buf(M, K, ld=K + pad, offset=offset), Buf(K, 2 * N, ld=2 * N + pad, offset=offset)
+        g.gemm_bf16_swiglu_bwd(M, N, K, bD.ptr(), bD.ld, bG.ptr(), bG.ld, bA.ptr(), bA.ld, bB.ptr(), bB.ld, dG.ptr(),
+                               dG.ld, dA.ptr(), dA.ld, dB.ptr(), dB.ld, g.current_stream_handle())
+        torch.cuda.synchronize()
+        out.append((dG.bits(), dA.bits(), dB.bits()))
+    for x, y in zip(*out):
+        assert np.array_equal(x, y), "dGU in GU's memory gives other bits"
+    dg, da, db = out[0]
+    check_dgu(dg, D, GU, f"dGU {M}x{N}x{K}")
+    check_product(da, dg, B.T, f"dA {M}x{N}x{K}")
+    check_product(db, np.ascontiguousarray(A.T), dg, f"dB {M}x{N}x{K}")
+
+
+def test_gate_gradient_at_extreme_gates():
+    """Saturated gates, zeros and infinities: the limits of the formula, and no NaN at finite gates."""
+    gates = np.array([0.0, -0.0, 1e-30, -1e-30, 20, -20, 88, -88, 89, -89, 200, -200, 3e38, -3e38], np.float32)
+    M, N = 3, 24
+    gu = np.ones((M, 2 * N), np.float32)
+    gu[:, : len(gates)] = gates
+    gu[:, N:] = 2.0
+    D, GU = oracle.bf16_rne(np.full((M, N), 0.5)), oracle.bf16_rne(gu.astype(np.float64))
+    bD, bG, dG = Buf(M, N, D), Buf(M, 2 * N, GU), Buf(M, 2 * N)
+    g.gemm_bf16_swiglu_bwd(M, N, 8, bD.ptr(), N, bG.ptr(), 2 * N, None, 0, None, 0, dG.ptr(), 2 * N, None, 0, None, 0,
+                           g.current_stream_handle())
+    torch.cuda.synchronize()
+    check_dgu(dG.bits(), D, GU, "extreme gates")
+
+
+def test_gate_gradient_against_differences():
+    """dGU element by element against central differences of the forward in float64: step 1e-4, whose
+    own error is 1e-8 / 6 of the third derivative (at most 2 |d u|) and 1e-12 of rounding."""
+    M, N = 37, 64
+    D, GU = matrix("normal", M, N, seed=5, sigma=1.0), matrix("normal", M, 2 * N, seed=6, sigma=2.0)
+    bD, bG, dG = Buf(M, N, D), Buf(M, 2 * N, GU), Buf(M, 2 * N)
+    g.gemm_bf16_swiglu_bwd(M, N, 8, bD.ptr(), N, bG.ptr(), 2 * N, None, 0, None, 0, dG.ptr(), 2 * N, None, 0, None, 0,
+                           g.current_stream_handle())
+    torch.cuda.synchronize()
+    d, gu = bf16_to_f64(D), bf16_to_f64(GU)
+    gate, up, eps = gu[:, :N], gu[:, N:], 1e-4
+    f = lambda a, b: d * osw.silu(a) * b  # noqa: E731
+    fd = np.concatenate([(f(gate + eps, up) - f(gate - eps, up)) / (2 * eps),
+                         (f(gate, up + eps) - f(gate, up - eps)) / (2 * eps)], 1)
+    size = np.concatenate([np.abs(d * up) * (1 + np.abs(gate)), np.abs(d * gate)], 1)
+    tol = 2.0**-8 * np.abs(fd) + 2.0**-18 * size + 1e-8 * np.tile((1 + np.abs(d)) * (1 + np.abs(gate) + np.abs(up)), 2)
+    assert (np.abs(bf16_to_f64(dG.bits()) - fd) <= tol).all()
+
+
+def test_block_gradient_against_differences():
+    """dA and dB of the whole block against central differences of sum(dC * C) along random
+    directions, in float64. A and B are small integers, so that g and u are exact in bf16 and the
+    kernels' only errors are the roundings of dGU and of the gradients to bf16, 2^-8 of each at
+    most, plus the products' 2^-16 of their absolute sums."""
+    M, N, K = 40, 24, 8
+    rng = np.random.default_rng(3)
+    A, B = rng.integers(-1, 2, (M, K)).astype(np.float64), rng.integers(-1, 2, (K, 2 * N)).astype(np.float64)
+    Db = oracle.bf16_rne(rng.normal(size=(M, N)))
+    d = bf16_to_f64(Db)
+    dev = lambda x: torch.from_numpy(oracle.bf16_rne(x).view(np.int16)).view(torch.bfloat16).cuda()  # noqa: E731
+    tA, tB, tD = dev(A), dev(B), torch.from_numpy(Db.view(np.int16)).view(torch.bfloat16).cuda()
+    C, GU = g.swiglu_forward(tA, tB)
+    assert np.array_equal(GU.double().cpu().numpy(), A @ B)
+    dA, dB, dGU = (x.double().cpu().numpy() for x in g.swiglu_backward(tD, GU, tA, tB))
+
+    def loss(a, b):
+        y = a @ b
+        return (d * osw.silu(y[:, :N]) * y[:, N:]).sum()
+
+    absD = np.abs(dGU)
+    eA = 2.0**-7 * (absD @ np.abs(B).T) + 2.0**-8 * np.abs(dA)
+    eB = 2.0**-7 * (np.abs(A).T @ absD) + 2.0**-8 * np.abs(dB)
+    for _ in range(8):
+        da, db, eps = rng.normal(size=A.shape), rng.normal(size=B.shape), 1e-5
+        fd = (loss(A + eps * da, B + eps * db) - loss(A - eps * da, B - eps * db)) / (2 * eps)
+        tol = (np.abs(da) * eA).sum() + (np.abs(db) * eB).sum() + 1e-6 * (1 + abs(fd))
+        assert abs((dA * da).sum() + (dB * db).sum() - fd) <= tol
+
+
+def test_infinities_stay_in_their_rows():
+    """An infinity in one token reaches that token's dA only; in one output column's dC, only that
+    column of dB. Rows and columns past the matrix do not mix in."""
+    M, N, K = 130, 136, 264
+    A, B = matrix("normal", M, K, seed=31), matrix("normal", K, N, seed=32, sigma=0.05)
+    D = matrix("normal", M, N, seed=33, sigma=0.1)
+    D[5, 9] = 0x7F80
+    dA, dB = g.matmul_backward(*(torch.from_numpy(x.view(np.int16)).view(torch.bfloat16).cuda() for x in (D, A, B)))
+    fa, fb = torch.isfinite(dA).cpu().numpy(), torch.isfinite(dB).cpu().numpy()
+    assert fa[np.arange(M) != 5].all() and fb[:, np.arange(N) != 9].all()
+    assert not fa[5].all() and not fb[:, 9].all()
+
+
+def test_streams_graphs_and_repeats():
+    M, N, K = 300, 1000, 520
+    t = lambda *s, sd=1.0: (torch.randn(*s, generator=torch.Generator().manual_seed(sum(s))) * sd).bfloat16().cuda()  # noqa: E731
+    A, B, D = t(M, K), t(K, 2 * N, sd=0.05), t(M, N, sd=0.1)
+
+    def step():
+        C, GU = g.swiglu_forward(A, B)
+        return (C, GU, *g.swiglu_backward(D, GU, A, B), *g.matmul_backward(D, A, B[:, :N]))
+
+    want = [x.clone() for x in step()]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(3):
+        got = []
+        for s in streams:
+            with torch.cuda.stream(s):
+                got.append(step())
+        torch.cuda.synchronize()
+        for outs in got:
+            for x, y in zip(outs, want):
+                assert torch.equal(x.view(torch.int16), y.view(torch.int16))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = step()
+    for _ in range(4):
+        for x in outs:
+            x.fill_(float("nan"))
+        step()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for x, y in zip(outs, want):
+            assert torch.equal(x.view(torch.int16), y.view(torch.int16))
