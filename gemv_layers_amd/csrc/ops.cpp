@@ -29,6 +29,53 @@ const char* op_name(int mode, bool glu) {
     }
 }
 
+// Whether the matrix kernels take these operands: 16-byte aligned rows, 32-bit offsets within a tile.
+// Codes need no multiple in any size (a C without 16-byte rows is stored element by element); bf16
+// widths are multiples of 8, except along the summed index where it is the row index.
+bool matrix_ok(int mode, bool glu, const OpArgs& a) {
+    const int64_t unit = mode == glk::kOpI8 ? 16 : 8;
+    const int64_t max_ld = int64_t(1) << 20, max_dim = int64_t(1) << 26;
+    if (misaligned(a.A, 16) || misaligned(a.B, 16) || (a.lda % unit) || (a.ldb % unit)) return false;
+    if (a.lda > max_ld || a.ldb > max_ld || a.ldc > max_ld || a.ldgu > max_ld) return false;
+    if (a.M > max_dim || a.N > max_dim || a.K > max_dim) return false;
+    if (mode == glk::kOpI8) return true;
+    if (misaligned(a.C, 16) || (a.ldc % 8) || (a.N % 8)) return false;
+    if (mode == glk::kOpTrain && (misaligned(a.GU, 16) || (a.ldgu % 8))) return false;
+    return mode == glk::kOpAtb ? a.M % 8 == 0 : a.K % 8 == 0;
+}
+
+// One launch of the tile kernels for plan `p` over rows m0 .. m0 + M - 1 and columns n0 .. n0 + N - 1.
+hipError_t launch_tiles(int mode, bool glu, const OpArgs& a, const glk::Plan& p, int64_t m0, int64_t M, int64_t n0,
+                        int64_t N, const glk::Workspace& w, hipStream_t stream) {
+    const int64_t es = mode == glk::kOpI8 ? 1 : 2;
+    const bool a_contig = mode != glk::kOpAtb, b_contig = mode == glk::kOpI8 || mode == glk::kOpAbt;
+    glk::OpTileArgs t;
+    t.A = static_cast<const char*>(a.A) + es * m0 * (a_contig ? a.lda : 1);
+    t.B = static_cast<const char*>(a.B) + es * n0 * (b_contig ? a.ldb : 1);
+    t.C = a.C + m0 * a.ldc + n0;
+    t.GU = a.GU ? a.GU + m0 * a.ldgu + n0 : nullptr;
+    t.sa = a.sa ? a.sa + m0 : nullptr;
+    t.sb = a.sb ? a.sb + n0 : nullptr;
+    t.M = (int)M;
+    t.N = (int)N;
+    t.K = (int)a.K;
+    t.lda = (int)a.lda;
+    t.ldb = (int)a.ldb;
+    t.ldc = (int)a.ldc;
+    t.ldgu = (int)a.ldgu;
+    t.sb_up = t.gu_up = (int)a.N;
+    t.vec = !misaligned(t.C, 16) && a.ldc % 8 == 0 && N % 8 == 0;
+    t.tiles_m = (int)p.tiles_m;
+    t.tiles_n = (int)p.tiles_n;
+    t.group_m = p.group_m;
+    t.nxcd = p.nxcd;
+    t.splits = p.sched == glk::kSchedSplitK ? p.splits : 1;
+    t.kt_per_split = p.kt_per_split;
+    t.ws = w.ws;
+    t.counters = w.counters;
+    return glk::launch_op_tile(mode, glu, p.bm == 256, t, (int)p.grid, stream);
+}
+
 // One product on the current device: M, N > 0, operands checked.
 int run_op(int mode, bool glu, const OpArgs& a, hipStream_t stream) {
     int st = GEMM_OK;
@@ -40,9 +87,24 @@ int run_op(int mode, bool glu, const OpArgs& a, hipStream_t stream) {
         p = glk::make_plan(a.M, a.N, 0, *dev, false, 2, glu);
         e = glk::launch_zero_c(a.C, a.M, a.N, a.ldc, stream);
         if (e == hipSuccess && mode == glk::kOpTrain) e = glk::launch_zero_c(a.GU, a.M, 2 * a.N, a.ldgu, stream);
-    } else {
+    } else if (!matrix_ok(mode, glu, a)) {
         p = glk::make_plan(a.M, a.N, a.K, *dev, false, 2, glu);
         e = glk::launch_op_generic(mode, glu, a, stream);
+    } else {
+        // planned as the bf16 product whose k-steps have the same bytes and matrix-core cycles
+        p = glk::make_plan(a.M, a.N, mode == glk::kOpI8 ? (a.K + 1) / 2 : a.K, *dev, true, 2, glu);
+        if (p.grid > INT32_MAX) return GEMM_ERR_UNSUPPORTED;
+        glk::Workspace w;
+        if (p.ws_floats > 0) {
+            st = glk::stream_workspace(stream, &w);
+            if (st != GEMM_OK) return st;
+        }
+        const int64_t Mm = p.cut_axis == 2 ? p.cut_at : a.M, Nm = p.cut_axis == 1 ? p.cut_at : a.N;
+        e = launch_tiles(mode, glu, a, p, 0, Mm, 0, Nm, w, stream);
+        if (e == hipSuccess && p.cut_axis == 1)
+            e = launch_tiles(mode, glu, a, p.rest[0], 0, a.M, Nm, a.N - Nm, w, stream);
+        else if (e == hipSuccess && p.cut_axis == 2)
+            e = launch_tiles(mode, glu, a, p.rest[0], Mm, a.M - Mm, 0, a.N, w, stream);
     }
     if (e != hipSuccess) return GEMM_ERR_HIP;
     glk::set_last_plan(p, a.M, a.N, a.K, op_name(mode, glu));

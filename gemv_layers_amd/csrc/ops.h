@@ -30,6 +30,28 @@ struct OpArgs {
 // ---- general kernel (any alignment, leading dimension or size) -------------------------------
 hipError_t launch_op_generic(int mode, bool glu, const OpArgs& a, hipStream_t s);
 
+// ---- MFMA tiles ---------------------------------------------------------------------------------
+// One launch over an M x N output (or a rectangle of it), sizes in elements.
+struct OpTileArgs {
+    const void* A;
+    const void* B;
+    uint16_t* C;
+    uint16_t* GU;
+    const float* sa;
+    const float* sb;
+    int M, N, K;
+    int lda, ldb, ldc, ldgu;
+    int sb_up, gu_up;    // where the up half's scales and GU's up columns start
+    int vec;             // C takes 16-byte stores
+    int tiles_m, tiles_n, group_m, nxcd;
+    int splits, kt_per_split;  // pieces of K per tile, 64-byte k-steps in each (128 x 128 tiles)
+    float* ws;
+    uint32_t* counters;
+};
+// big: 256 x 256 tiles, else 128 x 128 (the gated forms' tiles make half as many output columns)
+hipError_t launch_op_tile(int mode, bool glu, bool big, const OpTileArgs& a, int grid, hipStream_t s);
+hipError_t configure_op_kernels();
+
 // ---- row kernels --------------------------------------------------------------------------------
 // symmetric 8-bit codes of each row: see gemm_i8_quantize
 hipError_t launch_i8_quantize(const uint16_t* X, int64_t R, int64_t K, int64_t ldx, int8_t* Q, int64_t ldq,

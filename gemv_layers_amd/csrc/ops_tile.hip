@@ -1,0 +1,531 @@
+// Matrix kernels of the 8-bit and training products for gfx950, on MFMA tiles.
+//
+// One k-step is 64 bytes of the summed index: 64 codes or 32 bf16 values, one
+// v_mfma_i32_16x16x64_i8 or v_mfma_f32_16x16x32_bf16 for each 16 x 16 output block (16 bytes of each
+// operand per lane, the same cycles, the same accumulator layout). An operand comes in one of two
+// forms, and every product is a pair of them:
+//   contiguous: the summed index is contiguous in memory (codes; dC and B of dA = dC B^T). A stage of
+//     one k-step is R rows of 64 bytes; 16-byte chunk c of row r is stored at c ^ ((r >> 2) & 3), so
+//     the 16 rows that one cycle of a ds_read_b128 serves cover all 64 banks.
+//   strided: the summed index is the row (A and dC of dB = A^T dC; B of the forward). A stage is 32
+//     rows of R elements, and ds_read_b64_tr_b16 transposes 4 x 16 blocks on the way to registers; the
+//     32-byte column groups of row k are stored at group ^ s(k), s(k) = (k & 3) | ((k >> 1) & 4).
+// Both take 64 R bytes a stage. Stages are copied HBM -> LDS without registers, into rings of 5 slots
+// for each operand: 160 KB for the 256 x 256 tile, 80 KB (two workgroups a CU) for 128 x 128.
+//
+// Schedules. 256 x 256 (op_pp): two groups of four waves, one of each group on every SIMD; in turn
+// one group reads its operands and issues copies while the other runs 32 MFMAs back to back, and they
+// swap at each barrier. 128 x 128 (op_small): four waves in step, operands double-buffered in
+// registers, K split over idle CUs with partial sums in a workspace that the last arriver adds in
+// order (the same bits on every run; integer sums are exact in any order).
+//
+// Epilogues round once to bf16, staged through LDS so that each row segment is written by one
+// instruction. Codes: the 32-bit sum times the row's and the column's scale in float32, and for the
+// gated form silu(g) u. Training forward: g and u, then silu(g) u from their float32 values.
+// Codes past K in the last 16-byte chunk of a row are whatever the caller's padding holds: they are
+// cleared in the A operand, which is enough, as 0 times any code is 0.
+
+#include <type_traits>
+
+#include "common.h"
+#include "ops.h"
+
+namespace glk {
+
+typedef short i16x4 __attribute__((ext_vector_type(4)));
+typedef short i16x8 __attribute__((ext_vector_type(8)));
+typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
+
+template <int BM_, int BN_, int WM, int WN, int MODE>
+struct OpTile {
+    static constexpr int BM = BM_, BN = BN_;
+    static constexpr bool I8 = MODE == kOpI8;
+    static constexpr bool A_CONTIG = MODE != kOpAtb;
+    static constexpr bool B_CONTIG = MODE == kOpI8 || MODE == kOpAbt;
+    static constexpr int ES = I8 ? 1 : 2;            // bytes per element
+    static constexpr int KE = 64 / ES;               // elements per k-step
+    static constexpr int SLOTS = 5;
+    static constexpr int NW = WM * WN, NT = NW * 64;
+    static constexpr int WTM = BM / WM, WTN = BN / WN;
+    static constexpr int TM = WTM / 16, TN = WTN / 16;
+    static constexpr int A_BYTES = BM * 64, B_BYTES = BN * 64;
+    static constexpr int B_RING = SLOTS * A_BYTES;
+    static constexpr int LDS_BYTES = SLOTS * (A_BYTES + B_BYTES);
+    static constexpr int A_PW = A_BYTES / 1024 / NW;  // 1 KB copy instructions per wave and stage
+    static constexpr int B_PW = B_BYTES / 1024 / NW;
+    static constexpr int LOADS = A_PW + B_PW;
+    using Acc = std::conditional_t<I8, i32x4, f32x4>;
+    static_assert(A_PW * NW * 1024 == A_BYTES && B_PW * NW * 1024 == B_BYTES, "copies split evenly");
+    static_assert(LDS_BYTES <= 160 * 1024, "LDS");
+};
+
+// strided operands: physical 32-byte column group of logical group u in row k
+__device__ __forceinline__ int op_group(int u, int k) { return u ^ ((k & 3) | ((k >> 1) & 4)); }
+
+__device__ __forceinline__ f32x4 op_mfma(const u32x4& x, const u32x4& y, const f32x4& c) {
+    return mfma16(__builtin_bit_cast(bf16x8, x), __builtin_bit_cast(bf16x8, y), c);
+}
+__device__ __forceinline__ i32x4 op_mfma(const u32x4& x, const u32x4& y, const i32x4& c) {
+    return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, x), __builtin_bit_cast(i32x4, y), c, 0, 0, 0);
+}
+
+// The copies of one operand (R rows or columns of the tile from r0, `rows` of them in all) by one wave.
+template <int R, int PW, bool CONTIG, int ES, bool GLU, int WT>
+struct OpCopy {
+    uint32_t off[PW];
+    int chunk[PW];       // contiguous: byte of the lane's chunk in the 64-byte row
+    bool ok[PW];
+    const char* base[GLU && CONTIG ? PW : 1];
+    int64_t ld_bytes;
+
+    // gated operands hold `rows` gate rows (columns) and then `rows` up ones; the tile's WT-wide
+    // share of each wave is WT / 2 gate and the same WT / 2 up
+    __device__ __forceinline__ void init(const void* p, int64_t ld, int64_t r0, int64_t rows, int wave, int lane) {
+        ld_bytes = ld * ES;
+        const char* at = static_cast<const char*>(p);
+#pragma unroll
+        for (int i = 0; i < PW; ++i) {
+            const int idx = wave * PW + i;
+            if constexpr (CONTIG) {
+                const int r = 16 * idx + (lane >> 2);
+                chunk[i] = 16 * ((lane & 3) ^ ((r >> 2) & 3));
+                if constexpr (GLU) {  // 16 rows are all gate or all up: one base for the instruction
+                    const int q = 16 * idx, out = (q / WT) * (WT / 2) + q % (WT / 2);
+                    const int64_t src = r0 + out + (q % WT < WT / 2 ? 0 : rows);
+                    base[i] = at + src * ld_bytes;
+                    off[i] = (uint32_t)((lane >> 2) * (int)ld_bytes + chunk[i]);
+                    ok[i] = r0 + out + (lane >> 2) < rows;
+                } else {
+                    off[i] = (uint32_t)(r * (int)ld_bytes + chunk[i]);
+                    ok[i] = r0 + r < rows;
+                }
+            } else {
+                constexpr int RPI = 512 / R, CH = R / 8;  // k rows per instruction, chunks per row
+                const int k = idx * RPI + lane / CH, pc = lane % CH;
+                const int col = 16 * op_group(pc >> 1, k) + 8 * (pc & 1);
+                int src = col, out = col;
+                if constexpr (GLU) {
+                    const int q = col % WT;
+                    out = (col / WT) * (WT / 2) + q % (WT / 2);
+                    src = out + (q < WT / 2 ? 0 : (int)rows);
+                }
+                off[i] = sel_off(r0 + out < rows, (uint32_t)(k * (int)ld_bytes + src * ES));
+            }
+        }
+        if constexpr (!(GLU && CONTIG)) base[0] = at + (CONTIG ? r0 * ld_bytes : r0 * ES);
+    }
+    // the k-step that starts `k` elements into the sum, `left` elements of it remaining (0: zeros)
+    __device__ __forceinline__ void issue(uint32_t lds, int64_t k, int left, int wave) const {
+        if constexpr (CONTIG) {
+            const int bytes = left * ES;
+#pragma unroll
+            for (int i = 0; i < PW; ++i) {
+                const i32x4 r = rsrc_words(base[GLU ? i : 0] + k * ES, kBufRecords);
+                dma16(r, lds + (wave * PW + i) * 1024, sel_off(ok[i] & (chunk[i] < bytes), off[i]));
+            }
+        } else {
+            const int krows = __builtin_amdgcn_readfirstlane(min(left, 32));
+            const i32x4 r = rsrc_words(base[0] + k * ld_bytes, (uint32_t)krows * (uint32_t)ld_bytes);
+#pragma unroll
+            for (int i = 0; i < PW; ++i) dma16(r, lds + (wave * PW + i) * 1024, off[i]);
+        }
+    }
+};
+
+// T tiles of 16 rows (columns) from `w0` of a stage: lane l gets row w0 + 16 i + (l & 15), bytes
+// 16 (l >> 4) .. + 15 of the k-step
+template <int R, int T, bool CONTIG>
+__device__ __forceinline__ void op_read(const char* stage, int w0, int lane, u32x4 (&f)[T]) {
+    const int j = lane & 15, G = lane >> 4;
+    if constexpr (CONTIG) {
+        const char* at = stage + (w0 + j) * 64 + 16 * (G ^ ((j >> 2) & 3));
+#pragma unroll
+        for (int i = 0; i < T; ++i) f[i] = *reinterpret_cast<const u32x4*>(at + i * 1024);
+    } else {
+#pragma unroll
+        for (int i = 0; i < T; ++i) {
+            i16x4 v[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int k = 8 * G + 4 * h + (j >> 2);
+                const char* at = stage + k * (2 * R) + 32 * op_group((w0 >> 4) + i, k) + 8 * (j & 3);
+                v[h] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)at);
+            }
+            const i16x8 x = {v[0][0], v[0][1], v[0][2], v[0][3], v[1][0], v[1][1], v[1][2], v[1][3]};
+            f[i] = __builtin_bit_cast(u32x4, x);
+        }
+    }
+}
+
+// clears the codes at `left` and after in a fragment of the last k-step
+template <int T>
+__device__ __forceinline__ void op_clear_tail(int left, int lane, u32x4 (&f)[T]) {
+    const int n = left - 16 * (lane >> 4);  // codes of the lane's 16 that count
+    u32x4 mask;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        const int b = n - 4 * w;
+        mask[w] = b >= 4 ? 0xFFFFFFFFu : (b <= 0 ? 0u : (1u << (8 * b)) - 1u);
+    }
+#pragma unroll
+    for (int i = 0; i < T; ++i) f[i] &= mask;
+}
+
+struct OpPlace {
+    int m0, n0, piece, tile;
+};
+// which tile, in grouped order over the XCDs' contiguous shares
+template <int BM, int BNO>
+__device__ __forceinline__ OpPlace op_place(const OpTileArgs& p) {
+    const int pieces = p.splits, ntiles = p.tiles_m * p.tiles_n;
+    const int unit = xcd_remap((int)blockIdx.x, ntiles * pieces, p.nxcd);
+    const int tile = unit / pieces;
+    const int per_group = p.group_m * p.tiles_n;
+    const int g = tile / per_group, first = g * p.group_m;
+    const int gm = min(p.tiles_m - first, p.group_m);
+    const int in = tile - g * per_group;
+    // (uniform, but the divisions leave them in vector registers)
+    auto uni = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
+    return OpPlace{uni((first + in % gm) * BM), uni((in / gm) * BNO), uni(unit - tile * pieces), uni(tile)};
+}
+
+// ---- epilogue ------------------------------------------------------------------------------------
+// Lane layout of acc[ni][mi][r]: row wm WTM + 16 mi + (lane & 15), column wn WTN + 16 ni + 4 (lane >> 4) + r.
+// Each wave rounds its block into an LDS area of its own (rows of RB bytes, 16-byte chunk c of row r
+// at c ^ (r & (RB / 16 - 1))) and writes it out in whole row segments.
+
+// writes the wave's staged WTM x W block: `vec` 16-byte stores, else one element at a time
+template <int WTM, int W>
+__device__ __forceinline__ void op_store_rows(const char* ob, uint16_t* C, int64_t ldc, int m0, int M, int n0, int N,
+                                              int lane, bool vec) {
+    constexpr int RB = W * 2, CPR = RB / 16, ROWS = 64 / CPR;
+    const int lr = lane / CPR, lc = lane % CPR, n = n0 + lc * 8;
+    const __amdgpu_buffer_rsrc_t rc = make_rsrc(C + (size_t)m0 * ldc);
+#pragma unroll
+    for (int s = 0; s < WTM / ROWS; ++s) {
+        const int r = s * ROWS + lr;
+        const u32x4 v = *reinterpret_cast<const u32x4*>(ob + r * RB + (lc ^ (r & (CPR - 1))) * 16);
+        const bool ok = m0 + r < M && n < N;
+        if (vec) {
+            // non-temporal: written once, and far larger than the L2s when it is large
+            __builtin_amdgcn_raw_buffer_store_b128(v, rc, ok ? (uint32_t)(r * (int)ldc + n) * 2u : kBufInvalid, 0,
+                                                   kAuxNonTemporal);
+        } else if (ok) {
+            uint16_t* c = C + (size_t)(m0 + r) * ldc + n;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (n + j < N) c[j] = (uint16_t)(v[j >> 1] >> (16 * (j & 1)));
+        }
+    }
+}
+
+template <class T, int MODE, bool GLU>
+__device__ __forceinline__ void op_epilogue(const OpTileArgs& p, char* lds, const OpPlace& at, int wave, int wm, int wn,
+                                            int lane, typename T::Acc (&acc)[T::TN][T::TM]) {
+    constexpr int TM = T::TM, TN = T::TN, TNO = GLU ? TN / 2 : TN, WTNO = TNO * 16;
+    const int row = lane & 15, G = lane >> 4;
+    const int mw = at.m0 + wm * T::WTM, nw = at.n0 + wn * WTNO;  // the wave's first row and output column
+    char* ob = lds + wave * (T::WTM * T::WTN * 2);
+    auto put = [&](auto width, int mi, int ni, const f32x4& h) {
+        constexpr int RB = decltype(width)::value * 2;
+        const int r = mi * 16 + row, byte = ni * 32 + G * 8;
+        *reinterpret_cast<u32x2*>(ob + r * RB + (((byte >> 4) ^ (r & (RB / 16 - 1))) << 4) + (byte & 15)) =
+            u32x2{pack_bf16x2(h[0], h[1]), pack_bf16x2(h[2], h[3])};
+    };
+    using Full = std::integral_constant<int, T::WTN>;
+    using Out = std::integral_constant<int, WTNO>;
+    if constexpr (MODE == kOpI8) {
+        float sa[TM];
+#pragma unroll
+        for (int mi = 0; mi < TM; ++mi) {
+            const int m = mw + mi * 16 + row;
+            sa[mi] = m < p.M ? p.sa[m] : 0.f;
+        }
+#pragma unroll
+        for (int ni = 0; ni < TNO; ++ni) {
+            f32x4 sg, su;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int n = nw + ni * 16 + 4 * G + r;
+                sg[r] = n < p.N ? p.sb[n] : 0.f;
+                if constexpr (GLU) su[r] = n < p.N ? p.sb[(int64_t)p.sb_up + n] : 0.f;
+            }
+#pragma unroll
+            for (int mi = 0; mi < TM; ++mi) {
+                f32x4 h;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    h[r] = (float)acc[ni][mi][r] * sa[mi] * sg[r];
+                    if constexpr (GLU) h[r] = swiglu1(h[r], (float)acc[ni + TNO][mi][r] * sa[mi] * su[r]);
+                }
+                put(Out{}, mi, ni, h);
+            }
+        }
+    } else {
+        if constexpr (MODE == kOpTrain) {
+#pragma unroll
+            for (int mi = 0; mi < TM; ++mi)
+#pragma unroll
+                for (int ni = 0; ni < TN; ++ni) put(Full{}, mi, ni, acc[ni][mi]);
+            // rows of WTNO gate and WTNO up values: two row segments
+            constexpr int RB = T::WTN * 2, CPR = RB / 16, ROWS = 64 / CPR;
+            const int lr = lane / CPR, lc = lane % CPR;
+            const int n = nw + (lc % (CPR / 2)) * 8;
+            const int64_t col = (lc < CPR / 2 ? 0 : (int64_t)p.gu_up) + n;
+            const __amdgpu_buffer_rsrc_t rg = make_rsrc(p.GU + (size_t)mw * p.ldgu);
+#pragma unroll
+            for (int s = 0; s < T::WTM / ROWS; ++s) {
+                const int r = s * ROWS + lr;
+                const u32x4 v = *reinterpret_cast<const u32x4*>(ob + r * RB + (lc ^ (r & (CPR - 1))) * 16);
+                const bool ok = mw + r < p.M && n < p.N;
+                __builtin_amdgcn_raw_buffer_store_b128(v, rg, ok ? (uint32_t)(r * p.ldgu + (int)col) * 2u : kBufInvalid,
+                                                       0, kAuxNonTemporal);
+            }
+        }
+#pragma unroll
+        for (int mi = 0; mi < TM; ++mi)
+#pragma unroll
+            for (int ni = 0; ni < TNO; ++ni) {
+                if constexpr (GLU)
+                    put(Out{}, mi, ni, swiglu4(acc[ni][mi], acc[ni + TNO][mi]));
+                else
+                    put(Out{}, mi, ni, acc[ni][mi]);
+            }
+    }
+    op_store_rows<T::WTM, WTNO>(ob, p.C, p.ldc, mw, p.M, nw, p.N, lane, p.vec != 0);
+}
+
+// ---- 256 x 256: two wave groups alternating memory and MFMA phases --------------------------------
+// Phases are separated by workgroup barriers b1, b2, ...; group 0 runs the memory phase of step s
+// before b(2 s + 1) and its MFMAs before b(2 s + 2), group 1 one barrier later. The last read of step
+// s - 1's slot is group 1's, before b(2 s); both groups refill that slot with stage s + 4 in their
+// memory phase of step s, after b(2 s). Each wave ends its memory phase of step s waiting for its own
+// copies of stage s + 1 (issued in step s - 3: three later steps' copies may be in flight), and a
+// barrier follows before any wave reads that stage.
+template <int MODE, bool GLU>
+__global__ void __attribute__((amdgpu_flat_work_group_size(512, 512), amdgpu_waves_per_eu(2, 2)))
+op_pp_kernel(OpTileArgs p) {
+    using T = OpTile<256, 256, 2, 4, MODE>;
+    constexpr int TM = T::TM, TN = T::TN, AHEAD = T::SLOTS - 1;
+    extern __shared__ __attribute__((aligned(1024))) char lds[];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int grp = wave >> 2, wm = grp, wn = wave & 3;
+    const OpPlace at = op_place<256, GLU ? 128 : 256>(p);
+    const int nsteps = (p.K + T::KE - 1) / T::KE;
+
+    OpCopy<256, T::A_PW, T::A_CONTIG, T::ES, false, T::WTM> ca;
+    OpCopy<256, T::B_PW, T::B_CONTIG, T::ES, GLU, T::WTN> cb;
+    ca.init(p.A, p.lda, at.m0, p.M, wave, lane);
+    cb.init(p.B, p.ldb, at.n0, p.N, wave, lane);
+    const uint32_t ring = lds_addr(lds);
+    auto issue = [&](int s, int slot) {
+        const int k = s * T::KE, left = max(p.K - k, 0);
+        ca.issue(ring + slot * T::A_BYTES, left ? k : 0, left, wave);
+        cb.issue(ring + T::B_RING + slot * T::B_BYTES, left ? k : 0, left, wave);
+    };
+    typename T::Acc acc[TN][TM];
+#pragma unroll
+    for (int ni = 0; ni < TN; ++ni)
+#pragma unroll
+        for (int mi = 0; mi < TM; ++mi) acc[ni][mi] = typename T::Acc{};
+    auto phase_barrier = [&]() {
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    const int tail = (T::I8 && (p.K & 15)) ? nsteps - 1 : -1;
+
+#pragma unroll
+    for (int s = 0; s < AHEAD; ++s) issue(s, s);
+    wait_vmcnt<T::LOADS * (AHEAD - 1)>();
+    lds_barrier();
+    if (grp == 1) phase_barrier();
+    int slot = 0;
+    for (int s = 0; s < nsteps; ++s) {
+        u32x4 fa[TM], fb[TN];
+        op_read<256, TM, T::A_CONTIG>(lds + slot * T::A_BYTES, wm * T::WTM, lane, fa);
+        op_read<256, TN, T::B_CONTIG>(lds + T::B_RING + slot * T::B_BYTES, wn * T::WTN, lane, fb);
+        issue(s + AHEAD, slot == 0 ? AHEAD : slot - 1);
+        if constexpr (T::I8) {
+            if (s == tail) op_clear_tail(p.K - s * T::KE, lane, fa);
+        }
+        wait_vmcnt<T::LOADS * (AHEAD - 1)>();
+        wait_lgkmcnt0();
+        phase_barrier();
+#pragma unroll
+        for (int ni = 0; ni < TN; ++ni)
+#pragma unroll
+            for (int mi = 0; mi < TM; ++mi) acc[ni][mi] = op_mfma(fb[ni], fa[mi], acc[ni][mi]);
+        phase_barrier();
+        slot = slot == AHEAD ? 0 : slot + 1;
+    }
+    if (grp == 0) phase_barrier();
+    wait_vmcnt<0>();  // the copies past K included
+    lds_barrier();    // the rings are free for the output
+    op_epilogue<T, MODE, GLU>(p, lds, at, wave, wm, wn, lane, acc);
+}
+
+// ---- 128 x 128, K split over idle CUs -------------------------------------------------------------
+// Iteration i reads the operands of step i + 1 while the MFMAs of step i run. The slot of stage i was
+// last read in iteration i - 1, which every wave ends (its LDS reads waited for) at the barrier of
+// iteration i; stage i + 5 goes there. Stages i + 2 .. i + 4 may be in flight at that barrier.
+template <int MODE, bool GLU>
+__global__ void __attribute__((amdgpu_flat_work_group_size(256, 256), amdgpu_waves_per_eu(2, 2)))
+op_small_kernel(OpTileArgs p) {
+    using T = OpTile<128, 128, 2, 2, MODE>;
+    constexpr int TM = T::TM, TN = T::TN, S = T::SLOTS;
+    extern __shared__ __attribute__((aligned(1024))) char lds[];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave >> 1, wn = wave & 1;
+    const OpPlace at = op_place<128, GLU ? 64 : 128>(p);
+    const int total = (p.K + T::KE - 1) / T::KE;
+    const int first = at.piece * p.kt_per_split;
+    const int nsteps = max(min(total - first, p.kt_per_split), 0);
+    const int kend = min(p.K, (first + nsteps) * T::KE);
+
+    OpCopy<128, T::A_PW, T::A_CONTIG, T::ES, false, T::WTM> ca;
+    OpCopy<128, T::B_PW, T::B_CONTIG, T::ES, GLU, T::WTN> cb;
+    ca.init(p.A, p.lda, at.m0, p.M, wave, lane);
+    cb.init(p.B, p.ldb, at.n0, p.N, wave, lane);
+    const uint32_t ring = lds_addr(lds);
+    auto issue = [&](int s, int slot) {
+        const int k = (first + s) * T::KE, left = max(kend - k, 0);
+        ca.issue(ring + slot * T::A_BYTES, left ? k : 0, left, wave);
+        cb.issue(ring + T::B_RING + slot * T::B_BYTES, left ? k : 0, left, wave);
+    };
+    typename T::Acc acc[TN][TM];
+#pragma unroll
+    for (int ni = 0; ni < TN; ++ni)
+#pragma unroll
+        for (int mi = 0; mi < TM; ++mi) acc[ni][mi] = typename T::Acc{};
+    const int tail = (T::I8 && (p.K & 15)) ? total - 1 - first : -1;
+    auto read = [&](int s, int slot, u32x4 (&fa)[TM], u32x4 (&fb)[TN]) {
+        op_read<128, TM, T::A_CONTIG>(lds + slot * T::A_BYTES, wm * T::WTM, lane, fa);
+        op_read<128, TN, T::B_CONTIG>(lds + T::B_RING + slot * T::B_BYTES, wn * T::WTN, lane, fb);
+        if constexpr (T::I8) {
+            if (s == tail) op_clear_tail(p.K - (first + s) * T::KE, lane, fa);
+        }
+    };
+
+    u32x4 fa0[TM], fb0[TN], fa1[TM], fb1[TN];
+#pragma unroll
+    for (int s = 0; s < S; ++s) issue(s, s);
+    wait_vmcnt<T::LOADS * (S - 1)>();
+    lds_barrier();
+    read(0, 0, fa0, fb0);
+    int slot = 0;
+    auto step = [&](int i, u32x4 (&fa)[TM], u32x4 (&fb)[TN], u32x4 (&na)[TM], u32x4 (&nb)[TN]) {
+        const int next = slot == S - 1 ? 0 : slot + 1;
+        wait_vmcnt<T::LOADS * (S - 2)>();  // this wave's copies of stage i + 1 landed
+        lds_barrier();                     // every wave's did, and step i's operands are in registers
+        issue(i + S, slot);
+        read(i + 1, next, na, nb);
+#pragma unroll
+        for (int ni = 0; ni < TN; ++ni)
+#pragma unroll
+            for (int mi = 0; mi < TM; ++mi) acc[ni][mi] = op_mfma(fb[ni], fa[mi], acc[ni][mi]);
+        slot = next;
+    };
+    int i = 0;
+    for (; i + 1 < nsteps; i += 2) {
+        step(i, fa0, fb0, fa1, fb1);
+        step(i + 1, fa1, fb1, fa0, fb0);
+    }
+    if (i < nsteps) step(i, fa0, fb0, fa1, fb1);
+    wait_vmcnt<0>();
+    lds_barrier();
+
+    if (p.splits > 1) {
+        volatile uint32_t& last_flag = *reinterpret_cast<volatile uint32_t*>(lds);
+        constexpr uint32_t kSlot = 128 * 128 * 4;
+        const __amdgpu_buffer_rsrc_t ws = make_rsrc(p.ws + (size_t)at.tile * p.splits * (128 * 128));
+        auto slot_off = [&](int pc, int ni, int mi) {
+            return (uint32_t)pc * kSlot + (uint32_t)((((wave * TN + ni) * TM + mi) * 64 + lane) * 16);
+        };
+#pragma unroll
+        for (int ni = 0; ni < TN; ++ni)
+#pragma unroll
+            for (int mi = 0; mi < TM; ++mi)
+                buf_store16_dev(ws, slot_off(at.piece, ni, mi), __builtin_bit_cast(u32x4, acc[ni][mi]));
+        wait_all_memory();
+        __syncthreads();
+        if (threadIdx.x == 0)
+            last_flag = (counter_arrive(&p.counters[at.tile]) == (uint32_t)(p.splits - 1)) ? 1u : 0u;
+        __syncthreads();
+        if (!last_flag) return;
+        if (threadIdx.x == 0) counter_reset(&p.counters[at.tile]);
+        typename T::Acc sum[TN][TM];
+#pragma unroll
+        for (int ni = 0; ni < TN; ++ni)
+#pragma unroll
+            for (int mi = 0; mi < TM; ++mi) sum[ni][mi] = typename T::Acc{};
+        for (int pc = 0; pc < p.splits; ++pc) {  // in K order, its own piece from registers
+            if (pc == at.piece) {
+#pragma unroll
+                for (int ni = 0; ni < TN; ++ni)
+#pragma unroll
+                    for (int mi = 0; mi < TM; ++mi) sum[ni][mi] += acc[ni][mi];
+                continue;
+            }
+            u32x4 v[TN][TM];
+#pragma unroll
+            for (int ni = 0; ni < TN; ++ni)
+#pragma unroll
+                for (int mi = 0; mi < TM; ++mi) v[ni][mi] = buf_load16_dev(ws, slot_off(pc, ni, mi));
+#pragma unroll
+            for (int ni = 0; ni < TN; ++ni)
+#pragma unroll
+                for (int mi = 0; mi < TM; ++mi) sum[ni][mi] += __builtin_bit_cast(typename T::Acc, v[ni][mi]);
+        }
+#pragma unroll
+        for (int ni = 0; ni < TN; ++ni)
+#pragma unroll
+            for (int mi = 0; mi < TM; ++mi) acc[ni][mi] = sum[ni][mi];
+        __syncthreads();  // the flag has been read: its place is free for the output
+    }
+    op_epilogue<T, MODE, GLU>(p, lds, at, wave, wm, wn, lane, acc);
+}
+
+template <int MODE, bool GLU>
+static hipError_t launch_mode(bool big, const OpTileArgs& a, int grid, hipStream_t s) {
+    if (big) {
+        if (a.splits != 1) return hipErrorInvalidValue;
+        op_pp_kernel<MODE, GLU><<<grid, 512, OpTile<256, 256, 2, 4, MODE>::LDS_BYTES, s>>>(a);
+    } else {
+        op_small_kernel<MODE, GLU><<<grid, 256, OpTile<128, 128, 2, 2, MODE>::LDS_BYTES, s>>>(a);
+    }
+    return hipGetLastError();
+}
+
+hipError_t launch_op_tile(int mode, bool glu, bool big, const OpTileArgs& a, int grid, hipStream_t s) {
+    switch (mode) {
+        case kOpI8: return glu ? launch_mode<kOpI8, true>(big, a, grid, s) : launch_mode<kOpI8, false>(big, a, grid, s);
+        case kOpAbt: return launch_mode<kOpAbt, false>(big, a, grid, s);
+        case kOpAtb: return launch_mode<kOpAtb, false>(big, a, grid, s);
+        case kOpTrain: return launch_mode<kOpTrain, true>(big, a, grid, s);
+        default: return hipErrorInvalidValue;
+    }
+}
+
+template <int MODE, bool GLU>
+static hipError_t configure_mode() {
+    hipError_t e = hipFuncSetAttribute((const void*)op_pp_kernel<MODE, GLU>, hipFuncAttributeMaxDynamicSharedMemorySize,
+                                       OpTile<256, 256, 2, 4, MODE>::LDS_BYTES);
+    if (e == hipSuccess)
+        e = hipFuncSetAttribute((const void*)op_small_kernel<MODE, GLU>, hipFuncAttributeMaxDynamicSharedMemorySize,
+                                OpTile<128, 128, 2, 2, MODE>::LDS_BYTES);
+    return e;
+}
+
+hipError_t configure_op_kernels() {
+    hipError_t e = configure_mode<kOpI8, false>();
+    if (e == hipSuccess) e = configure_mode<kOpI8, true>();
+    if (e == hipSuccess) e = configure_mode<kOpAbt, false>();
+    if (e == hipSuccess) e = configure_mode<kOpAtb, false>();
+    if (e == hipSuccess) e = configure_mode<kOpTrain, true>();
+    return e;
+}
+
+}  // namespace glk
