@@ -48,7 +48,7 @@ struct OpTile {
     static constexpr int NW = WM * WN, NT = NW * 64;
     static constexpr int WTM = BM / WM, WTN = BN / WN;
     static constexpr int TM = WTM / 16, TN = WTN / 16;
-    static constexpr int A_BYTES = BM * 64, B_BYTES = BN * 64;
+    static constexpr int A_BYTES = BM * 64, B_BYTES = BN * 64;  // one slot of each ring
     static constexpr int B_RING = SLOTS * A_BYTES;
     static constexpr int LDS_BYTES = SLOTS * (A_BYTES + B_BYTES);
     static constexpr int A_PW = A_BYTES / 1024 / NW;  // 1 KB copy instructions per wave and stage
@@ -69,79 +69,95 @@ __device__ __forceinline__ i32x4 op_mfma(const u32x4& x, const u32x4& y, const i
     return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, x), __builtin_bit_cast(i32x4, y), c, 0, 0, 0);
 }
 
-// The copies of one operand (R rows or columns of the tile from r0, `rows` of them in all) by one wave.
+__device__ __forceinline__ int op_wrap(int slot) { return slot >= 5 ? slot - 5 : slot; }
+
+// The copies of one operand (R rows or columns of the tile from r0, `rows` of them in all) by one
+// wave: PW instructions of 1 KB for one slot. Issue number u fills slot u % 5: of a contiguous
+// operand with half u & 1 of the rows, 128 bytes (two k-steps, u / 2) of each; of a strided one with
+// the 32 rows of k-step u.
 template <int R, int PW, bool CONTIG, int ES, bool GLU, int WT>
 struct OpCopy {
-    uint32_t off[PW];
-    int chunk[PW];       // contiguous: byte of the lane's chunk in the 64-byte row
-    bool ok[PW];
-    const char* base[GLU && CONTIG ? PW : 1];
+    static constexpr int HALVES = CONTIG ? 2 : 1;
+    uint32_t off[HALVES][PW];  // byte offset of the lane's 16 bytes, or kBufInvalid outside the matrix
+    int chunk[2];              // contiguous: byte of the lane's chunk in the 128-byte row, by parity of i
+    const char* base[GLU && CONTIG ? HALVES * PW : 1];
     int64_t ld_bytes;
+    int sum;                   // bytes (contiguous) or rows (strided) of the summed index
 
     // gated operands hold `rows` gate rows (columns) and then `rows` up ones; the tile's WT-wide
     // share of each wave is WT / 2 gate and the same WT / 2 up
-    __device__ __forceinline__ void init(const void* p, int64_t ld, int64_t r0, int64_t rows, int wave, int lane) {
+    __device__ __forceinline__ void init(const void* p, int64_t ld, int64_t r0, int64_t rows, int64_t k0, int k_count,
+                                         int wave, int lane) {
+        static_assert(!CONTIG || PW == 2, "chunk by parity of i");
         ld_bytes = ld * ES;
-        const char* at = static_cast<const char*>(p);
+        sum = CONTIG ? k_count * ES : k_count;
+        const char* at = static_cast<const char*>(p) + k0 * (CONTIG ? ES : ld_bytes);
+        chunk[0] = 16 * ((lane & 7) ^ (lane >> 4));  // row 8 idx + lane / 8: (row >> 1) & 7, idx even
+        chunk[1] = chunk[0] ^ 64;                    // idx odd
 #pragma unroll
-        for (int i = 0; i < PW; ++i) {
-            const int idx = wave * PW + i;
-            if constexpr (CONTIG) {
-                const int r = 16 * idx + (lane >> 2);
-                chunk[i] = 16 * ((lane & 3) ^ ((r >> 2) & 3));
-                if constexpr (GLU) {  // 16 rows are all gate or all up: one base for the instruction
-                    const int q = 16 * idx, out = (q / WT) * (WT / 2) + q % (WT / 2);
-                    const int64_t src = r0 + out + (q % WT < WT / 2 ? 0 : rows);
-                    base[i] = at + src * ld_bytes;
-                    off[i] = (uint32_t)((lane >> 2) * (int)ld_bytes + chunk[i]);
-                    ok[i] = r0 + out + (lane >> 2) < rows;
-                } else {
-                    off[i] = (uint32_t)(r * (int)ld_bytes + chunk[i]);
-                    ok[i] = r0 + r < rows;
-                }
-            } else {
-                constexpr int RPI = 512 / R, CH = R / 8;  // k rows per instruction, chunks per row
-                const int k = idx * RPI + lane / CH, pc = lane % CH;
-                const int col = 16 * op_group(pc >> 1, k) + 8 * (pc & 1);
-                int src = col, out = col;
-                if constexpr (GLU) {
-                    const int q = col % WT;
-                    out = (col / WT) * (WT / 2) + q % (WT / 2);
-                    src = out + (q < WT / 2 ? 0 : (int)rows);
-                }
-                off[i] = sel_off(r0 + out < rows, (uint32_t)(k * (int)ld_bytes + src * ES));
-            }
-        }
-        if constexpr (!(GLU && CONTIG)) base[0] = at + (CONTIG ? r0 * ld_bytes : r0 * ES);
-    }
-    // the k-step that starts `k` elements into the sum, `left` elements of it remaining (0: zeros)
-    __device__ __forceinline__ void issue(uint32_t lds, int64_t k, int left, int wave) const {
-        if constexpr (CONTIG) {
-            const int bytes = left * ES;
+        for (int h = 0; h < HALVES; ++h)
 #pragma unroll
             for (int i = 0; i < PW; ++i) {
-                const i32x4 r = rsrc_words(base[GLU ? i : 0] + k * ES, kBufRecords);
-                dma16(r, lds + (wave * PW + i) * 1024, sel_off(ok[i] & (chunk[i] < bytes), off[i]));
+                const int idx = wave * PW + i;
+                if constexpr (CONTIG) {
+                    const int q = h * (R / 2) + 8 * idx, r = q + (lane >> 3);
+                    if constexpr (GLU) {  // 8 rows are all gate or all up: one base for the instruction
+                        const int out = (q / WT) * (WT / 2) + q % (WT / 2);
+                        const int64_t src = r0 + out + (q % WT < WT / 2 ? 0 : rows);
+                        base[h * PW + i] = at + src * ld_bytes;
+                        off[h][i] = sel_off(r0 + out + (lane >> 3) < rows,
+                                            (uint32_t)((lane >> 3) * (int)ld_bytes + chunk[i & 1]));
+                    } else {
+                        off[h][i] = sel_off(r0 + r < rows, (uint32_t)(r * (int)ld_bytes + chunk[i & 1]));
+                    }
+                } else {
+                    constexpr int RPI = 512 / R, CH = R / 8;  // k rows per instruction, chunks per row
+                    const int k = idx * RPI + lane / CH, pc = lane % CH;
+                    const int col = 16 * op_group(pc >> 1, k) + 8 * (pc & 1);
+                    int src = col, out = col;
+                    if constexpr (GLU) {
+                        const int q = col % WT;
+                        out = (col / WT) * (WT / 2) + q % (WT / 2);
+                        src = out + (q < WT / 2 ? 0 : (int)rows);
+                    }
+                    off[h][i] = sel_off(r0 + out < rows, (uint32_t)(k * (int)ld_bytes + src * ES));
+                }
+            }
+        if constexpr (!(GLU && CONTIG)) base[0] = at + (CONTIG ? r0 * ld_bytes : r0 * ES);
+    }
+    // issue number u with u & 1 == H (a constant where it matters) into the slot at LDS address `lds`
+    template <int H>
+    __device__ __forceinline__ void issue(int u, uint32_t lds, int wave) const {
+        if constexpr (CONTIG) {
+            const int at = (u >> 1) * 128, left = sum - at;  // left <= 0: zeros
+            const int from = left > 0 ? at : 0;
+#pragma unroll
+            for (int i = 0; i < PW; ++i) {
+                const i32x4 r = rsrc_words(base[GLU ? H * PW + i : 0] + from, kBufRecords);
+                dma16(r, lds + (wave * PW + i) * 1024, sel_off(chunk[i & 1] < left, off[H][i]));
             }
         } else {
-            const int krows = __builtin_amdgcn_readfirstlane(min(left, 32));
-            const i32x4 r = rsrc_words(base[0] + k * ld_bytes, (uint32_t)krows * (uint32_t)ld_bytes);
+            const int at = u * 32;
+            const int krows = __builtin_amdgcn_readfirstlane(max(min(sum - at, 32), 0));
+            const i32x4 r = rsrc_words(base[0] + (krows > 0 ? at : 0) * ld_bytes, (uint32_t)krows * (uint32_t)ld_bytes);
 #pragma unroll
-            for (int i = 0; i < PW; ++i) dma16(r, lds + (wave * PW + i) * 1024, off[i]);
+            for (int i = 0; i < PW; ++i) dma16(r, lds + (wave * PW + i) * 1024, off[0][i]);
         }
     }
 };
 
-// T tiles of 16 rows (columns) from `w0` of a stage: lane l gets row w0 + 16 i + (l & 15), bytes
-// 16 (l >> 4) .. + 15 of the k-step
-template <int R, int T, bool CONTIG>
-__device__ __forceinline__ void op_read(const char* stage, int w0, int lane, u32x4 (&f)[T]) {
+// The operands of k-step t (t % 5 == slot, t & 1 == P) from one ring: T tiles of 16 rows (columns)
+// from `w0`. Lane l gets row w0 + 16 i + (l & 15), bytes 16 (l >> 4) .. + 15 of the k-step.
+template <int R, int T, bool CONTIG, int P>
+__device__ __forceinline__ void op_read(const char* ring, int slot, int w0, int lane, u32x4 (&f)[T]) {
     const int j = lane & 15, G = lane >> 4;
     if constexpr (CONTIG) {
-        const char* at = stage + (w0 + j) * 64 + 16 * (G ^ ((j >> 2) & 3));
+        const int at = op_wrap(slot + (w0 >= R / 2 ? 1 : 0) + (P ? 4 : 0));  // unit (t - P) + half
+        const char* row = ring + at * (64 * R) + (w0 % (R / 2) + j) * 128 + 16 * ((4 * P + G) ^ (j >> 1));
 #pragma unroll
-        for (int i = 0; i < T; ++i) f[i] = *reinterpret_cast<const u32x4*>(at + i * 1024);
+        for (int i = 0; i < T; ++i) f[i] = *reinterpret_cast<const u32x4*>(row + i * 2048);
     } else {
+        const char* stage = ring + slot * (64 * R);
 #pragma unroll
         for (int i = 0; i < T; ++i) {
             i16x4 v[2];
@@ -154,6 +170,23 @@ __device__ __forceinline__ void op_read(const char* stage, int w0, int lane, u32
             const i16x8 x = {v[0][0], v[0][1], v[0][2], v[0][3], v[1][0], v[1][1], v[1][2], v[1][3]};
             f[i] = __builtin_bit_cast(u32x4, x);
         }
+    }
+}
+
+// Waits until this wave's copies for the next k-step have landed, in a step (parity P) that issued
+// A's slot and then B's. A strided operand's were issued three whole steps before this one's last; a
+// contiguous one's second half in the step before, and only odd steps are followed by a new pair.
+template <class T, int P>
+__device__ __forceinline__ void op_wait() {
+    if constexpr (T::A_CONTIG && T::B_CONTIG) {
+        if constexpr (P == 1) wait_vmcnt<T::LOADS>();
+    } else if constexpr (T::A_CONTIG) {
+        if constexpr (P == 1)
+            wait_vmcnt<T::LOADS + T::B_PW>();
+        else
+            wait_vmcnt<3 * T::LOADS>();
+    } else {
+        wait_vmcnt<3 * T::LOADS>();
     }
 }
 
@@ -292,21 +325,23 @@ __device__ __forceinline__ void op_epilogue(const OpTileArgs& p, char* lds, cons
                     put(Out{}, mi, ni, acc[ni][mi]);
             }
     }
-    op_store_rows<T::WTM, WTNO>(ob, p.C, p.ldc, mw, p.M, nw, p.N, lane, p.vec != 0);
+    op_store_rows<T::WTM, WTNO>(ob, p.C, p.ldc, mw, p.M, nw, p.N, lane, MODE != kOpI8 || p.vec != 0);
 }
 
 // ---- 256 x 256: two wave groups alternating memory and MFMA phases --------------------------------
-// Phases are separated by workgroup barriers b1, b2, ...; group 0 runs the memory phase of step s
-// before b(2 s + 1) and its MFMAs before b(2 s + 2), group 1 one barrier later. The last read of step
-// s - 1's slot is group 1's, before b(2 s); both groups refill that slot with stage s + 4 in their
-// memory phase of step s, after b(2 s). Each wave ends its memory phase of step s waiting for its own
-// copies of stage s + 1 (issued in step s - 3: three later steps' copies may be in flight), and a
-// barrier follows before any wave reads that stage.
+// Phases are separated by workgroup barriers b1, b2, ...; group 0 runs the memory phase of step t
+// before b(2 t + 1) and its MFMAs before b(2 t + 2), group 1 one barrier later, so every read of step
+// t - 1 is over at b(2 t), before either group's memory phase of step t. That phase refills: a strided
+// operand's slot of step t - 1 with step t + 4; a contiguous one's slot of unit t - 2 (of steps t - 2
+// and t - 1 for even t, t - 3 and t - 2 for odd t) with unit t + 3. Each wave ends its memory phase
+// waiting for its own copies that step t + 1 reads, and a barrier follows before any wave reads them.
 template <int MODE, bool GLU>
 __global__ void __attribute__((amdgpu_flat_work_group_size(512, 512), amdgpu_waves_per_eu(2, 2)))
 op_pp_kernel(OpTileArgs p) {
     using T = OpTile<256, 256, 2, 4, MODE>;
-    constexpr int TM = T::TM, TN = T::TN, AHEAD = T::SLOTS - 1;
+    constexpr int TM = T::TM, TN = T::TN;
+    // issue number of step t: t + 3 (contiguous) or t + 4 (strided)
+    constexpr int A_AHEAD = T::A_CONTIG ? 3 : 4, B_AHEAD = T::B_CONTIG ? 3 : 4;
     extern __shared__ __attribute__((aligned(1024))) char lds[];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -316,13 +351,14 @@ op_pp_kernel(OpTileArgs p) {
 
     OpCopy<256, T::A_PW, T::A_CONTIG, T::ES, false, T::WTM> ca;
     OpCopy<256, T::B_PW, T::B_CONTIG, T::ES, GLU, T::WTN> cb;
-    ca.init(p.A, p.lda, at.m0, p.M, wave, lane);
-    cb.init(p.B, p.ldb, at.n0, p.N, wave, lane);
+    ca.init(p.A, p.lda, at.m0, p.M, 0, p.K, wave, lane);
+    cb.init(p.B, p.ldb, at.n0, p.N, 0, p.K, wave, lane);
     const uint32_t ring = lds_addr(lds);
-    auto issue = [&](int s, int slot) {
-        const int k = s * T::KE, left = max(p.K - k, 0);
-        ca.issue(ring + slot * T::A_BYTES, left ? k : 0, left, wave);
-        cb.issue(ring + T::B_RING + slot * T::B_BYTES, left ? k : 0, left, wave);
+    auto issue_a = [&](auto h, int u, int slot) {
+        ca.template issue<decltype(h)::value>(u, ring + slot * T::A_BYTES, wave);
+    };
+    auto issue_b = [&](auto h, int u, int slot) {
+        cb.template issue<decltype(h)::value>(u, ring + T::B_RING + slot * T::B_BYTES, wave);
     };
     typename T::Acc acc[TN][TM];
 #pragma unroll
@@ -335,22 +371,34 @@ op_pp_kernel(OpTileArgs p) {
         __builtin_amdgcn_sched_barrier(0);
     };
     const int tail = (T::I8 && (p.K & 15)) ? nsteps - 1 : -1;
+    using P0 = std::integral_constant<int, 0>;
+    using P1 = std::integral_constant<int, 1>;
 
-#pragma unroll
-    for (int s = 0; s < AHEAD; ++s) issue(s, s);
-    wait_vmcnt<T::LOADS * (AHEAD - 1)>();
+    // as steps -4 .. -1 would issue, in their order
+    if (!T::A_CONTIG) issue_a(P0{}, 0, 0);
+    if (!T::B_CONTIG) issue_b(P0{}, 0, 0);
+    issue_a(P0{}, A_AHEAD - 3, A_AHEAD - 3);
+    issue_b(P0{}, B_AHEAD - 3, B_AHEAD - 3);
+    issue_a(P1{}, A_AHEAD - 2, A_AHEAD - 2);
+    issue_b(P1{}, B_AHEAD - 2, B_AHEAD - 2);
+    issue_a(P0{}, A_AHEAD - 1, A_AHEAD - 1);
+    issue_b(P0{}, B_AHEAD - 1, B_AHEAD - 1);
+    op_wait<T, 1>();
     lds_barrier();
     if (grp == 1) phase_barrier();
     int slot = 0;
-    for (int s = 0; s < nsteps; ++s) {
+    auto step = [&](int t, auto par) {
+        constexpr int P = decltype(par)::value;
+        using H = std::integral_constant<int, 1 - P>;  // parity of t + 3; strided copies have no halves
         u32x4 fa[TM], fb[TN];
-        op_read<256, TM, T::A_CONTIG>(lds + slot * T::A_BYTES, wm * T::WTM, lane, fa);
-        op_read<256, TN, T::B_CONTIG>(lds + T::B_RING + slot * T::B_BYTES, wn * T::WTN, lane, fb);
-        issue(s + AHEAD, slot == 0 ? AHEAD : slot - 1);
+        op_read<256, TM, T::A_CONTIG, P>(lds, slot, wm * T::WTM, lane, fa);
+        op_read<256, TN, T::B_CONTIG, P>(lds + T::B_RING, slot, wn * T::WTN, lane, fb);
+        issue_a(H{}, t + A_AHEAD, op_wrap(slot + A_AHEAD));
+        issue_b(H{}, t + B_AHEAD, op_wrap(slot + B_AHEAD));
         if constexpr (T::I8) {
-            if (s == tail) op_clear_tail(p.K - s * T::KE, lane, fa);
+            if (t == tail) op_clear_tail(p.K - t * T::KE, lane, fa);
         }
-        wait_vmcnt<T::LOADS * (AHEAD - 1)>();
+        op_wait<T, P>();
         wait_lgkmcnt0();
         phase_barrier();
 #pragma unroll
@@ -358,8 +406,14 @@ op_pp_kernel(OpTileArgs p) {
 #pragma unroll
             for (int mi = 0; mi < TM; ++mi) acc[ni][mi] = op_mfma(fb[ni], fa[mi], acc[ni][mi]);
         phase_barrier();
-        slot = slot == AHEAD ? 0 : slot + 1;
+        slot = op_wrap(slot + 1);
+    };
+    int t = 0;
+    for (; t + 1 < nsteps; t += 2) {
+        step(t, P0{});
+        step(t + 1, P1{});
     }
+    if (t < nsteps) step(t, P0{});
     if (grp == 0) phase_barrier();
     wait_vmcnt<0>();  // the copies past K included
     lds_barrier();    // the rings are free for the output
@@ -367,14 +421,17 @@ op_pp_kernel(OpTileArgs p) {
 }
 
 // ---- 128 x 128, K split over idle CUs -------------------------------------------------------------
-// Iteration i reads the operands of step i + 1 while the MFMAs of step i run. The slot of stage i was
-// last read in iteration i - 1, which every wave ends (its LDS reads waited for) at the barrier of
-// iteration i; stage i + 5 goes there. Stages i + 2 .. i + 4 may be in flight at that barrier.
+// Iteration i reads the operands of step i + 1 while the MFMAs of step i run. At its barrier the reads
+// of step i, made in iteration i - 1, are over in every wave; after it, a strided operand's slot of
+// step i takes step i + 5, and a contiguous one's slot of unit i - 1 (steps i - 1 and i for odd i, i - 2
+// and i - 1 for even i) takes unit i + 4. Its barrier also needs step i + 1's copies landed, which is
+// what op_wait says of the step that iteration i - 1 would be in the other schedule's count.
 template <int MODE, bool GLU>
 __global__ void __attribute__((amdgpu_flat_work_group_size(256, 256), amdgpu_waves_per_eu(2, 2)))
 op_small_kernel(OpTileArgs p) {
     using T = OpTile<128, 128, 2, 2, MODE>;
-    constexpr int TM = T::TM, TN = T::TN, S = T::SLOTS;
+    constexpr int TM = T::TM, TN = T::TN;
+    constexpr int A_AHEAD = T::A_CONTIG ? 4 : 5, B_AHEAD = T::B_CONTIG ? 4 : 5;
     extern __shared__ __attribute__((aligned(1024))) char lds[];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -383,45 +440,66 @@ op_small_kernel(OpTileArgs p) {
     const int total = (p.K + T::KE - 1) / T::KE;
     const int first = at.piece * p.kt_per_split;
     const int nsteps = max(min(total - first, p.kt_per_split), 0);
-    const int kend = min(p.K, (first + nsteps) * T::KE);
+    const int count = max(min(p.K - first * T::KE, nsteps * T::KE), 0);  // of the summed index
 
     OpCopy<128, T::A_PW, T::A_CONTIG, T::ES, false, T::WTM> ca;
     OpCopy<128, T::B_PW, T::B_CONTIG, T::ES, GLU, T::WTN> cb;
-    ca.init(p.A, p.lda, at.m0, p.M, wave, lane);
-    cb.init(p.B, p.ldb, at.n0, p.N, wave, lane);
+    ca.init(p.A, p.lda, at.m0, p.M, (int64_t)first * T::KE, count, wave, lane);
+    cb.init(p.B, p.ldb, at.n0, p.N, (int64_t)first * T::KE, count, wave, lane);
     const uint32_t ring = lds_addr(lds);
-    auto issue = [&](int s, int slot) {
-        const int k = (first + s) * T::KE, left = max(kend - k, 0);
-        ca.issue(ring + slot * T::A_BYTES, left ? k : 0, left, wave);
-        cb.issue(ring + T::B_RING + slot * T::B_BYTES, left ? k : 0, left, wave);
+    auto issue_a = [&](auto h, int u, int slot) {
+        ca.template issue<decltype(h)::value>(u, ring + slot * T::A_BYTES, wave);
+    };
+    auto issue_b = [&](auto h, int u, int slot) {
+        cb.template issue<decltype(h)::value>(u, ring + T::B_RING + slot * T::B_BYTES, wave);
     };
     typename T::Acc acc[TN][TM];
 #pragma unroll
     for (int ni = 0; ni < TN; ++ni)
 #pragma unroll
         for (int mi = 0; mi < TM; ++mi) acc[ni][mi] = typename T::Acc{};
-    const int tail = (T::I8 && (p.K & 15)) ? total - 1 - first : -1;
-    auto read = [&](int s, int slot, u32x4 (&fa)[TM], u32x4 (&fb)[TN]) {
-        op_read<128, TM, T::A_CONTIG>(lds + slot * T::A_BYTES, wm * T::WTM, lane, fa);
-        op_read<128, TN, T::B_CONTIG>(lds + T::B_RING + slot * T::B_BYTES, wn * T::WTN, lane, fb);
+    const int tail = (T::I8 && (count & 15)) ? nsteps - 1 : -1;
+    auto read = [&](int s, auto par, int slot, u32x4 (&fa)[TM], u32x4 (&fb)[TN]) {
+        constexpr int P = decltype(par)::value;
+        op_read<128, TM, T::A_CONTIG, P>(lds, slot, wm * T::WTM, lane, fa);
+        op_read<128, TN, T::B_CONTIG, P>(lds + T::B_RING, slot, wn * T::WTN, lane, fb);
         if constexpr (T::I8) {
-            if (s == tail) op_clear_tail(p.K - (first + s) * T::KE, lane, fa);
+            if (s == tail) op_clear_tail(count - s * T::KE, lane, fa);
         }
     };
+    using P0 = std::integral_constant<int, 0>;
+    using P1 = std::integral_constant<int, 1>;
 
+    // as iterations -5 .. -1 would issue, in their order
     u32x4 fa0[TM], fb0[TN], fa1[TM], fb1[TN];
-#pragma unroll
-    for (int s = 0; s < S; ++s) issue(s, s);
-    wait_vmcnt<T::LOADS * (S - 1)>();
+    if (!T::A_CONTIG) issue_a(P0{}, 0, 0);
+    if (!T::B_CONTIG) issue_b(P0{}, 0, 0);
+    issue_a(P0{}, A_AHEAD - 4, A_AHEAD - 4);
+    issue_b(P0{}, B_AHEAD - 4, B_AHEAD - 4);
+    issue_a(P1{}, A_AHEAD - 3, A_AHEAD - 3);
+    issue_b(P1{}, B_AHEAD - 3, B_AHEAD - 3);
+    issue_a(P0{}, A_AHEAD - 2, A_AHEAD - 2);
+    issue_b(P0{}, B_AHEAD - 2, B_AHEAD - 2);
+    issue_a(P1{}, A_AHEAD - 1, A_AHEAD - 1);
+    issue_b(P1{}, B_AHEAD - 1, B_AHEAD - 1);
+    if constexpr (T::A_CONTIG && T::B_CONTIG)
+        wait_vmcnt<2 * T::LOADS>();            // units 0 and 1; 2 and 3 may be in flight
+    else if constexpr (T::A_CONTIG)
+        wait_vmcnt<2 * T::LOADS + T::B_PW>();  // A's units 0 and 1 (B's step 0 before them)
+    else
+        wait_vmcnt<4 * T::LOADS>();
     lds_barrier();
-    read(0, 0, fa0, fb0);
+    read(0, P0{}, 0, fa0, fb0);
     int slot = 0;
-    auto step = [&](int i, u32x4 (&fa)[TM], u32x4 (&fb)[TN], u32x4 (&na)[TM], u32x4 (&nb)[TN]) {
-        const int next = slot == S - 1 ? 0 : slot + 1;
-        wait_vmcnt<T::LOADS * (S - 2)>();  // this wave's copies of stage i + 1 landed
-        lds_barrier();                     // every wave's did, and step i's operands are in registers
-        issue(i + S, slot);
-        read(i + 1, next, na, nb);
+    auto step = [&](int i, auto par, u32x4 (&fa)[TM], u32x4 (&fb)[TN], u32x4 (&na)[TM], u32x4 (&nb)[TN]) {
+        constexpr int P = decltype(par)::value;
+        using H = std::integral_constant<int, P>;  // parity of i + 4
+        const int next = op_wrap(slot + 1);
+        op_wait<T, P>();  // this wave's copies of step i + 1 landed
+        lds_barrier();    // every wave's did, and step i's operands are in registers
+        issue_a(H{}, i + A_AHEAD, op_wrap(slot + A_AHEAD));
+        issue_b(H{}, i + B_AHEAD, op_wrap(slot + B_AHEAD));
+        read(i + 1, std::integral_constant<int, 1 - P>{}, next, na, nb);
 #pragma unroll
         for (int ni = 0; ni < TN; ++ni)
 #pragma unroll
@@ -430,10 +508,10 @@ op_small_kernel(OpTileArgs p) {
     };
     int i = 0;
     for (; i + 1 < nsteps; i += 2) {
-        step(i, fa0, fb0, fa1, fb1);
-        step(i + 1, fa1, fb1, fa0, fb0);
+        step(i, P0{}, fa0, fb0, fa1, fb1);
+        step(i + 1, P1{}, fa1, fb1, fa0, fb0);
     }
-    if (i < nsteps) step(i, fa0, fb0, fa1, fb1);
+    if (i < nsteps) step(i, P0{}, fa0, fb0, fa1, fb1);
     wait_vmcnt<0>();
     lds_barrier();
 
