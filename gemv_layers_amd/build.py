@@ -16,7 +16,7 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 
 SOURCES = ["gemm_tile.hip", "gemm_skinny.hip", "gemm_generic.hip", "gemm_mx.hip", "gemm_packed.hip",
-           "ops_tile.hip", "ops_generic.hip", "ops_rows.hip", "peak.hip", "plan.cpp", "abi.cpp", "ops.cpp"]
+           "ops_tile.hip", "i8_decode.hip", "ops_generic.hip", "ops_rows.hip", "peak.hip", "plan.cpp", "abi.cpp", "ops.cpp"]
 
 COMMON = [
     "-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",

@@ -76,11 +76,30 @@ hipError_t launch_tiles(int mode, bool glu, const OpArgs& a, const glk::Plan& p,
     return glk::launch_op_tile(mode, glu, p.bm == 256, t, (int)p.grid, stream);
 }
 
+// The 8-bit product of at most 64 rows on the weight-streaming kernel.
+int run_i8_decode(bool glu, const OpArgs& a, const glk::DeviceInfo& dev, hipStream_t stream) {
+    const glk::Plan p = glk::make_i8_decode_plan(a.M, a.N, a.K, dev, glu);
+    glk::Workspace w;
+    if (p.splits > 1) {
+        const int st = glk::stream_workspace(stream, &w);
+        if (st != GEMM_OK) return st;
+    }
+    const glk::I8DecodeArgs t{static_cast<const int8_t*>(a.A), static_cast<const int8_t*>(a.B), a.C, a.sa, a.sb,
+                              (int)a.M, (int)a.N, (int)a.K, (int)a.lda, (int)a.ldb, (int)a.ldc,
+                              !misaligned(a.C, 8) && a.ldc % 4 == 0 && a.N % 4 == 0, p.splits,
+                              reinterpret_cast<int32_t*>(w.ws), w.counters};
+    if (glk::launch_i8_decode(glu, p.mtiles, p.strip / 16, p.threads / 64, t, (int)p.grid, stream) != hipSuccess)
+        return GEMM_ERR_HIP;
+    glk::set_last_plan(p, a.M, a.N, a.K, op_name(glk::kOpI8, glu));
+    return GEMM_OK;
+}
+
 // One product on the current device: M, N > 0, operands checked.
 int run_op(int mode, bool glu, const OpArgs& a, hipStream_t stream) {
     int st = GEMM_OK;
     const glk::DeviceInfo* dev = glk::current_device(&st);
     if (!dev) return st;
+    if (mode == glk::kOpI8 && a.M <= 64 && a.K > 0 && matrix_ok(mode, glu, a)) return run_i8_decode(glu, a, *dev, stream);
     glk::Plan p;
     hipError_t e = hipSuccess;
     if (a.K == 0) {

@@ -52,6 +52,24 @@ struct OpTileArgs {
 hipError_t launch_op_tile(int mode, bool glu, bool big, const OpTileArgs& a, int grid, hipStream_t s);
 hipError_t configure_op_kernels();
 
+// ---- 8-bit product of few tokens -------------------------------------------------------------------
+struct I8DecodeArgs {
+    const int8_t* A;
+    const int8_t* W;
+    uint16_t* C;
+    const float* sa;
+    const float* sb;     // N scales, or 2N gated
+    int M, N, K;         // M <= 64
+    int lda, ldw, ldc;
+    int vec;             // C takes 8-byte stores
+    int pieces;          // of K, one workgroup each
+    int32_t* ws;         // pieces > 1: groups * pieces * tn * mt * 256
+    uint32_t* counters;  // one per group, zero between launches
+};
+// mt: 16-row tiles of M; tn: 16-row weight tiles per workgroup (gated: half gate, half up); nw waves
+hipError_t launch_i8_decode(bool glu, int mt, int tn, int nw, const I8DecodeArgs& a, int grid, hipStream_t s);
+hipError_t configure_i8_decode();
+
 // ---- row kernels --------------------------------------------------------------------------------
 // symmetric 8-bit codes of each row: see gemm_i8_quantize
 hipError_t launch_i8_quantize(const uint16_t* X, int64_t R, int64_t K, int64_t ldx, int8_t* Q, int64_t ldq,

@@ -1,52 +1,18 @@
 // Row kernels of the 8-bit and training operators: one pass over memory each.
 //
-// Quantisation, s = max|x| / 127 in float32 and q = round(x / s) for each row. A row stays in the
-// registers of its workgroup between the maximum and the codes, so that memory is read once (2
-// bytes an element) and written once (1 byte). The maximum is an integer one over the magnitude
-// bits of bf16, whose order is that of the values, infinities and NaN last: no value is lost to a
-// comparison with NaN. The codes are those of the correctly rounded float32 quotient x / s, from
-// one multiplication by 127 / max|x|: with bf16 x, 127 x / max|x| = k + 1/2 means 254 x = (2 k + 1)
-// max|x|, so 127 divides 2 k + 1 (then |x| = max|x| / 2, whose code is divided out once a row) or the
-// mantissa of max|x| (then s and the factor are powers of two and nothing rounds). Any other x is
-// off half-way by 1 / (254 * 255) of its size at least, 100 times the float32 roundings of either way.
-
+// Quantisation of rows (the arithmetic is in codes.h). A row stays in the registers of its workgroup
+// between the maximum and the codes, so that memory is read once (2 bytes an element) and written
+// once (1 byte). Few rows are bound by latency, a load, a reduction and a store, and take wide
+// workgroups; many rows by memory.
+//
 // The gated block's gradient, element by element: reads dC, g and u, writes dg and du, 10 bytes an
 // element.
 
+#include "codes.h"
 #include "common.h"
 #include "ops.h"
 
 namespace glk {
-
-struct CodeScale {
-    float s, inv;     // the row's scale, and 127 / max|x|
-    float half, qh;   // max|x| / 2, and the magnitude of its code
-    bool divide;      // a row so small that the scale may be subnormal: every code by division
-    bool none;        // a row of zeros, or with an infinity or NaN: codes 0
-};
-__device__ __forceinline__ CodeScale code_scale(uint32_t amax_bits) {
-    const float amax = __builtin_bit_cast(float, amax_bits << 16);
-    CodeScale c;
-    c.none = amax_bits == 0 || amax_bits >= 0x7F80u;
-    c.s = amax_bits >= 0x7F80u ? __builtin_nanf("") : amax / 127.0f;
-    c.divide = amax < 0x1p-60f;
-    c.inv = 127.0f / amax;
-    c.half = 0.5f * amax;
-    c.qh = rintf(c.half / c.s);
-    return c;
-}
-__device__ __forceinline__ int code_of(float x, const CodeScale& c) {
-    if (c.none) return 0;
-    if (c.divide) return (int)rintf(x / c.s);
-    const float q = rintf(x * c.inv);
-    return (int)(fabsf(x) == c.half ? copysignf(c.qh, x) : q);
-}
-
-__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) v = max(v, (uint32_t)__shfl_xor((int)v, o));
-    return v;
-}
 
 // one row per workgroup of NW waves, NC 16-byte chunks per thread in registers
 template <int NW, int NC>
@@ -66,17 +32,11 @@ __global__ void __launch_bounds__(64 * NW) i8_quantize_kernel(const uint16_t* __
         if (k + 8 <= K) {
             v[c] = *reinterpret_cast<const u32x4*>(x + k);
         } else if (k < K) {
-            uint32_t w[4] = {0, 0, 0, 0};
-#pragma unroll
-            for (int j = 0; j < 7; ++j)
-                if (k + j < K) w[j >> 1] |= (uint32_t)x[k + j] << (16 * (j & 1));
-            v[c] = u32x4{w[0], w[1], w[2], w[3]};
+            v[c] = load_some(x + k, K - k);
         }
     }
 #pragma unroll
-    for (int c = 0; c < NC; ++c)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) amax = max(amax, max(v[c][j] & 0x7FFFu, (v[c][j] >> 16) & 0x7FFFu));
+    for (int c = 0; c < NC; ++c) amax = magnitude8(v[c], amax);
     amax = wave_max(amax);
     if constexpr (NW > 1) {
         if ((tid & 63) == 0) part[tid >> 6] = amax;
@@ -93,14 +53,9 @@ __global__ void __launch_bounds__(64 * NW) i8_quantize_kernel(const uint16_t* __
     for (int c = 0; c < NC; ++c) {
         const int64_t k = 8 * ((int64_t)c * 64 * NW + tid);
         if (k >= padded) continue;
-        uint32_t w[2] = {0, 0};  // (elements past K are zero in v)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float e = (j & 1) ? bf16_hi(v[c][j >> 1]) : bf16_lo(v[c][j >> 1]);
-            w[j >> 2] |= ((uint32_t)code_of(e, cs) & 0xFFu) << (8 * (j & 3));
-        }
+        const u32x2 w = codes8(v[c], cs);  // (elements past K are zero in v)
         if (wide && k + 8 <= padded) {
-            *reinterpret_cast<u32x2*>(q + k) = u32x2{w[0], w[1]};
+            *reinterpret_cast<u32x2*>(q + k) = w;
         } else {
 #pragma unroll
             for (int j = 0; j < 8; ++j)
@@ -140,6 +95,8 @@ hipError_t launch_i8_quantize(const uint16_t* X, int64_t R, int64_t K, int64_t l
     const int64_t chunks = (K + 15) / 16 * 2;
     if (!aligned || chunks > 256 * 8)
         i8_quantize_any_kernel<<<grid, 256, 0, s>>>(X, K, ldx, Q, ldq, S);
+    else if (chunks > 256 && R <= 512)
+        i8_quantize_kernel<16, 2><<<grid, 1024, 0, s>>>(X, (int)K, ldx, Q, ldq, S);
     else if (chunks <= 64)
         i8_quantize_kernel<1, 1><<<grid, 64, 0, s>>>(X, (int)K, ldx, Q, ldq, S);
     else if (chunks <= 256)

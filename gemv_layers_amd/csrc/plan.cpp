@@ -388,6 +388,53 @@ Plan make_packed_plan(int64_t M, int64_t N, int64_t K, const DeviceInfo& dev) {
     return decode_groups_plan(kKernPacked, M, N, K, K / 32, pk_decode_tiles_per_group(M), dev);
 }
 
+// The 8-bit product of few rows streams the weight once, and a workgroup of `tn` 16-row tiles also
+// reads its K range of all activation rows, which costs like as many weight bytes: the L1 returns
+// hits in order behind the stream's misses. So one tile up to 4 rows or while one-tile groups are at
+// most two a CU, four tiles beyond (M = 16: 11008 x 4096 weight 12.1 us against 13.9 with one), and
+// above 16 rows one, two or four as the weight outgrows the 2 us that summing K pieces costs (M =
+// 64: 1000 x 2000 5.3 us with one and 6.3 with two; 2048 x 8192 12.1 with two and 13.4 with four;
+// 4096 x 11008 17.9 with four and 20.7 with two). The gated form takes gate and up tiles in pairs, one
+// pair up to 16 rows (M = 16, 11008 x 4096: 21.7 us) and two for a large weight beyond (M = 64: 37.6
+// us against 40.1 with one). K is split as far as the groups leave CUs idle and 32 k-steps remain to
+// each piece (4 x 2048 x 2048 codes: 4.0 us whole, 4.9 in two pieces; 1 x 1000 x 11008: 6.7 in four,
+// 7.6 whole).
+Plan make_i8_decode_plan(int64_t M, int64_t N, int64_t K, const DeviceInfo& dev, bool glu) {
+    Plan p;
+    p.kernel = kKernI8Decode;
+    p.glu = glu;
+    p.mtiles = (int)cdiv(M, 16);
+    const int64_t tiles = cdiv(N, 16), steps = cdiv(K, 64);
+    const int64_t weight = (glu ? 2 : 1) * N * K;
+    int tn;  // 16-row weight tiles per workgroup
+    if (glu)
+        tn = p.mtiles > 1 && weight > (int64_t(20) << 20) ? 4 : 2;
+    else if (p.mtiles == 1)
+        tn = M <= 4 || tiles <= 2 * (int64_t)dev.cus ? 1 : 4;
+    else
+        tn = weight <= (int64_t(8) << 20) ? 1 : (weight <= (int64_t(20) << 20) ? 2 : 4);
+    p.strip = 16 * tn;
+    p.strips = (int)cdiv(tiles, glu ? tn / 2 : tn);
+    p.ks = (int)steps;
+    const int64_t slot_floats = (int64_t)tn * p.mtiles * 256;
+    int64_t s = std::max<int64_t>(1, std::min<int64_t>(dev.cus / p.strips, steps / 32));
+    while (s > 1 && p.strips * s * slot_floats > dev.ws_floats) --s;
+    if (s > 1 && p.strips > dev.ws_counters) s = 1;
+    p.splits = (int)s;
+    p.grid = p.strips * s;
+    p.ws_floats = s > 1 ? p.strips * s * slot_floats : 0;
+    p.counters = s > 1 ? p.strips : 0;
+    // eight waves where four would leave a CU short of loads in flight: a long K over at most two
+    // workgroups a CU (1 x 4096 x 11008: 10.1 us against 10.7), and four tiles of M > 16 (17.9 against 18.6)
+    const bool wide = (tn == 1 && p.grid < 2 * (int64_t)dev.cus && steps >= 128) || (!glu && tn == 4 && p.mtiles > 1);
+    p.threads = wide ? 512 : 256;
+    p.slots = 2 * (int64_t)dev.cus;
+    finish_waves(p);
+    p.reason = "8-bit decode: " + std::to_string(p.strips) + " groups of " + std::to_string(tn) +
+               " weight tiles, K in " + std::to_string(s) + " pieces";
+    return p;
+}
+
 static const char* kernel_name(int k) {
     switch (k) {
         case kKernNone: return "none";
@@ -397,6 +444,7 @@ static const char* kernel_name(int k) {
         case kKernSkinny: return "skinny";
         case kKernMx: return "mx";
         case kKernPacked: return "packed";
+        case kKernI8Decode: return "i8_decode";
         default: return "?";
     }
 }
@@ -413,7 +461,8 @@ std::string plan_json(const Plan& p, int64_t M, int64_t N, int64_t K) {
              (long long)M, (long long)N, (long long)K, kernel_name(p.kernel), p.bm, p.bn, p.bk,
              p.threads, (long long)p.tiles_m, (long long)p.tiles_n, (long long)p.tiles,
              p.kernel == kKernTile ? (p.sched == kSchedSplitK ? "split-k" : "data-parallel")
-                                   : (p.kernel == kKernSkinny || p.kernel == kKernMx || p.kernel == kKernPacked
+                                   : (p.kernel == kKernSkinny || p.kernel == kKernMx || p.kernel == kKernPacked ||
+                                           p.kernel == kKernI8Decode
                                           ? "strips"
                                           : "-"),
              p.splits, p.kt_per_split, p.group_m, p.nxcd, p.mtiles, p.strip, p.strips, p.ks,

@@ -11,7 +11,7 @@ namespace glk {
 
 enum KernelKind : int {
     kKernNone = 0, kKernZero = 1, kKernGeneric = 2, kKernTile = 3, kKernSkinny = 4, kKernMx = 5,
-    kKernPacked = 6
+    kKernPacked = 6, kKernI8Decode = 7
 };
 
 struct Plan {
@@ -77,6 +77,10 @@ Plan make_mx_plan(int64_t M, int64_t N, int64_t K, const DeviceInfo& dev);
 // The decode product on a packed bf16 weight (1 <= M <= 64, N % 16 == 0, K % 32 == 0): the same
 // decomposition over 32-k steps.
 Plan make_packed_plan(int64_t M, int64_t N, int64_t K, const DeviceInfo& dev);
+
+// The 8-bit product of few rows (1 <= M <= 64, K >= 1; N outputs, gated: 2N weight rows): groups of
+// 16-row weight tiles (strip rows) times K pieces (splits), one workgroup of `threads` each.
+Plan make_i8_decode_plan(int64_t M, int64_t N, int64_t K, const DeviceInfo& dev, bool glu);
 
 std::string plan_json(const Plan& p, int64_t M, int64_t N, int64_t K);
 
