@@ -364,86 +364,103 @@ def swiglu_matmul(A, B, out=None, stream=None):
 
 
 # ---- 8-bit products and training: PyTorch marshalling ----------------------------------------
+#
+# A small product takes the GPU a few microseconds, less than careless marshalling takes the host, so
+# each tensor is asked for its properties once and the stream's handle is read without a Stream object.
+
+_t = None
 
 
-def _rows(t, name, dtype, cols=None):
-    """Checks a 2-D device tensor of `dtype` with unit column stride and non-overlapping rows;
-    returns its leading dimension."""
+def _torch():
+    """PyTorch, imported on first use."""
+    global _t
+    if _t is None:
+        import torch
+
+        _t = torch
+    return _t
+
+
+def _stream(stream, device: int):
+    """The given stream's handle, or that of the device's current stream."""
+    if stream is not None:
+        return stream
+    raw = getattr(_t._C, "_cuda_getCurrentRawStream", None)
+    return raw(device) if raw is not None else _t.cuda.current_stream(device).cuda_stream
+
+
+def _rows(t, name, dtype, rows=None, cols=None, device=None):
+    """Checks a 2-D device tensor of `dtype` with unit column stride and rows that do not overlap.
+    Returns (rows, columns, leading dimension, address)."""
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}")
-    if t.dim() != 2 or (cols is not None and t.shape[1] != cols):
-        raise ValueError(f"{name} must have {'two dimensions' if cols is None else f'{cols} columns'}")
+    shape = t.shape
+    if len(shape) != 2 or (cols is not None and shape[1] != cols) or (rows is not None and shape[0] != rows):
+        raise ValueError(f"{name} must be {'M' if rows is None else rows} x {'N' if cols is None else cols}, "
+                         f"not {tuple(shape)}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
-    r, c = t.shape
-    sr, sc = t.stride()
-    if sc != 1 and c > 1 and r > 0:
+    if device is not None and t.get_device() != device:
+        raise ValueError("all tensors must be on one device")
+    r, c = shape
+    ld, unit = t.stride()
+    if unit != 1 and c > 1 and r > 0:
         raise ValueError(f"{name} needs unit column stride")
-    if r <= 1 or sr >= c:
-        return sr if sr > c else c
-    raise ValueError(f"{name} has overlapping rows")
+    if ld < c:
+        if r > 1:
+            raise ValueError(f"{name} has overlapping rows")
+        ld = c
+    return r, c, ld, t.data_ptr()
 
 
-def _scales(t, name, n):
-    import torch
-
-    if t.dtype != torch.float32 or t.dim() != 1 or t.shape[0] != n or not t.is_cuda:
+def _scales(t, name, n, device):
+    if t.dtype != _t.float32 or t.dim() != 1 or t.shape[0] != n or not t.is_cuda:
         raise ValueError(f"{name} must be a device vector of {n} float32 values")
     if n > 1 and t.stride(0) != 1:
         raise ValueError(f"{name} needs unit stride")
+    if t.get_device() != device:
+        raise ValueError("all tensors must be on one device")
     return t.data_ptr()
 
 
-def _same_device(*ts):
-    d = ts[0].device
-    for t in ts:
-        if t is not None and t.device != d:
-            raise ValueError("all tensors must be on one device")
-
-
-def _out(out, shape, device):
-    import torch
-
+def _out(out, M, N, like, device):
+    """(tensor, leading dimension, address) of the M x N output, made when it is not given."""
     if out is None:
-        return torch.empty(shape, dtype=torch.bfloat16, device=device)
-    if tuple(out.shape) != shape:
-        raise ValueError(f"the output must have shape {shape}")
-    return out
+        out = _t.empty((M, N), dtype=_t.bfloat16, device=like.device)
+        return out, N, out.data_ptr()
+    _, _, ld, ptr = _rows(out, "out", _t.bfloat16, M, N, device)
+    return out, ld, ptr
 
 
 def i8_quantize(X, stream=None):
     """8-bit codes and scales of each row of a bf16 matrix: (Q int8 of X's shape, S float32).
     Q's rows are padded to 16 bytes in memory, as the matrix kernels want them. For an nn.Linear
     weight the rows are output channels; for activations they are tokens."""
-    import torch
-
-    ldx = _rows(X, "X", torch.bfloat16)
-    R, K = X.shape
+    torch = _torch()
+    R, K, ldx, x = _rows(X, "X", torch.bfloat16)
     ldq = -(-K // 16) * 16
     Q = torch.empty((R, ldq), dtype=torch.int8, device=X.device)[:, :K]
     S = torch.empty((R,), dtype=torch.float32, device=X.device)
-    gemm_i8_quantize(R, K, X.data_ptr(), ldx, Q.data_ptr(), ldq, S.data_ptr(),
-                     stream if stream is not None else current_stream_handle())
+    gemm_i8_quantize(R, K, x, ldx, Q.data_ptr(), ldq, S.data_ptr(), _stream(stream, X.get_device()))
     return Q, S
 
 
-def _i8_codes(name, Aq, Sa, Wq, Sw, out, stream, glu):
-    import torch
+def _i8_weight(Wq, Sw, K, glu, device):
+    """(N, leading dimension, codes, scales) of an 8-bit weight; gated: 2N rows, gate then up."""
+    rows, _, ldw, w = _rows(Wq, "Wq", _t.int8, None, K, device)
+    if glu and rows % 2:
+        raise ValueError("Wq must have 2N rows, gate then up")
+    return rows // 2 if glu else rows, ldw, w, _scales(Sw, "Sw", rows, device)
 
-    lda, ldw = _rows(Aq, "Aq", torch.int8), _rows(Wq, "Wq", torch.int8, Aq.shape[1])
-    M, K = Aq.shape
-    N = Wq.shape[0]
-    if glu:
-        if N % 2:
-            raise ValueError("Wq must have 2N rows, gate then up")
-        N //= 2
-    sa, sw = _scales(Sa, "Sa", M), _scales(Sw, "Sw", Wq.shape[0])
-    out = _out(out, (M, N), Aq.device)
-    ldc = _rows(out, "out", torch.bfloat16)
-    _same_device(Aq, Sa, Wq, Sw, out)
-    st = getattr(lib(), name)(M, N, K, Aq.data_ptr(), lda, sa, Wq.data_ptr(), ldw, sw, out.data_ptr(), ldc,
-                              stream if stream is not None else current_stream_handle())
-    _check(name, st)
+
+def _i8_codes(name, Aq, Sa, Wq, Sw, out, stream, glu):
+    torch = _torch()
+    M, K, lda, a = _rows(Aq, "Aq", torch.int8)
+    device = Aq.get_device()
+    N, ldw, w, sw = _i8_weight(Wq, Sw, K, glu, device)
+    sa = _scales(Sa, "Sa", M, device)
+    out, ldc, c = _out(out, M, N, Aq, device)
+    _check(name, getattr(lib(), name)(M, N, K, a, lda, sa, w, ldw, sw, c, ldc, _stream(stream, device)))
     return out
 
 
@@ -458,27 +475,17 @@ def i8_swiglu_matmul(Aq, Sa, Wq, Sw, out=None, stream=None):
 
 
 def _i8_dynamic(name, A, Wq, Sw, out, work, stream, glu):
-    import torch
-
-    lda, ldw = _rows(A, "A", torch.bfloat16), _rows(Wq, "Wq", torch.int8, A.shape[1])
-    M, K = A.shape
-    N = Wq.shape[0]
-    if glu:
-        if N % 2:
-            raise ValueError("Wq must have 2N rows, gate then up")
-        N //= 2
-    sw = _scales(Sw, "Sw", Wq.shape[0])
-    out = _out(out, (M, N), A.device)
-    ldc = _rows(out, "out", torch.bfloat16)
-    if work is None:
-        work = torch.empty((max(gemm_i8_work_bytes(M, K), 16),), dtype=torch.uint8, device=A.device)
-    elif work.dtype != torch.uint8 or not work.is_contiguous():
-        raise ValueError("work must be a contiguous uint8 tensor")
-    _same_device(A, Wq, Sw, out, work)
-    st = getattr(lib(), name)(M, N, K, A.data_ptr(), lda, Wq.data_ptr(), ldw, sw, out.data_ptr(), ldc,
-                              work.data_ptr(), work.numel(),
-                              stream if stream is not None else current_stream_handle())
-    _check(name, st)
+    torch = _torch()
+    M, K, lda, a = _rows(A, "A", torch.bfloat16)
+    device = A.get_device()
+    N, ldw, w, sw = _i8_weight(Wq, Sw, K, glu, device)
+    out, ldc, c = _out(out, M, N, A, device)
+    if work is None:  # gemm_i8_work_bytes(M, K)
+        work = torch.empty((M * (-(-K // 16) * 16 + 4),), dtype=torch.uint8, device=A.device)
+    elif work.dtype != torch.uint8 or not work.is_contiguous() or work.get_device() != device:
+        raise ValueError("work must be a contiguous uint8 tensor on the same device")
+    _check(name, getattr(lib(), name)(M, N, K, a, lda, w, ldw, sw, c, ldc, work.data_ptr(), work.numel(),
+                                      _stream(stream, device)))
     return out
 
 
@@ -494,58 +501,53 @@ def i8_swiglu_linear(A, Wq, Sw, out=None, work=None, stream=None):
     return _i8_dynamic("gemm_i8_swiglu_bf16", A, Wq, Sw, out, work, stream, True)
 
 
+def _empty(shape, like):
+    t = _t.empty(shape, dtype=_t.bfloat16, device=like.device)
+    return t, t.data_ptr()
+
+
 def matmul_backward(dC, A, B, need_dA=True, need_dB=True, stream=None):
     """(dA, dB) = (dC @ B.T, A.T @ dC), the gradients of matmul(A, B); None for one not needed."""
-    import torch
-
-    bf16 = torch.bfloat16
-    lda, ldb = _rows(A, "A", bf16), _rows(B, "B", bf16)
-    (M, K), N = A.shape, B.shape[1]
-    lddc = _rows(dC, "dC", bf16, N)
-    if B.shape[0] != K or dC.shape[0] != M:
-        raise ValueError("shapes do not form the gradient of a matrix product")
-    _same_device(dC, A, B)
-    dA = torch.empty((M, K), dtype=bf16, device=A.device) if need_dA else None
-    dB = torch.empty((K, N), dtype=bf16, device=A.device) if need_dB else None
-    gemm_bf16_bwd(M, N, K, dC.data_ptr(), lddc, A.data_ptr(), lda, B.data_ptr(), ldb,
-                  dA.data_ptr() if need_dA else None, K, dB.data_ptr() if need_dB else None, N,
-                  stream if stream is not None else current_stream_handle())
+    bf16 = _torch().bfloat16
+    M, K, lda, a = _rows(A, "A", bf16)
+    device = A.get_device()
+    _, N, ldb, b = _rows(B, "B", bf16, K, None, device)
+    _, _, lddc, d = _rows(dC, "dC", bf16, M, N, device)
+    dA, da = _empty((M, K), A) if need_dA else (None, None)
+    dB, db = _empty((K, N), A) if need_dB else (None, None)
+    gemm_bf16_bwd(M, N, K, d, lddc, a, lda, b, ldb, da, K, db, N, _stream(stream, device))
     return dA, dB
 
 
 def swiglu_forward(A, B, stream=None):
     """(C, GU) of the gated block for training: GU = A @ B (M x 2N, gate then up), C = silu(g) * u."""
-    import torch
-
-    bf16 = torch.bfloat16
-    lda, ldb = _rows(A, "A", bf16), _rows(B, "B", bf16)
-    (M, K), N = A.shape, B.shape[1] // 2
-    if B.shape[0] != K or B.shape[1] % 2:
+    bf16 = _torch().bfloat16
+    M, K, lda, a = _rows(A, "A", bf16)
+    device = A.get_device()
+    _, N, ldb, b = _rows(B, "B", bf16, K, None, device)
+    if N % 2:
         raise ValueError("B must be K x 2N for A of shape M x K")
-    _same_device(A, B)
-    C = torch.empty((M, N), dtype=bf16, device=A.device)
-    GU = torch.empty((M, 2 * N), dtype=bf16, device=A.device)
-    gemm_bf16_swiglu_train(M, N, K, A.data_ptr(), lda, B.data_ptr(), ldb, GU.data_ptr(), 2 * N, C.data_ptr(), N,
-                           stream if stream is not None else current_stream_handle())
+    N //= 2
+    C, c = _empty((M, N), A)
+    GU, gu = _empty((M, 2 * N), A)
+    gemm_bf16_swiglu_train(M, N, K, a, lda, b, ldb, gu, 2 * N, c, N, _stream(stream, device))
     return C, GU
 
 
 def swiglu_backward(dC, GU, A, B, need_dA=True, need_dB=True, inplace=False, stream=None):
     """(dA, dB, dGU): the gradients of swiglu_forward's C. With `inplace`, dGU takes GU's memory."""
-    import torch
-
-    bf16 = torch.bfloat16
-    lda, ldb = _rows(A, "A", bf16), _rows(B, "B", bf16)
-    (M, K), N = A.shape, B.shape[1] // 2
-    lddc, ldgu = _rows(dC, "dC", bf16, N), _rows(GU, "GU", bf16, 2 * N)
-    if B.shape[0] != K or B.shape[1] % 2 or dC.shape[0] != M or GU.shape[0] != M:
-        raise ValueError("shapes do not form the gradient of the gated block")
-    _same_device(dC, GU, A, B)
-    dGU = GU if inplace else torch.empty((M, 2 * N), dtype=bf16, device=A.device)
-    dA = torch.empty((M, K), dtype=bf16, device=A.device) if need_dA else None
-    dB = torch.empty((K, 2 * N), dtype=bf16, device=A.device) if need_dB else None
-    gemm_bf16_swiglu_bwd(M, N, K, dC.data_ptr(), lddc, GU.data_ptr(), ldgu, A.data_ptr(), lda, B.data_ptr(), ldb,
-                         dGU.data_ptr(), ldgu if inplace else 2 * N, dA.data_ptr() if need_dA else None, K,
-                         dB.data_ptr() if need_dB else None, 2 * N,
-                         stream if stream is not None else current_stream_handle())
+    bf16 = _torch().bfloat16
+    M, K, lda, a = _rows(A, "A", bf16)
+    device = A.get_device()
+    _, N, ldb, b = _rows(B, "B", bf16, K, None, device)
+    if N % 2:
+        raise ValueError("B must be K x 2N for A of shape M x K")
+    N //= 2
+    _, _, lddc, d = _rows(dC, "dC", bf16, M, N, device)
+    _, _, ldgu, gu = _rows(GU, "GU", bf16, M, 2 * N, device)
+    dGU, dgu, lddgu = (GU, gu, ldgu) if inplace else (*_empty((M, 2 * N), A), 2 * N)
+    dA, da = _empty((M, K), A) if need_dA else (None, None)
+    dB, db = _empty((K, 2 * N), A) if need_dB else (None, None)
+    gemm_bf16_swiglu_bwd(M, N, K, d, lddc, gu, ldgu, a, lda, b, ldb, dgu, lddgu, da, K, db, 2 * N,
+                         _stream(stream, device))
     return dA, dB, dGU
