@@ -426,7 +426,7 @@ def _scales(t, name, n, device):
 def _out(out, M, N, like, device):
     """(tensor, leading dimension, address) of the M x N output, made when it is not given."""
     if out is None:
-        out = _t.empty((M, N), dtype=_t.bfloat16, device=like.device)
+        out = like.new_empty((M, N), dtype=_t.bfloat16)
         return out, N, out.data_ptr()
     _, _, ld, ptr = _rows(out, "out", _t.bfloat16, M, N, device)
     return out, ld, ptr
@@ -481,7 +481,7 @@ def _i8_dynamic(name, A, Wq, Sw, out, work, stream, glu):
     N, ldw, w, sw = _i8_weight(Wq, Sw, K, glu, device)
     out, ldc, c = _out(out, M, N, A, device)
     if work is None:  # gemm_i8_work_bytes(M, K)
-        work = torch.empty((M * (-(-K // 16) * 16 + 4),), dtype=torch.uint8, device=A.device)
+        work = A.new_empty((M * (-(-K // 16) * 16 + 4),), dtype=torch.uint8)
     elif work.dtype != torch.uint8 or not work.is_contiguous() or work.get_device() != device:
         raise ValueError("work must be a contiguous uint8 tensor on the same device")
     _check(name, getattr(lib(), name)(M, N, K, a, lda, w, ldw, sw, c, ldc, work.data_ptr(), work.numel(),
@@ -502,7 +502,7 @@ def i8_swiglu_linear(A, Wq, Sw, out=None, work=None, stream=None):
 
 
 def _empty(shape, like):
-    t = _t.empty(shape, dtype=_t.bfloat16, device=like.device)
+    t = like.new_empty(shape)
     return t, t.data_ptr()
 
 

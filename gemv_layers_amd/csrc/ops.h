@@ -48,8 +48,10 @@ struct OpTileArgs {
     float* ws;
     uint32_t* counters;
 };
-// big: 256 x 256 tiles, else 128 x 128 (the gated forms' tiles make half as many output columns)
-hipError_t launch_op_tile(int mode, bool glu, bool big, const OpTileArgs& a, int grid, hipStream_t s);
+// tile: 256, 128 or 64 rows and (weight) columns; the gated forms make half as many output columns
+hipError_t launch_op_tile(int mode, bool glu, int tile, const OpTileArgs& a, int grid, hipStream_t s);
+// kOpAbt on `a` and kOpAtb on `b` in one launch, tiles of 128 or 64
+hipError_t launch_op_pair(int tile, const OpTileArgs& a, const OpTileArgs& b, int grid, hipStream_t s);
 hipError_t configure_op_kernels();
 
 // ---- 8-bit product of few tokens -------------------------------------------------------------------

@@ -119,42 +119,42 @@ __device__ __forceinline__ void swiglu_grad1(float d, float g, float u, float& d
     dg = d * u * (sig * (1.0f + g * (1.0f - sig)));
 }
 
-// dGU may be GU itself: every element is read by the thread that writes it, before it does
+// dGU may be GU itself: every element is read by the thread that writes it, before it does. VEC: eight
+// elements a thread. I: the type that counts them (the division by a row's length costs a 64-bit index
+// more than the rest of a small call).
+template <bool VEC, class I>
 __global__ void __launch_bounds__(256) swiglu_grad_kernel(const uint16_t* __restrict__ dC, int64_t lddc,
                                                           const uint16_t* GU, int64_t ldgu, uint16_t* dGU,
-                                                          int64_t lddgu, int64_t M, int64_t N) {
-    const int64_t per_row = N / 8, total = M * per_row;
-    const int64_t step = (int64_t)gridDim.x * 256;
-    for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < total; e += step) {
-        const int64_t m = e / per_row, n = 8 * (e - m * per_row);
-        const u32x4 d = *reinterpret_cast<const u32x4*>(dC + m * lddc + n);
-        const u32x4 g = *reinterpret_cast<const u32x4*>(GU + m * ldgu + n);
-        const u32x4 u = *reinterpret_cast<const u32x4*>(GU + m * ldgu + N + n);
-        u32x4 og, ou;
+                                                          int64_t lddgu, I total, I per_row, int64_t N) {
+    const I step = (I)gridDim.x * 256;
+    for (I e = (I)blockIdx.x * 256 + threadIdx.x; e < total; e += step) {
+        const I m = e / per_row;
+        const int64_t n = (VEC ? 8 : 1) * (int64_t)(e - m * per_row);
+        const uint16_t* pd = dC + m * lddc + n;
+        const uint16_t* pg = GU + m * ldgu + n;
+        uint16_t* po = dGU + m * lddgu + n;
+        if constexpr (VEC) {
+            const u32x4 d = *reinterpret_cast<const u32x4*>(pd);
+            const u32x4 g = *reinterpret_cast<const u32x4*>(pg);
+            const u32x4 u = *reinterpret_cast<const u32x4*>(pg + N);
+            u32x4 og, ou;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            float g0, g1, u0, u1;
-            swiglu_grad1(bf16_lo(d[j]), bf16_lo(g[j]), bf16_lo(u[j]), g0, u0);
-            swiglu_grad1(bf16_hi(d[j]), bf16_hi(g[j]), bf16_hi(u[j]), g1, u1);
-            og[j] = pack_bf16x2(g0, g1);
-            ou[j] = pack_bf16x2(u0, u1);
+            for (int j = 0; j < 4; ++j) {
+                float g0, g1, u0, u1;
+                swiglu_grad1(bf16_lo(d[j]), bf16_lo(g[j]), bf16_lo(u[j]), g0, u0);
+                swiglu_grad1(bf16_hi(d[j]), bf16_hi(g[j]), bf16_hi(u[j]), g1, u1);
+                og[j] = pack_bf16x2(g0, g1);
+                ou[j] = pack_bf16x2(u0, u1);
+            }
+            *reinterpret_cast<u32x4*>(po) = og;
+            *reinterpret_cast<u32x4*>(po + N) = ou;
+        } else {
+            auto wide = [](uint16_t h) { return __builtin_bit_cast(float, (uint32_t)h << 16); };
+            float dg, du;
+            swiglu_grad1(wide(*pd), wide(*pg), wide(pg[N]), dg, du);
+            *po = __builtin_bit_cast(uint16_t, (__bf16)dg);
+            po[N] = __builtin_bit_cast(uint16_t, (__bf16)du);
         }
-        *reinterpret_cast<u32x4*>(dGU + m * lddgu + n) = og;
-        *reinterpret_cast<u32x4*>(dGU + m * lddgu + N + n) = ou;
-    }
-}
-
-__global__ void __launch_bounds__(256) swiglu_grad_any_kernel(const uint16_t* __restrict__ dC, int64_t lddc,
-                                                              const uint16_t* GU, int64_t ldgu, uint16_t* dGU,
-                                                              int64_t lddgu, int64_t M, int64_t N) {
-    const int64_t total = M * N, step = (int64_t)gridDim.x * 256;
-    auto wide = [](uint16_t h) { return __builtin_bit_cast(float, (uint32_t)h << 16); };
-    for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < total; e += step) {
-        const int64_t m = e / N, n = e - m * N;
-        float dg, du;
-        swiglu_grad1(wide(dC[m * lddc + n]), wide(GU[m * ldgu + n]), wide(GU[m * ldgu + N + n]), dg, du);
-        dGU[m * lddgu + n] = __builtin_bit_cast(uint16_t, (__bf16)dg);
-        dGU[m * lddgu + N + n] = __builtin_bit_cast(uint16_t, (__bf16)du);
     }
 }
 
@@ -162,12 +162,22 @@ hipError_t launch_swiglu_grad(const uint16_t* dC, int64_t lddc, const uint16_t* 
                               int64_t lddgu, int64_t M, int64_t N, hipStream_t s) {
     const uintptr_t at = reinterpret_cast<uintptr_t>(dC) | reinterpret_cast<uintptr_t>(GU) | reinterpret_cast<uintptr_t>(dGU);
     const bool vec = (at & 15) == 0 && ((N | lddc | ldgu | lddgu) & 7) == 0;
-    int64_t blocks = ((vec ? M * (N / 8) : M * N) + 255) / 256;
-    if (blocks > (1 << 20)) blocks = 1 << 20;
-    if (vec)
-        swiglu_grad_kernel<<<(unsigned)blocks, 256, 0, s>>>(dC, lddc, GU, ldgu, dGU, lddgu, M, N);
+    const int64_t per_row = vec ? N / 8 : N, total = M * per_row;
+    const unsigned blocks = (unsigned)(total < (int64_t(1) << 28) ? (total + 255) / 256 : 1 << 20);
+    auto run = [&](auto kernel, auto zero) {
+        using I = decltype(zero);
+        kernel<<<blocks, 256, 0, s>>>(dC, lddc, GU, ldgu, dGU, lddgu, (I)total, (I)per_row, N);
+    };
+    // (32-bit counting: the last index plus the grid's stride stays below 2^32)
+    const bool small = total < (int64_t(1) << 31);
+    if (vec && small)
+        run(swiglu_grad_kernel<true, uint32_t>, uint32_t());
+    else if (vec)
+        run(swiglu_grad_kernel<true, int64_t>, int64_t());
+    else if (small)
+        run(swiglu_grad_kernel<false, uint32_t>, uint32_t());
     else
-        swiglu_grad_any_kernel<<<(unsigned)blocks, 256, 0, s>>>(dC, lddc, GU, ldgu, dGU, lddgu, M, N);
+        run(swiglu_grad_kernel<false, int64_t>, int64_t());
     return hipGetLastError();
 }
 

@@ -59,8 +59,12 @@ struct OpTile {
     static_assert(LDS_BYTES <= 160 * 1024, "LDS");
 };
 
-// strided operands: physical 32-byte column group of logical group u in row k
-__device__ __forceinline__ int op_group(int u, int k) { return u ^ ((k & 3) | ((k >> 1) & 4)); }
+// strided operands of R columns: physical 32-byte column group of logical group u in row k (R = 64
+// has four groups a row and two rows in the 256 bytes of all banks)
+template <int R>
+__device__ __forceinline__ int op_group(int u, int k) {
+    return u ^ (R >= 128 ? ((k & 3) | ((k >> 1) & 4)) : (k & 3));
+}
 
 __device__ __forceinline__ f32x4 op_mfma(const u32x4& x, const u32x4& y, const f32x4& c) {
     return mfma16(__builtin_bit_cast(bf16x8, x), __builtin_bit_cast(bf16x8, y), c);
@@ -79,7 +83,7 @@ template <int R, int PW, bool CONTIG, int ES, bool GLU, int WT>
 struct OpCopy {
     static constexpr int HALVES = CONTIG ? 2 : 1;
     uint32_t off[HALVES][PW];  // byte offset of the lane's 16 bytes, or kBufInvalid outside the matrix
-    int chunk[2];              // contiguous: byte of the lane's chunk in the 128-byte row, by parity of i
+    int chunk[PW];             // contiguous: byte of the lane's chunk in the 128-byte row
     const char* base[GLU && CONTIG ? HALVES * PW : 1];
     int64_t ld_bytes;
     int sum;                   // bytes (contiguous) or rows (strided) of the summed index
@@ -88,12 +92,12 @@ struct OpCopy {
     // share of each wave is WT / 2 gate and the same WT / 2 up
     __device__ __forceinline__ void init(const void* p, int64_t ld, int64_t r0, int64_t rows, int64_t k0, int k_count,
                                          int wave, int lane) {
-        static_assert(!CONTIG || PW == 2, "chunk by parity of i");
         ld_bytes = ld * ES;
         sum = CONTIG ? k_count * ES : k_count;
         const char* at = static_cast<const char*>(p) + k0 * (CONTIG ? ES : ld_bytes);
-        chunk[0] = 16 * ((lane & 7) ^ (lane >> 4));  // row 8 idx + lane / 8: (row >> 1) & 7, idx even
-        chunk[1] = chunk[0] ^ 64;                    // idx odd
+#pragma unroll
+        for (int i = 0; i < PW; ++i)  // row 8 idx + lane / 8, of which (row >> 1) & 7 is ...
+            chunk[i] = 16 * ((lane & 7) ^ (4 * ((wave * PW + i) & 1) + (lane >> 4)));
 #pragma unroll
         for (int h = 0; h < HALVES; ++h)
 #pragma unroll
@@ -106,14 +110,14 @@ struct OpCopy {
                         const int64_t src = r0 + out + (q % WT < WT / 2 ? 0 : rows);
                         base[h * PW + i] = at + src * ld_bytes;
                         off[h][i] = sel_off(r0 + out + (lane >> 3) < rows,
-                                            (uint32_t)((lane >> 3) * (int)ld_bytes + chunk[i & 1]));
+                                            (uint32_t)((lane >> 3) * (int)ld_bytes + chunk[i]));
                     } else {
-                        off[h][i] = sel_off(r0 + r < rows, (uint32_t)(r * (int)ld_bytes + chunk[i & 1]));
+                        off[h][i] = sel_off(r0 + r < rows, (uint32_t)(r * (int)ld_bytes + chunk[i]));
                     }
                 } else {
                     constexpr int RPI = 512 / R, CH = R / 8;  // k rows per instruction, chunks per row
                     const int k = idx * RPI + lane / CH, pc = lane % CH;
-                    const int col = 16 * op_group(pc >> 1, k) + 8 * (pc & 1);
+                    const int col = 16 * op_group<R>(pc >> 1, k) + 8 * (pc & 1);
                     int src = col, out = col;
                     if constexpr (GLU) {
                         const int q = col % WT;
@@ -134,7 +138,7 @@ struct OpCopy {
 #pragma unroll
             for (int i = 0; i < PW; ++i) {
                 const i32x4 r = rsrc_words(base[GLU ? H * PW + i : 0] + from, kBufRecords);
-                dma16(r, lds + (wave * PW + i) * 1024, sel_off(chunk[i & 1] < left, off[H][i]));
+                dma16(r, lds + (wave * PW + i) * 1024, sel_off(chunk[i] < left, off[H][i]));
             }
         } else {
             const int at = u * 32;
@@ -164,7 +168,7 @@ __device__ __forceinline__ void op_read(const char* ring, int slot, int w0, int 
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int k = 8 * G + 4 * h + (j >> 2);
-                const char* at = stage + k * (2 * R) + 32 * op_group((w0 >> 4) + i, k) + 8 * (j & 3);
+                const char* at = stage + k * (2 * R) + 32 * op_group<R>((w0 >> 4) + i, k) + 8 * (j & 3);
                 v[h] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)at);
             }
             const i16x8 x = {v[0][0], v[0][1], v[0][2], v[0][3], v[1][0], v[1][1], v[1][2], v[1][3]};
@@ -209,9 +213,9 @@ struct OpPlace {
 };
 // which tile, in grouped order over the XCDs' contiguous shares
 template <int BM, int BNO>
-__device__ __forceinline__ OpPlace op_place(const OpTileArgs& p) {
+__device__ __forceinline__ OpPlace op_place(const OpTileArgs& p, int block) {
     const int pieces = p.splits, ntiles = p.tiles_m * p.tiles_n;
-    const int unit = xcd_remap((int)blockIdx.x, ntiles * pieces, p.nxcd);
+    const int unit = xcd_remap(block, ntiles * pieces, p.nxcd);
     const int tile = unit / pieces;
     const int per_group = p.group_m * p.tiles_n;
     const int g = tile / per_group, first = g * p.group_m;
@@ -227,27 +231,30 @@ __device__ __forceinline__ OpPlace op_place(const OpTileArgs& p) {
 // Each wave rounds its block into an LDS area of its own (rows of RB bytes, 16-byte chunk c of row r
 // at c ^ (r & (RB / 16 - 1))) and writes it out in whole row segments.
 
-// writes the wave's staged WTM x W block: `vec` 16-byte stores, else one element at a time
+// Writes the wave's staged WTM x W block: `vec` 16-byte stores, else (rows of C without 16-byte
+// alignment) 2-byte stores whose lanes are neighbours in a row.
 template <int WTM, int W>
 __device__ __forceinline__ void op_store_rows(const char* ob, uint16_t* C, int64_t ldc, int m0, int M, int n0, int N,
                                               int lane, bool vec) {
     constexpr int RB = W * 2, CPR = RB / 16, ROWS = 64 / CPR;
-    const int lr = lane / CPR, lc = lane % CPR, n = n0 + lc * 8;
-    const __amdgpu_buffer_rsrc_t rc = make_rsrc(C + (size_t)m0 * ldc);
+    if (vec) {
+        const int lr = lane / CPR, lc = lane % CPR, n = n0 + lc * 8;
+        const __amdgpu_buffer_rsrc_t rc = make_rsrc(C + (size_t)m0 * ldc);
 #pragma unroll
-    for (int s = 0; s < WTM / ROWS; ++s) {
-        const int r = s * ROWS + lr;
-        const u32x4 v = *reinterpret_cast<const u32x4*>(ob + r * RB + (lc ^ (r & (CPR - 1))) * 16);
-        const bool ok = m0 + r < M && n < N;
-        if (vec) {
+        for (int s = 0; s < WTM / ROWS; ++s) {
+            const int r = s * ROWS + lr;
+            const u32x4 v = *reinterpret_cast<const u32x4*>(ob + r * RB + (lc ^ (r & (CPR - 1))) * 16);
             // non-temporal: written once, and far larger than the L2s when it is large
-            __builtin_amdgcn_raw_buffer_store_b128(v, rc, ok ? (uint32_t)(r * (int)ldc + n) * 2u : kBufInvalid, 0,
-                                                   kAuxNonTemporal);
-        } else if (ok) {
-            uint16_t* c = C + (size_t)(m0 + r) * ldc + n;
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (n + j < N) c[j] = (uint16_t)(v[j >> 1] >> (16 * (j & 1)));
+            __builtin_amdgcn_raw_buffer_store_b128(
+                v, rc, m0 + r < M && n < N ? (uint32_t)(r * (int)ldc + n) * 2u : kBufInvalid, 0, kAuxNonTemporal);
+        }
+    } else {
+        constexpr int PER = 64 / W;  // rows per instruction
+        const int c = lane % W;
+        for (int s = 0; s < WTM / PER; ++s) {
+            const int r = s * PER + lane / W;
+            const uint16_t v = *reinterpret_cast<const uint16_t*>(ob + r * RB + ((c >> 3) ^ (r & (CPR - 1))) * 16 + 2 * (c & 7));
+            if (m0 + r < M && n0 + c < N) C[(size_t)(m0 + r) * ldc + n0 + c] = v;
         }
     }
 }
@@ -346,7 +353,7 @@ op_pp_kernel(OpTileArgs p) {
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int grp = wave >> 2, wm = grp, wn = wave & 3;
-    const OpPlace at = op_place<256, GLU ? 128 : 256>(p);
+    const OpPlace at = op_place<256, GLU ? 128 : 256>(p, (int)blockIdx.x);
     const int nsteps = (p.K + T::KE - 1) / T::KE;
 
     OpCopy<256, T::A_PW, T::A_CONTIG, T::ES, false, T::WTM> ca;
@@ -426,24 +433,22 @@ op_pp_kernel(OpTileArgs p) {
 // step i takes step i + 5, and a contiguous one's slot of unit i - 1 (steps i - 1 and i for odd i, i - 2
 // and i - 1 for even i) takes unit i + 4. Its barrier also needs step i + 1's copies landed, which is
 // what op_wait says of the step that iteration i - 1 would be in the other schedule's count.
-template <int MODE, bool GLU>
-__global__ void __attribute__((amdgpu_flat_work_group_size(256, 256), amdgpu_waves_per_eu(2, 2)))
-op_small_kernel(OpTileArgs p) {
-    using T = OpTile<128, 128, 2, 2, MODE>;
+template <int BT, int MODE, bool GLU>
+__device__ __forceinline__ void op_small(const OpTileArgs& p, int block, char* lds) {
+    using T = OpTile<BT, BT, 2, 2, MODE>;
     constexpr int TM = T::TM, TN = T::TN;
     constexpr int A_AHEAD = T::A_CONTIG ? 4 : 5, B_AHEAD = T::B_CONTIG ? 4 : 5;
-    extern __shared__ __attribute__((aligned(1024))) char lds[];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave >> 1, wn = wave & 1;
-    const OpPlace at = op_place<128, GLU ? 64 : 128>(p);
+    const OpPlace at = op_place<BT, GLU ? BT / 2 : BT>(p, block);
     const int total = (p.K + T::KE - 1) / T::KE;
     const int first = at.piece * p.kt_per_split;
     const int nsteps = max(min(total - first, p.kt_per_split), 0);
     const int count = max(min(p.K - first * T::KE, nsteps * T::KE), 0);  // of the summed index
 
-    OpCopy<128, T::A_PW, T::A_CONTIG, T::ES, false, T::WTM> ca;
-    OpCopy<128, T::B_PW, T::B_CONTIG, T::ES, GLU, T::WTN> cb;
+    OpCopy<BT, T::A_PW, T::A_CONTIG, T::ES, false, T::WTM> ca;
+    OpCopy<BT, T::B_PW, T::B_CONTIG, T::ES, GLU, T::WTN> cb;
     ca.init(p.A, p.lda, at.m0, p.M, (int64_t)first * T::KE, count, wave, lane);
     cb.init(p.B, p.ldb, at.n0, p.N, (int64_t)first * T::KE, count, wave, lane);
     const uint32_t ring = lds_addr(lds);
@@ -461,8 +466,8 @@ op_small_kernel(OpTileArgs p) {
     const int tail = (T::I8 && (count & 15)) ? nsteps - 1 : -1;
     auto read = [&](int s, auto par, int slot, u32x4 (&fa)[TM], u32x4 (&fb)[TN]) {
         constexpr int P = decltype(par)::value;
-        op_read<128, TM, T::A_CONTIG, P>(lds, slot, wm * T::WTM, lane, fa);
-        op_read<128, TN, T::B_CONTIG, P>(lds + T::B_RING, slot, wn * T::WTN, lane, fb);
+        op_read<BT, TM, T::A_CONTIG, P>(lds, slot, wm * T::WTM, lane, fa);
+        op_read<BT, TN, T::B_CONTIG, P>(lds + T::B_RING, slot, wn * T::WTN, lane, fb);
         if constexpr (T::I8) {
             if (s == tail) op_clear_tail(count - s * T::KE, lane, fa);
         }
@@ -517,8 +522,8 @@ op_small_kernel(OpTileArgs p) {
 
     if (p.splits > 1) {
         volatile uint32_t& last_flag = *reinterpret_cast<volatile uint32_t*>(lds);
-        constexpr uint32_t kSlot = 128 * 128 * 4;
-        const __amdgpu_buffer_rsrc_t ws = make_rsrc(p.ws + (size_t)at.tile * p.splits * (128 * 128));
+        constexpr uint32_t kSlot = BT * BT * 4;
+        const __amdgpu_buffer_rsrc_t ws = make_rsrc(p.ws + (size_t)at.tile * p.splits * (BT * BT));
         auto slot_off = [&](int pc, int ni, int mi) {
             return (uint32_t)pc * kSlot + (uint32_t)((((wave * TN + ni) * TM + mi) * 64 + lane) * 16);
         };
@@ -566,34 +571,67 @@ op_small_kernel(OpTileArgs p) {
     op_epilogue<T, MODE, GLU>(p, lds, at, wave, wm, wn, lane, acc);
 }
 
+template <int BT, int MODE, bool GLU>
+__global__ void __attribute__((amdgpu_flat_work_group_size(256, 256), amdgpu_waves_per_eu(2, BT == 64 ? 4 : 2)))
+op_small_kernel(OpTileArgs p) {
+    extern __shared__ __attribute__((aligned(1024))) char lds[];
+    op_small<BT, MODE, GLU>(p, (int)blockIdx.x, lds);
+}
+
+// Both gradients of a product in one launch: dA = dC B^T first, dB = A^T dC after. They share dC and
+// neither fills the card when it is small.
+template <int BT>
+__global__ void __attribute__((amdgpu_flat_work_group_size(256, 256), amdgpu_waves_per_eu(2, BT == 64 ? 4 : 2)))
+op_pair_kernel(OpTileArgs pa, OpTileArgs pb) {
+    extern __shared__ __attribute__((aligned(1024))) char lds[];
+    const int first = pa.tiles_m * pa.tiles_n * pa.splits;
+    if ((int)blockIdx.x < first)
+        op_small<BT, kOpAbt, false>(pa, (int)blockIdx.x, lds);
+    else
+        op_small<BT, kOpAtb, false>(pb, (int)blockIdx.x - first, lds);
+}
+
 template <int MODE, bool GLU>
-static hipError_t launch_mode(bool big, const OpTileArgs& a, int grid, hipStream_t s) {
-    if (big) {
+static hipError_t launch_mode(int tile, const OpTileArgs& a, int grid, hipStream_t s) {
+    if (tile == 256) {
         if (a.splits != 1) return hipErrorInvalidValue;
         op_pp_kernel<MODE, GLU><<<grid, 512, OpTile<256, 256, 2, 4, MODE>::LDS_BYTES, s>>>(a);
+    } else if (tile == 128) {
+        op_small_kernel<128, MODE, GLU><<<grid, 256, OpTile<128, 128, 2, 2, MODE>::LDS_BYTES, s>>>(a);
     } else {
-        op_small_kernel<MODE, GLU><<<grid, 256, OpTile<128, 128, 2, 2, MODE>::LDS_BYTES, s>>>(a);
+        op_small_kernel<64, MODE, GLU><<<grid, 256, OpTile<64, 64, 2, 2, MODE>::LDS_BYTES, s>>>(a);
     }
     return hipGetLastError();
 }
 
-hipError_t launch_op_tile(int mode, bool glu, bool big, const OpTileArgs& a, int grid, hipStream_t s) {
+hipError_t launch_op_tile(int mode, bool glu, int tile, const OpTileArgs& a, int grid, hipStream_t s) {
     switch (mode) {
-        case kOpI8: return glu ? launch_mode<kOpI8, true>(big, a, grid, s) : launch_mode<kOpI8, false>(big, a, grid, s);
-        case kOpAbt: return launch_mode<kOpAbt, false>(big, a, grid, s);
-        case kOpAtb: return launch_mode<kOpAtb, false>(big, a, grid, s);
-        case kOpTrain: return launch_mode<kOpTrain, true>(big, a, grid, s);
+        case kOpI8: return glu ? launch_mode<kOpI8, true>(tile, a, grid, s) : launch_mode<kOpI8, false>(tile, a, grid, s);
+        case kOpAbt: return launch_mode<kOpAbt, false>(tile, a, grid, s);
+        case kOpAtb: return launch_mode<kOpAtb, false>(tile, a, grid, s);
+        case kOpTrain: return launch_mode<kOpTrain, true>(tile, a, grid, s);
         default: return hipErrorInvalidValue;
     }
 }
 
+hipError_t launch_op_pair(int tile, const OpTileArgs& a, const OpTileArgs& b, int grid, hipStream_t s) {
+    if (tile == 128)
+        op_pair_kernel<128><<<grid, 256, OpTile<128, 128, 2, 2, kOpAbt>::LDS_BYTES, s>>>(a, b);
+    else
+        op_pair_kernel<64><<<grid, 256, OpTile<64, 64, 2, 2, kOpAbt>::LDS_BYTES, s>>>(a, b);
+    return hipGetLastError();
+}
+
+static hipError_t set_lds(const void* kernel, int bytes) {
+    return hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
+// (the 64 x 64 kernels ask for 40 KB, which needs no setting)
 template <int MODE, bool GLU>
 static hipError_t configure_mode() {
-    hipError_t e = hipFuncSetAttribute((const void*)op_pp_kernel<MODE, GLU>, hipFuncAttributeMaxDynamicSharedMemorySize,
-                                       OpTile<256, 256, 2, 4, MODE>::LDS_BYTES);
+    hipError_t e = set_lds((const void*)op_pp_kernel<MODE, GLU>, OpTile<256, 256, 2, 4, MODE>::LDS_BYTES);
     if (e == hipSuccess)
-        e = hipFuncSetAttribute((const void*)op_small_kernel<MODE, GLU>, hipFuncAttributeMaxDynamicSharedMemorySize,
-                                OpTile<128, 128, 2, 2, MODE>::LDS_BYTES);
+        e = set_lds((const void*)op_small_kernel<128, MODE, GLU>, OpTile<128, 128, 2, 2, MODE>::LDS_BYTES);
     return e;
 }
 
@@ -603,6 +641,7 @@ hipError_t configure_op_kernels() {
     if (e == hipSuccess) e = configure_mode<kOpAbt, false>();
     if (e == hipSuccess) e = configure_mode<kOpAtb, false>();
     if (e == hipSuccess) e = configure_mode<kOpTrain, true>();
+    if (e == hipSuccess) e = set_lds((const void*)op_pair_kernel<128>, OpTile<128, 128, 2, 2, kOpAbt>::LDS_BYTES);
     return e;
 }
 

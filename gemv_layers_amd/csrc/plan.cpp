@@ -388,6 +388,50 @@ Plan make_packed_plan(int64_t M, int64_t N, int64_t K, const DeviceInfo& dev) {
     return decode_groups_plan(kKernPacked, M, N, K, K / 32, pk_decode_tiles_per_group(M), dev);
 }
 
+// Small outputs leave 128 x 128 tiles on a fraction of the CUs, each copying at the 40-50 bytes a ns
+// that one CU takes, and splitting K buys CUs at about 3 us of fixup. 64 x 64 tiles spread the same
+// copies over four times as many CUs without it (us, 64 against the best of 128; C = A B^T unless
+// noted: 512^3 4.8 against 6.9, 1000^3 8.0 against 11.2, codes 509 x 2501 x 1003 8.2 against 11.7,
+// gated forward 300 x 520 x 328 6.0 against 9.0), but copy twice the bytes, which decides once all CUs
+// are busy: 2048 x 2048 x 512 10.0 against 8.3, codes 777 x 4096 x 4096 28.3 against 23.1, 2000 x 512 x
+// 8192 30.0 against 25.9. So 64 x 64 tiles up to one and a half a CU and 32768 k-steps in all (128
+// x 4096 x 4096, 16384 steps: 13.2 against 16.1; codes 128 x 11008 x 4096, 22016 steps: 15.9 against
+// 17.2), and for a quarter as many tiles as CUs whatever K is. A piece of K keeps 28 k-steps or
+// more (509 x 512 x 2752, 86 steps: 9.3 in three pieces, 13.2 before; 512^3, 16 steps: 4.8 whole, 6.0
+// in two).
+Plan make_op_plan(int64_t M, int64_t N, int64_t K, const DeviceInfo& dev, bool glu) {
+    const int64_t tm = cdiv(M, 64), tn = cdiv(glu ? 2 * N : N, 64), kt = cdiv(K, 32);
+    const int64_t most = dev.cus + dev.cus / 2;
+    if (tm > most || tn > most || tm * tn > most || (tm * tn * kt > 32768 && tm * tn > dev.cus / 4))
+        return make_plan(M, N, K, dev, true, 2, glu);
+    Plan p;
+    p.kernel = kKernTile;
+    p.glu = glu;
+    p.tile_cfg = kTileConfigCount;  // none of make_plan's
+    p.bm = p.bn = 64;
+    p.bk = 32;
+    p.threads = 256;
+    p.tiles_m = tm;
+    p.tiles_n = tn;
+    p.tiles = tm * tn;
+    p.nxcd = dev.nxcd;
+    p.group_m = (int)std::min<int64_t>(4, tm);
+    p.slots = 4 * (int64_t)dev.cus;
+    int64_t s = std::max<int64_t>(1, std::min<int64_t>({kt / 28, 16, 3 * (int64_t)dev.cus / p.tiles}));
+    while (s > 1 && p.tiles * s * 4096 > dev.ws_floats / 2) --s;  // (two products may share a launch)
+    p.kt_per_split = (int)cdiv(kt, s);
+    p.splits = (int)cdiv(kt, p.kt_per_split);
+    p.sched = p.splits > 1 ? kSchedSplitK : kSchedDataParallel;
+    p.grid = p.tiles * p.splits;
+    if (p.splits > 1) {
+        p.ws_floats = p.grid * 4096;
+        p.counters = p.tiles;
+    }
+    finish_waves(p);
+    p.reason = "64x64 tiles";
+    return p;
+}
+
 // The 8-bit product of few rows streams the weight once, and a workgroup of `tn` 16-row tiles also
 // reads its K range of all activation rows, which costs like as many weight bytes: the L1 returns
 // hits in order behind the stream's misses. So one tile up to 4 rows or while one-tile groups are at
@@ -398,7 +442,7 @@ Plan make_packed_plan(int64_t M, int64_t N, int64_t K, const DeviceInfo& dev) {
 // pair up to 16 rows (M = 16, 11008 x 4096: 21.7 us) and two for a large weight beyond (M = 64: 37.6
 // us against 40.1 with one). K is split as far as the groups leave CUs idle and 32 k-steps remain to
 // each piece (4 x 2048 x 2048 codes: 4.0 us whole, 4.9 in two pieces; 1 x 1000 x 11008: 6.7 in four,
-// 7.6 whole).
+// 7.0 in three).
 Plan make_i8_decode_plan(int64_t M, int64_t N, int64_t K, const DeviceInfo& dev, bool glu) {
     Plan p;
     p.kernel = kKernI8Decode;
