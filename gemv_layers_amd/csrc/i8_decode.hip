@@ -13,6 +13,7 @@
 
 #include "common.h"
 #include "ops.h"
+#include "ops_math.h"
 
 namespace glk {
 
@@ -129,7 +130,7 @@ __global__ void __launch_bounds__(64 * NW) i8_decode_kernel(I8DecodeArgs p) {
         for (int r = 0; r < 4; ++r) {
             const int c = min(n + r, p.N - 1);
             y[r] = (float)v[0][r] * sa * p.sb[c];
-            if constexpr (GLU) y[r] = swiglu1(y[r], (float)v[H - 1][r] * sa * p.sb[(int64_t)p.N + c]);
+            if constexpr (GLU) y[r] = op_swiglu(y[r], (float)v[H - 1][r] * sa * p.sb[(int64_t)p.N + c]);
         }
         const u32x2 o = {pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3])};
         uint16_t* c = p.C + (int64_t)m * p.ldc + n;

@@ -63,7 +63,7 @@ glk::OpTileArgs tile_args(int mode, const OpArgs& a, const glk::Plan& p, int64_t
     t.ldb = (int)a.ldb;
     t.ldc = (int)a.ldc;
     t.ldgu = (int)a.ldgu;
-    t.sb_up = t.gu_up = (int)a.N;
+    t.up = (int)a.N;
     t.vec = !misaligned(t.C, 16) && a.ldc % 8 == 0 && N % 8 == 0;
     t.tiles_m = (int)p.tiles_m;
     t.tiles_n = (int)p.tiles_n;

@@ -41,7 +41,7 @@ struct OpTileArgs {
     const float* sb;
     int M, N, K;
     int lda, ldb, ldc, ldgu;
-    int sb_up, gu_up;    // where the up half's scales and GU's up columns start
+    int up;              // gated: where the up half starts in the weight, its scales and GU
     int vec;             // C takes 16-byte stores
     int tiles_m, tiles_n, group_m, nxcd;
     int splits, kt_per_split;  // pieces of K per tile, 64-byte k-steps in each (128 x 128 tiles)

@@ -7,6 +7,7 @@
 
 #include "common.h"
 #include "ops.h"
+#include "ops_math.h"
 
 namespace glk {
 
@@ -98,7 +99,7 @@ __global__ void __launch_bounds__(256) op_generic_kernel(OpArgs p, int64_t tiles
                 p.GU[m * p.ldgu + n] = __builtin_bit_cast(uint16_t, (__bf16)g);
                 p.GU[m * p.ldgu + p.N + n] = __builtin_bit_cast(uint16_t, (__bf16)u);
             }
-            const float h = GLU ? swiglu1(g, u) : g;
+            const float h = GLU ? op_swiglu(g, u) : g;
             p.C[m * p.ldc + n] = __builtin_bit_cast(uint16_t, (__bf16)h);
         }
     }

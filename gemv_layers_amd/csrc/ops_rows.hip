@@ -11,6 +11,7 @@
 #include "codes.h"
 #include "common.h"
 #include "ops.h"
+#include "ops_math.h"
 
 namespace glk {
 
@@ -114,7 +115,7 @@ hipError_t launch_i8_quantize(const uint16_t* X, int64_t R, int64_t K, int64_t l
 
 // du = d silu(g), dg = d u s (1 + g (1 - s)) with s = sigmoid(g), in float32
 __device__ __forceinline__ void swiglu_grad1(float d, float g, float u, float& dg, float& du) {
-    const float sig = 1.0f / (1.0f + expf(-g));
+    const float sig = op_sigmoid(g);
     du = d * (g * sig);
     dg = d * u * (sig * (1.0f + g * (1.0f - sig)));
 }

@@ -29,6 +29,7 @@
 
 #include "common.h"
 #include "ops.h"
+#include "ops_math.h"
 
 namespace glk {
 
@@ -88,10 +89,10 @@ struct OpCopy {
     int64_t ld_bytes;
     int sum;                   // bytes (contiguous) or rows (strided) of the summed index
 
-    // gated operands hold `rows` gate rows (columns) and then `rows` up ones; the tile's WT-wide
+    // gated operands hold gate rows (columns) and, `up` of them later, the up ones; the tile's WT-wide
     // share of each wave is WT / 2 gate and the same WT / 2 up
-    __device__ __forceinline__ void init(const void* p, int64_t ld, int64_t r0, int64_t rows, int64_t k0, int k_count,
-                                         int wave, int lane) {
+    __device__ __forceinline__ void init(const void* p, int64_t ld, int64_t r0, int64_t rows, int up, int64_t k0,
+                                         int k_count, int wave, int lane) {
         ld_bytes = ld * ES;
         sum = CONTIG ? k_count * ES : k_count;
         const char* at = static_cast<const char*>(p) + k0 * (CONTIG ? ES : ld_bytes);
@@ -107,7 +108,7 @@ struct OpCopy {
                     const int q = h * (R / 2) + 8 * idx, r = q + (lane >> 3);
                     if constexpr (GLU) {  // 8 rows are all gate or all up: one base for the instruction
                         const int out = (q / WT) * (WT / 2) + q % (WT / 2);
-                        const int64_t src = r0 + out + (q % WT < WT / 2 ? 0 : rows);
+                        const int64_t src = r0 + out + (q % WT < WT / 2 ? 0 : up);
                         base[h * PW + i] = at + src * ld_bytes;
                         off[h][i] = sel_off(r0 + out + (lane >> 3) < rows,
                                             (uint32_t)((lane >> 3) * (int)ld_bytes + chunk[i]));
@@ -122,7 +123,7 @@ struct OpCopy {
                     if constexpr (GLU) {
                         const int q = col % WT;
                         out = (col / WT) * (WT / 2) + q % (WT / 2);
-                        src = out + (q < WT / 2 ? 0 : (int)rows);
+                        src = out + (q < WT / 2 ? 0 : up);
                     }
                     off[h][i] = sel_off(r0 + out < rows, (uint32_t)(k * (int)ld_bytes + src * ES));
                 }
@@ -288,7 +289,7 @@ __device__ __forceinline__ void op_epilogue(const OpTileArgs& p, char* lds, cons
             for (int r = 0; r < 4; ++r) {
                 const int n = nw + ni * 16 + 4 * G + r;
                 sg[r] = n < p.N ? p.sb[n] : 0.f;
-                if constexpr (GLU) su[r] = n < p.N ? p.sb[(int64_t)p.sb_up + n] : 0.f;
+                if constexpr (GLU) su[r] = n < p.N ? p.sb[(int64_t)p.up + n] : 0.f;
             }
 #pragma unroll
             for (int mi = 0; mi < TM; ++mi) {
@@ -296,7 +297,7 @@ __device__ __forceinline__ void op_epilogue(const OpTileArgs& p, char* lds, cons
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     h[r] = (float)acc[ni][mi][r] * sa[mi] * sg[r];
-                    if constexpr (GLU) h[r] = swiglu1(h[r], (float)acc[ni + TNO][mi][r] * sa[mi] * su[r]);
+                    if constexpr (GLU) h[r] = op_swiglu(h[r], (float)acc[ni + TNO][mi][r] * sa[mi] * su[r]);
                 }
                 put(Out{}, mi, ni, h);
             }
@@ -311,7 +312,7 @@ __device__ __forceinline__ void op_epilogue(const OpTileArgs& p, char* lds, cons
             constexpr int RB = T::WTN * 2, CPR = RB / 16, ROWS = 64 / CPR;
             const int lr = lane / CPR, lc = lane % CPR;
             const int n = nw + (lc % (CPR / 2)) * 8;
-            const int64_t col = (lc < CPR / 2 ? 0 : (int64_t)p.gu_up) + n;
+            const int64_t col = (lc < CPR / 2 ? 0 : (int64_t)p.up) + n;
             const __amdgpu_buffer_rsrc_t rg = make_rsrc(p.GU + (size_t)mw * p.ldgu);
 #pragma unroll
             for (int s = 0; s < T::WTM / ROWS; ++s) {
@@ -327,7 +328,12 @@ __device__ __forceinline__ void op_epilogue(const OpTileArgs& p, char* lds, cons
 #pragma unroll
             for (int ni = 0; ni < TNO; ++ni) {
                 if constexpr (GLU)
-                    put(Out{}, mi, ni, swiglu4(acc[ni][mi], acc[ni + TNO][mi]));
+                    {
+                    f32x4 h;
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) h[r] = op_swiglu(acc[ni][mi][r], acc[ni + TNO][mi][r]);
+                    put(Out{}, mi, ni, h);
+                }
                 else
                     put(Out{}, mi, ni, acc[ni][mi]);
             }
@@ -358,8 +364,8 @@ op_pp_kernel(OpTileArgs p) {
 
     OpCopy<256, T::A_PW, T::A_CONTIG, T::ES, false, T::WTM> ca;
     OpCopy<256, T::B_PW, T::B_CONTIG, T::ES, GLU, T::WTN> cb;
-    ca.init(p.A, p.lda, at.m0, p.M, 0, p.K, wave, lane);
-    cb.init(p.B, p.ldb, at.n0, p.N, 0, p.K, wave, lane);
+    ca.init(p.A, p.lda, at.m0, p.M, 0, 0, p.K, wave, lane);
+    cb.init(p.B, p.ldb, at.n0, p.N, p.up, 0, p.K, wave, lane);
     const uint32_t ring = lds_addr(lds);
     auto issue_a = [&](auto h, int u, int slot) {
         ca.template issue<decltype(h)::value>(u, ring + slot * T::A_BYTES, wave);
@@ -449,8 +455,8 @@ __device__ __forceinline__ void op_small(const OpTileArgs& p, int block, char* l
 
     OpCopy<BT, T::A_PW, T::A_CONTIG, T::ES, false, T::WTM> ca;
     OpCopy<BT, T::B_PW, T::B_CONTIG, T::ES, GLU, T::WTN> cb;
-    ca.init(p.A, p.lda, at.m0, p.M, (int64_t)first * T::KE, count, wave, lane);
-    cb.init(p.B, p.ldb, at.n0, p.N, (int64_t)first * T::KE, count, wave, lane);
+    ca.init(p.A, p.lda, at.m0, p.M, 0, (int64_t)first * T::KE, count, wave, lane);
+    cb.init(p.B, p.ldb, at.n0, p.N, p.up, (int64_t)first * T::KE, count, wave, lane);
     const uint32_t ring = lds_addr(lds);
     auto issue_a = [&](auto h, int u, int slot) {
         ca.template issue<decltype(h)::value>(u, ring + slot * T::A_BYTES, wave);

@@ -403,7 +403,16 @@ Plan make_op_plan(int64_t M, int64_t N, int64_t K, const DeviceInfo& dev, bool g
     const int64_t tm = cdiv(M, 64), tn = cdiv(glu ? 2 * N : N, 64), kt = cdiv(K, 32);
     const int64_t most = dev.cus + dev.cus / 2;
     if (tm > most || tn > most || tm * tn > most || (tm * tn * kt > 32768 && tm * tn > dev.cus / 4))
-        return make_plan(M, N, K, dev, true, 2, glu);
+    {
+        // the gated form is planned over its 2N weight columns: a 256-column tile makes 128 outputs, and
+        // the strip of a sparse last wave may be cut off across columns too, as its kernels take the
+        // up half's offset apart from the width
+        Plan q = make_plan(M, glu ? 2 * N : N, K, dev, true, 2, false);
+        q.glu = glu;
+        for (Plan& r : q.rest) r.glu = glu;
+        if (glu && q.cut_axis == 1) q.cut_at /= 2;
+        return q;
+    }
     Plan p;
     p.kernel = kKernTile;
     p.glu = glu;
