@@ -10,7 +10,14 @@
 // flight. The waves' 32-bit sums meet in LDS, the pieces' in the workspace, where the last arriver
 // adds them and returns its counter to zero; integer sums are exact, so the result does not depend
 // on the split. Rows past M and N load nothing and store nothing.
+//
+// FUSED (M = 1): the activations come as bf16, and every workgroup quantises the row itself, with its
+// first weight loads already in flight, into LDS, where the loop reads the codes. That is 2 K bytes
+// more through the L1 for each workgroup, against a launch and a round trip to memory (us, fused
+// against two launches: 11008 x 4096 11.3 and 13.1, 4096 x 11008 12.3 and 13.7, gated 11008 x 4096 18.3 and
+// 21.1, 1000 x 1000 4.8 and 7.1; with two rows it lost, 13.6 and 13.2, 15.1 and 13.9).
 
+#include "codes.h"
 #include "common.h"
 #include "ops.h"
 #include "ops_math.h"
@@ -26,8 +33,42 @@ struct I8Stage {
     u32x4 w[TN], a[MT];
 };
 
-template <int MT, int TN, int NW, int D, bool GLU>
+// Quantises the row p.A16 into `codes` (`pitch` bytes, zeros past K); returns its scale.
+template <int NW>
+__device__ __forceinline__ float quantise_row(const I8DecodeArgs& p, char* codes, int pitch, uint32_t* part) {
+    constexpr int NC = kI8FusedK / (8 * 64 * NW);  // chunks of 8 values a thread
+    const int tid = threadIdx.x;
+    u32x4 v[NC];
+    uint32_t amax = 0;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+        const int k = 8 * (c * 64 * NW + tid);
+        v[c] = u32x4{0, 0, 0, 0};
+        if (k + 8 <= p.K)
+            v[c] = *reinterpret_cast<const u32x4*>(p.A16 + k);
+        else if (k < p.K)
+            v[c] = load_some(p.A16 + k, p.K - k);
+    }
+#pragma unroll
+    for (int c = 0; c < NC; ++c) amax = magnitude8(v[c], amax);
+    amax = wave_max(amax);
+    if ((tid & 63) == 0) part[tid >> 6] = amax;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < NW; ++w) amax = max(amax, part[w]);
+    const CodeScale cs = code_scale(amax);
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+        const int k = 8 * (c * 64 * NW + tid);
+        if (k < pitch) *reinterpret_cast<u32x2*>(codes + k) = codes8(v[c], cs);
+    }
+    __syncthreads();
+    return cs.s;
+}
+
+template <int MT, int TN, int NW, int D, bool GLU, bool FUSED>
 __global__ void __launch_bounds__(64 * NW) i8_decode_kernel(I8DecodeArgs p) {
+    static_assert(!FUSED || MT == 1, "one row");
     constexpr int NJ = TN * MT;               // 16 x 16 blocks of sums
     constexpr int TO = GLU ? TN / 2 : TN;     // tiles of outputs
     extern __shared__ __attribute__((aligned(16))) char lds[];
@@ -57,12 +98,16 @@ __global__ void __launch_bounds__(64 * NW) i8_decode_kernel(I8DecodeArgs p) {
         a_off[mt] = sel_off(16 * mt + i16 < p.M, (uint32_t)((16 * mt + i16) * p.lda + 16 * g16));
 
     // (offsets of rows outside stay outside when a step's bytes are added: 2^31 - 16 + K < 2^32)
+    char* codes = lds + NW * NJ * 1024;  // FUSED: the row's codes, whole k-steps, after the waves' sums
+    __shared__ uint32_t s_part[NW];
     auto load = [&](I8Stage<MT, TN>& st, int s) {
         const bool in = s < we && 64 * s + 16 * g16 < p.K;
 #pragma unroll
         for (int t = 0; t < TN; ++t) st.w[t] = buf_load16(rw[t], sel_off(in, w_off[t] + 64u * s));
+        if constexpr (!FUSED) {
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) st.a[mt] = buf_load16(ra, sel_off(in, a_off[mt] + 64u * s));
+            for (int mt = 0; mt < MT; ++mt) st.a[mt] = buf_load16(ra, sel_off(in, a_off[mt] + 64u * s));
+        }
     };
     i32x4 acc[TN][MT];
 #pragma unroll
@@ -70,8 +115,12 @@ __global__ void __launch_bounds__(64 * NW) i8_decode_kernel(I8DecodeArgs p) {
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) acc[t][mt] = i32x4{};
     // the codes past K in a row's last 16 bytes are the caller's padding: cleared in A
-    const int tail = (p.K & 15) ? steps - 1 : -1;
+    const int tail = !FUSED && (p.K & 15) ? steps - 1 : -1;
     auto compute = [&](I8Stage<MT, TN>& st, int s) {
+        if constexpr (FUSED) {
+            st.a[0] = u32x4{0, 0, 0, 0};
+            if (i16 == 0 && s < we) st.a[0] = *reinterpret_cast<const u32x4*>(codes + 64 * s + 16 * g16);
+        }
         if (s == tail) {
             const int n = p.K - 64 * s - 16 * g16;
 #pragma unroll
@@ -90,6 +139,8 @@ __global__ void __launch_bounds__(64 * NW) i8_decode_kernel(I8DecodeArgs p) {
     I8Stage<MT, TN> st[D];
 #pragma unroll
     for (int j = 0; j < D; ++j) load(st[j], wb + j);
+    float row_scale = 0.f;
+    if constexpr (FUSED) row_scale = quantise_row<NW>(p, codes, 64 * steps, s_part);
     for (int s = wb; s < we; s += D) {
 #pragma unroll
         for (int j = 0; j < D; ++j) {
@@ -124,7 +175,7 @@ __global__ void __launch_bounds__(64 * NW) i8_decode_kernel(I8DecodeArgs p) {
     auto store_c = [&](int q, const i32x4 (&v)[H]) {
         const int m = 16 * (q % MT) + i16, n = n0 + 16 * (q / MT) + 4 * g16;
         if (m >= p.M || n >= p.N) return;
-        const float sa = p.sa[m];
+        const float sa = FUSED ? row_scale : p.sa[m];
         f32x4 y;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
@@ -189,16 +240,17 @@ __global__ void __launch_bounds__(64 * NW) i8_decode_kernel(I8DecodeArgs p) {
 static constexpr int depth(int tn) { return tn == 4 ? 2 : 4; }
 
 // calls f with the kernel and its LDS bytes for a shape that the planner makes, else returns an error
-template <int MT, class F>
+template <int MT, bool FUSED, class F>
 static hipError_t with_kernel(bool glu, int tn, int nw, F f) {
-#define GLK_DECODE(TN, NW, GLU) \
-    if (glu == GLU && tn == TN && nw == NW) return f(i8_decode_kernel<MT, TN, NW, depth(TN), GLU>, NW * TN * MT * 1024);
+#define GLK_DECODE(TN, NW, GLU)           \
+    if (glu == GLU && tn == TN && nw == NW) \
+        return f(i8_decode_kernel<MT, TN, NW, depth(TN), GLU, FUSED>, NW * TN * MT * 1024);
     GLK_DECODE(1, 4, false)
     GLK_DECODE(1, 8, false)
     GLK_DECODE(2, 4, true)
-    if constexpr (MT == 1) {
+    if constexpr (MT == 1 && !FUSED) {
         GLK_DECODE(4, 4, false)
-    } else {
+    } else if constexpr (!FUSED) {
         GLK_DECODE(2, 4, false)
         GLK_DECODE(4, 8, false)
         GLK_DECODE(4, 4, true)
@@ -209,25 +261,28 @@ static hipError_t with_kernel(bool glu, int tn, int nw, F f) {
 
 hipError_t launch_i8_decode(bool glu, int mt, int tn, int nw, const I8DecodeArgs& a, int grid, hipStream_t s) {
     auto run = [&](void (*k)(I8DecodeArgs), int lds) {
+        if (a.A16) lds += (a.K + 63) / 64 * 64;
         k<<<grid, 64 * nw, lds, s>>>(a);
         return hipGetLastError();
     };
+    if (a.A16) return mt == 1 ? with_kernel<1, true>(glu, tn, nw, run) : hipErrorInvalidValue;
     switch (mt) {
-        case 1: return with_kernel<1>(glu, tn, nw, run);
-        case 2: return with_kernel<2>(glu, tn, nw, run);
-        case 3: return with_kernel<3>(glu, tn, nw, run);
-        case 4: return with_kernel<4>(glu, tn, nw, run);
+        case 1: return with_kernel<1, false>(glu, tn, nw, run);
+        case 2: return with_kernel<2, false>(glu, tn, nw, run);
+        case 3: return with_kernel<3, false>(glu, tn, nw, run);
+        case 4: return with_kernel<4, false>(glu, tn, nw, run);
         default: return hipErrorInvalidValue;
     }
 }
 
+// (the others ask for at most 64 KB: the fused ones 24 KB with the codes of a row of kI8FusedK)
 hipError_t configure_i8_decode() {
     auto set = [](void (*k)(I8DecodeArgs), int lds) {
         return hipFuncSetAttribute((const void*)k, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
     };
-    hipError_t e = with_kernel<2>(false, 4, 8, set);
-    if (e == hipSuccess) e = with_kernel<3>(false, 4, 8, set);
-    if (e == hipSuccess) e = with_kernel<4>(false, 4, 8, set);
+    hipError_t e = with_kernel<2, false>(false, 4, 8, set);
+    if (e == hipSuccess) e = with_kernel<3, false>(false, 4, 8, set);
+    if (e == hipSuccess) e = with_kernel<4, false>(false, 4, 8, set);
     return e;
 }
 

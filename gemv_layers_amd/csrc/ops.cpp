@@ -81,16 +81,17 @@ hipError_t launch_tiles(int mode, bool glu, const OpArgs& a, const glk::Plan& p,
     return glk::launch_op_tile(mode, glu, p.bm, tile_args(mode, a, p, m0, M, n0, N, w), (int)p.grid, stream);
 }
 
-// The 8-bit product of at most 64 rows on the weight-streaming kernel.
-int run_i8_decode(bool glu, const OpArgs& a, const glk::DeviceInfo& dev, hipStream_t stream) {
+// The 8-bit product of at most 64 rows on the weight-streaming kernel. `fused`: a.A holds bf16.
+int run_i8_decode(bool glu, const OpArgs& a, const glk::DeviceInfo& dev, bool fused, hipStream_t stream) {
     const glk::Plan p = glk::make_i8_decode_plan(a.M, a.N, a.K, dev, glu);
     glk::Workspace w;
     if (p.splits > 1) {
         const int st = glk::stream_workspace(stream, &w);
         if (st != GEMM_OK) return st;
     }
-    const glk::I8DecodeArgs t{static_cast<const int8_t*>(a.A), static_cast<const int8_t*>(a.B), a.C, a.sa, a.sb,
-                              (int)a.M, (int)a.N, (int)a.K, (int)a.lda, (int)a.ldb, (int)a.ldc,
+    const glk::I8DecodeArgs t{fused ? nullptr : static_cast<const int8_t*>(a.A),
+                              fused ? static_cast<const uint16_t*>(a.A) : nullptr,
+                              static_cast<const int8_t*>(a.B), a.C, a.sa, a.sb, (int)a.M, (int)a.N, (int)a.K, (int)a.lda, (int)a.ldb, (int)a.ldc,
                               !misaligned(a.C, 8) && a.ldc % 4 == 0 && a.N % 4 == 0, p.splits,
                               reinterpret_cast<int32_t*>(w.ws), w.counters};
     if (glk::launch_i8_decode(glu, p.mtiles, p.strip / 16, p.threads / 64, t, (int)p.grid, stream) != hipSuccess)
@@ -104,7 +105,7 @@ int run_op(int mode, bool glu, const OpArgs& a, hipStream_t stream) {
     int st = GEMM_OK;
     const glk::DeviceInfo* dev = glk::current_device(&st);
     if (!dev) return st;
-    if (mode == glk::kOpI8 && a.M <= 64 && a.K > 0 && matrix_ok(mode, glu, a)) return run_i8_decode(glu, a, *dev, stream);
+    if (mode == glk::kOpI8 && a.M <= 64 && a.K > 0 && matrix_ok(mode, glu, a)) return run_i8_decode(glu, a, *dev, false, stream);
     glk::Plan p;
     hipError_t e = hipSuccess;
     if (a.K == 0) {
@@ -184,6 +185,12 @@ int i8_product_bf16(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda,
     if (M > kMaxRows) return GEMM_ERR_UNSUPPORTED;
     if (M == 0 || N == 0) return GEMM_OK;
     if (!work || misaligned(work, 16) || work_bytes < work_bytes_of(M, K)) return GEMM_ERR_INVALID_ARG;
+    // one row: quantised in the product's kernel (its leading dimension does not matter)
+    const OpArgs one{A, Wq, static_cast<uint16_t*>(C), nullptr, nullptr, Sw, M, N, K, 16, ldwq, ldc, 0};
+    if (M == 1 && K > 0 && K <= glk::kI8FusedK && matrix_ok(glk::kOpI8, glu, one)) {
+        const glk::DeviceInfo* dev = glk::current_device(&st);
+        return dev ? run_i8_decode(glu, one, *dev, true, stream) : st;
+    }
     const int64_t ldq = padded_codes(K);
     float* sa = reinterpret_cast<float*>(static_cast<char*>(work) + M * ldq);
     st = quantize(M, K, A, lda, work, ldq, sa, stream);

@@ -55,8 +55,10 @@ hipError_t launch_op_pair(int tile, const OpTileArgs& a, const OpTileArgs& b, in
 hipError_t configure_op_kernels();
 
 // ---- 8-bit product of few tokens -------------------------------------------------------------------
+constexpr int kI8FusedK = 16384;  // the longest row that the fused form quantises
 struct I8DecodeArgs {
-    const int8_t* A;
+    const int8_t* A;      // M rows of codes, with scales sa; or, fused, null and
+    const uint16_t* A16;  // one row of bf16, quantised in the kernel
     const int8_t* W;
     uint16_t* C;
     const float* sa;

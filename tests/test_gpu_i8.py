@@ -291,7 +291,9 @@ def act(M, K, seed, ld=None):
 
 @pytest.mark.parametrize("M,N,K,ld", [(1, 520, 328, None), (2, 11008, 4096, None), (3, 40, 33, None), (5, 24, 1000, 1001),
                                       (16, 4096, 4096, None), (17, 264, 20000, None), (64, 1000, 4104, None),
-                                      (300, 1000, 1000, 1008), (1100, 520, 328, None)])
+                                      (300, 1000, 1000, 1008), (1100, 520, 328, None), (1, 17, 7, 8),
+                                      (2, 40, 1000, 1008), (1, 1000, 16384, None), (2, 24, 16392, None),
+                                      (2, 4096, 11008, None), (1, 72, 4104, 4112)])
 def test_dynamic_equals_quantize_then_product(M, N, K, ld):
     A = act(M, K, M + K, ld)
     W = (torch.randn(2 * N, K, generator=torch.Generator().manual_seed(N)) * 0.02).bfloat16().cuda()
