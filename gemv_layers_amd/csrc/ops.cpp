@@ -82,8 +82,7 @@ hipError_t launch_tiles(int mode, bool glu, const OpArgs& a, const glk::Plan& p,
 }
 
 // The 8-bit product of at most 64 rows on the weight-streaming kernel. `fused`: a.A holds bf16.
-int run_i8_decode(bool glu, const OpArgs& a, const glk::DeviceInfo& dev, bool fused, hipStream_t stream) {
-    const glk::Plan p = glk::make_i8_decode_plan(a.M, a.N, a.K, dev, glu);
+int run_i8_decode(bool glu, const OpArgs& a, const glk::Plan& p, bool fused, hipStream_t stream) {
     glk::Workspace w;
     if (p.splits > 1) {
         const int st = glk::stream_workspace(stream, &w);
@@ -105,7 +104,10 @@ int run_op(int mode, bool glu, const OpArgs& a, hipStream_t stream) {
     int st = GEMM_OK;
     const glk::DeviceInfo* dev = glk::current_device(&st);
     if (!dev) return st;
-    if (mode == glk::kOpI8 && a.M <= 64 && a.K > 0 && matrix_ok(mode, glu, a)) return run_i8_decode(glu, a, *dev, false, stream);
+    if (mode == glk::kOpI8 && a.M <= 64 && a.K > 0 && matrix_ok(mode, glu, a)) {
+        const glk::Plan few = glk::make_i8_decode_plan(a.M, a.N, a.K, *dev, glu);
+        if (glk::i8_decode_fits(a.M, a.K, few)) return run_i8_decode(glu, a, few, false, stream);
+    }
     glk::Plan p;
     hipError_t e = hipSuccess;
     if (a.K == 0) {
@@ -189,7 +191,7 @@ int i8_product_bf16(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda,
     const OpArgs one{A, Wq, static_cast<uint16_t*>(C), nullptr, nullptr, Sw, M, N, K, 16, ldwq, ldc, 0};
     if (M == 1 && K > 0 && K <= glk::kI8FusedK && matrix_ok(glk::kOpI8, glu, one)) {
         const glk::DeviceInfo* dev = glk::current_device(&st);
-        return dev ? run_i8_decode(glu, one, *dev, true, stream) : st;
+        return dev ? run_i8_decode(glu, one, glk::make_i8_decode_plan(M, N, K, *dev, glu), true, stream) : st;
     }
     const int64_t ldq = padded_codes(K);
     float* sa = reinterpret_cast<float*>(static_cast<char*>(work) + M * ldq);

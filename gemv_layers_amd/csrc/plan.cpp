@@ -396,9 +396,12 @@ Plan make_packed_plan(int64_t M, int64_t N, int64_t K, const DeviceInfo& dev) {
 // are busy: 2048 x 2048 x 512 10.0 against 8.3, codes 777 x 4096 x 4096 28.3 against 23.1, 2000 x 512 x
 // 8192 30.0 against 25.9. So 64 x 64 tiles up to one and a half a CU and 32768 k-steps in all (128
 // x 4096 x 4096, 16384 steps: 13.2 against 16.1; codes 128 x 11008 x 4096, 22016 steps: 15.9 against
-// 17.2), and for a quarter as many tiles as CUs whatever K is. A piece of K keeps 28 k-steps or
-// more (509 x 512 x 2752, 86 steps: 9.3 in three pieces, 13.2 before; 512^3, 16 steps: 4.8 whole, 6.0
-// in two).
+// 17.2), and for a quarter as many tiles as CUs whatever K is.
+// Pieces of K: a fixup costs like a few k-steps for each piece, so about sqrt(steps / 6) of them (512^3,
+// 16 steps: 4.8 us whole, 6.0 in two pieces; codes 300 x 300 x 5008, 79 steps: 9.6 in three, 10.9 in
+// two), but none of less than 28 steps once the tiles alone fill the CUs (1000^3, 32 steps: 8.0 whole,
+// 9.8 in two), and not a few more workgroups than CUs, whose second round is nearly empty (codes 64
+// x 4096 x 11008 in four pieces, 256 workgroups, 15.4; in five, 320 workgroups, 18.8).
 Plan make_op_plan(int64_t M, int64_t N, int64_t K, const DeviceInfo& dev, bool glu) {
     const int64_t tm = cdiv(M, 64), tn = cdiv(glu ? 2 * N : N, 64), kt = cdiv(K, 32);
     const int64_t most = dev.cus + dev.cus / 2;
@@ -426,7 +429,11 @@ Plan make_op_plan(int64_t M, int64_t N, int64_t K, const DeviceInfo& dev, bool g
     p.nxcd = dev.nxcd;
     p.group_m = (int)std::min<int64_t>(4, tm);
     p.slots = 4 * (int64_t)dev.cus;
-    int64_t s = std::max<int64_t>(1, std::min<int64_t>({kt / 28, 16, 3 * (int64_t)dev.cus / p.tiles}));
+    int64_t root = 1;
+    while ((root + 1) * (root + 1) * 6 <= kt) ++root;
+    int64_t s = std::min<int64_t>({root, std::max<int64_t>(kt / 28, dev.cus / p.tiles), 16, 3 * (int64_t)dev.cus / p.tiles});
+    if (p.tiles * s > dev.cus && p.tiles * s <= most) s = dev.cus / p.tiles;
+    s = std::max<int64_t>(s, 1);
     while (s > 1 && p.tiles * s * 4096 > dev.ws_floats / 2) --s;  // (two products may share a launch)
     p.kt_per_split = (int)cdiv(kt, s);
     p.splits = (int)cdiv(kt, p.kt_per_split);
@@ -441,6 +448,16 @@ Plan make_op_plan(int64_t M, int64_t N, int64_t K, const DeviceInfo& dev, bool g
     return p;
 }
 
+// Whether the weight-streaming kernel takes an 8-bit product of at most 64 rows. It has no LDS staging
+// to fill and drain, but each of its groups reads all activation rows, where the 64 x 64 tiles read
+// them once for 64 weight rows through LDS. Measured with the weights out of the L2s, it wins up to 22
+// MB of such reads (us, streaming against tiles: M = 16, 11008 x 4096 12.0 and 12.6; M = 32, 4096 x 4096
+// 8.8 and 9.7; M = 64, 1000 x 2000 5.4 and 7.0) and loses beyond (M = 32, 11008 x 4096 14.4 and 12.7; M =
+// 64, 4096 x 11008 17.9 and 15.4; gated 11008 x 4096, M = 16 21.7 and 20.6, M = 64 36.8 and 22.2).
+bool i8_decode_fits(int64_t M, int64_t K, const Plan& p) {
+    return M <= 64 && (int64_t)p.strips * M * K <= int64_t(22) * 1000 * 1000;
+}
+
 // The 8-bit product of few rows streams the weight once, and a workgroup of `tn` 16-row tiles also
 // reads its K range of all activation rows, which costs like as many weight bytes: the L1 returns
 // hits in order behind the stream's misses. So one tile up to 4 rows or while one-tile groups are at
@@ -448,8 +465,7 @@ Plan make_op_plan(int64_t M, int64_t N, int64_t K, const DeviceInfo& dev, bool g
 // above 16 rows one, two or four as the weight outgrows the 2 us that summing K pieces costs (M =
 // 64: 1000 x 2000 5.3 us with one and 6.3 with two; 2048 x 8192 12.1 with two and 13.4 with four;
 // 4096 x 11008 17.9 with four and 20.7 with two). The gated form takes gate and up tiles in pairs, one
-// pair up to 16 rows (M = 16, 11008 x 4096: 21.7 us) and two for a large weight beyond (M = 64: 37.6
-// us against 40.1 with one). K is split as far as the groups leave CUs idle and 32 k-steps remain to
+// pair up to 16 rows and two for a large weight beyond (M = 64, 11008 x 4096: 37.6 us against 40.1). K is split as far as the groups leave CUs idle and 32 k-steps remain to
 // each piece (4 x 2048 x 2048 codes: 4.0 us whole, 4.9 in two pieces; 1 x 1000 x 11008: 6.7 in four,
 // 7.0 in three).
 Plan make_i8_decode_plan(int64_t M, int64_t N, int64_t K, const DeviceInfo& dev, bool glu) {

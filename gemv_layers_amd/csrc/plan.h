@@ -86,6 +86,8 @@ Plan make_op_plan(int64_t M, int64_t N, int64_t K, const DeviceInfo& dev, bool g
 // The 8-bit product of few rows (1 <= M <= 64, K >= 1; N outputs, gated: 2N weight rows): groups of
 // 16-row weight tiles (strip rows) times K pieces (splits), one workgroup of `threads` each.
 Plan make_i8_decode_plan(int64_t M, int64_t N, int64_t K, const DeviceInfo& dev, bool glu);
+// whether that plan beats the tiles (M may be any)
+bool i8_decode_fits(int64_t M, int64_t K, const Plan& p);
 
 std::string plan_json(const Plan& p, int64_t M, int64_t N, int64_t K);
 
