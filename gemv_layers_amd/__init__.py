@@ -369,14 +369,17 @@ def swiglu_matmul(A, B, out=None, stream=None):
 # each tensor is asked for its properties once and the stream's handle is read without a Stream object.
 
 _t = None
+_raw_stream = None
 
 
 def _torch():
     """PyTorch, imported on first use."""
-    global _t
+    global _t, _raw_stream
     if _t is None:
         import torch
 
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda device: torch.cuda.current_stream(device).cuda_stream)
         _t = torch
     return _t
 
@@ -385,8 +388,7 @@ def _stream(stream, device: int):
     """The given stream's handle, or that of the device's current stream."""
     if stream is not None:
         return stream
-    raw = getattr(_t._C, "_cuda_getCurrentRawStream", None)
-    return raw(device) if raw is not None else _t.cuda.current_stream(device).cuda_stream
+    return _raw_stream(device)
 
 
 def _rows(t, name, dtype, rows=None, cols=None, device=None):
@@ -395,14 +397,17 @@ def _rows(t, name, dtype, rows=None, cols=None, device=None):
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}")
     shape = t.shape
-    if len(shape) != 2 or (cols is not None and shape[1] != cols) or (rows is not None and shape[0] != rows):
+    if len(shape) != 2:
+        raise ValueError(f"{name} must have two dimensions, not {tuple(shape)}")
+    r, c = shape
+    if (cols is not None and c != cols) or (rows is not None and r != rows):
         raise ValueError(f"{name} must be {'M' if rows is None else rows} x {'N' if cols is None else cols}, "
                          f"not {tuple(shape)}")
-    if not t.is_cuda:
+    at = t.get_device()
+    if at < 0:
         raise ValueError(f"{name} must be a device tensor")
-    if device is not None and t.get_device() != device:
+    if device is not None and at != device:
         raise ValueError("all tensors must be on one device")
-    r, c = shape
     ld, unit = t.stride()
     if unit != 1 and c > 1 and r > 0:
         raise ValueError(f"{name} needs unit column stride")
@@ -414,12 +419,13 @@ def _rows(t, name, dtype, rows=None, cols=None, device=None):
 
 
 def _scales(t, name, n, device):
-    if t.dtype != _t.float32 or t.dim() != 1 or t.shape[0] != n or not t.is_cuda:
+    at = t.get_device()
+    if t.dtype != _t.float32 or t.shape != (n,) or at < 0:
         raise ValueError(f"{name} must be a device vector of {n} float32 values")
+    if at != device:
+        raise ValueError("all tensors must be on one device")
     if n > 1 and t.stride(0) != 1:
         raise ValueError(f"{name} needs unit stride")
-    if t.get_device() != device:
-        raise ValueError("all tensors must be on one device")
     return t.data_ptr()
 
 
@@ -501,9 +507,11 @@ def i8_swiglu_linear(A, Wq, Sw, out=None, work=None, stream=None):
     return _i8_dynamic("gemm_i8_swiglu_bf16", A, Wq, Sw, out, work, stream, True)
 
 
-def _empty(shape, like):
-    t = like.new_empty(shape)
-    return t, t.data_ptr()
+def _like(t, M, N):
+    """An uninitialised contiguous M x N tensor of t's type and device, and its address."""
+    # (t has that shape: copying its layout is the cheaper call)
+    out = _t.empty_like(t) if t.is_contiguous() else t.new_empty((M, N))
+    return out, out.data_ptr()
 
 
 def matmul_backward(dC, A, B, need_dA=True, need_dB=True, stream=None):
@@ -513,9 +521,10 @@ def matmul_backward(dC, A, B, need_dA=True, need_dB=True, stream=None):
     device = A.get_device()
     _, N, ldb, b = _rows(B, "B", bf16, K, None, device)
     _, _, lddc, d = _rows(dC, "dC", bf16, M, N, device)
-    dA, da = _empty((M, K), A) if need_dA else (None, None)
-    dB, db = _empty((K, N), A) if need_dB else (None, None)
-    gemm_bf16_bwd(M, N, K, d, lddc, a, lda, b, ldb, da, K, db, N, _stream(stream, device))
+    dA, da = _like(A, M, K) if need_dA else (None, None)
+    dB, db = _like(B, K, N) if need_dB else (None, None)
+    _check("gemm_bf16_bwd", lib().gemm_bf16_bwd(M, N, K, d, lddc, a, lda, b, ldb, da, K, db, N,
+                                                _stream(stream, device)))
     return dA, dB
 
 
@@ -528,9 +537,10 @@ def swiglu_forward(A, B, stream=None):
     if N % 2:
         raise ValueError("B must be K x 2N for A of shape M x K")
     N //= 2
-    C, c = _empty((M, N), A)
-    GU, gu = _empty((M, 2 * N), A)
-    gemm_bf16_swiglu_train(M, N, K, a, lda, b, ldb, gu, 2 * N, c, N, _stream(stream, device))
+    C, GU = A.new_empty((M, N)), A.new_empty((M, 2 * N))
+    _check("gemm_bf16_swiglu_train",
+           lib().gemm_bf16_swiglu_train(M, N, K, a, lda, b, ldb, GU.data_ptr(), 2 * N, C.data_ptr(), N,
+                                        _stream(stream, device)))
     return C, GU
 
 
@@ -545,9 +555,10 @@ def swiglu_backward(dC, GU, A, B, need_dA=True, need_dB=True, inplace=False, str
     N //= 2
     _, _, lddc, d = _rows(dC, "dC", bf16, M, N, device)
     _, _, ldgu, gu = _rows(GU, "GU", bf16, M, 2 * N, device)
-    dGU, dgu, lddgu = (GU, gu, ldgu) if inplace else (*_empty((M, 2 * N), A), 2 * N)
-    dA, da = _empty((M, K), A) if need_dA else (None, None)
-    dB, db = _empty((K, 2 * N), A) if need_dB else (None, None)
-    gemm_bf16_swiglu_bwd(M, N, K, d, lddc, gu, ldgu, a, lda, b, ldb, dgu, lddgu, da, K, db, 2 * N,
-                         _stream(stream, device))
+    dGU, dgu, lddgu = (GU, gu, ldgu) if inplace else (*_like(GU, M, 2 * N), 2 * N)
+    dA, da = _like(A, M, K) if need_dA else (None, None)
+    dB, db = _like(B, K, 2 * N) if need_dB else (None, None)
+    _check("gemm_bf16_swiglu_bwd",
+           lib().gemm_bf16_swiglu_bwd(M, N, K, d, lddc, gu, ldgu, a, lda, b, ldb, dgu, lddgu, da, K, db, 2 * N,
+                                      _stream(stream, device)))
     return dA, dB, dGU
