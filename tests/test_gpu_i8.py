@@ -371,3 +371,22 @@ def test_refusals_on_the_device():
         g.i8_linear(A, Wq, Sw, out=torch.empty(4, 23, dtype=torch.bfloat16, device="cuda"))
     with pytest.raises(g.GemmError):
         g.i8_linear(A, Wq, Sw, work=torch.empty(16, dtype=torch.uint8, device="cuda"))
+
+
+def test_offsets_past_32_bits():
+    """Activations, codes and outputs of more than 2^32 bytes: the last rows are the first ones."""
+    M, N, K = 1_060_003, 2056, 4104
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    head = torch.randn(64, K, generator=gen, device="cuda").bfloat16()
+    A = torch.zeros(M, K, dtype=torch.bfloat16, device="cuda")
+    A[:64] = head
+    A[-64:] = head
+    Wq, Sw = g.i8_quantize((torch.randn(N, K, generator=gen, device="cuda") * 0.02).bfloat16())
+    Aq, Sa = g.i8_quantize(A)
+    assert torch.equal(Aq[-64:], Aq[:64]) and torch.equal(Sa[-64:], Sa[:64])
+    del A
+    C = g.i8_matmul(Aq, Sa, Wq, Sw)
+    assert C.numel() * 2 > 1 << 32 and Aq.numel() > 1 << 32
+    assert torch.equal(C[-64:], C[:64]) and not C[64:-64].any()
+    acc = Aq[:64].cpu().numpy().astype(np.float64) @ Wq.cpu().numpy().astype(np.float64).T
+    assert np.array_equal(bits(C[:64]), expect(acc, Sa[:64].cpu().numpy(), Sw.cpu().numpy()))

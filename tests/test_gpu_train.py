@@ -284,3 +284,26 @@ def test_streams_graphs_and_repeats():
         torch.cuda.synchronize()
         for x, y in zip(outs, want):
             assert torch.equal(x.view(torch.int16), y.view(torch.int16))
+
+
+def test_offsets_past_32_bits():
+    """More than 2^32 bytes of activations and of g and u: only the first and last tokens are not zero,
+    and both gradients are those of these tokens alone."""
+    M, N, K = 540_001, 2056, 4104
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    r = lambda *s: torch.randn(*s, generator=gen, device="cuda")  # noqa: E731
+    few = torch.cat([torch.arange(64), torch.arange(M - 65, M)]).cuda()
+    x, d, B = r(len(few), K).bfloat16(), (r(len(few), N) * 0.1).bfloat16(), (r(K, 2 * N) * 0.02).bfloat16()
+    A = torch.zeros(M, K, dtype=torch.bfloat16, device="cuda")
+    D = torch.zeros(M, N, dtype=torch.bfloat16, device="cuda")
+    A[few], D[few] = x, d
+    C, GU = g.swiglu_forward(A, B)
+    c, gu = g.swiglu_forward(x, B)
+    assert A.numel() * 2 > 1 << 32 and GU.numel() * 2 > 1 << 32
+    err = lambda a, b: float((a.double() - b.double()).norm() / b.double().norm())  # noqa: E731
+    # the same products in another order of sums, each rounded to bf16
+    assert err(C[few], c) < 2.0**-8 and err(GU[few], gu) < 2.0**-8 and not C[64:-65].any()
+    dA, dB, dGU = g.swiglu_backward(D, GU, A, B, inplace=True)
+    da, db, dgu = g.swiglu_backward(d, gu, x, B)
+    assert err(dGU[few], dgu) < 2.0**-7 and err(dA[few], da) < 2.0**-7 and err(dB, db) < 2.0**-7
+    assert not dA[64:-65].any() and not dGU[64:-65].any()
