@@ -365,200 +365,70 @@ def swiglu_matmul(A, B, out=None, stream=None):
 
 # ---- 8-bit products and training: PyTorch marshalling ----------------------------------------
 #
-# A small product takes the GPU a few microseconds, less than careless marshalling takes the host, so
-# each tensor is asked for its properties once and the stream's handle is read without a Stream object.
+# A small product takes the GPU a few microseconds, so the tensors are checked, and the outputs made,
+# in a C++ module (_torch_ops). The functions below name its arguments.
 
-_t = None
-_raw_stream = None
-
-
-def _torch():
-    """PyTorch, imported on first use."""
-    global _t, _raw_stream
-    if _t is None:
-        import torch
-
-        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-            lambda device: torch.cuda.current_stream(device).cuda_stream)
-        _t = torch
-    return _t
+_ops = None
 
 
-def _stream(stream, device: int):
-    """The given stream's handle, or that of the device's current stream."""
-    if stream is not None:
-        return stream
-    return _raw_stream(device)
+def _load_ops():
+    """The marshalling module (built by gemv_layers_amd.build), with the library's addresses in it."""
+    global _ops
+    if _ops is None:
+        import torch  # noqa: F401  (the module links to it)
 
-
-def _rows(t, name, dtype, rows=None, cols=None, device=None):
-    """Checks a 2-D device tensor of `dtype` with unit column stride and rows that do not overlap.
-    Returns (rows, columns, leading dimension, address)."""
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}")
-    shape = t.shape
-    if len(shape) != 2:
-        raise ValueError(f"{name} must have two dimensions, not {tuple(shape)}")
-    r, c = shape
-    if (cols is not None and c != cols) or (rows is not None and r != rows):
-        raise ValueError(f"{name} must be {'M' if rows is None else rows} x {'N' if cols is None else cols}, "
-                         f"not {tuple(shape)}")
-    at = t.get_device()
-    if at < 0:
-        raise ValueError(f"{name} must be a device tensor")
-    if device is not None and at != device:
-        raise ValueError("all tensors must be on one device")
-    ld, unit = t.stride()
-    if unit != 1 and c > 1 and r > 0:
-        raise ValueError(f"{name} needs unit column stride")
-    if ld < c:
-        if r > 1:
-            raise ValueError(f"{name} has overlapping rows")
-        ld = c
-    return r, c, ld, t.data_ptr()
-
-
-def _scales(t, name, n, device):
-    at = t.get_device()
-    if t.dtype != _t.float32 or t.shape != (n,) or at < 0:
-        raise ValueError(f"{name} must be a device vector of {n} float32 values")
-    if at != device:
-        raise ValueError("all tensors must be on one device")
-    if n > 1 and t.stride(0) != 1:
-        raise ValueError(f"{name} needs unit stride")
-    return t.data_ptr()
-
-
-def _out(out, M, N, like, device):
-    """(tensor, leading dimension, address) of the M x N output, made when it is not given."""
-    if out is None:
-        out = like.new_empty((M, N), dtype=_t.bfloat16)
-        return out, N, out.data_ptr()
-    _, _, ld, ptr = _rows(out, "out", _t.bfloat16, M, N, device)
-    return out, ld, ptr
+        L = lib()
+        try:
+            from . import _torch_ops as m
+        except ImportError as e:
+            raise RuntimeError(f"_torch_ops.so is not built or does not fit this PyTorch ({e}); run "
+                               "`python -m gemv_layers_amd.build` (there is no fallback path)") from e
+        m.bind(_check, *(ctypes.cast(getattr(L, f), ctypes.c_void_p).value for f in (
+            "gemm_i8_quantize", "gemm_i8", "gemm_i8_swiglu", "gemm_i8_bf16", "gemm_i8_swiglu_bf16", "gemm_bf16_bwd",
+            "gemm_bf16_swiglu_train", "gemm_bf16_swiglu_bwd")))
+        _ops = m
+    return _ops
 
 
 def i8_quantize(X, stream=None):
     """8-bit codes and scales of each row of a bf16 matrix: (Q int8 of X's shape, S float32).
     Q's rows are padded to 16 bytes in memory, as the matrix kernels want them. For an nn.Linear
     weight the rows are output channels; for activations they are tokens."""
-    torch = _torch()
-    R, K, ldx, x = _rows(X, "X", torch.bfloat16)
-    ldq = -(-K // 16) * 16
-    Q = torch.empty((R, ldq), dtype=torch.int8, device=X.device)[:, :K]
-    S = torch.empty((R,), dtype=torch.float32, device=X.device)
-    gemm_i8_quantize(R, K, x, ldx, Q.data_ptr(), ldq, S.data_ptr(), _stream(stream, X.get_device()))
-    return Q, S
-
-
-def _i8_weight(Wq, Sw, K, glu, device):
-    """(N, leading dimension, codes, scales) of an 8-bit weight; gated: 2N rows, gate then up."""
-    rows, _, ldw, w = _rows(Wq, "Wq", _t.int8, None, K, device)
-    if glu and rows % 2:
-        raise ValueError("Wq must have 2N rows, gate then up")
-    return rows // 2 if glu else rows, ldw, w, _scales(Sw, "Sw", rows, device)
-
-
-def _i8_codes(name, Aq, Sa, Wq, Sw, out, stream, glu):
-    torch = _torch()
-    M, K, lda, a = _rows(Aq, "Aq", torch.int8)
-    device = Aq.get_device()
-    N, ldw, w, sw = _i8_weight(Wq, Sw, K, glu, device)
-    sa = _scales(Sa, "Sa", M, device)
-    out, ldc, c = _out(out, M, N, Aq, device)
-    _check(name, getattr(lib(), name)(M, N, K, a, lda, sa, w, ldw, sw, c, ldc, _stream(stream, device)))
-    return out
+    return (_ops or _load_ops()).quantize(X, stream)
 
 
 def i8_matmul(Aq, Sa, Wq, Sw, out=None, stream=None):
     """(Aq @ Wq.T) * Sa[:, None] * Sw as bf16: int8 codes Aq (M x K) and Wq (N x K), float32 scales."""
-    return _i8_codes("gemm_i8", Aq, Sa, Wq, Sw, out, stream, False)
+    return (_ops or _load_ops()).i8(Aq, Sa, Wq, Sw, out, stream, False)
 
 
 def i8_swiglu_matmul(Aq, Sa, Wq, Sw, out=None, stream=None):
     """silu(g) * u of the 8-bit product with a 2N x K gate/up weight (gate rows first); M x N bf16."""
-    return _i8_codes("gemm_i8_swiglu", Aq, Sa, Wq, Sw, out, stream, True)
-
-
-def _i8_dynamic(name, A, Wq, Sw, out, work, stream, glu):
-    torch = _torch()
-    M, K, lda, a = _rows(A, "A", torch.bfloat16)
-    device = A.get_device()
-    N, ldw, w, sw = _i8_weight(Wq, Sw, K, glu, device)
-    out, ldc, c = _out(out, M, N, A, device)
-    if work is None:  # gemm_i8_work_bytes(M, K)
-        work = A.new_empty((M * (-(-K // 16) * 16 + 4),), dtype=torch.uint8)
-    elif work.dtype != torch.uint8 or not work.is_contiguous() or work.get_device() != device:
-        raise ValueError("work must be a contiguous uint8 tensor on the same device")
-    _check(name, getattr(lib(), name)(M, N, K, a, lda, w, ldw, sw, c, ldc, work.data_ptr(), work.numel(),
-                                      _stream(stream, device)))
-    return out
+    return (_ops or _load_ops()).i8(Aq, Sa, Wq, Sw, out, stream, True)
 
 
 def i8_linear(A, Wq, Sw, out=None, work=None, stream=None):
     """The 8-bit product of bf16 activations A (M x K), quantised row by row in the call, with an
     8-bit weight (N x K codes, N scales); M x N bf16. `work`: a uint8 tensor of
     gemm_i8_work_bytes(M, K) bytes to reuse, else one is allocated on the current stream."""
-    return _i8_dynamic("gemm_i8_bf16", A, Wq, Sw, out, work, stream, False)
+    return (_ops or _load_ops()).i8_dynamic(A, Wq, Sw, out, work, stream, False)
 
 
 def i8_swiglu_linear(A, Wq, Sw, out=None, work=None, stream=None):
     """silu(g) * u of the 8-bit product of bf16 activations with a 2N x K gate/up weight."""
-    return _i8_dynamic("gemm_i8_swiglu_bf16", A, Wq, Sw, out, work, stream, True)
-
-
-def _like(t, M, N):
-    """An uninitialised contiguous M x N tensor of t's type and device, and its address."""
-    # (t has that shape: copying its layout is the cheaper call)
-    out = _t.empty_like(t) if t.is_contiguous() else t.new_empty((M, N))
-    return out, out.data_ptr()
+    return (_ops or _load_ops()).i8_dynamic(A, Wq, Sw, out, work, stream, True)
 
 
 def matmul_backward(dC, A, B, need_dA=True, need_dB=True, stream=None):
     """(dA, dB) = (dC @ B.T, A.T @ dC), the gradients of matmul(A, B); None for one not needed."""
-    bf16 = _torch().bfloat16
-    M, K, lda, a = _rows(A, "A", bf16)
-    device = A.get_device()
-    _, N, ldb, b = _rows(B, "B", bf16, K, None, device)
-    _, _, lddc, d = _rows(dC, "dC", bf16, M, N, device)
-    dA, da = _like(A, M, K) if need_dA else (None, None)
-    dB, db = _like(B, K, N) if need_dB else (None, None)
-    _check("gemm_bf16_bwd", lib().gemm_bf16_bwd(M, N, K, d, lddc, a, lda, b, ldb, da, K, db, N,
-                                                _stream(stream, device)))
-    return dA, dB
+    return (_ops or _load_ops()).bwd(dC, A, B, need_dA, need_dB, stream)
 
 
 def swiglu_forward(A, B, stream=None):
     """(C, GU) of the gated block for training: GU = A @ B (M x 2N, gate then up), C = silu(g) * u."""
-    bf16 = _torch().bfloat16
-    M, K, lda, a = _rows(A, "A", bf16)
-    device = A.get_device()
-    _, N, ldb, b = _rows(B, "B", bf16, K, None, device)
-    if N % 2:
-        raise ValueError("B must be K x 2N for A of shape M x K")
-    N //= 2
-    C, GU = A.new_empty((M, N)), A.new_empty((M, 2 * N))
-    _check("gemm_bf16_swiglu_train",
-           lib().gemm_bf16_swiglu_train(M, N, K, a, lda, b, ldb, GU.data_ptr(), 2 * N, C.data_ptr(), N,
-                                        _stream(stream, device)))
-    return C, GU
+    return (_ops or _load_ops()).train(A, B, stream)
 
 
 def swiglu_backward(dC, GU, A, B, need_dA=True, need_dB=True, inplace=False, stream=None):
     """(dA, dB, dGU): the gradients of swiglu_forward's C. With `inplace`, dGU takes GU's memory."""
-    bf16 = _torch().bfloat16
-    M, K, lda, a = _rows(A, "A", bf16)
-    device = A.get_device()
-    _, N, ldb, b = _rows(B, "B", bf16, K, None, device)
-    if N % 2:
-        raise ValueError("B must be K x 2N for A of shape M x K")
-    N //= 2
-    _, _, lddc, d = _rows(dC, "dC", bf16, M, N, device)
-    _, _, ldgu, gu = _rows(GU, "GU", bf16, M, 2 * N, device)
-    dGU, dgu, lddgu = (GU, gu, ldgu) if inplace else (*_like(GU, M, 2 * N), 2 * N)
-    dA, da = _like(A, M, K) if need_dA else (None, None)
-    dB, db = _like(B, K, 2 * N) if need_dB else (None, None)
-    _check("gemm_bf16_swiglu_bwd",
-           lib().gemm_bf16_swiglu_bwd(M, N, K, d, lddc, gu, ldgu, a, lda, b, ldb, dgu, lddgu, da, K, db, 2 * N,
-                                      _stream(stream, device)))
-    return dA, dB, dGU
+    return (_ops or _load_ops()).swiglu_bwd(dC, GU, A, B, need_dA, need_dB, inplace, stream)

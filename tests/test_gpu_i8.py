@@ -390,3 +390,37 @@ def test_offsets_past_32_bits():
     assert torch.equal(C[-64:], C[:64]) and not C[64:-64].any()
     acc = Aq[:64].cpu().numpy().astype(np.float64) @ Wq.cpu().numpy().astype(np.float64).T
     assert np.array_equal(bits(C[:64]), expect(acc, Sa[:64].cpu().numpy(), Sw.cpu().numpy()))
+
+
+def test_helpers_keep_references_and_take_streams():
+    """The helpers neither leak nor lose a reference, and take a stream as a handle of either kind."""
+    import sys
+
+    A, (Wq, Sw) = act(3, 64, 1), g.i8_quantize(act(24, 64, 2))
+    out = torch.empty(3, 24, dtype=torch.bfloat16, device="cuda")
+    want = g.i8_linear(A, Wq, Sw)
+    counts = [sys.getrefcount(x) for x in (A, Wq, Sw, out, None)]
+    before = torch.cuda.memory_allocated()
+    for _ in range(200):
+        g.i8_linear(A, Wq, Sw)
+        y = g.i8_linear(A, Wq, Sw, out=out)
+        assert y is out
+        with pytest.raises(ValueError):
+            g.i8_linear(A, Wq, Sw[:5])
+        with pytest.raises(g.GemmError):
+            g.i8_linear(A, Wq, Sw, work=torch.empty(16, dtype=torch.uint8, device="cuda"))
+    del y
+    after = [sys.getrefcount(x) for x in (A, Wq, Sw, out, None)]
+    assert after[:4] == counts[:4] and abs(after[4] - counts[4]) < 50
+    torch.cuda.synchronize()
+    assert torch.cuda.memory_allocated() == before
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for handle in (side.cuda_stream, ctypes.c_void_p(side.cuda_stream)):
+        out.fill_(float("nan"))
+        side.wait_stream(torch.cuda.current_stream())
+        g.i8_linear(A, Wq, Sw, out=out, stream=handle)
+        side.synchronize()
+        assert torch.equal(out.view(torch.int16), want.view(torch.int16))
+    with pytest.raises(AttributeError):
+        g.i8_linear(A, Wq, Sw, stream="s")
