@@ -3,11 +3,13 @@
 // No arithmetic, and no tensor is kept. It is C++ because a small product takes the GPU 5 us: the
 // same steps in Python take the host 5 us on top of the launch, these 1.5.
 //
-// The C ABI's functions come in by address (bind), so that this module links to PyTorch alone.
+// The C ABI's functions come in by address (bind), so that this module links to PyTorch alone. A call
+// runs with its tensors' device as the current one, as the library asks.
 
 #include <Python.h>
 
 #include <ATen/ops/empty.h>
+#include <c10/core/DeviceGuard.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -167,6 +169,7 @@ at::Tensor output(PyObject* out, const at::Tensor& like, int64_t M, int64_t N, i
 PyObject* quantize(PyObject* const* a) {
     const at::Tensor& X = tensor(a[0], "X");
     const Rows x = rows_of(X, "X", at::kBFloat16);
+    const c10::DeviceGuard guard(X.device());
     const int64_t ldq = (x.cols + 15) / 16 * 16;
     at::Tensor Q = make(X, at::kChar, x.rows, ldq);
     at::Tensor S = at::empty({x.rows}, X.options().dtype(at::kFloat).requires_grad(false).memory_format(std::nullopt));
@@ -202,6 +205,7 @@ PyObject* i8(PyObject* const* a) {
     const int device = A.get_device();
     const Weight w = weight_of(a[2], a[3], q.cols, glu, device);
     const float* sa = scales_of(tensor(a[1], "Sa"), "Sa", q.rows, device);
+    const c10::DeviceGuard guard(A.device());
     Rows c;
     at::Tensor C = output(a[4], A, q.rows, w.N, device, &c);
     const gemm_stream_t s = stream_of(a[5], device);
@@ -218,6 +222,7 @@ PyObject* i8_dynamic(PyObject* const* a) {
     const Rows x = rows_of(A, "A", at::kBFloat16);
     const int device = A.get_device();
     const Weight w = weight_of(a[1], a[2], x.cols, glu, device);
+    const c10::DeviceGuard guard(A.device());
     Rows c;
     at::Tensor C = output(a[3], A, x.rows, w.N, device, &c);
     at::Tensor work;
@@ -259,6 +264,7 @@ PyObject* bwd(PyObject* const* a) {
     const at::Tensor& A = tensor(a[1], "A");
     Operands o(A, tensor(a[2], "B"));
     const Rows d = rows_of(tensor(a[0], "dC"), "dC", at::kBFloat16, o.a.rows, o.b.cols, o.device);
+    const c10::DeviceGuard guard(A.device());
     o.gradients(A, truth(a[3]), truth(a[4]));
     const gemm_stream_t s = stream_of(a[5], o.device);
     check("gemm_bf16_bwd", unlocked([&] {
@@ -275,6 +281,7 @@ PyObject* train(PyObject* const* a) {
     const Operands o(A, tensor(a[1], "B"));
     if (o.b.cols % 2) fail(PyExc_ValueError, "B must be K x 2N, gate then up");
     const int64_t N = o.b.cols / 2;
+    const c10::DeviceGuard guard(A.device());
     at::Tensor C = make(A, at::kBFloat16, o.a.rows, N), GU = make(A, at::kBFloat16, o.a.rows, 2 * N);
     const gemm_stream_t s = stream_of(a[2], o.device);
     check("gemm_bf16_swiglu_train", unlocked([&] {
@@ -292,6 +299,7 @@ PyObject* swiglu_bwd(PyObject* const* a) {
     const int64_t N = o.b.cols / 2;
     const Rows d = rows_of(tensor(a[0], "dC"), "dC", at::kBFloat16, o.a.rows, N, o.device);
     const Rows gu = rows_of(GU, "GU", at::kBFloat16, o.a.rows, 2 * N, o.device);
+    const c10::DeviceGuard guard(A.device());
     o.gradients(A, truth(a[4]), truth(a[5]));
     const bool inplace = truth(a[6]);
     at::Tensor dGU = inplace ? GU : make(A, at::kBFloat16, o.a.rows, 2 * N);
