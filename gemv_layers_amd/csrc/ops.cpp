@@ -90,7 +90,8 @@ int run_i8_decode(bool glu, const OpArgs& a, const glk::Plan& p, bool fused, hip
     }
     const glk::I8DecodeArgs t{fused ? nullptr : static_cast<const int8_t*>(a.A),
                               fused ? static_cast<const uint16_t*>(a.A) : nullptr,
-                              static_cast<const int8_t*>(a.B), a.C, a.sa, a.sb, (int)a.M, (int)a.N, (int)a.K, (int)a.lda, (int)a.ldb, (int)a.ldc,
+                              static_cast<const int8_t*>(a.B), a.C, a.sa, a.sb, (int)a.M, (int)a.N, (int)a.K,
+                              (int)a.lda, (int)a.ldb, (int)a.ldc,
                               !misaligned(a.C, 8) && a.ldc % 4 == 0 && a.N % 4 == 0, p.splits,
                               reinterpret_cast<int32_t*>(w.ws), w.counters};
     if (glk::launch_i8_decode(glu, p.mtiles, p.strip / 16, p.threads / 64, t, (int)p.grid, stream) != hipSuccess)
@@ -115,6 +116,8 @@ int run_op(int mode, bool glu, const OpArgs& a, hipStream_t stream) {
         e = glk::launch_zero_c(a.C, a.M, a.N, a.ldc, stream);
         if (e == hipSuccess && mode == glk::kOpTrain) e = glk::launch_zero_c(a.GU, a.M, 2 * a.N, a.ldgu, stream);
     } else if (!matrix_ok(mode, glu, a)) {
+        // 64 x 64 tiles of 256 threads, 32-bit grids
+        if ((a.M - 1) / 64 + 1 > kMaxRows / ((a.N - 1) / 64 + 1)) return GEMM_ERR_UNSUPPORTED;
         p = glk::make_plan(a.M, a.N, a.K, *dev, false, 2, glu);
         e = glk::launch_op_generic(mode, glu, a, stream);
     } else {

@@ -106,7 +106,7 @@ __global__ void __launch_bounds__(256) op_generic_kernel(OpArgs p, int64_t tiles
 }
 
 hipError_t launch_op_generic(int mode, bool glu, const OpArgs& a, hipStream_t s) {
-    const int64_t tn = (a.N + 63) / 64, tm = (a.M + 63) / 64;
+    const int64_t tn = (a.N - 1) / 64 + 1, tm = (a.M - 1) / 64 + 1;
     if (tm > 0xFFFFFF / tn) return hipErrorInvalidValue;
     const unsigned grid = (unsigned)(tm * tn);
     if (mode == kOpI8 && glu)

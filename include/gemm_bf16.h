@@ -277,12 +277,12 @@ int gemm_i8_quantize(int64_t R, int64_t K, const void *X, int64_t ldx, void *Q, 
  * inputs). Any code from -128 to 127 is taken. Aq and Wq with 16-byte aligned pointers and
  * leading dimensions (what gemm_i8_quantize writes with ldq a multiple of 16) run the matrix
  * kernels for any M, N and K; other operands run a general kernel with the same result, bit for
- * bit. Bytes between K and the leading dimension may hold anything.
+ * bit, tens of times slower. Bytes between K and the leading dimension may hold anything.
  * M == 0 or N == 0: nothing. K == 0: C = 0. GEMM_ERR_INVALID_ARG for negative sizes, a leading
  * dimension that is too small, a null pointer with a non-empty extent, a C that is not 2-byte or
  * a scale that is not 4-byte aligned; GEMM_ERR_UNSUPPORTED for K > 131071, beyond which 32-bit
- * sums could overflow. Deterministic, enqueued without synchronising, and using the stream's
- * workspace region like gemm_bf16.
+ * sums could overflow, and for a general kernel's C of 2^24 or more 64 x 64 tiles. Deterministic,
+ * enqueued without synchronising, and using the stream's workspace region like gemm_bf16.
  */
 int gemm_i8(int64_t M, int64_t N, int64_t K, const void *Aq, int64_t ldaq, const float *Sa,
             const void *Wq, int64_t ldwq, const float *Sw, void *C, int64_t ldc,
@@ -311,7 +311,8 @@ int gemm_i8_work_bytes(int64_t M, int64_t K, int64_t *bytes);
  * gemm_i8: the 8-bit product with dynamic activation scales in one call, the same bits as the two.
  * `work` is device memory of at least gemm_i8_work_bytes(M, K) bytes, 16-byte aligned, that the
  * caller owns and may reuse once the call's work on the stream is done; `work_bytes` is its size
- * (GEMM_ERR_INVALID_ARG when it is too small or misaligned).
+ * (GEMM_ERR_INVALID_ARG when it is too small or misaligned). Other errors as gemm_i8, and
+ * GEMM_ERR_UNSUPPORTED for M >= 2^24.
  */
 int gemm_i8_bf16(int64_t M, int64_t N, int64_t K, const void *A, int64_t lda, const void *Wq,
                  int64_t ldwq, const float *Sw, void *C, int64_t ldc, void *work,
@@ -326,9 +327,10 @@ int gemm_i8_swiglu_bf16(int64_t M, int64_t N, int64_t K, const void *A, int64_t 
  * Training: the backward pass of gemm_bf16, and the gated block's forward and backward pass.
  * bf16 operands row-major as in gemm_bf16, float32 accumulation, each output rounded once to bf16
  * (round to nearest even). Operands whose pointers are not 16-byte aligned, or whose widths or
- * leading dimensions are not multiples of 8, run a general kernel with the same contract; the
- * number of tokens M is free. Deterministic (sums in a fixed order, no atomics on data), enqueued
- * on `stream` without synchronising, using the stream's workspace region like gemm_bf16.
+ * leading dimensions are not multiples of 8, run a general kernel with the same contract, tens of
+ * times slower (GEMM_ERR_UNSUPPORTED for an output of 2^24 or more 64 x 64 tiles there); the number
+ * of tokens M is free. Deterministic (sums in a fixed order, no atomics on data), enqueued on
+ * `stream` without synchronising, using the stream's workspace region like gemm_bf16.
  * ------------------------------------------------------------------------------------------ */
 
 /*

@@ -373,6 +373,15 @@ def test_refusals_on_the_device():
         g.i8_linear(A, Wq, Sw, work=torch.empty(16, dtype=torch.uint8, device="cuda"))
 
 
+@pytest.mark.parametrize("M,N", [(1 << 24, 1 << 12), (1 << 18, 1 << 18), (1 << 62, 1 << 61)])
+def test_general_outputs_beyond_a_grid_are_refused(M, N):
+    """Unaligned operands whose output has 2^24 or more 64 x 64 tiles: refused on the host, before a launch."""
+    p, q = ctypes.c_void_p(66), ctypes.c_void_p(64)
+    lib, s = g.lib(), g.current_stream_handle()
+    assert lib.gemm_i8(M, N, 8, p, 9, q, p, 9, q, q, N, s) == g.GEMM_ERR_UNSUPPORTED
+    assert lib.gemm_bf16_bwd(8, N, M, p, N + 1, p, M + 1, None, N, None, M, p, N + 1, s) == g.GEMM_ERR_UNSUPPORTED
+
+
 def test_offsets_past_32_bits():
     """Activations, codes and outputs of more than 2^32 bytes: the last rows are the first ones."""
     M, N, K = 1_060_003, 2056, 4104
