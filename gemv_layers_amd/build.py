@@ -44,7 +44,8 @@ def _build_torch_ops() -> str:
     from torch.utils.cpp_extension import include_paths, library_paths
 
     tmp = TORCH_OUT + ".tmp%d" % os.getpid()
-    cmd = [HIPCC, "-no-hip-rt", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", f"-I{os.path.join(ROOT, 'include')}", f"-I{sysconfig.get_paths()['include']}",
+    cmd = [HIPCC, "-no-hip-rt", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+           f"-I{os.path.join(ROOT, 'include')}", f"-I{sysconfig.get_paths()['include']}",
            *(f"-isystem{p}" for p in include_paths()), os.path.join(CSRC, "torch_ops.cpp"), "-o", tmp,
            *(f"-L{p}" for p in library_paths()), "-ltorch_python", "-ltorch_cpu", "-lc10_hip", "-lc10"]
     r = subprocess.run(cmd, capture_output=True, text=True)

@@ -16,6 +16,10 @@
 // more through the L1 for each workgroup, against a launch and a round trip to memory (us, fused
 // against two launches: 11008 x 4096 11.3 and 13.1, 4096 x 11008 12.3 and 13.7, gated 11008 x 4096 18.3 and
 // 21.1, 1000 x 1000 4.8 and 7.1; with two rows it lost, 13.6 and 13.2, 15.1 and 13.9).
+//
+// Bound by the weight's bytes from HBM: one row through 11008 x 4096 codes, 45 MB, takes 10.2 us a call,
+// 4.4 TB/s, where a kernel that only reads as many takes 9.3. Non-temporal weight loads cost 1.7 us of
+// it, eight tiles a workgroup at 64 rows 25.7 us against 18.5.
 
 #include "codes.h"
 #include "common.h"

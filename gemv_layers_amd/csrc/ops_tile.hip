@@ -4,19 +4,22 @@
 // v_mfma_i32_16x16x64_i8 or v_mfma_f32_16x16x32_bf16 for each 16 x 16 output block (16 bytes of each
 // operand per lane, the same cycles, the same accumulator layout). An operand comes in one of two
 // forms, and every product is a pair of them:
-//   contiguous: the summed index is contiguous in memory (codes; dC and B of dA = dC B^T). A stage of
-//     one k-step is R rows of 64 bytes; 16-byte chunk c of row r is stored at c ^ ((r >> 2) & 3), so
-//     the 16 rows that one cycle of a ds_read_b128 serves cover all 64 banks.
-//   strided: the summed index is the row (A and dC of dB = A^T dC; B of the forward). A stage is 32
-//     rows of R elements, and ds_read_b64_tr_b16 transposes 4 x 16 blocks on the way to registers; the
-//     32-byte column groups of row k are stored at group ^ s(k), s(k) = (k & 3) | ((k >> 1) & 4).
-// Both take 64 R bytes a stage. Stages are copied HBM -> LDS without registers, into rings of 5 slots
-// for each operand: 160 KB for the 256 x 256 tile, 80 KB (two workgroups a CU) for 128 x 128.
+//   contiguous: the summed index is contiguous in memory (codes; dC and B of dA = dC B^T). A slot of
+//     its LDS ring holds half of the tile's rows, 128 bytes (two k-steps) of each, so that copies
+//     read whole lines: with one k-step of all rows, 64-byte rows, every line crossed the L1 twice
+//     (8-bit 4096 x 4096 x 11008: 152 us against 124). 16-byte chunk c of row r is stored at c ^
+//     ((r >> 1) & 7): the 16 rows that one cycle of a ds_read_b128 serves cover all 64 banks.
+//   strided: the summed index is the row (A and dC of dB = A^T dC; B of the forward). A slot holds one
+//     k-step, 32 rows of R elements, and ds_read_b64_tr_b16 transposes 4 x 16 blocks on the way to
+//     registers; the 32-byte column groups of row k are stored at group ^ s(k), s(k) = (k & 3) | ((k >>
+//     1) & 4).
+// Both take 64 R bytes a slot. Slots are filled HBM -> LDS without registers, in rings of 5 for each
+// operand: 160 KB for the 256 x 256 tile, 80 KB (two workgroups a CU) for 128 x 128, 40 KB for 64 x 64.
 //
-// Schedules. 256 x 256 (op_pp): two groups of four waves, one of each group on every SIMD; in turn
-// one group reads its operands and issues copies while the other runs 32 MFMAs back to back, and they
-// swap at each barrier. 128 x 128 (op_small): four waves in step, operands double-buffered in
-// registers, K split over idle CUs with partial sums in a workspace that the last arriver adds in
+// Schedules. 256 x 256 (op_pp_kernel): two groups of four waves, one of each group on every SIMD; in
+// turn one group reads its operands and issues copies while the other runs 32 MFMAs back to back, and
+// they swap at each barrier. 128 x 128 and 64 x 64 (op_small): four waves in step, operands double-buffered
+// in registers, K split over idle CUs with partial sums in a workspace that the last arriver adds in
 // order (the same bits on every run; integer sums are exact in any order).
 //
 // Epilogues round once to bf16, staged through LDS so that each row segment is written by one
@@ -24,6 +27,19 @@
 // gated form silu(g) u. Training forward: g and u, then silu(g) u from their float32 values.
 // Codes past K in the last 16-byte chunk of a row are whatever the caller's padding holds: they are
 // cleared in the A operand, which is enough, as 0 times any code is 0.
+//
+// Measured, 256 x 256 tiles, kernel medians: 8-bit 4096 x 4096 x 11008 136 us, 2.7 POP/s; dA = dC B^T
+// 4096 x 4096 x 22016 481 us, 1.54 PFLOP/s; of dB = A^T dC 4096 x 22016 x 4096 the 1280 tiles of its
+// full waves 560 us, 1.23, and as many of the forward 552 us. What bounds them, from timing-only
+// copies that leave one part out (us, in that order, the whole 124, 470, 556, and 666 for the forward's
+// 1376 tiles): without the copies 105, 362, 443, 478; without the operand reads 113, 469, 451, 641;
+// without the MFMAs 84, 430, 360, 474; the operand reads alone 59, 187, 280, 273. dA gains from its
+// copies alone (moving 32 KB a k-step from the L2 into each CU); in the others copies and MFMAs weigh
+// alike, and in dB the reads too: a transposing read of a k-step's operands takes 0.44 us, a plain one 0.27.
+// Where the copied lines come from does not matter (all tiles on the same panels: dA 459, dB 552), nor
+// do wave priorities, copies issued before the reads, or tile rows walked in groups of 8 for 4 (all
+// within 1%). Four waves of 128 x 128, which read a third less from LDS, gained nothing (dB 597-608
+// against 599).
 
 #include <type_traits>
 
@@ -46,7 +62,7 @@ struct OpTile {
     static constexpr int ES = I8 ? 1 : 2;            // bytes per element
     static constexpr int KE = 64 / ES;               // elements per k-step
     static constexpr int SLOTS = 5;
-    static constexpr int NW = WM * WN, NT = NW * 64;
+    static constexpr int NW = WM * WN;
     static constexpr int WTM = BM / WM, WTN = BN / WN;
     static constexpr int TM = WTM / 16, TN = WTN / 16;
     static constexpr int A_BYTES = BM * 64, B_BYTES = BN * 64;  // one slot of each ring
@@ -433,12 +449,16 @@ op_pp_kernel(OpTileArgs p) {
     op_epilogue<T, MODE, GLU>(p, lds, at, wave, wm, wn, lane, acc);
 }
 
-// ---- 128 x 128, K split over idle CUs -------------------------------------------------------------
+// ---- 128 x 128 and 64 x 64, K split over idle CUs -------------------------------------------------------------
 // Iteration i reads the operands of step i + 1 while the MFMAs of step i run. At its barrier the reads
 // of step i, made in iteration i - 1, are over in every wave; after it, a strided operand's slot of
 // step i takes step i + 5, and a contiguous one's slot of unit i - 1 (steps i - 1 and i for odd i, i - 2
-// and i - 1 for even i) takes unit i + 4. Its barrier also needs step i + 1's copies landed, which is
-// what op_wait says of the step that iteration i - 1 would be in the other schedule's count.
+// and i - 1 for even i) takes unit i + 4. Before the barrier the wave waits for its copies of step i + 1.
+// What it has issued by then, up to i + 3 or i + 4, is what the other schedule's step i has, so op_wait
+// counts the same.
+//
+// With one or two tiles a CU what bounds it is the latency of each k-step, not a rate: 509 x 2501 x 1003
+// codes 8.6 us, the gated forward 300 x 520 x 328 6.2 us (64 x 64 tiles).
 template <int BT, int MODE, bool GLU>
 __device__ __forceinline__ void op_small(const OpTileArgs& p, int block, char* lds) {
     using T = OpTile<BT, BT, 2, 2, MODE>;

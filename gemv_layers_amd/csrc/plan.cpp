@@ -431,7 +431,8 @@ Plan make_op_plan(int64_t M, int64_t N, int64_t K, const DeviceInfo& dev, bool g
     p.slots = 4 * (int64_t)dev.cus;
     int64_t root = 1;
     while ((root + 1) * (root + 1) * 6 <= kt) ++root;
-    int64_t s = std::min<int64_t>({root, std::max<int64_t>(kt / 28, dev.cus / p.tiles), 16, 3 * (int64_t)dev.cus / p.tiles});
+    int64_t s = std::min<int64_t>(
+        {root, std::max<int64_t>(kt / 28, dev.cus / p.tiles), 16, 3 * (int64_t)dev.cus / p.tiles});
     if (p.tiles * s > dev.cus && p.tiles * s <= most) s = dev.cus / p.tiles;
     s = std::max<int64_t>(s, 1);
     while (s > 1 && p.tiles * s * 4096 > dev.ws_floats / 2) --s;  // (two products may share a launch)
@@ -465,9 +466,9 @@ bool i8_decode_fits(int64_t M, int64_t K, const Plan& p) {
 // above 16 rows one, two or four as the weight outgrows the 2 us that summing K pieces costs (M =
 // 64: 1000 x 2000 5.3 us with one and 6.3 with two; 2048 x 8192 12.1 with two and 13.4 with four;
 // 4096 x 11008 17.9 with four and 20.7 with two). The gated form takes gate and up tiles in pairs, one
-// pair up to 16 rows and two for a large weight beyond (M = 64, 11008 x 4096: 37.6 us against 40.1). K is split as far as the groups leave CUs idle and 32 k-steps remain to
-// each piece (4 x 2048 x 2048 codes: 4.0 us whole, 4.9 in two pieces; 1 x 1000 x 11008: 6.7 in four,
-// 7.0 in three).
+// pair up to 16 rows and two for a large weight beyond (M = 64, 11008 x 4096: 37.6 us against 40.1). K is
+// split as far as the groups leave CUs idle and 32 k-steps remain to each piece (4 x 2048 x 2048 codes:
+// 4.0 us whole, 4.9 in two pieces; 1 x 1000 x 11008: 6.7 in four, 7.0 in three).
 Plan make_i8_decode_plan(int64_t M, int64_t N, int64_t K, const DeviceInfo& dev, bool glu) {
     Plan p;
     p.kernel = kKernI8Decode;
