@@ -366,7 +366,8 @@ def swiglu_matmul(A, B, out=None, stream=None):
 # ---- 8-bit products and training: PyTorch marshalling ----------------------------------------
 #
 # A small product takes the GPU a few microseconds, so the tensors are checked, and the outputs made,
-# in a C++ module (_torch_ops). The functions below name its arguments.
+# in a C++ module (_torch_ops). The functions below name its arguments. With `stream`, a handle, a call
+# runs as under torch.cuda.stream of it: its outputs belong to that stream.
 
 _ops = None
 
@@ -410,7 +411,7 @@ def i8_swiglu_matmul(Aq, Sa, Wq, Sw, out=None, stream=None):
 def i8_linear(A, Wq, Sw, out=None, work=None, stream=None):
     """The 8-bit product of bf16 activations A (M x K), quantised row by row in the call, with an
     8-bit weight (N x K codes, N scales); M x N bf16. `work`: a uint8 tensor of
-    gemm_i8_work_bytes(M, K) bytes to reuse, else one is allocated on the current stream."""
+    gemm_i8_work_bytes(M, K) bytes to reuse, else one is allocated."""
     return (_ops or _load_ops()).i8_dynamic(A, Wq, Sw, out, work, stream, False)
 
 

@@ -91,9 +91,8 @@ at::Tensor make(const at::Tensor& like, at::ScalarType type, int64_t rows, int64
     return at::empty({rows, cols}, like.options().dtype(type).requires_grad(false).memory_format(std::nullopt));
 }
 
-// None: the device's current stream; else a handle as an integer or a ctypes pointer
-gemm_stream_t stream_of(PyObject* o, int device) {
-    if (o == Py_None) return c10::hip::getCurrentHIPStream((c10::DeviceIndex)device).stream();
+// a handle as an integer or a ctypes pointer
+gemm_stream_t handle_of(PyObject* o) {
     if (PyLong_Check(o)) {
         void* p = PyLong_AsVoidPtr(o);
         if (PyErr_Occurred()) throw Failed();
@@ -106,6 +105,33 @@ gemm_stream_t stream_of(PyObject* o, int device) {
     if (PyErr_Occurred()) throw Failed();
     return static_cast<gemm_stream_t>(p);
 }
+
+// Where a call runs: on the tensors' device and, None, its current stream, else the given one, which is
+// the current one meanwhile. So outputs and work buffers come from the memory of the stream that uses
+// them: memory of another stream could still be in use there, and be given out again when a work buffer
+// is dropped at the end of the call.
+class Place {
+    const c10::DeviceGuard guard;
+    const c10::hip::HIPStream before;
+    bool moved = false;
+
+public:
+    gemm_stream_t stream;
+    Place(PyObject* o, const at::Tensor& t)
+        : guard(t.device()), before(c10::hip::getCurrentHIPStream(t.get_device())), stream(before.stream()) {
+        if (o == Py_None) return;
+        const gemm_stream_t s = handle_of(o);
+        if (s == stream) return;
+        c10::hip::setCurrentHIPStream(c10::hip::getStreamFromExternal(static_cast<hipStream_t>(s), t.get_device()));
+        stream = s;
+        moved = true;
+    }
+    ~Place() {
+        if (moved) c10::hip::setCurrentHIPStream(before);
+    }
+    Place(const Place&) = delete;
+    Place& operator=(const Place&) = delete;
+};
 
 void check(const char* name, int status) {
     if (status == GEMM_OK) return;
@@ -169,13 +195,13 @@ at::Tensor output(PyObject* out, const at::Tensor& like, int64_t M, int64_t N, i
 PyObject* quantize(PyObject* const* a) {
     const at::Tensor& X = tensor(a[0], "X");
     const Rows x = rows_of(X, "X", at::kBFloat16);
-    const c10::DeviceGuard guard(X.device());
+    const Place at(a[1], X);
     const int64_t ldq = (x.cols + 15) / 16 * 16;
     at::Tensor Q = make(X, at::kChar, x.rows, ldq);
     at::Tensor S = at::empty({x.rows}, X.options().dtype(at::kFloat).requires_grad(false).memory_format(std::nullopt));
-    const gemm_stream_t s = stream_of(a[1], X.get_device());
     check("gemm_i8_quantize", unlocked([&] {
-              return abi.quantize(x.rows, x.cols, x.p, x.ld, Q.data_ptr(), ldq, static_cast<float*>(S.data_ptr()), s);
+              return abi.quantize(x.rows, x.cols, x.p, x.ld, Q.data_ptr(), ldq, static_cast<float*>(S.data_ptr()),
+                                  at.stream);
           }));
     if (ldq != x.cols) Q = Q.narrow(1, 0, x.cols);
     PyObject* q = wrap(std::move(Q));
@@ -205,12 +231,12 @@ PyObject* i8(PyObject* const* a) {
     const int device = A.get_device();
     const Weight w = weight_of(a[2], a[3], q.cols, glu, device);
     const float* sa = scales_of(tensor(a[1], "Sa"), "Sa", q.rows, device);
-    const c10::DeviceGuard guard(A.device());
+    const Place at(a[5], A);
     Rows c;
     at::Tensor C = output(a[4], A, q.rows, w.N, device, &c);
-    const gemm_stream_t s = stream_of(a[5], device);
     check(glu ? "gemm_i8_swiglu" : "gemm_i8", unlocked([&] {
-              return (glu ? abi.i8_swiglu : abi.i8)(q.rows, w.N, q.cols, q.p, q.ld, sa, w.w.p, w.w.ld, w.scales, c.p, c.ld, s);
+              return (glu ? abi.i8_swiglu : abi.i8)(q.rows, w.N, q.cols, q.p, q.ld, sa, w.w.p, w.w.ld, w.scales,
+                                                c.p, c.ld, at.stream);
           }));
     return wrap(std::move(C));
 }
@@ -222,7 +248,7 @@ PyObject* i8_dynamic(PyObject* const* a) {
     const Rows x = rows_of(A, "A", at::kBFloat16);
     const int device = A.get_device();
     const Weight w = weight_of(a[1], a[2], x.cols, glu, device);
-    const c10::DeviceGuard guard(A.device());
+    const Place at(a[5], A);
     Rows c;
     at::Tensor C = output(a[3], A, x.rows, w.N, device, &c);
     at::Tensor work;
@@ -234,10 +260,9 @@ PyObject* i8_dynamic(PyObject* const* a) {
         if (work.scalar_type() != at::kByte || !work.is_contiguous() || !work.is_cuda() || work.get_device() != device)
             fail(PyExc_ValueError, "work must be a contiguous uint8 tensor on the same device");
     }
-    const gemm_stream_t s = stream_of(a[5], device);
     check(glu ? "gemm_i8_swiglu_bf16" : "gemm_i8_bf16", unlocked([&] {
               return (glu ? abi.i8_swiglu_bf16 : abi.i8_bf16)(x.rows, w.N, x.cols, x.p, x.ld, w.w.p, w.w.ld, w.scales,
-                                                              c.p, c.ld, work.data_ptr(), work.numel(), s);
+                                                              c.p, c.ld, work.data_ptr(), work.numel(), at.stream);
           }));
     return wrap(std::move(C));
 }
@@ -264,12 +289,11 @@ PyObject* bwd(PyObject* const* a) {
     const at::Tensor& A = tensor(a[1], "A");
     Operands o(A, tensor(a[2], "B"));
     const Rows d = rows_of(tensor(a[0], "dC"), "dC", at::kBFloat16, o.a.rows, o.b.cols, o.device);
-    const c10::DeviceGuard guard(A.device());
+    const Place at(a[5], A);
     o.gradients(A, truth(a[3]), truth(a[4]));
-    const gemm_stream_t s = stream_of(a[5], o.device);
     check("gemm_bf16_bwd", unlocked([&] {
               return abi.bwd(o.a.rows, o.b.cols, o.a.cols, d.p, d.ld, o.a.p, o.a.ld, o.b.p, o.b.ld, o.da, o.a.cols, o.db,
-                             o.b.cols, s);
+                             o.b.cols, at.stream);
           }));
     PyObject* ga = o.grad_a();
     return pack({ga, o.grad_b()});
@@ -281,11 +305,11 @@ PyObject* train(PyObject* const* a) {
     const Operands o(A, tensor(a[1], "B"));
     if (o.b.cols % 2) fail(PyExc_ValueError, "B must be K x 2N, gate then up");
     const int64_t N = o.b.cols / 2;
-    const c10::DeviceGuard guard(A.device());
+    const Place at(a[2], A);
     at::Tensor C = make(A, at::kBFloat16, o.a.rows, N), GU = make(A, at::kBFloat16, o.a.rows, 2 * N);
-    const gemm_stream_t s = stream_of(a[2], o.device);
     check("gemm_bf16_swiglu_train", unlocked([&] {
-              return abi.train(o.a.rows, N, o.a.cols, o.a.p, o.a.ld, o.b.p, o.b.ld, GU.data_ptr(), 2 * N, C.data_ptr(), N, s);
+              return abi.train(o.a.rows, N, o.a.cols, o.a.p, o.a.ld, o.b.p, o.b.ld, GU.data_ptr(), 2 * N,
+                               C.data_ptr(), N, at.stream);
           }));
     PyObject* c = wrap(std::move(C));
     return pack({c, wrap(std::move(GU))});
@@ -299,14 +323,13 @@ PyObject* swiglu_bwd(PyObject* const* a) {
     const int64_t N = o.b.cols / 2;
     const Rows d = rows_of(tensor(a[0], "dC"), "dC", at::kBFloat16, o.a.rows, N, o.device);
     const Rows gu = rows_of(GU, "GU", at::kBFloat16, o.a.rows, 2 * N, o.device);
-    const c10::DeviceGuard guard(A.device());
+    const Place at(a[7], A);
     o.gradients(A, truth(a[4]), truth(a[5]));
     const bool inplace = truth(a[6]);
     at::Tensor dGU = inplace ? GU : make(A, at::kBFloat16, o.a.rows, 2 * N);
-    const gemm_stream_t s = stream_of(a[7], o.device);
     check("gemm_bf16_swiglu_bwd", unlocked([&] {
               return abi.swiglu_bwd(o.a.rows, N, o.a.cols, d.p, d.ld, gu.p, gu.ld, o.a.p, o.a.ld, o.b.p, o.b.ld,
-                                    dGU.data_ptr(), inplace ? gu.ld : 2 * N, o.da, o.a.cols, o.db, o.b.cols, s);
+                                    dGU.data_ptr(), inplace ? gu.ld : 2 * N, o.da, o.a.cols, o.db, o.b.cols, at.stream);
           }));
     PyObject* ga = o.grad_a();
     PyObject* gb = o.grad_b();

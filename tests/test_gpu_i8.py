@@ -401,6 +401,45 @@ def test_offsets_past_32_bits():
     assert np.array_equal(bits(C[:64]), expect(acc, Sa[:64].cpu().numpy(), Sw.cpu().numpy()))
 
 
+def test_memory_belongs_to_the_stream_given():
+    """With a stream's handle, new outputs and the work buffer come from that stream's memory: the work
+    buffer is dropped when the call returns, and another stream's memory could be given out again then."""
+    A, (Wq, Sw) = act(2048, 4096, 1), g.i8_quantize(act(24, 4096, 2))
+    want = g.i8_linear(A, Wq, Sw)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+
+    def segments():
+        return [s for s in torch.cuda.memory_snapshot() if s["stream"] == side.cuda_stream]
+
+    def owns(t):
+        return any(s["address"] <= t.data_ptr() < s["address"] + s["total_size"] for s in segments())
+
+    assert not segments()
+    here = torch.cuda.current_stream()
+    out = torch.empty_like(want)
+    C = g.i8_linear(A, Wq, Sw, out=out, stream=side.cuda_stream)
+    assert C is out or C.data_ptr() == out.data_ptr()
+    assert sum(s["total_size"] for s in segments()) >= g.gemm_i8_work_bytes(2048, 4096)
+    D = g.i8_linear(A, Wq, Sw, stream=ctypes.c_void_p(side.cuda_stream))
+    Aq, Sa = g.i8_quantize(A, stream=side.cuda_stream)
+    E = g.i8_matmul(Aq, Sa, Wq, Sw, stream=side.cuda_stream)
+    F, GU = g.swiglu_forward(A, A.view(4096, 2048), stream=side.cuda_stream)
+    dA, dB, dGU = g.swiglu_backward(F, GU, A, A.view(4096, 2048), stream=side.cuda_stream)
+    lA, lB = g.matmul_backward(C, A, A.view(4096, 2048)[:, :24], stream=side.cuda_stream)
+    for t in (D, Aq, Sa, E, F, GU, dA, dB, dGU, lA, lB):
+        assert owns(t)
+    assert not owns(out) and torch.cuda.current_stream() == here
+    assert not owns(g.i8_linear(A, Wq, Sw))  # and the current stream is what it was
+    with pytest.raises(ValueError):
+        g.i8_linear(A, Wq, Sw, out=out[:, :23], stream=side.cuda_stream)
+    assert torch.cuda.current_stream() == here
+    torch.cuda.synchronize()
+    for t in (C, D, E):
+        assert torch.equal(t.view(torch.int16), want.view(torch.int16))
+
+
 def test_helpers_keep_references_and_take_streams():
     """The helpers neither leak nor lose a reference, and take a stream as a handle of either kind."""
     import sys
