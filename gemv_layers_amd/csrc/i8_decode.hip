@@ -49,7 +49,7 @@ __device__ __forceinline__ float quantise_row(const I8DecodeArgs& p, char* codes
         const int k = 8 * (c * 64 * NW + tid);
         v[c] = u32x4{0, 0, 0, 0};
         if (k + 8 <= p.K)
-            v[c] = *reinterpret_cast<const u32x4*>(p.A16 + k);
+            v[c] = load8(p.A16 + k);
         else if (k < p.K)
             v[c] = load_some(p.A16 + k, p.K - k);
     }

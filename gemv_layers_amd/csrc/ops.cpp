@@ -190,9 +190,10 @@ int i8_product_bf16(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda,
     if (M > kMaxRows) return GEMM_ERR_UNSUPPORTED;
     if (M == 0 || N == 0) return GEMM_OK;
     if (!work || misaligned(work, 16) || work_bytes < work_bytes_of(M, K)) return GEMM_ERR_INVALID_ARG;
-    // one row: quantised in the product's kernel (its leading dimension does not matter)
-    const OpArgs one{A, Wq, static_cast<uint16_t*>(C), nullptr, nullptr, Sw, M, N, K, 16, ldwq, ldc, 0};
+    // one row: quantised in the product's kernel (neither its alignment nor its leading dimension matters)
+    OpArgs one{nullptr, Wq, static_cast<uint16_t*>(C), nullptr, nullptr, Sw, M, N, K, 16, ldwq, ldc, 0};
     if (M == 1 && K > 0 && K <= glk::kI8FusedK && matrix_ok(glk::kOpI8, glu, one)) {
+        one.A = A;
         const glk::DeviceInfo* dev = glk::current_device(&st);
         return dev ? run_i8_decode(glu, one, glk::make_i8_decode_plan(M, N, K, *dev, glu), true, stream) : st;
     }

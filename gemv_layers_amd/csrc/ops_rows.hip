@@ -3,7 +3,10 @@
 // Quantisation of rows (the arithmetic is in codes.h). A row stays in the registers of its workgroup
 // between the maximum and the codes, so that memory is read once (2 bytes an element) and written
 // once (1 byte). Few rows are bound by latency, a load, a reduction and a store, and take wide
-// workgroups; many rows by memory. 16 rows of 4096 take 4.8 us, 4096 rows 13 us (3.8 TB/s).
+// workgroups; many rows by memory. 16 rows of 4096 take 4.8 us, 4096 rows 13 us (3.8 TB/s). Rows may start
+// at any element: the 16-byte loads need no alignment, and cost a quarter more without it (4096 x 4095: 15
+// us, where element by element it took 24). Rows of up to 65536 stay in registers (16 x 28672: 5.6 us
+// against 35 in two passes).
 //
 // The gated block's gradient, element by element: reads dC, g and u, writes dg and du, 10 bytes an
 // element. 4096 x 11008: 67 us, 6.7 TB/s.
@@ -31,7 +34,7 @@ __global__ void __launch_bounds__(64 * NW) i8_quantize_kernel(const uint16_t* __
         const int k = 8 * (c * 64 * NW + tid);
         v[c] = u32x4{0, 0, 0, 0};
         if (k + 8 <= K) {
-            v[c] = *reinterpret_cast<const u32x4*>(x + k);
+            v[c] = load8(x + k);
         } else if (k < K) {
             v[c] = load_some(x + k, K - k);
         }
@@ -65,7 +68,7 @@ __global__ void __launch_bounds__(64 * NW) i8_quantize_kernel(const uint16_t* __
     }
 }
 
-// any alignment and length: two passes over the row, element by element
+// longer rows than registers hold: two passes over the row, element by element
 __global__ void __launch_bounds__(256) i8_quantize_any_kernel(const uint16_t* __restrict__ X, int64_t K, int64_t ldx,
                                                               int8_t* __restrict__ Q, int64_t ldq,
                                                               float* __restrict__ S) {
@@ -91,11 +94,14 @@ hipError_t launch_i8_quantize(const uint16_t* X, int64_t R, int64_t K, int64_t l
                               float* S, hipStream_t s) {
     if (R > 0xFFFFFF) return hipErrorInvalidValue;
     const unsigned grid = (unsigned)R;
-    const bool aligned = ((reinterpret_cast<uintptr_t>(X) & 15) == 0) && (ldx % 8 == 0);
     // chunks of 8 elements, a padded row's among them
     const int64_t chunks = (K + 15) / 16 * 2;
-    if (!aligned || chunks > 256 * 8)
+    if (chunks > 1024 * 8)
         i8_quantize_any_kernel<<<grid, 256, 0, s>>>(X, K, ldx, Q, ldq, S);
+    else if (chunks > 1024 * 4)
+        i8_quantize_kernel<16, 8><<<grid, 1024, 0, s>>>(X, (int)K, ldx, Q, ldq, S);
+    else if (chunks > 1024 * 2)
+        i8_quantize_kernel<16, 4><<<grid, 1024, 0, s>>>(X, (int)K, ldx, Q, ldq, S);
     else if (chunks > 256 && R <= 512)
         i8_quantize_kernel<16, 2><<<grid, 1024, 0, s>>>(X, (int)K, ldx, Q, ldq, S);
     else if (chunks <= 64)

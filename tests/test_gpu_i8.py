@@ -218,7 +218,8 @@ def quantize(xbits, K, ldx, ldq, offset=0):
     (1, 1, 1, 1, 0), (1, 1, 8, 16, 0), (3, 7, 8, 16, 0), (4, 64, 64, 64, 0), (5, 505, 512, 512, 0),
     (2, 1000, 1000, 1003, 0), (3, 2048, 2048, 2048, 0), (2, 4096, 4096, 4096, 0), (3, 11008, 11008, 11008, 0),
     (2, 16384, 16384, 16384, 0), (2, 16392, 16392, 16400, 0), (3, 1000, 1001, 1008, 1), (2, 40000, 40000, 40064, 0),
-    (700, 200, 208, 256, 0)])
+    (700, 200, 208, 256, 0), (4, 9118, 9118, 9120, 0), (600, 3711, 3711, 3712, 3), (3, 20001, 20001, 20016, 5),
+    (3, 65529, 65531, 65536, 7), (2, 70000, 70001, 70016, 1)])
 def test_quantize_codes(R, K, ldx, ldq, offset):
     rng = np.random.default_rng(R + K)
     x = rng.normal(size=(R, ldx)).astype(np.float32)
@@ -293,7 +294,8 @@ def act(M, K, seed, ld=None):
                                       (16, 4096, 4096, None), (17, 264, 20000, None), (64, 1000, 4104, None),
                                       (300, 1000, 1000, 1008), (1100, 520, 328, None), (1, 17, 7, 8),
                                       (2, 40, 1000, 1008), (1, 1000, 16384, None), (2, 24, 16392, None),
-                                      (2, 4096, 11008, None), (1, 72, 4104, 4112)])
+                                      (2, 4096, 11008, None), (1, 72, 4104, 4112), (7, 75, 3711, None),
+                                      (2, 520, 9118, None), (1, 75, 3711, None)])
 def test_dynamic_equals_quantize_then_product(M, N, K, ld):
     A = act(M, K, M + K, ld)
     W = (torch.randn(2 * N, K, generator=torch.Generator().manual_seed(N)) * 0.02).bfloat16().cuda()
@@ -309,6 +311,16 @@ def test_dynamic_equals_quantize_then_product(M, N, K, ld):
     acc = Aq.cpu().numpy().astype(np.float64) @ Wq[:N].cpu().numpy().astype(np.float64).T
     got = g.i8_linear(A, Wq[:N], Sw[:N])
     assert np.array_equal(bits(got), expect(acc, Sa.cpu().numpy(), Sw[:N].cpu().numpy()))
+
+
+def test_a_token_at_any_address():
+    """One token whose row starts at an odd element: its bits are those of a copy."""
+    A = act(8, 1001, 5)
+    Wq, Sw = g.i8_quantize((torch.randn(520, 1001, generator=torch.Generator().manual_seed(6)) * 0.02).bfloat16().cuda())
+    for r in range(8):
+        for f in (g.i8_linear, g.i8_swiglu_linear):
+            got, want = f(A[r : r + 1], Wq, Sw), f(A[r : r + 1].clone(), Wq, Sw)
+            assert torch.equal(got.view(torch.int16), want.view(torch.int16))
 
 
 def test_non_finite_token_gives_nan_outputs_only_in_its_row():
