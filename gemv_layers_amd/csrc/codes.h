@@ -59,11 +59,6 @@ __device__ __forceinline__ u32x2 codes8(const u32x4& v, const CodeScale& c) {
     }
     return w;
 }
-// eight bf16 values at any element: one 16-byte load, which needs no alignment
-__device__ __forceinline__ u32x4 load8(const uint16_t* x) {
-    typedef uint32_t u32x4_at2 __attribute__((ext_vector_type(4), aligned(2)));
-    return *reinterpret_cast<const u32x4_at2*>(x);
-}
 // eight bf16 values from `left` (1 .. 7) of them, the rest zeros, element by element
 __device__ __forceinline__ u32x4 load_some(const uint16_t* x, int left) {
     uint32_t w[4] = {0, 0, 0, 0};
@@ -72,5 +67,4 @@ __device__ __forceinline__ u32x4 load_some(const uint16_t* x, int left) {
         if (j < left) w[j >> 1] |= (uint32_t)x[j] << (16 * (j & 1));
     return u32x4{w[0], w[1], w[2], w[3]};
 }
-
 }  // namespace glk

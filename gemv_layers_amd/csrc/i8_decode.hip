@@ -189,8 +189,9 @@ __global__ void __launch_bounds__(64 * NW) i8_decode_kernel(I8DecodeArgs p) {
         }
         const u32x2 o = {pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3])};
         uint16_t* c = p.C + (int64_t)m * p.ldc + n;
-        if (p.vec) {
-            *reinterpret_cast<u32x2*>(c) = o;
+        if (n + 4 <= p.N) {  // at any element: the store needs no alignment
+            typedef uint32_t u32x2_at2 __attribute__((ext_vector_type(2), aligned(2)));
+            *reinterpret_cast<u32x2_at2*>(c) = o;
         } else {
 #pragma unroll
             for (int r = 0; r < 4; ++r)

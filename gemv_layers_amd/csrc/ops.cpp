@@ -30,8 +30,8 @@ const char* op_name(int mode, bool glu) {
 }
 
 // Whether the matrix kernels take these operands: 16-byte aligned rows, 32-bit offsets within a tile.
-// Codes need no multiple in any size (a C without 16-byte rows is stored element by element); bf16
-// widths are multiples of 8, except along the summed index where it is the row index.
+// Codes need no multiple in any size, and C any rows; bf16 widths are multiples of 8, except along the
+// summed index where it is the row index.
 bool matrix_ok(int mode, bool glu, const OpArgs& a) {
     const int64_t unit = mode == glk::kOpI8 ? 16 : 8;
     const int64_t max_ld = int64_t(1) << 20, max_dim = int64_t(1) << 26;
@@ -91,8 +91,7 @@ int run_i8_decode(bool glu, const OpArgs& a, const glk::Plan& p, bool fused, hip
     const glk::I8DecodeArgs t{fused ? nullptr : static_cast<const int8_t*>(a.A),
                               fused ? static_cast<const uint16_t*>(a.A) : nullptr,
                               static_cast<const int8_t*>(a.B), a.C, a.sa, a.sb, (int)a.M, (int)a.N, (int)a.K,
-                              (int)a.lda, (int)a.ldb, (int)a.ldc,
-                              !misaligned(a.C, 8) && a.ldc % 4 == 0 && a.N % 4 == 0, p.splits,
+                              (int)a.lda, (int)a.ldb, (int)a.ldc, p.splits,
                               reinterpret_cast<int32_t*>(w.ws), w.counters};
     if (glk::launch_i8_decode(glu, p.mtiles, p.strip / 16, p.threads / 64, t, (int)p.grid, stream) != hipSuccess)
         return GEMM_ERR_HIP;

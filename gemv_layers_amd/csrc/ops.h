@@ -65,7 +65,6 @@ struct I8DecodeArgs {
     const float* sb;     // N scales, or 2N gated
     int M, N, K;         // M <= 64
     int lda, ldw, ldc;
-    int vec;             // C takes 8-byte stores
     int pieces;          // of K, one workgroup each
     int32_t* ws;         // pieces > 1: groups * pieces * tn * mt * 256
     uint32_t* counters;  // one per group, zero between launches

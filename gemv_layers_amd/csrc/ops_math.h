@@ -1,4 +1,5 @@
-// The gated block's activation, shared by the 8-bit and training kernels (device side).
+// The gated block's activation, and accesses at any element, shared by the 8-bit and training kernels
+// (device side).
 #pragma once
 
 #include "common.h"
@@ -22,5 +23,22 @@ __device__ __forceinline__ float op_sigmoid(float g) {
 
 // silu(g) u
 __device__ __forceinline__ float op_swiglu(float g, float u) { return g * op_sigmoid(g) * u; }
+
+// eight bf16 values at any element: one 16-byte load, which needs no alignment
+__device__ __forceinline__ u32x4 load8(const uint16_t* x) {
+    typedef uint32_t u32x4_at2 __attribute__((ext_vector_type(4), aligned(2)));
+    return *reinterpret_cast<const u32x4_at2*>(x);
+}
+// stores the first `left` of eight bf16 values at any element: one 16-byte store where all count
+__device__ __forceinline__ void store8(uint16_t* x, const u32x4& v, int left) {
+    typedef uint32_t u32x4_at2 __attribute__((ext_vector_type(4), aligned(2)));
+    if (left >= 8) {
+        *reinterpret_cast<u32x4_at2*>(x) = v;
+    } else {
+#pragma unroll
+        for (int j = 0; j < 7; ++j)
+            if (j < left) x[j] = (uint16_t)(v[j >> 1] >> (16 * (j & 1)));
+    }
+}
 
 }  // namespace glk
