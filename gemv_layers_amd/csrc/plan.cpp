@@ -394,9 +394,11 @@ Plan make_packed_plan(int64_t M, int64_t N, int64_t K, const DeviceInfo& dev) {
 // noted: 512^3 4.8 against 6.9, 1000^3 8.0 against 11.2, codes 509 x 2501 x 1003 8.2 against 11.7,
 // gated forward 300 x 520 x 328 6.0 against 9.0), but copy twice the bytes, which decides once all CUs
 // are busy: 2048 x 2048 x 512 10.0 against 8.3, codes 777 x 4096 x 4096 28.3 against 23.1, 2000 x 512 x
-// 8192 30.0 against 25.9. So 64 x 64 tiles up to one and a half a CU and 32768 k-steps in all (128
-// x 4096 x 4096, 16384 steps: 13.2 against 16.1; codes 128 x 11008 x 4096, 22016 steps: 15.9 against
-// 17.2), and for a quarter as many tiles as CUs whatever K is.
+// 8192 30.0 against 25.9. So 64 x 64 tiles up to two a CU and 16384 k-steps in all (of 480 random products,
+// the bounds of one and a half a CU and 32768 steps lost on 35 where these differ, by 1.16 in the mean:
+// codes gated 1404 x 655 x 991, 462 tiles of 16 steps, 7.6 against 12.0; C = A^T B 480 x 2552 x 2306, 320 of
+// 73, 21.2 against 16.2), of 32768 where M leaves half of a 128-row tile empty (gated codes 16 x 11008 x
+// 4096, 22016 steps: 18.2 of 64 x 64 tiles), and for a quarter as many tiles as CUs whatever K is.
 // Pieces of K: a fixup costs like a few k-steps for each piece, so about sqrt(steps / 6) of them (512^3,
 // 16 steps: 4.8 us whole, 6.0 in two pieces; codes 300 x 300 x 5008, 79 steps: 9.6 in three, 10.9 in
 // two), but none of less than 28 steps once the tiles alone fill the CUs (1000^3, 32 steps: 8.0 whole,
@@ -405,8 +407,8 @@ Plan make_packed_plan(int64_t M, int64_t N, int64_t K, const DeviceInfo& dev) {
 Plan make_op_plan(int64_t M, int64_t N, int64_t K, const DeviceInfo& dev, bool glu) {
     const int64_t tm = cdiv(M, 64), tn = cdiv(glu ? 2 * N : N, 64), kt = cdiv(K, 32);
     const int64_t most = dev.cus + dev.cus / 2;
-    if (tm > most || tn > most || tm * tn > most || (tm * tn * kt > 32768 && tm * tn > dev.cus / 4))
-    {
+    const int64_t tiles = 2 * (int64_t)dev.cus, all_steps = tm == 1 ? 32768 : 16384;
+    if (tm > tiles || tn > tiles || tm * tn > tiles || (tm * tn * kt > all_steps && tm * tn > dev.cus / 4)) {
         // the gated form is planned over its 2N weight columns: a 256-column tile makes 128 outputs, and
         // the strip of a sparse last wave may be cut off across columns too, as its kernels take the
         // up half's offset apart from the width
