@@ -28,9 +28,9 @@
 // Codes past K in the last 16-byte chunk of a row are whatever the caller's padding holds: they are
 // cleared in the A operand, which is enough, as 0 times any code is 0.
 //
-// Measured, 256 x 256 tiles: 8-bit 4096 x 4096 x 11008 124 us a call, 3.0 POP/s; medians of the kernel, dA
-// = dC B^T 4096 x 4096 x 22016 479 us, 1.54 PFLOP/s; of dB = A^T dC 4096 x 22016 x 4096 the 1280 tiles of
-// its full waves 560-574 us, 1.2, and as many of the forward 552-556 us. What bounds them, from timing-only
+// Measured, 256 x 256 tiles: 8-bit 4096 x 4096 x 11008 126 us a call, 2.9 POP/s; medians of the kernel, dA
+// = dC B^T 4096 x 4096 x 22016 484 us, 1.53 PFLOP/s; of dB = A^T dC 4096 x 22016 x 4096 the 1280 tiles of
+// its full waves 560-574 us, 1.2, and as many of the forward 552-566 us. What bounds them, from timing-only
 // copies that leave one part out (us, in that order, the whole 124, 470, 556, and 666 for the forward's
 // 1376 tiles): without the copies 105, 362, 443, 478; without the operand reads 113, 469, 451, 641;
 // without the MFMAs 84, 430, 360, 474; the operand reads alone 59, 187, 280, 273. dA waits
@@ -459,7 +459,7 @@ op_pp_kernel(OpTileArgs p) {
 // counts the same.
 //
 // With one or two tiles a CU what bounds it is the latency of each k-step, not a rate: 509 x 2501 x 1003
-// codes 8.6 us, the gated forward 300 x 520 x 328 6.0 us (64 x 64 tiles). It is not a want of bytes in
+// codes 7.7 us, the gated forward 300 x 520 x 328 6.1 us (64 x 64 tiles). It is not a want of bytes in
 // flight: 64 x 64 rings of 7, 9 and 13 slots gave 64 x 4096 x 11008 codes 2% at best and cost the other
 // small products 2 to 50%, as fewer workgroups fit a CU.
 template <int BT, int MODE, bool GLU>

@@ -414,9 +414,8 @@ Plan make_op_plan(int64_t M, int64_t N, int64_t K, const DeviceInfo& dev, bool g
         // up half's offset apart from the width
         Plan q = make_plan(M, glu ? 2 * N : N, K, dev, true, 2, false);
         // two pieces on more than two thirds of the CUs, which pay for the other products (make_plan),
-        // lose here: on all of twelve random products of
-        // 175 to 252 tiles and 99 to 141 k-steps, by 8-15% (C = A B^T 1249 x 2232 x 3472 33.2 us whole, 38.4
-        // in two)
+        // lose here: on all of twelve random products of 175 to 252 tiles and 99 to 141 k-steps, by 8-15%
+        // (C = A B^T 1249 x 2232 x 3472 33.2 us whole, 38.4 in two)
         if (q.bm == 128 && q.splits == 2 && 3 * q.tiles > 2 * (int64_t)dev.cus) {
             q.sched = kSchedDataParallel;
             q.splits = 1;
