@@ -259,23 +259,33 @@ int check_gradients(int64_t M, int64_t W, int64_t K, const void* A, int64_t lda,
     return GEMM_OK;
 }
 
+// No C++ exception leaves a C entry point: a plan's text or a lock that the host has no memory for.
+template <class F>
+int guarded(F f) {
+    try {
+        return f();
+    } catch (...) {
+        return GEMM_ERR_HIP;
+    }
+}
+
 }  // namespace
 
 extern "C" {
 
 int gemm_i8_quantize(int64_t R, int64_t K, const void* X, int64_t ldx, void* Q, int64_t ldq, float* S,
                      gemm_stream_t stream) {
-    return quantize(R, K, X, ldx, Q, ldq, S, hip_stream(stream));
+    return guarded([&] { return quantize(R, K, X, ldx, Q, ldq, S, hip_stream(stream)); });
 }
 
 int gemm_i8(int64_t M, int64_t N, int64_t K, const void* Aq, int64_t ldaq, const float* Sa, const void* Wq,
             int64_t ldwq, const float* Sw, void* C, int64_t ldc, gemm_stream_t stream) {
-    return i8_product(M, N, K, Aq, ldaq, Sa, Wq, ldwq, Sw, C, ldc, false, hip_stream(stream));
+    return guarded([&] { return i8_product(M, N, K, Aq, ldaq, Sa, Wq, ldwq, Sw, C, ldc, false, hip_stream(stream)); });
 }
 
 int gemm_i8_swiglu(int64_t M, int64_t N, int64_t K, const void* Aq, int64_t ldaq, const float* Sa, const void* Wq,
                    int64_t ldwq, const float* Sw, void* C, int64_t ldc, gemm_stream_t stream) {
-    return i8_product(M, N, K, Aq, ldaq, Sa, Wq, ldwq, Sw, C, ldc, true, hip_stream(stream));
+    return guarded([&] { return i8_product(M, N, K, Aq, ldaq, Sa, Wq, ldwq, Sw, C, ldc, true, hip_stream(stream)); });
 }
 
 int gemm_i8_work_bytes(int64_t M, int64_t K, int64_t* bytes) {
@@ -287,54 +297,64 @@ int gemm_i8_work_bytes(int64_t M, int64_t K, int64_t* bytes) {
 
 int gemm_i8_bf16(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const void* Wq, int64_t ldwq,
                  const float* Sw, void* C, int64_t ldc, void* work, int64_t work_bytes, gemm_stream_t stream) {
-    return i8_product_bf16(M, N, K, A, lda, Wq, ldwq, Sw, C, ldc, work, work_bytes, false, hip_stream(stream));
+    return guarded([&] {
+        return i8_product_bf16(M, N, K, A, lda, Wq, ldwq, Sw, C, ldc, work, work_bytes, false, hip_stream(stream));
+    });
 }
 
 int gemm_i8_swiglu_bf16(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const void* Wq, int64_t ldwq,
                         const float* Sw, void* C, int64_t ldc, void* work, int64_t work_bytes,
                         gemm_stream_t stream) {
-    return i8_product_bf16(M, N, K, A, lda, Wq, ldwq, Sw, C, ldc, work, work_bytes, true, hip_stream(stream));
+    return guarded([&] {
+        return i8_product_bf16(M, N, K, A, lda, Wq, ldwq, Sw, C, ldc, work, work_bytes, true, hip_stream(stream));
+    });
 }
 
 int gemm_bf16_bwd(int64_t M, int64_t N, int64_t K, const void* dC, int64_t lddc, const void* A, int64_t lda,
                   const void* B, int64_t ldb, void* dA, int64_t ldda, void* dB, int64_t lddb,
                   gemm_stream_t stream) {
-    if (M < 0 || N < 0 || K < 0 || lddc < N || misaligned(dC, 2)) return GEMM_ERR_INVALID_ARG;
-    if ((dA || dB) && M > 0 && N > 0 && K > 0 && !dC) return GEMM_ERR_INVALID_ARG;
-    const int st = check_gradients(M, N, K, A, lda, B, ldb, dA, ldda, dB, lddb);
-    if (st != GEMM_OK) return st;
-    return gradients(M, N, K, dC, lddc, A, lda, B, ldb, dA, ldda, dB, lddb, hip_stream(stream));
+    return guarded([&]() -> int {
+        if (M < 0 || N < 0 || K < 0 || lddc < N || misaligned(dC, 2)) return GEMM_ERR_INVALID_ARG;
+        if ((dA || dB) && M > 0 && N > 0 && K > 0 && !dC) return GEMM_ERR_INVALID_ARG;
+        const int st = check_gradients(M, N, K, A, lda, B, ldb, dA, ldda, dB, lddb);
+        if (st != GEMM_OK) return st;
+        return gradients(M, N, K, dC, lddc, A, lda, B, ldb, dA, ldda, dB, lddb, hip_stream(stream));
+    });
 }
 
 int gemm_bf16_swiglu_train(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const void* B, int64_t ldb,
                            void* GU, int64_t ldgu, void* C, int64_t ldc, gemm_stream_t stream) {
-    if (M < 0 || N < 0 || K < 0 || N > INT64_MAX / 2) return GEMM_ERR_INVALID_ARG;
-    if (lda < K || ldb < 2 * N || ldgu < 2 * N || ldc < N) return GEMM_ERR_INVALID_ARG;
-    if ((M > 0 && K > 0 && !A) || (K > 0 && N > 0 && !B) || (M > 0 && N > 0 && (!GU || !C)))
-        return GEMM_ERR_INVALID_ARG;
-    if (misaligned(A, 2) || misaligned(B, 2) || misaligned(GU, 2) || misaligned(C, 2)) return GEMM_ERR_INVALID_ARG;
-    if (M == 0 || N == 0) return GEMM_OK;
-    const OpArgs a{A, B, static_cast<uint16_t*>(C), static_cast<uint16_t*>(GU), nullptr, nullptr,
-                   M, N, K, lda, ldb, ldc, ldgu};
-    return run_op(glk::kOpTrain, true, a, hip_stream(stream));
+    return guarded([&]() -> int {
+        if (M < 0 || N < 0 || K < 0 || N > INT64_MAX / 2) return GEMM_ERR_INVALID_ARG;
+        if (lda < K || ldb < 2 * N || ldgu < 2 * N || ldc < N) return GEMM_ERR_INVALID_ARG;
+        if ((M > 0 && K > 0 && !A) || (K > 0 && N > 0 && !B) || (M > 0 && N > 0 && (!GU || !C)))
+            return GEMM_ERR_INVALID_ARG;
+        if (misaligned(A, 2) || misaligned(B, 2) || misaligned(GU, 2) || misaligned(C, 2)) return GEMM_ERR_INVALID_ARG;
+        if (M == 0 || N == 0) return GEMM_OK;
+        const OpArgs a{A, B, static_cast<uint16_t*>(C), static_cast<uint16_t*>(GU), nullptr, nullptr,
+                       M, N, K, lda, ldb, ldc, ldgu};
+        return run_op(glk::kOpTrain, true, a, hip_stream(stream));
+    });
 }
 
 int gemm_bf16_swiglu_bwd(int64_t M, int64_t N, int64_t K, const void* dC, int64_t lddc, const void* GU,
                          int64_t ldgu, const void* A, int64_t lda, const void* B, int64_t ldb, void* dGU,
                          int64_t lddgu, void* dA, int64_t ldda, void* dB, int64_t lddb, gemm_stream_t stream) {
-    if (M < 0 || N < 0 || K < 0 || N > INT64_MAX / 2) return GEMM_ERR_INVALID_ARG;
-    if (lddc < N || ldgu < 2 * N || lddgu < 2 * N) return GEMM_ERR_INVALID_ARG;
-    if (M > 0 && N > 0 && (!dC || !GU || !dGU)) return GEMM_ERR_INVALID_ARG;
-    if (misaligned(dC, 2) || misaligned(GU, 2) || misaligned(dGU, 2)) return GEMM_ERR_INVALID_ARG;
-    int st = check_gradients(M, 2 * N, K, A, lda, B, ldb, dA, ldda, dB, lddb);
-    if (st != GEMM_OK) return st;
-    if (M > 0 && N > 0) {
-        if (!glk::current_device(&st)) return st;
-        if (glk::launch_swiglu_grad(static_cast<const uint16_t*>(dC), lddc, static_cast<const uint16_t*>(GU), ldgu,
-                                    static_cast<uint16_t*>(dGU), lddgu, M, N, hip_stream(stream)) != hipSuccess)
-            return GEMM_ERR_HIP;
-    }
-    return gradients(M, 2 * N, K, dGU, lddgu, A, lda, B, ldb, dA, ldda, dB, lddb, hip_stream(stream));
+    return guarded([&]() -> int {
+        if (M < 0 || N < 0 || K < 0 || N > INT64_MAX / 2) return GEMM_ERR_INVALID_ARG;
+        if (lddc < N || ldgu < 2 * N || lddgu < 2 * N) return GEMM_ERR_INVALID_ARG;
+        if (M > 0 && N > 0 && (!dC || !GU || !dGU)) return GEMM_ERR_INVALID_ARG;
+        if (misaligned(dC, 2) || misaligned(GU, 2) || misaligned(dGU, 2)) return GEMM_ERR_INVALID_ARG;
+        int st = check_gradients(M, 2 * N, K, A, lda, B, ldb, dA, ldda, dB, lddb);
+        if (st != GEMM_OK) return st;
+        if (M > 0 && N > 0) {
+            if (!glk::current_device(&st)) return st;
+            if (glk::launch_swiglu_grad(static_cast<const uint16_t*>(dC), lddc, static_cast<const uint16_t*>(GU), ldgu,
+                                        static_cast<uint16_t*>(dGU), lddgu, M, N, hip_stream(stream)) != hipSuccess)
+                return GEMM_ERR_HIP;
+        }
+        return gradients(M, 2 * N, K, dGU, lddgu, A, lda, B, ldb, dA, ldda, dB, lddb, hip_stream(stream));
+    });
 }
 
 }  // extern "C"

@@ -42,7 +42,7 @@ struct OpTileArgs {
     int M, N, K;
     int lda, ldb, ldc, ldgu;
     int up;              // gated: where the up half starts in the weight, its scales and GU
-    int vec;             // C takes 16-byte stores
+    int vec;             // C takes aligned 16-byte stores
     int tiles_m, tiles_n, group_m, nxcd;
     int splits, kt_per_split;  // pieces of K per tile, 64-byte k-steps in each (128 x 128 tiles)
     float* ws;
