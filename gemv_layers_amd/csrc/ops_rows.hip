@@ -121,9 +121,9 @@ hipError_t launch_i8_quantize(const uint16_t* X, int64_t R, int64_t K, int64_t l
 
 // du = d silu(g), dg = d u s (1 + g (1 - s)) with s = sigmoid(g), in float32
 __device__ __forceinline__ void swiglu_grad1(float d, float g, float u, float& dg, float& du) {
-    const float sig = op_sigmoid(g);
-    du = d * (g * sig);
-    dg = d * u * (sig * (1.0f + g * (1.0f - sig)));
+    const OpSigmoid sig = op_sigmoid(g);
+    du = d * (g * sig.r * sig.p);
+    dg = d * u * (sig.r * (1.0f + g * (1.0f - sig.r * sig.p)) * sig.p);
 }
 
 // dGU may be GU itself: every element is read by the thread that writes it, before it does. VEC: eight

@@ -348,7 +348,8 @@ int gemm_bf16_bwd(int64_t M, int64_t N, int64_t K, const void *dC, int64_t lddc,
 /*
  * gemm_bf16_swiglu_train: gemm_bf16_swiglu that also keeps what the backward pass needs:
  *   GU = A * B (M x 2N bf16, ldgu >= 2N: g, then u),   C = silu(g) .* u (M x N bf16).
- * C is made from the float32 g and u, so it is gemm_bf16_swiglu's C within float32 rounding.
+ * C is made from the float32 g and u, so it is gemm_bf16_swiglu's C within float32 rounding for g above
+ * -88.7; below, where that call's silu is zero, silu(g) u is computed down to float32's smallest step.
  * M == 0 or N == 0: nothing. K == 0: GU = 0 and C = 0. Errors as gemm_bf16_swiglu, and
  * GEMM_ERR_INVALID_ARG for ldgu < 2N or a null GU.
  */

@@ -484,3 +484,28 @@ def test_helpers_keep_references_and_take_streams():
         assert torch.equal(out.view(torch.int16), want.view(torch.int16))
     with pytest.raises(AttributeError):
         g.i8_linear(A, Wq, Sw, stream="s")
+
+
+@pytest.mark.parametrize("M", [1, 20, 130])
+def test_gates_below_the_normal_range(M):
+    """Gates at which the sigmoid is below float32's normal range (g < -87.3) while silu(g) u is not:
+    silu(g) carries 2^-20 of its size and float32's smallest step 2^-149, which u multiplies; g is exact
+    and the rounding to bf16 adds 2^-8 of the result."""
+    gates = np.array([-87.0, -87.5, -88.0, -88.5, -89.0, -91.0, -95.0, -100.0])
+    N, K, up = len(gates), 5, 2.0**100
+    W = np.zeros((2 * N, 16), np.int8)
+    W[:, 0] = 1
+    sw = np.concatenate([gates, np.full(N, up)]).astype(np.float32)   # codes of one: the scale is the product
+    sa = np.ones(M, np.float32)
+    s = gates / (1 + np.exp(-gates))
+    slack = 2.0**-8 * np.abs(s * up) + (2.0**-20 * np.abs(s) + 2.0**-149) * up
+    for ld in (16, 17):     # the matrix kernels, and the general one
+        A = np.zeros((M, ld), np.int8)
+        A[:, 0] = 1
+        (dA, _), (dW, _), (dsa, _), (dsw, _) = place(A), place(W), place(sa), place(sw)
+        C = poisoned(M * N)
+        g.gemm_i8_swiglu(M, N, K, dA.data_ptr(), ld, dsa.data_ptr(), dW.data_ptr(), 16, dsw.data_ptr(), C.data_ptr(), N,
+                         g.current_stream_handle())
+        torch.cuda.synchronize()
+        off = np.abs(widen(bits(C)).reshape(M, N) - s * up) - slack
+        assert (off <= 0).all(), (g.gemm_last_plan()["kernel"], gates[(off > 0).any(0)])

@@ -307,3 +307,34 @@ def test_offsets_past_32_bits():
     da, db, dgu = g.swiglu_backward(d, gu, x, B)
     assert err(dGU[few], dgu) < 2.0**-7 and err(dA[few], da) < 2.0**-7 and err(dB, db) < 2.0**-7
     assert not dA[64:-65].any() and not dGU[64:-65].any()
+
+
+def test_gates_below_the_normal_range():
+    """Gates at which the sigmoid is below float32's normal range (g < -87.3) while g s, or g s u with a
+    large u, is not. silu(g) carries 2^-20 of its size and, below 2^-126 itself, float32's smallest step
+    2^-149; u multiplies both, and the rounding to bf16 adds 2^-8 of the result."""
+    gates = np.array([-87.0, -87.5, -88.0, -88.5, -89.0, -91.0, -95.0, -100.0], np.float64)
+    M, N, K = 70, 8, 8
+    for scale in (2.0**100, 2.0**20):
+        A, B = np.zeros((M, K)), np.zeros((K, 2 * N))
+        A[:, 0], B[0, :N], B[0, N:] = 1, gates, scale
+        dev = lambda x: torch.from_numpy(oracle.bf16_rne(x).view(np.int16)).view(torch.bfloat16).cuda()  # noqa: E731
+        # the matrix kernels, and the general one (rows without 16-byte alignment)
+        for tA in (dev(A), dev(np.concatenate([A, A[:, :1]], 1))[:, :K]):
+            C, GU = g.swiglu_forward(tA, dev(B))
+            assert np.array_equal(GU.double().cpu().numpy(), A @ B)
+            s = gates / (1 + np.exp(-gates))
+            slack = 2.0**-8 * np.abs(s * scale) + (2.0**-20 * np.abs(s) + 2.0**-149) * scale + 2.0**-133
+            off = np.abs(C.double().cpu().numpy() - s * scale) - slack
+            assert (off <= 0).all(), (scale, gates[(off > 0).any(0)])
+        # du = d silu(g), dg = d u s (1 + g (1 - s))
+        D = dev(np.full((M, N), scale))
+        GU = dev(np.concatenate([np.tile(gates, (M, 1)), np.ones((M, N))], 1))
+        _, _, dGU = g.swiglu_backward(D, GU, dev(A), dev(B), need_dA=False, need_dB=False)
+        sig = 1 / (1 + np.exp(-gates))
+        ds = sig * (1 + gates * (1 - sig))
+        want = np.concatenate([ds, s]) * scale
+        size = np.concatenate([sig * (1 + np.abs(gates)), np.abs(s)])
+        slack = 2.0**-8 * np.abs(want) + (2.0**-19 * size + 2.0**-149) * scale + 2.0**-133
+        off = np.abs(dGU.double().cpu().numpy() - want) - slack
+        assert (off <= 0).all(), (scale, np.argwhere((off > 0).any(0)).ravel())
