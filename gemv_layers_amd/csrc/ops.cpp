@@ -81,62 +81,88 @@ hipError_t launch_tiles(int mode, bool glu, const OpArgs& a, const glk::Plan& p,
     return glk::launch_op_tile(mode, glu, p.bm, tile_args(mode, a, p, m0, M, n0, N, w), (int)p.grid, stream);
 }
 
-// The 8-bit product of at most 64 rows on the weight-streaming kernel. `fused`: a.A holds bf16.
-int run_i8_decode(bool glu, const OpArgs& a, const glk::Plan& p, bool fused, hipStream_t stream) {
+// A product that is ready to launch: planned, its limits checked, its workspace at hand. A call prepares
+// every product it makes before it launches anything, so that a refusal leaves its outputs, and inputs
+// that it overwrites, as they were.
+struct Ready {
+    enum Route { kZero, kGeneral, kTiles, kDecode } route = kZero;
+    int mode = 0;
+    bool glu = false;
+    bool fused = false;  // kDecode: a.A holds bf16
+    OpArgs a{};
+    glk::Plan p;
     glk::Workspace w;
-    if (p.splits > 1) {
-        const int st = glk::stream_workspace(stream, &w);
-        if (st != GEMM_OK) return st;
-    }
-    const glk::I8DecodeArgs t{fused ? nullptr : static_cast<const int8_t*>(a.A),
-                              fused ? static_cast<const uint16_t*>(a.A) : nullptr,
-                              static_cast<const int8_t*>(a.B), a.C, a.sa, a.sb, (int)a.M, (int)a.N, (int)a.K,
-                              (int)a.lda, (int)a.ldb, (int)a.ldc, p.splits,
-                              reinterpret_cast<int32_t*>(w.ws), w.counters};
-    if (glk::launch_i8_decode(glu, p.mtiles, p.strip / 16, p.threads / 64, t, (int)p.grid, stream) != hipSuccess)
-        return GEMM_ERR_HIP;
-    glk::set_last_plan(p, a.M, a.N, a.K, op_name(glk::kOpI8, glu));
-    return GEMM_OK;
-}
+};
 
-// One product on the current device: M, N > 0, operands checked.
-int run_op(int mode, bool glu, const OpArgs& a, hipStream_t stream) {
+// One product on the current device: M, N > 0, operands checked. `fused`: one row of bf16 activations
+// and a weight that the weight-streaming kernel takes.
+int prepare(int mode, bool glu, const OpArgs& a, bool fused, hipStream_t stream, Ready* r) {
     int st = GEMM_OK;
     const glk::DeviceInfo* dev = glk::current_device(&st);
     if (!dev) return st;
-    if (mode == glk::kOpI8 && a.M <= 64 && a.K > 0 && matrix_ok(mode, glu, a)) {
-        const glk::Plan few = glk::make_i8_decode_plan(a.M, a.N, a.K, *dev, glu);
-        if (glk::i8_decode_fits(a.M, a.K, few)) return run_i8_decode(glu, a, few, false, stream);
+    r->mode = mode;
+    r->glu = glu;
+    r->fused = fused;
+    r->a = a;
+    const bool matrix = fused || (a.K > 0 && matrix_ok(mode, glu, a));
+    if (mode == glk::kOpI8 && a.M <= 64 && matrix) {  // at most 64 rows: the weight-streaming kernel
+        r->p = glk::make_i8_decode_plan(a.M, a.N, a.K, *dev, glu);
+        if (fused || glk::i8_decode_fits(a.M, a.K, r->p)) {
+            r->route = Ready::kDecode;
+            return r->p.splits > 1 ? glk::stream_workspace(stream, &r->w) : GEMM_OK;
+        }
     }
-    glk::Plan p;
-    hipError_t e = hipSuccess;
     if (a.K == 0) {
-        p = glk::make_plan(a.M, a.N, 0, *dev, false, 2, glu);
-        e = glk::launch_zero_c(a.C, a.M, a.N, a.ldc, stream);
-        if (e == hipSuccess && mode == glk::kOpTrain) e = glk::launch_zero_c(a.GU, a.M, 2 * a.N, a.ldgu, stream);
-    } else if (!matrix_ok(mode, glu, a)) {
+        r->route = Ready::kZero;
+        r->p = glk::make_plan(a.M, a.N, 0, *dev, false, 2, glu);
+    } else if (!matrix) {
         // 64 x 64 tiles of 256 threads, 32-bit grids
         if ((a.M - 1) / 64 + 1 > kMaxRows / ((a.N - 1) / 64 + 1)) return GEMM_ERR_UNSUPPORTED;
-        p = glk::make_plan(a.M, a.N, a.K, *dev, false, 2, glu);
-        e = glk::launch_op_generic(mode, glu, a, stream);
+        r->route = Ready::kGeneral;
+        r->p = glk::make_plan(a.M, a.N, a.K, *dev, false, 2, glu);
     } else {
         // codes: planned as the bf16 product whose k-steps have the same bytes and matrix-core cycles
-        p = glk::make_op_plan(a.M, a.N, mode == glk::kOpI8 ? (a.K + 1) / 2 : a.K, *dev, glu);
-        if (p.grid > INT32_MAX) return GEMM_ERR_UNSUPPORTED;
-        glk::Workspace w;
-        if (p.ws_floats > 0) {
-            st = glk::stream_workspace(stream, &w);
-            if (st != GEMM_OK) return st;
+        r->route = Ready::kTiles;
+        r->p = glk::make_op_plan(a.M, a.N, mode == glk::kOpI8 ? (a.K + 1) / 2 : a.K, *dev, glu);
+        if (r->p.grid > INT32_MAX) return GEMM_ERR_UNSUPPORTED;
+        if (r->p.ws_floats > 0) return glk::stream_workspace(stream, &r->w);
+    }
+    return GEMM_OK;
+}
+
+int launch(const Ready& r, hipStream_t stream) {
+    const OpArgs& a = r.a;
+    const glk::Plan& p = r.p;
+    hipError_t e = hipSuccess;
+    switch (r.route) {
+        case Ready::kDecode: {
+            const glk::I8DecodeArgs t{r.fused ? nullptr : static_cast<const int8_t*>(a.A),
+                                      r.fused ? static_cast<const uint16_t*>(a.A) : nullptr,
+                                      static_cast<const int8_t*>(a.B), a.C, a.sa, a.sb, (int)a.M, (int)a.N, (int)a.K,
+                                      (int)a.lda, (int)a.ldb, (int)a.ldc, p.splits,
+                                      reinterpret_cast<int32_t*>(r.w.ws), r.w.counters};
+            e = glk::launch_i8_decode(r.glu, p.mtiles, p.strip / 16, p.threads / 64, t, (int)p.grid, stream);
+            break;
         }
-        const int64_t Mm = p.cut_axis == 2 ? p.cut_at : a.M, Nm = p.cut_axis == 1 ? p.cut_at : a.N;
-        e = launch_tiles(mode, glu, a, p, 0, Mm, 0, Nm, w, stream);
-        if (e == hipSuccess && p.cut_axis == 1)
-            e = launch_tiles(mode, glu, a, p.rest[0], 0, a.M, Nm, a.N - Nm, w, stream);
-        else if (e == hipSuccess && p.cut_axis == 2)
-            e = launch_tiles(mode, glu, a, p.rest[0], Mm, a.M - Mm, 0, a.N, w, stream);
+        case Ready::kZero:
+            e = glk::launch_zero_c(a.C, a.M, a.N, a.ldc, stream);
+            if (e == hipSuccess && r.mode == glk::kOpTrain) e = glk::launch_zero_c(a.GU, a.M, 2 * a.N, a.ldgu, stream);
+            break;
+        case Ready::kGeneral:
+            e = glk::launch_op_generic(r.mode, r.glu, a, stream);
+            break;
+        case Ready::kTiles: {
+            const int64_t Mm = p.cut_axis == 2 ? p.cut_at : a.M, Nm = p.cut_axis == 1 ? p.cut_at : a.N;
+            e = launch_tiles(r.mode, r.glu, a, p, 0, Mm, 0, Nm, r.w, stream);
+            if (e == hipSuccess && p.cut_axis == 1)
+                e = launch_tiles(r.mode, r.glu, a, p.rest[0], 0, a.M, Nm, a.N - Nm, r.w, stream);
+            else if (e == hipSuccess && p.cut_axis == 2)
+                e = launch_tiles(r.mode, r.glu, a, p.rest[0], Mm, a.M - Mm, 0, a.N, r.w, stream);
+            break;
+        }
     }
     if (e != hipSuccess) return GEMM_ERR_HIP;
-    glk::set_last_plan(p, a.M, a.N, a.K, op_name(mode, glu));
+    glk::set_last_plan(p, a.M, a.N, a.K, op_name(r.mode, r.glu));
     return GEMM_OK;
 }
 
@@ -154,12 +180,14 @@ int check_i8(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const 
 
 int i8_product(int64_t M, int64_t N, int64_t K, const void* Aq, int64_t ldaq, const float* Sa, const void* Wq,
                int64_t ldwq, const float* Sw, void* C, int64_t ldc, bool glu, hipStream_t stream) {
-    const int st = check_i8(M, N, K, Aq, ldaq, Wq, ldwq, Sw, C, ldc, glu);
+    int st = check_i8(M, N, K, Aq, ldaq, Wq, ldwq, Sw, C, ldc, glu);
     if (st != GEMM_OK) return st;
     if (M > 0 && (!Sa || misaligned(Sa, 4))) return GEMM_ERR_INVALID_ARG;
     if (M == 0 || N == 0) return GEMM_OK;
+    Ready r;
     const OpArgs a{Aq, Wq, static_cast<uint16_t*>(C), nullptr, Sa, Sw, M, N, K, ldaq, ldwq, ldc, 0};
-    return run_op(glk::kOpI8, glu, a, stream);
+    st = prepare(glk::kOpI8, glu, a, false, stream, &r);
+    return st == GEMM_OK ? launch(r, stream) : st;
 }
 
 int quantize(int64_t R, int64_t K, const void* X, int64_t ldx, void* Q, int64_t ldq, float* S, hipStream_t stream) {
@@ -189,67 +217,84 @@ int i8_product_bf16(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda,
     if (M > kMaxRows) return GEMM_ERR_UNSUPPORTED;
     if (M == 0 || N == 0) return GEMM_OK;
     if (!work || misaligned(work, 16) || work_bytes < work_bytes_of(M, K)) return GEMM_ERR_INVALID_ARG;
+    Ready r;
     // one row: quantised in the product's kernel (neither its alignment nor its leading dimension matters)
-    OpArgs one{nullptr, Wq, static_cast<uint16_t*>(C), nullptr, nullptr, Sw, M, N, K, 16, ldwq, ldc, 0};
-    if (M == 1 && K > 0 && K <= glk::kI8FusedK && matrix_ok(glk::kOpI8, glu, one)) {
-        one.A = A;
-        const glk::DeviceInfo* dev = glk::current_device(&st);
-        return dev ? run_i8_decode(glu, one, glk::make_i8_decode_plan(M, N, K, *dev, glu), true, stream) : st;
+    OpArgs a{nullptr, Wq, static_cast<uint16_t*>(C), nullptr, nullptr, Sw, M, N, K, 16, ldwq, ldc, 0};
+    if (M == 1 && K > 0 && K <= glk::kI8FusedK && matrix_ok(glk::kOpI8, glu, a)) {
+        a.A = A;
+        st = prepare(glk::kOpI8, glu, a, true, stream, &r);
+        return st == GEMM_OK ? launch(r, stream) : st;
     }
-    const int64_t ldq = padded_codes(K);
-    float* sa = reinterpret_cast<float*>(static_cast<char*>(work) + M * ldq);
-    st = quantize(M, K, A, lda, work, ldq, sa, stream);
-    if (st != GEMM_OK) return st;
-    return i8_product(M, N, K, work, ldq, sa, Wq, ldwq, Sw, C, ldc, glu, stream);
+    a.A = work;
+    a.lda = padded_codes(K);
+    float* sa = reinterpret_cast<float*>(static_cast<char*>(work) + M * a.lda);
+    a.sa = sa;
+    st = prepare(glk::kOpI8, glu, a, false, stream, &r);
+    if (st == GEMM_OK) st = quantize(M, K, A, lda, work, a.lda, sa, stream);
+    return st == GEMM_OK ? launch(r, stream) : st;
 }
+
+// dA = D B^T and dB = A^T D for D (M x W), ready to launch
+struct Gradients {
+    bool need_a = false, need_b = false;
+    bool pair = false;  // both in one launch
+    Ready a, b;
+};
 
 // Both gradients as one launch where each is a grid of the same small tiles that leaves CUs idle, with
 // the plans, and so the bits, of either alone (512^3: 4.8 and 5.5 us alone, 6.3 together; M = 509, N =
-// 2752, K = 512: 9.3 and 7.6 alone, 11.5 together). *done says whether it was.
-int paired_gradients(const OpArgs& a, const OpArgs& b, hipStream_t stream, bool* done) {
-    *done = false;
-    if (a.K == 0 || b.K == 0 || !matrix_ok(glk::kOpAbt, false, a) || !matrix_ok(glk::kOpAtb, false, b)) return GEMM_OK;
-    int st = GEMM_OK;
-    const glk::DeviceInfo* dev = glk::current_device(&st);
-    if (!dev) return st;
-    const glk::Plan pa = glk::make_op_plan(a.M, a.N, a.K, *dev, false), pb = glk::make_op_plan(b.M, b.N, b.K, *dev, false);
-    if (pa.bm != pb.bm || pa.bm == 256 || pa.cut_axis || pb.cut_axis) return GEMM_OK;
-    if (pa.grid > dev->cus * int64_t(4) || pb.grid > dev->cus * int64_t(4)) return GEMM_OK;
-    if (pa.ws_floats + pb.ws_floats > dev->ws_floats || pa.counters + pb.counters > dev->ws_counters) return GEMM_OK;
-    glk::Workspace wa, wb;
-    if (pa.ws_floats + pb.ws_floats > 0) {
-        st = glk::stream_workspace(stream, &wa);
-        if (st != GEMM_OK) return st;
-        wb.ws = wa.ws + pa.ws_floats;
-        wb.counters = wa.counters + pa.counters;
+// 2752, K = 512: 9.3 and 7.6 alone, 11.5 together): the second's partials follow the first's.
+void pair_gradients(const glk::DeviceInfo& dev, Gradients* g) {
+    const glk::Plan &pa = g->a.p, &pb = g->b.p;
+    if (g->a.route != Ready::kTiles || g->b.route != Ready::kTiles) return;
+    if (pa.bm != pb.bm || pa.bm == 256 || pa.cut_axis || pb.cut_axis) return;
+    if (pa.grid > dev.cus * int64_t(4) || pb.grid > dev.cus * int64_t(4)) return;
+    if (pa.ws_floats + pb.ws_floats > dev.ws_floats || pa.counters + pb.counters > dev.ws_counters) return;
+    g->pair = true;
+    if (pb.ws_floats > 0 && pa.ws_floats > 0) {
+        g->b.w.ws = g->a.w.ws + pa.ws_floats;
+        g->b.w.counters = g->a.w.counters + pa.counters;
     }
-    if (glk::launch_op_pair(pa.bm, tile_args(glk::kOpAbt, a, pa, 0, a.M, 0, a.N, wa),
-                            tile_args(glk::kOpAtb, b, pb, 0, b.M, 0, b.N, wb), (int)(pa.grid + pb.grid), stream) !=
-        hipSuccess)
-        return GEMM_ERR_HIP;
-    glk::set_last_plan(pb, b.M, b.N, b.K, op_name(glk::kOpAtb, false));
-    *done = true;
-    return GEMM_OK;
 }
 
-// dA = D B^T and dB = A^T D for D (M x W), either skipped when null
-int gradients(int64_t M, int64_t W, int64_t K, const void* D, int64_t ldd, const void* A, int64_t lda,
-              const void* B, int64_t ldb, void* dA, int64_t ldda, void* dB, int64_t lddb, hipStream_t stream) {
-    const OpArgs a{D, B, static_cast<uint16_t*>(dA), nullptr, nullptr, nullptr, M, K, W, ldd, ldb, ldda, 0};
-    const OpArgs b{A, D, static_cast<uint16_t*>(dB), nullptr, nullptr, nullptr, K, W, M, lda, ldd, lddb, 0};
-    const bool need_a = dA && M > 0 && K > 0, need_b = dB && K > 0 && W > 0;
+// either gradient skipped when null
+int prepare_gradients(int64_t M, int64_t W, int64_t K, const void* D, int64_t ldd, const void* A, int64_t lda,
+                      const void* B, int64_t ldb, void* dA, int64_t ldda, void* dB, int64_t lddb, hipStream_t stream,
+                      Gradients* g) {
+    g->need_a = dA && M > 0 && K > 0;
+    g->need_b = dB && K > 0 && W > 0;
     int st = GEMM_OK;
-    if (need_a && need_b) {
-        bool done = false;
-        st = paired_gradients(a, b, stream, &done);
-        if (done) return st;
+    if (g->need_a) {
+        const OpArgs a{D, B, static_cast<uint16_t*>(dA), nullptr, nullptr, nullptr, M, K, W, ldd, ldb, ldda, 0};
+        st = prepare(glk::kOpAbt, false, a, false, stream, &g->a);
     }
-    if (st == GEMM_OK && need_a) st = run_op(glk::kOpAbt, false, a, stream);
-    if (st == GEMM_OK && need_b) st = run_op(glk::kOpAtb, false, b, stream);
+    if (st == GEMM_OK && g->need_b) {
+        const OpArgs b{A, D, static_cast<uint16_t*>(dB), nullptr, nullptr, nullptr, K, W, M, lda, ldd, lddb, 0};
+        st = prepare(glk::kOpAtb, false, b, false, stream, &g->b);
+    }
+    if (st == GEMM_OK && g->need_a && g->need_b) {
+        const glk::DeviceInfo* dev = glk::current_device(&st);
+        if (dev) pair_gradients(*dev, g);
+    }
     return st;
 }
 
-// checks of the operands of `gradients`; W columns of D
+int launch_gradients(const Gradients& g, hipStream_t stream) {
+    if (!g.pair) {
+        int st = g.need_a ? launch(g.a, stream) : GEMM_OK;
+        if (st == GEMM_OK && g.need_b) st = launch(g.b, stream);
+        return st;
+    }
+    const OpArgs &a = g.a.a, &b = g.b.a;
+    if (glk::launch_op_pair(g.a.p.bm, tile_args(glk::kOpAbt, a, g.a.p, 0, a.M, 0, a.N, g.a.w),
+                            tile_args(glk::kOpAtb, b, g.b.p, 0, b.M, 0, b.N, g.b.w), (int)(g.a.p.grid + g.b.p.grid),
+                            stream) != hipSuccess)
+        return GEMM_ERR_HIP;
+    glk::set_last_plan(g.b.p, b.M, b.N, b.K, op_name(glk::kOpAtb, false));
+    return GEMM_OK;
+}
+
+// checks of the operands of the gradients; W columns of D
 int check_gradients(int64_t M, int64_t W, int64_t K, const void* A, int64_t lda, const void* B, int64_t ldb,
                     const void* dA, int64_t ldda, const void* dB, int64_t lddb) {
     if (dA && (ldb < W || ldda < K || (K > 0 && W > 0 && !B))) return GEMM_ERR_INVALID_ARG;
@@ -316,9 +361,11 @@ int gemm_bf16_bwd(int64_t M, int64_t N, int64_t K, const void* dC, int64_t lddc,
     return guarded([&]() -> int {
         if (M < 0 || N < 0 || K < 0 || lddc < N || misaligned(dC, 2)) return GEMM_ERR_INVALID_ARG;
         if ((dA || dB) && M > 0 && N > 0 && K > 0 && !dC) return GEMM_ERR_INVALID_ARG;
-        const int st = check_gradients(M, N, K, A, lda, B, ldb, dA, ldda, dB, lddb);
+        int st = check_gradients(M, N, K, A, lda, B, ldb, dA, ldda, dB, lddb);
         if (st != GEMM_OK) return st;
-        return gradients(M, N, K, dC, lddc, A, lda, B, ldb, dA, ldda, dB, lddb, hip_stream(stream));
+        Gradients g;
+        st = prepare_gradients(M, N, K, dC, lddc, A, lda, B, ldb, dA, ldda, dB, lddb, hip_stream(stream), &g);
+        return st == GEMM_OK ? launch_gradients(g, hip_stream(stream)) : st;
     });
 }
 
@@ -333,7 +380,9 @@ int gemm_bf16_swiglu_train(int64_t M, int64_t N, int64_t K, const void* A, int64
         if (M == 0 || N == 0) return GEMM_OK;
         const OpArgs a{A, B, static_cast<uint16_t*>(C), static_cast<uint16_t*>(GU), nullptr, nullptr,
                        M, N, K, lda, ldb, ldc, ldgu};
-        return run_op(glk::kOpTrain, true, a, hip_stream(stream));
+        Ready r;
+        const int st = prepare(glk::kOpTrain, true, a, false, hip_stream(stream), &r);
+        return st == GEMM_OK ? launch(r, hip_stream(stream)) : st;
     });
 }
 
@@ -347,13 +396,16 @@ int gemm_bf16_swiglu_bwd(int64_t M, int64_t N, int64_t K, const void* dC, int64_
         if (misaligned(dC, 2) || misaligned(GU, 2) || misaligned(dGU, 2)) return GEMM_ERR_INVALID_ARG;
         int st = check_gradients(M, 2 * N, K, A, lda, B, ldb, dA, ldda, dB, lddb);
         if (st != GEMM_OK) return st;
+        Gradients g;
+        st = prepare_gradients(M, 2 * N, K, dGU, lddgu, A, lda, B, ldb, dA, ldda, dB, lddb, hip_stream(stream), &g);
+        if (st != GEMM_OK) return st;
         if (M > 0 && N > 0) {
             if (!glk::current_device(&st)) return st;
             if (glk::launch_swiglu_grad(static_cast<const uint16_t*>(dC), lddc, static_cast<const uint16_t*>(GU), ldgu,
                                         static_cast<uint16_t*>(dGU), lddgu, M, N, hip_stream(stream)) != hipSuccess)
                 return GEMM_ERR_HIP;
         }
-        return gradients(M, 2 * N, K, dGU, lddgu, A, lda, B, ldb, dA, ldda, dB, lddb, hip_stream(stream));
+        return launch_gradients(g, hip_stream(stream));
     });
 }
 

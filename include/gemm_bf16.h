@@ -312,7 +312,7 @@ int gemm_i8_work_bytes(int64_t M, int64_t K, int64_t *bytes);
  * `work` is device memory of at least gemm_i8_work_bytes(M, K) bytes, 16-byte aligned, that the
  * caller owns and may reuse once the call's work on the stream is done; `work_bytes` is its size
  * (GEMM_ERR_INVALID_ARG when it is too small or misaligned). Other errors as gemm_i8, and
- * GEMM_ERR_UNSUPPORTED for M >= 2^24.
+ * GEMM_ERR_UNSUPPORTED for M >= 2^24. A refused call has not written to `work`.
  */
 int gemm_i8_bf16(int64_t M, int64_t N, int64_t K, const void *A, int64_t lda, const void *Wq,
                  int64_t ldwq, const float *Sw, void *C, int64_t ldc, void *work,
@@ -330,7 +330,10 @@ int gemm_i8_swiglu_bf16(int64_t M, int64_t N, int64_t K, const void *A, int64_t 
  * leading dimensions are not multiples of 8, run a general kernel with the same contract, tens of
  * times slower (GEMM_ERR_UNSUPPORTED for an output of 2^24 or more 64 x 64 tiles there); the number
  * of tokens M is free. Deterministic (sums in a fixed order, no atomics on data), enqueued on
- * `stream` without synchronising, using the stream's workspace region like gemm_bf16.
+ * `stream` without synchronising, using the stream's workspace region like gemm_bf16. A call makes all
+ * its checks and plans and gets its workspace before its first launch: one that is refused, or for
+ * which there is no workspace, has written nothing (a dGU that shares GU's memory leaves GU as it was,
+ * so the call may be made again once there is room).
  * ------------------------------------------------------------------------------------------ */
 
 /*

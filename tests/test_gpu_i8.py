@@ -509,3 +509,15 @@ def test_gates_below_the_normal_range(M):
         torch.cuda.synchronize()
         off = np.abs(widen(bits(C)).reshape(M, N) - s * up) - slack
         assert (off <= 0).all(), (g.gemm_last_plan()["kernel"], gates[(off > 0).any(0)])
+
+
+def test_a_refused_call_leaves_its_work_buffer_as_it_was():
+    """A product that the general kernel's grid does not hold: refused before the activations are quantised."""
+    M, N = 1 << 23, 1 << 13
+    A, W = torch.ones(M, 1, dtype=torch.bfloat16, device="cuda"), torch.ones(N, 1, dtype=torch.int8, device="cuda")
+    Sw = torch.ones(N, device="cuda")
+    work = torch.full((g.gemm_i8_work_bytes(M, 1),), 77, dtype=torch.uint8, device="cuda")
+    st = g.lib().gemm_i8_bf16(M, N, 1, A.data_ptr(), 1, W.data_ptr(), 1, Sw.data_ptr(), 64, N, work.data_ptr(), work.numel(),
+                              g.current_stream_handle())
+    torch.cuda.synchronize()
+    assert st == g.GEMM_ERR_UNSUPPORTED and bool((work == 77).all())

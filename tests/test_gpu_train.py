@@ -338,3 +338,68 @@ def test_gates_below_the_normal_range():
         slack = 2.0**-8 * np.abs(want) + (2.0**-19 * size + 2.0**-149) * scale + 2.0**-133
         off = np.abs(dGU.double().cpu().numpy() - want) - slack
         assert (off <= 0).all(), (scale, np.argwhere((off > 0).any(0)).ravel())
+
+
+def test_a_refused_call_leaves_gu_as_it_was():
+    """dGU in GU's memory, and a weight gradient with more tiles than the general kernel's grid holds: the
+    refusal comes before the pass that overwrites GU. (dB is never written: no such memory is needed.)"""
+    K = 1 << 17
+    bA = Buf(1, K, matrix("normal", 1, K, seed=7))
+    wide = 1 << 22           # past the matrix kernels' leading dimensions; 2^11 x 2^16 tiles
+    gu = Buf(1, wide, matrix("normal", 1, wide, seed=9))
+    d = Buf(1, wide // 2, matrix("normal", 1, wide // 2, seed=8))
+    before = gu.bits()
+    st = g.lib().gemm_bf16_swiglu_bwd(1, wide // 2, K, d.ptr(), wide // 2, gu.ptr(), wide, bA.ptr(), K, None, wide, gu.ptr(),
+                                      wide, None, K, 64, wide, g.current_stream_handle())
+    torch.cuda.synchronize()
+    assert st == g.GEMM_ERR_UNSUPPORTED
+    assert np.array_equal(gu.bits(), before)
+
+
+def test_a_call_without_a_workspace_leaves_gu_as_it_was():
+    """The library keeps a workspace for each of 64 streams; the next stream whose product needs one is
+    refused, before a dGU in GU's memory is written. The call then gives, on a stream that has one, the
+    bits of an out-of-place call."""
+    import ctypes
+
+    L = g.lib()
+    M, N, K = 64, 2048, 64          # dA sums over 4096: split
+    bD, bG, bA, bB = (Buf(r, c, matrix("normal", r, c, seed=r + c)) for r, c in ((M, N), (M, 2 * N), (M, K), (K, 2 * N)))
+    want, dA, dB = Buf(M, 2 * N), Buf(M, K), Buf(K, 2 * N)
+
+    def call(dGU, stream):
+        return L.gemm_bf16_swiglu_bwd(M, N, K, bD.ptr(), N, bG.ptr(), 2 * N, bA.ptr(), K, bB.ptr(), 2 * N, dGU.ptr(), 2 * N,
+                                      dA.ptr(), K, dB.ptr(), 2 * N, stream)
+
+    here = g.current_stream_handle()
+    assert call(want, here) == g.GEMM_OK
+    torch.cuda.synchronize()
+    before, want = bG.bits(), want.bits()
+    streams, refused = [], None
+    x, y, z = Buf(64, 4096, matrix("normal", 64, 4096, seed=5)), Buf(64, 4096, matrix("normal", 64, 4096, seed=6)), Buf(64, 64)
+    try:
+        for _ in range(66):
+            h = ctypes.c_void_p()
+            assert L.hipStreamCreate(ctypes.byref(h)) == 0
+            streams.append(h)
+            # x y^T over 4096: split over K, so with partial sums
+            st = L.gemm_bf16_bwd(64, 4096, 64, x.ptr(), 4096, None, 64, y.ptr(), 4096, z.ptr(), 64, None, 4096, h)
+            torch.cuda.synchronize()
+            if st != g.GEMM_OK:
+                assert st == g.GEMM_ERR_UNSUPPORTED
+                refused = h
+                break
+            assert g.gemm_last_plan()["splits"] > 1
+        assert refused is not None
+        assert call(bG, refused) == g.GEMM_ERR_UNSUPPORTED
+        torch.cuda.synchronize()
+        assert np.array_equal(bG.bits(), before)
+        assert call(bG, here) == g.GEMM_OK
+        torch.cuda.synchronize()
+        assert np.array_equal(bG.bits(), want)
+    finally:
+        torch.cuda.synchronize()
+        g.gemm_finalize()
+        g.gemm_init(0)
+        for h in streams:
+            L.hipStreamDestroy(h)
