@@ -14,7 +14,7 @@ namespace {
 using glk::OpArgs;
 
 constexpr int64_t kMaxCodesK = 131071;  // 128 * 128 * K < 2^31
-constexpr int64_t kMaxRows = (int64_t(1) << 24) - 1;  // one workgroup of 256 per row, 32-bit grids
+constexpr int64_t kMaxRows = (int64_t(1) << 24) - 1;  // rows, or tiles, of 256 threads in a 32-bit grid
 
 bool misaligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }
 

@@ -92,28 +92,33 @@ __global__ void __launch_bounds__(256) i8_quantize_any_kernel(const uint16_t* __
 
 hipError_t launch_i8_quantize(const uint16_t* X, int64_t R, int64_t K, int64_t ldx, int8_t* Q, int64_t ldq,
                               float* S, hipStream_t s) {
-    if (R > 0xFFFFFF) return hipErrorInvalidValue;
-    const unsigned grid = (unsigned)R;
+    // a launch holds at most 2^32 - 1 threads: 2^24 - 1 rows of 256, 2^22 - 1 of 1024
+    auto run = [&](auto kernel, int threads, auto k) {
+        const int64_t most = int64_t(0xFFFFFFFF) / threads;
+        for (int64_t r = 0; r < R; r += most)
+            kernel<<<(unsigned)(R - r < most ? R - r : most), threads, 0, s>>>(X + r * ldx, k, ldx, Q + r * ldq, ldq,
+                                                                            S + r);
+    };
     // chunks of 8 elements, a padded row's among them
     const int64_t chunks = (K + 15) / 16 * 2;
     if (chunks > 1024 * 8)
-        i8_quantize_any_kernel<<<grid, 256, 0, s>>>(X, K, ldx, Q, ldq, S);
+        run(i8_quantize_any_kernel, 256, K);
     else if (chunks > 1024 * 4)
-        i8_quantize_kernel<16, 8><<<grid, 1024, 0, s>>>(X, (int)K, ldx, Q, ldq, S);
+        run(i8_quantize_kernel<16, 8>, 1024, (int)K);
     else if (chunks > 1024 * 2)
-        i8_quantize_kernel<16, 4><<<grid, 1024, 0, s>>>(X, (int)K, ldx, Q, ldq, S);
+        run(i8_quantize_kernel<16, 4>, 1024, (int)K);
     else if (chunks > 256 && R <= 512)
-        i8_quantize_kernel<16, 2><<<grid, 1024, 0, s>>>(X, (int)K, ldx, Q, ldq, S);
+        run(i8_quantize_kernel<16, 2>, 1024, (int)K);
     else if (chunks <= 64)
-        i8_quantize_kernel<1, 1><<<grid, 64, 0, s>>>(X, (int)K, ldx, Q, ldq, S);
+        run(i8_quantize_kernel<1, 1>, 64, (int)K);
     else if (chunks <= 256)
-        i8_quantize_kernel<4, 1><<<grid, 256, 0, s>>>(X, (int)K, ldx, Q, ldq, S);
+        run(i8_quantize_kernel<4, 1>, 256, (int)K);
     else if (chunks <= 512)
-        i8_quantize_kernel<4, 2><<<grid, 256, 0, s>>>(X, (int)K, ldx, Q, ldq, S);
+        run(i8_quantize_kernel<4, 2>, 256, (int)K);
     else if (chunks <= 1024)
-        i8_quantize_kernel<4, 4><<<grid, 256, 0, s>>>(X, (int)K, ldx, Q, ldq, S);
+        run(i8_quantize_kernel<4, 4>, 256, (int)K);
     else
-        i8_quantize_kernel<4, 8><<<grid, 256, 0, s>>>(X, (int)K, ldx, Q, ldq, S);
+        run(i8_quantize_kernel<4, 8>, 256, (int)K);
     return hipGetLastError();
 }
 

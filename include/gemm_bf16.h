@@ -266,7 +266,8 @@ int gemm_bf16_packed(int64_t M, int64_t N, int64_t K, const void *A, int64_t lda
  * == 0 is up to a quarter faster.
  * R == 0: nothing. K == 0: S = 0. GEMM_ERR_INVALID_ARG for negative sizes, ldx < K, ldq < K, a
  * null pointer with a non-empty extent, or a misaligned X or S; GEMM_ERR_UNSUPPORTED for R >= 2^24.
- * Deterministic, one launch.
+ * Deterministic, one launch (more where a launch's 2^32 threads do not hold the rows: from 2^22
+ * rows of more than 16384 elements).
  */
 int gemm_i8_quantize(int64_t R, int64_t K, const void *X, int64_t ldx, void *Q, int64_t ldq,
                      float *S, gemm_stream_t stream);

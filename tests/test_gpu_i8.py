@@ -521,3 +521,30 @@ def test_a_refused_call_leaves_its_work_buffer_as_it_was():
                               g.current_stream_handle())
     torch.cuda.synchronize()
     assert st == g.GEMM_ERR_UNSUPPORTED and bool((work == 77).all())
+
+
+def test_quantize_rows_past_one_grid():
+    """2^22 + 3 rows of more than 16384 elements, 1024 threads each: more threads than one launch holds. Rows
+    on both sides of every launch's end get their codes; the others, zeros, get zeros."""
+    R, K = (1 << 22) + 3, 16385
+    ld = 16392
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < 220 << 30:
+        pytest.skip("needs 206 GB of device memory")
+    some = [0, 1, (1 << 22) - 2, (1 << 22) - 1, 1 << 22, R - 1]
+    rng = np.random.default_rng(1)
+    xb = bf16_of(rng.normal(size=(len(some), K)))
+    wq, ws = want_codes(widen(xb))
+    X = torch.zeros(R, ld, dtype=torch.bfloat16, device="cuda")
+    X[some, :K] = torch.from_numpy(xb.view(np.int16)).view(torch.bfloat16).cuda()
+    Q = torch.full((R, ld), 99, dtype=torch.int8, device="cuda")
+    S = torch.full((R,), -1.0, device="cuda")
+    g.gemm_i8_quantize(R, K, X.data_ptr(), ld, Q.data_ptr(), ld, S.data_ptr(), g.current_stream_handle())
+    torch.cuda.synchronize()
+    assert np.array_equal(Q[some, :K].cpu().numpy(), wq) and np.array_equal(S[some].cpu().numpy(), ws)
+    assert int((S != 0).sum()) == len(some) and not Q[some, K:].any()
+    for r in range(0, R, 1 << 19):
+        rows = Q[r: r + (1 << 19)].view(torch.int64).any(1)
+        assert [r + i for i in rows.nonzero().flatten().tolist()] == [i for i in some if r <= i < r + (1 << 19)]
+    del X, Q, S
+    torch.cuda.empty_cache()
