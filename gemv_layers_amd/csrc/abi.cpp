@@ -10,6 +10,7 @@
 #include <atomic>
 #include <mutex>
 #include <string>
+#include <utility>
 
 #include "abi.h"
 #include "gemm_bf16.h"
@@ -68,18 +69,16 @@ std::atomic<int> g_ready_count{0};
 std::string g_last_plan = "{}";
 // The 8-bit and training calls keep their plan as it is, with the operator's name, and
 // gemm_last_plan writes it out when asked (the text costs more than the rest of a small call's
-// host work). `op` null: g_last_plan is the newest.
+// host work). No op in it: g_last_plan is the newest. `with`: the product of the same launch, if any.
 struct LastOp {
-    const char* op = nullptr;
-    glk::Plan plan;
-    int64_t M = 0, N = 0, K = 0;
+    glk::OpPlan plan, with;
 };
 LastOp g_last_op;
 
 // (with g_mu held)
 void set_last_text(std::string s) {
     g_last_plan = std::move(s);
-    g_last_op.op = nullptr;
+    g_last_op.plan.op = nullptr;
 }
 
 // The workspace region of `stream` on the device of `ds` (the current device), made on the
@@ -462,13 +461,21 @@ int stream_workspace(hipStream_t stream, Workspace* out) {
     return GEMM_OK;
 }
 
-void set_last_plan(const Plan& p, int64_t M, int64_t N, int64_t K, const char* op) {
+void set_last_plan(OpPlan plan, OpPlan with) {
     std::lock_guard<std::mutex> lk(g_mu);
-    g_last_op.op = op;
-    g_last_op.plan = p;
-    g_last_op.M = M;
-    g_last_op.N = N;
-    g_last_op.K = K;
+    g_last_op.plan = std::move(plan);
+    g_last_op.with = std::move(with);
+}
+
+// the plan as JSON, with the operator's name in it and in a cut product's rest
+static std::string op_plan_json(const OpPlan& o) {
+    std::string s = plan_json(o.plan, o.M, o.N, o.K);
+    const std::string key = "\"op\": \"";
+    for (size_t at = s.find(key); at != std::string::npos; at = s.find(key, at)) {
+        at += key.size();
+        s.replace(at, s.find('"', at) - at, o.op);
+    }
+    return s;
 }
 
 }  // namespace glk
@@ -597,12 +604,11 @@ int gemm_wave_efficiency(int64_t ctas, int64_t slots, double* efficiency, int64_
 
 int gemm_last_plan(char* buf, int len) {
     std::lock_guard<std::mutex> lk(g_mu);
-    if (!g_last_op.op) return copy_out(g_last_plan, buf, len);
-    std::string s = glk::plan_json(g_last_op.plan, g_last_op.M, g_last_op.N, g_last_op.K);
-    const std::string key = "\"op\": \"";
-    for (size_t at = s.find(key); at != std::string::npos; at = s.find(key, at)) {
-        at += key.size();
-        s.replace(at, s.find('"', at) - at, g_last_op.op);
+    if (!g_last_op.plan.op) return copy_out(g_last_plan, buf, len);
+    std::string s = glk::op_plan_json(g_last_op.plan);
+    if (g_last_op.with.op) {
+        s.pop_back();
+        s += ", \"with\": " + glk::op_plan_json(g_last_op.with) + "}";
     }
     return copy_out(s, buf, len);
 }

@@ -18,7 +18,13 @@ struct Workspace {
 const DeviceInfo* current_device(int* status);
 // the workspace region of `stream` on the current device, made on its first use
 int stream_workspace(hipStream_t stream, Workspace* out);
-// the plan of the call that just succeeded; `op` is a static string
-void set_last_plan(const Plan& p, int64_t M, int64_t N, int64_t K, const char* op);
+// a product's plan and sizes; `op` is a static string
+struct OpPlan {
+    const char* op = nullptr;
+    Plan plan;
+    int64_t M = 0, N = 0, K = 0;
+};
+// the plan of the call that just succeeded, and that of the other product of its launch
+void set_last_plan(OpPlan plan, OpPlan with = {});
 
 }  // namespace glk

@@ -130,6 +130,8 @@ int prepare(int mode, bool glu, const OpArgs& a, bool fused, hipStream_t stream,
     return GEMM_OK;
 }
 
+glk::OpPlan plan_of(const Ready& r) { return {op_name(r.mode, r.glu), r.p, r.a.M, r.a.N, r.a.K}; }
+
 int launch(const Ready& r, hipStream_t stream) {
     const OpArgs& a = r.a;
     const glk::Plan& p = r.p;
@@ -162,7 +164,7 @@ int launch(const Ready& r, hipStream_t stream) {
         }
     }
     if (e != hipSuccess) return GEMM_ERR_HIP;
-    glk::set_last_plan(p, a.M, a.N, a.K, op_name(r.mode, r.glu));
+    glk::set_last_plan(plan_of(r));
     return GEMM_OK;
 }
 
@@ -290,7 +292,7 @@ int launch_gradients(const Gradients& g, hipStream_t stream) {
                             tile_args(glk::kOpAtb, b, g.b.p, 0, b.M, 0, b.N, g.b.w), (int)(g.a.p.grid + g.b.p.grid),
                             stream) != hipSuccess)
         return GEMM_ERR_HIP;
-    glk::set_last_plan(g.b.p, b.M, b.N, b.K, op_name(glk::kOpAtb, false));
+    glk::set_last_plan(plan_of(g.b), plan_of(g.a));
     return GEMM_OK;
 }
 

@@ -407,11 +407,13 @@ int gemm_wave_efficiency(int64_t ctas, int64_t slots, double *efficiency, int64_
 /*
  * gemm_last_plan: the JSON plan (the same fields as gemm_plan_describe) of the last successful
  * compute call in this process, any device or stream, copied into buf (len bytes, always
- * NUL-terminated when len > 0). The plan is chosen per call from the shape and the device, so
- * this is how a benchmark or test reads which kernel, tile and split a call took (spark-kernels
- * post, "1024 cubed and the decode shapes": the launch picks the tile per call). Host-only; touches
- * no HIP state. GEMM_ERR_INVALID_ARG for a null buf, len <= 0, or a plan longer than len - 1
- * (buf then holds the truncated text).
+ * NUL-terminated when len > 0). Of a call that makes two products it is the second one's (of a
+ * backward pass with both gradients, dB's); where one launch made both, "with" holds the first one's
+ * plan, and the launch's grid is the sum of the two. The plan is chosen per call from the shape and
+ * the device, so this is how a benchmark or test reads which kernel, tile and split a call took
+ * (spark-kernels post, "1024 cubed and the decode shapes": the launch picks the tile per call).
+ * Host-only; touches no HIP state. GEMM_ERR_INVALID_ARG for a null buf, len <= 0, or a plan longer
+ * than len - 1 (buf then holds the truncated text).
  */
 int gemm_last_plan(char *buf, int len);
 

@@ -403,3 +403,21 @@ def test_a_call_without_a_workspace_leaves_gu_as_it_was():
         g.gemm_init(0)
         for h in streams:
             L.hipStreamDestroy(h)
+
+
+def test_last_plan_names_both_gradients_of_one_launch():
+    def t(*s):
+        return torch.zeros(*s, dtype=torch.bfloat16, device="cuda")
+
+    sizes = lambda p: (p["op"], p["M"], p["N"], p["K"])  # noqa: E731
+    D, A, B = t(512, 264), t(512, 520), t(520, 264)
+    g.matmul_backward(D, A, B)
+    p = g.gemm_last_plan()
+    assert sizes(p) == ("grad_b", 520, 264, 512) and sizes(p["with"]) == ("grad_a", 512, 520, 264)
+    g.matmul_backward(D, A, B, need_dA=False)
+    assert sizes(g.gemm_last_plan()) == ("grad_b", 520, 264, 512) and "with" not in g.gemm_last_plan()
+    g.matmul_backward(D, A, B, need_dB=False)
+    assert sizes(g.gemm_last_plan()) == ("grad_a", 512, 520, 264) and "with" not in g.gemm_last_plan()
+    # a launch each: the plan is the second's
+    g.matmul_backward(t(4096, 4096), t(4096, 4096), t(4096, 4096))
+    assert g.gemm_last_plan()["op"] == "grad_b" and "with" not in g.gemm_last_plan()
