@@ -11,6 +11,7 @@
 #include <ATen/ops/empty.h>
 #include <c10/core/DeviceGuard.h>
 #include <c10/hip/HIPStream.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <exception>
@@ -170,7 +171,8 @@ bool truth(PyObject* o) {
     return v != 0;
 }
 
-// a call's Python face: `want` positional arguments, C++ exceptions turned into Python ones
+// a call's Python face: `want` positional arguments, C++ exceptions turned into the Python ones that
+// PyTorch's own functions raise for them (torch.OutOfMemoryError among them)
 template <PyObject* (*F)(PyObject* const*), Py_ssize_t want>
 PyObject* entry(PyObject*, PyObject* const* a, Py_ssize_t n) {
     try {
@@ -178,8 +180,8 @@ PyObject* entry(PyObject*, PyObject* const* a, Py_ssize_t n) {
         return F(a);
     } catch (const Failed&) {
         return nullptr;
-    } catch (const std::exception& e) {
-        PyErr_SetString(PyExc_RuntimeError, e.what());
+    } catch (...) {
+        torch::translate_exception_to_python(std::current_exception());
         return nullptr;
     }
 }

@@ -548,3 +548,15 @@ def test_quantize_rows_past_one_grid():
         assert [r + i for i in rows.nonzero().flatten().tolist()] == [i for i in some if r <= i < r + (1 << 19)]
     del X, Q, S
     torch.cuda.empty_cache()
+
+
+def test_an_output_that_does_not_fit_raises_what_torch_raises():
+    """torch.OutOfMemoryError, which callers catch to free memory and try again; the next call runs."""
+    n = 1 << 20                                            # outputs of 2^41 bytes
+    q, s = torch.ones(n, 16, dtype=torch.int8, device="cuda"), torch.ones(n, device="cuda")
+    x = torch.ones(n, 16, dtype=torch.bfloat16, device="cuda")
+    for call in (lambda: g.i8_matmul(q, s, q, s), lambda: g.i8_linear(x, q, s), lambda: g.i8_swiglu_linear(x, q, s),
+                 lambda: g.swiglu_forward(x, x.view(16, n))):
+        with pytest.raises(torch.OutOfMemoryError):
+            call()
+    assert bool((g.i8_matmul(q[:2], s[:2], q, s) == 16).all())
