@@ -367,7 +367,10 @@ def swiglu_matmul(A, B, out=None, stream=None):
 #
 # A small product takes the GPU a few microseconds, so the tensors are checked, and the outputs made,
 # in a C++ module (_torch_ops). The functions below name its arguments. With `stream`, a handle, a call
-# runs as under torch.cuda.stream of it: its outputs belong to that stream.
+# runs as under torch.cuda.stream of it: its outputs belong to that stream. They record no graph: a
+# tensor that requires grad, with grad mode on, is refused (RuntimeError) by all but i8_quantize, whose
+# codes have no gradient. Wrap swiglu_forward and swiglu_backward in a torch.autograd.Function to train
+# with autograd.
 
 _ops = None
 

@@ -10,6 +10,7 @@
 
 #include <ATen/ops/empty.h>
 #include <c10/core/DeviceGuard.h>
+#include <c10/core/GradMode.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -55,20 +56,32 @@ const char* type_name(at::ScalarType t) {
     }
 }
 
+// The calls record no graph. Their results' gradients would be lost without a word where autograd is to
+// follow them: refused, as PyTorch refuses out=.
+void no_graph(const at::Tensor& t, const char* name) {
+    if (c10::GradMode::is_enabled() && t.requires_grad())
+        fail(PyExc_RuntimeError,
+             "%s requires grad, and this call records no graph: use it in a torch.autograd.Function or under "
+             "torch.no_grad(), or detach %s",
+             name, name);
+}
+
 struct Rows {
     int64_t rows, cols, ld;
     void* p;
 };
 
-// a 2-D device tensor with unit column stride and rows that do not overlap; -1: any size
+// a 2-D device tensor with unit column stride and rows that do not overlap; -1: any size. `codes_only`:
+// the call's results are codes and their scales, which have no gradient.
 Rows rows_of(const at::Tensor& t, const char* name, at::ScalarType type, int64_t rows = -1, int64_t cols = -1,
-             int device = -1) {
+             int device = -1, bool codes_only = false) {
     if (t.scalar_type() != type) fail(PyExc_TypeError, "%s must be %s", name, type_name(type));
     if (t.dim() != 2) fail(PyExc_ValueError, "%s must have two dimensions, not %lld", name, (long long)t.dim());
     Rows r{t.size(0), t.size(1), t.stride(0), nullptr};
     if ((rows >= 0 && r.rows != rows) || (cols >= 0 && r.cols != cols))
         fail(PyExc_ValueError, "%s must be %lld x %lld (-1: any), not %lld x %lld", name, (long long)rows,
              (long long)cols, (long long)r.rows, (long long)r.cols);
+    if (!codes_only) no_graph(t, name);
     if (!t.is_cuda()) fail(PyExc_ValueError, "%s must be a device tensor", name);
     if (device >= 0 && t.get_device() != device) fail(PyExc_ValueError, "all tensors must be on one device");
     if (t.stride(1) != 1 && r.cols > 1 && r.rows > 0) fail(PyExc_ValueError, "%s needs unit column stride", name);
@@ -83,6 +96,7 @@ Rows rows_of(const at::Tensor& t, const char* name, at::ScalarType type, int64_t
 const float* scales_of(const at::Tensor& t, const char* name, int64_t n, int device) {
     if (t.scalar_type() != at::kFloat || t.dim() != 1 || t.size(0) != n || !t.is_cuda())
         fail(PyExc_ValueError, "%s must be a device vector of %lld float32 values", name, (long long)n);
+    no_graph(t, name);
     if (t.get_device() != device) fail(PyExc_ValueError, "all tensors must be on one device");
     if (n > 1 && t.stride(0) != 1) fail(PyExc_ValueError, "%s needs unit stride", name);
     return static_cast<const float*>(t.data_ptr());
@@ -196,7 +210,7 @@ at::Tensor output(PyObject* out, const at::Tensor& like, int64_t M, int64_t N, i
 // (X, stream) -> (Q, S)
 PyObject* quantize(PyObject* const* a) {
     const at::Tensor& X = tensor(a[0], "X");
-    const Rows x = rows_of(X, "X", at::kBFloat16);
+    const Rows x = rows_of(X, "X", at::kBFloat16, -1, -1, -1, true);
     const Place at(a[1], X);
     const int64_t ldq = (x.cols + 15) / 16 * 16;
     at::Tensor Q = make(X, at::kChar, x.rows, ldq);

@@ -421,3 +421,38 @@ def test_last_plan_names_both_gradients_of_one_launch():
     # a launch each: the plan is the second's
     g.matmul_backward(t(4096, 4096), t(4096, 4096), t(4096, 4096))
     assert g.gemm_last_plan()["op"] == "grad_b" and "with" not in g.gemm_last_plan()
+
+
+def test_in_an_autograd_function():
+    """The calls refuse tensors that require grad, and train inside a torch.autograd.Function, whose
+    gradients are those of the calls by themselves."""
+
+    class Gated(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, w):
+            C, GU = g.swiglu_forward(x, w)
+            ctx.save_for_backward(x, w, GU)
+            return C
+
+        @staticmethod
+        def backward(ctx, dC):
+            x, w, GU = ctx.saved_tensors
+            return g.swiglu_backward(dC, GU, x, w)[:2]
+
+    dev = lambda *s: (torch.randn(*s, generator=torch.Generator().manual_seed(s[0])) * 0.2).bfloat16().cuda()  # noqa: E731
+    x, w, d = dev(70, 136).requires_grad_(), dev(136, 160).requires_grad_(), dev(70, 80)
+    y, (q, s) = x.detach(), g.i8_quantize(w)
+    sg = s.clone().requires_grad_()
+    for call in (lambda: g.swiglu_forward(x, w.detach()), lambda: g.swiglu_forward(y, w),
+                 lambda: g.matmul_backward(d, y, w[:, :80]), lambda: g.i8_linear(y[:, :160] @ y.new_zeros(136, 160), q, sg),
+                 lambda: g.i8_linear(y, g.i8_quantize(y)[0], torch.ones(70, device="cuda"),
+                                     out=torch.zeros(70, 70, dtype=torch.bfloat16, device="cuda").requires_grad_())):
+        with pytest.raises(RuntimeError, match="requires grad"):
+            call()
+    C = Gated.apply(x, w)
+    C.backward(d)
+    want, GU = g.swiglu_forward(y, w.detach())
+    dA, dB, _ = g.swiglu_backward(d, GU, y, w.detach())
+    assert torch.equal(C, want) and torch.equal(x.grad, dA) and torch.equal(w.grad, dB)
+    with torch.no_grad():
+        assert torch.equal(g.swiglu_forward(x, w)[0], want)

@@ -39,3 +39,23 @@ def test_argument_counts():
             getattr(m, name)(*[None] * (n - 1))
         with pytest.raises(TypeError):
             getattr(m, name)(*[None] * (n + 1))
+
+
+def grad(t):
+    return t.clone().requires_grad_()
+
+
+@pytest.mark.parametrize("call,name", [
+    (lambda: g.swiglu_forward(grad(BF), BF.t()), "A"), (lambda: g.i8_linear(grad(BF), Q, S), "A"),
+    (lambda: g.i8_swiglu_linear(grad(BF), Q, S), "A"), (lambda: g.matmul_backward(BF, grad(BF), BF), "A"),
+    (lambda: g.swiglu_backward(BF, BF, grad(BF), BF), "A")])
+def test_a_graph_is_not_lost_without_a_word(call, name):
+    with pytest.raises(RuntimeError, match=f"{name} requires grad"):
+        call()
+    with torch.no_grad(), pytest.raises(ValueError):     # as for any host tensor
+        call()
+
+
+def test_codes_have_no_gradient():
+    with pytest.raises(ValueError):                      # refused as a host tensor only
+        g.i8_quantize(grad(BF))
