@@ -4,6 +4,7 @@ that hands PyTorch tensors to it."""
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.util
 import os
 import subprocess
 import sys
@@ -56,20 +57,24 @@ def _build_torch_ops() -> str:
 
 
 def build(jobs: int | None = None) -> str:
-    """Compile every source and link libgemm_bf16.so and _torch_ops.so next to this file. Always
-    recompiles."""
+    """Compile every source and link libgemm_bf16.so next to this file, then _torch_ops.so where PyTorch
+    is installed (the library needs none). Always recompiles."""
     os.makedirs(BUILD, exist_ok=True)
     jobs = jobs or min(len(SOURCES), max(1, min(16, len(os.sched_getaffinity(0)))))
     with cf.ThreadPoolExecutor(max_workers=jobs) as ex:
-        torch_ops = ex.submit(_build_torch_ops)
+        torch_ops = ex.submit(_build_torch_ops) if importlib.util.find_spec("torch") else None
         objs = list(ex.map(_compile, SOURCES))
-        torch_ops.result()
-    tmp = OUT + ".tmp%d" % os.getpid()
-    cmd = [HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *objs]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, OUT)
+        tmp = OUT + ".tmp%d" % os.getpid()
+        cmd = [HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *objs]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+        os.replace(tmp, OUT)
+        if torch_ops:
+            torch_ops.result()
+        else:
+            print("PyTorch is not installed: _torch_ops.so, the 8-bit and training helpers' module, is not built",
+                  file=sys.stderr)
     return OUT
 
 
