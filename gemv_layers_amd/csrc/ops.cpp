@@ -123,7 +123,8 @@ int prepare(int mode, bool glu, const OpArgs& a, bool fused, hipStream_t stream,
     } else {
         // codes: planned as the bf16 product whose k-steps have the same bytes and matrix-core cycles
         r->route = Ready::kTiles;
-        r->p = glk::make_op_plan(a.M, a.N, mode == glk::kOpI8 ? (a.K + 1) / 2 : a.K, *dev, glu);
+        r->p = glk::make_op_plan(a.M, a.N, mode == glk::kOpI8 ? (a.K + 1) / 2 : a.K, *dev, glu,
+                                 mode == glk::kOpI8 || mode == glk::kOpAbt);
         if (r->p.grid > INT32_MAX) return GEMM_ERR_UNSUPPORTED;
         if (r->p.ws_floats > 0) return glk::stream_workspace(stream, &r->w);
     }

@@ -404,7 +404,7 @@ Plan make_packed_plan(int64_t M, int64_t N, int64_t K, const DeviceInfo& dev) {
 // two), but none of less than 28 steps once the tiles alone fill the CUs (1000^3, 32 steps: 8.0 whole,
 // 9.8 in two), and not a few more workgroups than CUs, whose second round is nearly empty (codes 64
 // x 4096 x 11008 in four pieces, 256 workgroups, 15.4; in five, 320 workgroups, 18.8).
-Plan make_op_plan(int64_t M, int64_t N, int64_t K, const DeviceInfo& dev, bool glu) {
+Plan make_op_plan(int64_t M, int64_t N, int64_t K, const DeviceInfo& dev, bool glu, bool contiguous) {
     const int64_t tm = cdiv(M, 64), tn = cdiv(glu ? 2 * N : N, 64), kt = cdiv(K, 32);
     const int64_t most = dev.cus + dev.cus / 2;
     const int64_t tiles = 2 * (int64_t)dev.cus, all_steps = tm == 1 ? 32768 : 16384;
@@ -413,17 +413,28 @@ Plan make_op_plan(int64_t M, int64_t N, int64_t K, const DeviceInfo& dev, bool g
         // the strip of a sparse last wave may be cut off across columns too, as its kernels take the
         // up half's offset apart from the width
         Plan q = make_plan(M, glu ? 2 * N : N, K, dev, true, 2, false);
-        // two pieces on more than two thirds of the CUs, which pay for the other products (make_plan),
-        // lose here: on all of twelve random products of 175 to 252 tiles and 99 to 141 k-steps, by 8-15%
-        // (C = A B^T 1249 x 2232 x 3472 33.2 us whole, 38.4 in two)
+        // Two pieces on more than two thirds of the CUs, which pay for the other products from 96 k-steps on
+        // (make_plan), pay here from 200 where both operands hold the summed index contiguous, whose copies
+        // read lines of two k-steps, and from 120 where one is strided. Two pieces against whole, geometric
+        // means over 176, 192, 240 and 256 tiles at 96, 120, 141, 170, 200, 256, 344 and 688 k-steps: C = A
+        // B^T 1.12, 1.09, 1.15, 1.06, 1.03, 0.95, 1.03, 0.94; codes 1.06, 1.04, 1.08, 1.00, 0.97, 0.93, 0.96,
+        // 0.92; C = A^T B 1.01, 0.98, 0.97, 0.94, 0.93, 0.92, 0.90, 0.86; the gated forward 1.01, 0.99, 0.97,
+        // 0.93, 0.90, 0.88, 0.86, 0.85 (2048 x 2048 x 11008, us: C = A B^T 90.8 whole and 88.3, C = A^T B 101.7
+        // and 98.8; codes 2048 x 2048 x 22016 96.5 and 94.3). A piece takes an even number of k-steps there:
+        // one that starts inside a line reads it twice (170 steps, two of 85 against whole: C = A B^T 1.32,
+        // codes 1.25).
         if (q.bm == 128 && q.splits == 2 && 3 * q.tiles > 2 * (int64_t)dev.cus) {
-            q.sched = kSchedDataParallel;
-            q.splits = 1;
-            q.kt_per_split = (int)kt;
-            q.grid = q.tiles;
-            q.ws_floats = q.counters = 0;
-            q.reason = "128x128 tiles";
-            finish_waves(q);
+            if (kt < (contiguous ? 200 : 120)) {
+                q.sched = kSchedDataParallel;
+                q.splits = 1;
+                q.kt_per_split = (int)kt;
+                q.grid = q.tiles;
+                q.ws_floats = q.counters = 0;
+                q.reason = "128x128 tiles";
+                finish_waves(q);
+            } else {
+                q.kt_per_split += q.kt_per_split & 1;
+            }
         }
         q.glu = glu;
         for (Plan& r : q.rest) r.glu = glu;

@@ -80,8 +80,8 @@ Plan make_packed_plan(int64_t M, int64_t N, int64_t K, const DeviceInfo& dev);
 
 // The 8-bit and training products on MFMA tiles: an M x N output (gated: 2N weight columns) over K
 // bf16 elements, or the 8-bit codes that fill as many bytes. make_plan's tiles, and 64 x 64 ones for
-// small outputs.
-Plan make_op_plan(int64_t M, int64_t N, int64_t K, const DeviceInfo& dev, bool glu);
+// small outputs. `contiguous`: both operands hold the summed index contiguous in memory.
+Plan make_op_plan(int64_t M, int64_t N, int64_t K, const DeviceInfo& dev, bool glu, bool contiguous);
 
 // The 8-bit product of few rows (1 <= M <= 64, K >= 1; N outputs, gated: 2N weight rows): groups of
 // 16-row weight tiles (strip rows) times K pieces (splits), one workgroup of `threads` each.
