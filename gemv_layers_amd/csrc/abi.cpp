@@ -480,6 +480,92 @@ static std::string op_plan_json(const OpPlan& o) {
 
 }  // namespace glk
 
+// ---- bodies of C entries that make a plan's text ---------------------------------------------------
+
+namespace {
+
+int plan_describe(int64_t M, int64_t N, int64_t K, int cus, int flags, char* buf, int len) {
+    if (M < 0 || N < 0 || K < 0 || cus <= 0 || (flags & ~15)) return GEMM_ERR_INVALID_ARG;
+    if (flags & GEMM_PLAN_PACKED) {
+        if (flags != GEMM_PLAN_PACKED) return GEMM_ERR_INVALID_ARG;
+        if (M > 64 || (N % 16) || (K % 32)) return GEMM_ERR_UNSUPPORTED;
+        glk::DeviceInfo dev;
+        dev.cus = cus;
+        dev.nxcd = (cus % 8 == 0) ? 8 : 1;
+        dev.ws_floats = kWsFloats;
+        dev.ws_counters = kWsCounters;
+        return copy_out(glk::plan_json(glk::make_packed_plan(M, N, K, dev), M, N, K), buf, len);
+    }
+    if (flags & GEMM_PLAN_MX) {
+        if (flags != GEMM_PLAN_MX) return GEMM_ERR_INVALID_ARG;
+        if (M > 64 || (N % 16) || (K % 128)) return GEMM_ERR_UNSUPPORTED;
+        glk::DeviceInfo dev;
+        dev.cus = cus;
+        dev.nxcd = (cus % 8 == 0) ? 8 : 1;
+        dev.ws_floats = kMxPartialFloats;
+        dev.ws_counters = kWsCounters;
+        return copy_out(glk::plan_json(glk::make_mx_plan(M, N, K, dev), M, N, K), buf, len);
+    }
+    const bool skinny = (flags & GEMM_PLAN_SKINNY) != 0, glu = (flags & GEMM_PLAN_SWIGLU) != 0;
+    if (glu && N > INT64_MAX / 2) return GEMM_ERR_INVALID_ARG;
+    if (skinny && (M < 1 || M > 64)) return GEMM_ERR_UNSUPPORTED;
+    glk::DeviceInfo dev;
+    dev.cus = cus;
+    dev.nxcd = (cus % 8 == 0) ? 8 : 1;
+    dev.ws_floats = kWsFloats;
+    dev.ws_counters = kWsCounters;
+    const glk::Plan p = glk::make_plan(M, N, K, dev, true, skinny ? 1 : 0, glu);
+    return copy_out(glk::plan_json(p, M, N, K), buf, len);
+}
+
+int last_plan(char* buf, int len) {
+    std::lock_guard<std::mutex> lk(g_mu);
+    if (!g_last_op.plan.op) return copy_out(g_last_plan, buf, len);
+    std::string s = glk::op_plan_json(g_last_op.plan);
+    if (g_last_op.with.op) {
+        s.pop_back();
+        s += ", \"with\": " + glk::op_plan_json(g_last_op.with) + "}";
+    }
+    return copy_out(s, buf, len);
+}
+
+int mx_decode_bf16(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const void* Wp,
+                   const void* Sp, void* C, int64_t ldc, hipStream_t s) {
+    if (M < 0 || N < 0 || K < 0 || lda < K || ldc < N) return GEMM_ERR_INVALID_ARG;
+    if (M > 64 || (N % 16) || (K % 128)) return GEMM_ERR_UNSUPPORTED;
+    if (M == 0 || N == 0) return GEMM_OK;
+    if (M > 0 && K > 0 && !A) return GEMM_ERR_INVALID_ARG;
+    if (K == 0) return mx_decode(M, N, K, nullptr, 0, nullptr, 0, Wp, Sp, C, ldc, s);
+    int st = GEMM_OK;
+    DeviceState* ds = current_state(&st);
+    if (!ds) return st;
+    // one or two rows: converted inside the product, one launch (when the piece's rows fit LDS)
+    if (M <= 2) {
+        glk::DeviceInfo info = ds->info;
+        info.ws_floats = kMxPartialFloats;
+        const glk::Plan p = glk::make_mx_plan(M, N, K, info);
+        glk::MxArgs probe;
+        const int ks = (int)(K / 128);
+        if (p.kernel == glk::kKernMx && glk::mx_fused_layout((ks + p.splits - 1) / p.splits, p.strip / 16, probe) >= 0) {
+            return mx_decode(M, N, K, nullptr, K, nullptr, K / 32, Wp, Sp, C, ldc, s, A, lda);
+        }
+    }
+    // the quantised activations go to the workspace tail (both launches on the same stream)
+    const int64_t ldaq = (K + 15) / 16 * 16, ldas = K / 32;
+    if (M * ldaq + M * ldas + 16 > kMxActBytes) return GEMM_ERR_UNSUPPORTED;
+    Region* rg = nullptr;
+    st = region_for(*ds, s, &rg);
+    if (st != GEMM_OK) return st;
+    uint8_t* base = reinterpret_cast<uint8_t*>(rg->ws + kMxPartialFloats);
+    uint8_t* aq = base;
+    uint8_t* as = base + (M * ldaq + 15) / 16 * 16;
+    st = mx_quantize_act(M, K, A, lda, aq, ldaq, as, ldas, s);
+    if (st != GEMM_OK) return st;
+    return mx_decode(M, N, K, aq, ldaq, as, ldas, Wp, Sp, C, ldc, s);
+}
+
+}  // namespace
+
 extern "C" {
 
 int gemm_init(int device) {
@@ -539,61 +625,31 @@ int gemm_init(int device) {
 
 int gemm_bf16(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const void* B,
               int64_t ldb, void* C, int64_t ldc, gemm_stream_t stream) {
-    return run(M, N, K, A, lda, B, ldb, C, ldc, reinterpret_cast<hipStream_t>(stream), 0);
+    return glk::guarded([&] { return run(M, N, K, A, lda, B, ldb, C, ldc, reinterpret_cast<hipStream_t>(stream), 0); });
 }
 
 int gemm_bf16_noalloc(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const void* B,
                       int64_t ldb, void* C, int64_t ldc, gemm_stream_t stream) {
-    return run(M, N, K, A, lda, B, ldb, C, ldc, reinterpret_cast<hipStream_t>(stream), 0, false, true);
+    return glk::guarded([&] { return run(M, N, K, A, lda, B, ldb, C, ldc, reinterpret_cast<hipStream_t>(stream), 0, false, true); });
 }
 
 int gemm_bf16_skinny(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const void* B,
                      int64_t ldb, void* C, int64_t ldc, gemm_stream_t stream) {
-    return run(M, N, K, A, lda, B, ldb, C, ldc, reinterpret_cast<hipStream_t>(stream), 1);
+    return glk::guarded([&] { return run(M, N, K, A, lda, B, ldb, C, ldc, reinterpret_cast<hipStream_t>(stream), 1); });
 }
 
 int gemm_bf16_tiled(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const void* B,
                     int64_t ldb, void* C, int64_t ldc, gemm_stream_t stream) {
-    return run(M, N, K, A, lda, B, ldb, C, ldc, reinterpret_cast<hipStream_t>(stream), 2);
+    return glk::guarded([&] { return run(M, N, K, A, lda, B, ldb, C, ldc, reinterpret_cast<hipStream_t>(stream), 2); });
 }
 
 int gemm_bf16_swiglu(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const void* B,
                      int64_t ldb, void* C, int64_t ldc, gemm_stream_t stream) {
-    return run(M, N, K, A, lda, B, ldb, C, ldc, reinterpret_cast<hipStream_t>(stream), 0, true);
+    return glk::guarded([&] { return run(M, N, K, A, lda, B, ldb, C, ldc, reinterpret_cast<hipStream_t>(stream), 0, true); });
 }
 
 int gemm_plan_describe(int64_t M, int64_t N, int64_t K, int cus, int flags, char* buf, int len) {
-    if (M < 0 || N < 0 || K < 0 || cus <= 0 || (flags & ~15)) return GEMM_ERR_INVALID_ARG;
-    if (flags & GEMM_PLAN_PACKED) {
-        if (flags != GEMM_PLAN_PACKED) return GEMM_ERR_INVALID_ARG;
-        if (M > 64 || (N % 16) || (K % 32)) return GEMM_ERR_UNSUPPORTED;
-        glk::DeviceInfo dev;
-        dev.cus = cus;
-        dev.nxcd = (cus % 8 == 0) ? 8 : 1;
-        dev.ws_floats = kWsFloats;
-        dev.ws_counters = kWsCounters;
-        return copy_out(glk::plan_json(glk::make_packed_plan(M, N, K, dev), M, N, K), buf, len);
-    }
-    if (flags & GEMM_PLAN_MX) {
-        if (flags != GEMM_PLAN_MX) return GEMM_ERR_INVALID_ARG;
-        if (M > 64 || (N % 16) || (K % 128)) return GEMM_ERR_UNSUPPORTED;
-        glk::DeviceInfo dev;
-        dev.cus = cus;
-        dev.nxcd = (cus % 8 == 0) ? 8 : 1;
-        dev.ws_floats = kMxPartialFloats;
-        dev.ws_counters = kWsCounters;
-        return copy_out(glk::plan_json(glk::make_mx_plan(M, N, K, dev), M, N, K), buf, len);
-    }
-    const bool skinny = (flags & GEMM_PLAN_SKINNY) != 0, glu = (flags & GEMM_PLAN_SWIGLU) != 0;
-    if (glu && N > INT64_MAX / 2) return GEMM_ERR_INVALID_ARG;
-    if (skinny && (M < 1 || M > 64)) return GEMM_ERR_UNSUPPORTED;
-    glk::DeviceInfo dev;
-    dev.cus = cus;
-    dev.nxcd = (cus % 8 == 0) ? 8 : 1;
-    dev.ws_floats = kWsFloats;
-    dev.ws_counters = kWsCounters;
-    const glk::Plan p = glk::make_plan(M, N, K, dev, true, skinny ? 1 : 0, glu);
-    return copy_out(glk::plan_json(p, M, N, K), buf, len);
+    return glk::guarded([&] { return plan_describe(M, N, K, cus, flags, buf, len); });
 }
 
 int gemm_wave_efficiency(int64_t ctas, int64_t slots, double* efficiency, int64_t* waves) {
@@ -603,14 +659,7 @@ int gemm_wave_efficiency(int64_t ctas, int64_t slots, double* efficiency, int64_
 }
 
 int gemm_last_plan(char* buf, int len) {
-    std::lock_guard<std::mutex> lk(g_mu);
-    if (!g_last_op.plan.op) return copy_out(g_last_plan, buf, len);
-    std::string s = glk::op_plan_json(g_last_op.plan);
-    if (g_last_op.with.op) {
-        s.pop_back();
-        s += ", \"with\": " + glk::op_plan_json(g_last_op.with) + "}";
-    }
-    return copy_out(s, buf, len);
+    return glk::guarded([&] { return last_plan(buf, len); });
 }
 
 const char* gemm_status_string(int status) {
@@ -678,44 +727,13 @@ int gemm_mx_quantize_act(int64_t M, int64_t K, const void* A, int64_t lda, void*
 
 int gemm_mx_decode(int64_t M, int64_t N, int64_t K, const void* Aq, int64_t ldaq, const void* As,
                    int64_t ldas, const void* Wp, const void* Sp, void* C, int64_t ldc, gemm_stream_t stream) {
-    return mx_decode(M, N, K, Aq, ldaq, As, ldas, Wp, Sp, C, ldc, reinterpret_cast<hipStream_t>(stream));
+    return glk::guarded(
+        [&] { return mx_decode(M, N, K, Aq, ldaq, As, ldas, Wp, Sp, C, ldc, reinterpret_cast<hipStream_t>(stream)); });
 }
 
 int gemm_mx_decode_bf16(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const void* Wp,
                         const void* Sp, void* C, int64_t ldc, gemm_stream_t stream) {
-    if (M < 0 || N < 0 || K < 0 || lda < K || ldc < N) return GEMM_ERR_INVALID_ARG;
-    if (M > 64 || (N % 16) || (K % 128)) return GEMM_ERR_UNSUPPORTED;
-    if (M == 0 || N == 0) return GEMM_OK;
-    if (M > 0 && K > 0 && !A) return GEMM_ERR_INVALID_ARG;
-    if (K == 0) return mx_decode(M, N, K, nullptr, 0, nullptr, 0, Wp, Sp, C, ldc, reinterpret_cast<hipStream_t>(stream));
-    int st = GEMM_OK;
-    DeviceState* ds = current_state(&st);
-    if (!ds) return st;
-    const hipStream_t hs = reinterpret_cast<hipStream_t>(stream);
-    // one or two rows: converted inside the product, one launch (when the piece's rows fit LDS)
-    if (M <= 2) {
-        glk::DeviceInfo info = ds->info;
-        info.ws_floats = kMxPartialFloats;
-        const glk::Plan p = glk::make_mx_plan(M, N, K, info);
-        glk::MxArgs probe;
-        const int ks = (int)(K / 128);
-        if (p.kernel == glk::kKernMx && glk::mx_fused_layout((ks + p.splits - 1) / p.splits, p.strip / 16, probe) >= 0) {
-            return mx_decode(M, N, K, nullptr, K, nullptr, K / 32, Wp, Sp, C, ldc, hs, A, lda);
-        }
-    }
-    // the quantised activations go to the workspace tail (both launches on the same stream)
-    const int64_t ldaq = (K + 15) / 16 * 16, ldas = K / 32;
-    if (M * ldaq + M * ldas + 16 > kMxActBytes) return GEMM_ERR_UNSUPPORTED;
-    Region* rg = nullptr;
-    st = region_for(*ds, hs, &rg);
-    if (st != GEMM_OK) return st;
-    uint8_t* base = reinterpret_cast<uint8_t*>(rg->ws + kMxPartialFloats);
-    uint8_t* aq = base;
-    uint8_t* as = base + (M * ldaq + 15) / 16 * 16;
-    const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-    st = mx_quantize_act(M, K, A, lda, aq, ldaq, as, ldas, s);
-    if (st != GEMM_OK) return st;
-    return mx_decode(M, N, K, aq, ldaq, as, ldas, Wp, Sp, C, ldc, s);
+    return glk::guarded([&] { return mx_decode_bf16(M, N, K, A, lda, Wp, Sp, C, ldc, reinterpret_cast<hipStream_t>(stream)); });
 }
 
 int gemm_pack_weight_bf16(int64_t K, int64_t N, const void* B, int64_t ldb, void* Bp, gemm_stream_t stream) {
@@ -734,7 +752,7 @@ int gemm_pack_weight_bf16(int64_t K, int64_t N, const void* B, int64_t ldb, void
 
 int gemm_bf16_packed(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const void* Bp, void* C,
                      int64_t ldc, gemm_stream_t stream) {
-    return packed_decode(M, N, K, A, lda, Bp, C, ldc, reinterpret_cast<hipStream_t>(stream));
+    return glk::guarded([&] { return packed_decode(M, N, K, A, lda, Bp, C, ldc, reinterpret_cast<hipStream_t>(stream)); });
 }
 
 int gemm_peak_mfma_launch(int64_t iters, int blocks, float* sink, uint64_t* cycles,

@@ -5,6 +5,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "gemm_bf16.h"
 #include "plan.h"
 
 namespace glk {
@@ -26,5 +27,15 @@ struct OpPlan {
 };
 // the plan of the call that just succeeded, and that of the other product of its launch
 void set_last_plan(OpPlan plan, OpPlan with = {});
+
+// No C++ exception leaves a C entry point: a plan's text or a lock that the host has no memory for.
+template <class F>
+int guarded(F f) {
+    try {
+        return f();
+    } catch (...) {
+        return GEMM_ERR_HIP;
+    }
+}
 
 }  // namespace glk

@@ -11,6 +11,7 @@
 
 namespace {
 
+using glk::guarded;
 using glk::OpArgs;
 
 constexpr int64_t kMaxCodesK = 131071;  // 128 * 128 * K < 2^31
@@ -305,16 +306,6 @@ int check_gradients(int64_t M, int64_t W, int64_t K, const void* A, int64_t lda,
     if ((dA && (misaligned(dA, 2) || misaligned(B, 2))) || (dB && (misaligned(dB, 2) || misaligned(A, 2))))
         return GEMM_ERR_INVALID_ARG;
     return GEMM_OK;
-}
-
-// No C++ exception leaves a C entry point: a plan's text or a lock that the host has no memory for.
-template <class F>
-int guarded(F f) {
-    try {
-        return f();
-    } catch (...) {
-        return GEMM_ERR_HIP;
-    }
 }
 
 }  // namespace

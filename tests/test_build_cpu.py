@@ -1,6 +1,8 @@
-"""The build's order: the C library does not wait for, or need, PyTorch. The compilers are stood in for."""
+"""The build: the C library does not wait for, or need, PyTorch (the compilers are stood in for), and no C++
+exception leaves its C entries."""
 
 import os
+import shutil
 import subprocess
 import sys
 
@@ -44,3 +46,16 @@ def test_a_module_that_does_not_compile_leaves_a_library(made, monkeypatch, tmp_
     with pytest.raises(RuntimeError, match="torch_ops"):
         b.build()
     assert (tmp_path / "libgemm_bf16.so").exists()
+
+
+@pytest.mark.skipif(shutil.which("g++") is None, reason="no host C++ compiler")
+def test_no_exception_leaves_a_c_entry(tmp_path):
+    here, pkg = os.path.dirname(os.path.abspath(__file__)), os.path.dirname(b.__file__)
+    exe = str(tmp_path / "no_throw_check")
+    rocm = os.path.dirname(os.path.dirname(b.HIPCC))
+    subprocess.run(["g++", "-O1", "-std=c++17", "-D__HIP_PLATFORM_AMD__", f"-I{os.path.join(rocm, 'include')}",
+                    f"-I{os.path.join(pkg, 'csrc')}", f"-I{os.path.join(b.ROOT, 'include')}",
+                    os.path.join(here, "no_throw_check.cpp"), os.path.join(pkg, "libgemm_bf16.so"), f"-Wl,-rpath,{pkg}",
+                    "-Wl,--allow-shlib-undefined", "-o", exe], check=True)
+    r = subprocess.run([exe], capture_output=True, text=True, timeout=60)
+    assert r.returncode == 0 and r.stdout.endswith("ok\n"), r.stdout + r.stderr
