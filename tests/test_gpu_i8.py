@@ -560,3 +560,67 @@ def test_an_output_that_does_not_fit_raises_what_torch_raises():
         with pytest.raises(torch.OutOfMemoryError):
             call()
     assert bool((g.i8_matmul(q[:2], s[:2], q, s) == 16).all())
+
+
+# M, N, K, gated, and the streaming kernel it takes on 256 CUs: (16-row tiles of M, weight tiles a
+# workgroup, waves), each with K whole and in pieces where a shape can have both
+STREAMED = [
+    (2, 40, 100, False, (1, 1, 4)), (5, 520, 2100, False, (1, 1, 4)), (4, 4100, 8200, False, (1, 1, 8)),
+    (4, 1000, 9001, False, (1, 1, 8)), (16, 8300, 1000, False, (1, 4, 4)), (9, 9000, 1021, False, (1, 4, 4)),
+    (3, 1000, 1030, True, (1, 2, 4)), (16, 200, 4100, True, (1, 2, 4)),
+    (17, 300, 1000, False, (2, 1, 4)), (31, 200, 4099, False, (2, 1, 4)), (20, 333, 8200, False, (2, 1, 8)),
+    (17, 2000, 5000, False, (2, 2, 4)), (32, 11000, 900, False, (2, 2, 4)), (17, 5120, 4100, False, (2, 4, 8)),
+    (32, 20001, 1100, False, (2, 4, 8)),
+    (33, 300, 1000, False, (3, 1, 4)), (47, 200, 4099, False, (3, 1, 4)), (40, 333, 8200, False, (3, 1, 8)),
+    (33, 1500, 6001, False, (3, 2, 4)), (40, 9000, 1000, False, (3, 2, 4)), (33, 3000, 10001, False, (3, 4, 8)),
+    (48, 20500, 1040, False, (3, 4, 8)),
+    (49, 300, 1000, False, (4, 1, 4)), (64, 200, 4099, False, (4, 1, 4)), (60, 333, 8200, False, (4, 1, 8)),
+    (49, 1400, 9001, False, (4, 2, 4)), (64, 10000, 1000, False, (4, 2, 4)), (61, 2056, 10500, False, (4, 4, 8)),
+    (64, 20501, 1040, False, (4, 4, 8)),
+    (17, 100, 3000, True, (2, 2, 4)), (30, 2000, 500, True, (2, 2, 4)), (17, 2056, 8200, True, (2, 4, 4)),
+    (32, 10300, 1040, True, (2, 4, 4)), (33, 100, 3000, True, (3, 2, 4)), (48, 2000, 500, True, (3, 2, 4)),
+    (33, 2056, 8200, True, (3, 4, 4)), (48, 10301, 1040, True, (3, 4, 4)), (49, 100, 3000, True, (4, 2, 4)),
+    (64, 2000, 500, True, (4, 2, 4)), (49, 1400, 9001, True, (4, 4, 4)), (64, 10300, 1040, True, (4, 4, 4))]
+
+
+@pytest.mark.parametrize("M,N,K,glu,kernel", STREAMED)
+def test_every_streaming_kernel(M, N, K, glu, kernel):
+    C, acc, sa, sw, plan = product(M, N, K, ldc=N + 3, seed=M + N, full=True, glu=glu)
+    if torch.cuda.get_device_properties(0).multi_processor_count == 256:
+        assert (plan["kernel"], plan["mtiles"], plan["strip"] // 16, plan["threads"] // 64) == ("i8_decode", *kernel)
+    if glu:
+        check_glu(C, acc, sa, sw, plan)
+    else:
+        assert np.array_equal(C, expect(acc, sa, sw)), plan
+
+
+# 256 x 256 tiles in a partial wave and in full waves with the last one cut off across columns or rows,
+# ragged in every size, over odd and even numbers of k-steps that go round the five-slot rings
+LARGE = [(2300, 4090, 700, None), (2300, 4090, 1000, None), (4090, 4350, 1000, "n"), (4350, 4090, 1000, "m")]
+
+
+@pytest.mark.parametrize("M,N,K,cut", LARGE)
+@pytest.mark.parametrize("glu", [False, True])
+def test_large_tiles_over_many_steps(M, N, K, cut, glu):
+    C, acc, sa, sw, plan = product(M, N // 2 if glu else N, K, seed=K + M, glu=glu)
+    assert plan["kernel"] == "tile" and plan["bm"] == 256
+    if torch.cuda.get_device_properties(0).multi_processor_count == 256:
+        assert plan.get("cut", {}).get("axis") == cut, plan
+    if glu:
+        check_glu(C, acc, sa, sw, plan)
+    else:
+        assert np.array_equal(C, expect(acc, sa, sw)), plan
+
+
+@pytest.mark.parametrize("M,N,K", [(1400, 2040, 12900), (1400, 2040, 9000)])
+def test_two_pieces_on_most_cus(M, N, K):
+    """176 tiles of 128 x 128: two pieces of 102 k-steps for 202 of them, whole for 141."""
+    for glu in (False, True):
+        C, acc, sa, sw, plan = product(M, N // 2 if glu else N, K, seed=K, glu=glu)
+        assert plan["bm"] == 128
+        if torch.cuda.get_device_properties(0).multi_processor_count == 256:
+            assert (plan["splits"], plan["kt_per_split"]) == ((2, 102) if K == 12900 else (1, 141))
+        if glu:
+            check_glu(C, acc, sa, sw, plan)
+        else:
+            assert np.array_equal(C, expect(acc, sa, sw)), plan

@@ -456,3 +456,104 @@ def test_in_an_autograd_function():
     assert torch.equal(C, want) and torch.equal(x.grad, dA) and torch.equal(w.grad, dB)
     with torch.no_grad():
         assert torch.equal(g.swiglu_forward(x, w)[0], want)
+
+
+def some_rows(M, n=64):
+    """Rows of both halves of the first, of middle and of the last 256-row tiles, and both sides of a cut."""
+    rng = np.random.default_rng(M)
+    near = [r for t in range(0, M, 256) for r in (t, t + 127, t + 128, t + 255)] + [M - 1]
+    return np.unique([r for r in near if r < M] + rng.integers(0, M, n).tolist())
+
+
+def expect_large(plan, cut):
+    assert plan["kernel"] == "tile" and plan["bm"] == 256, plan
+    if torch.cuda.get_device_properties(0).multi_processor_count == 256:
+        assert plan.get("cut", {}).get("axis") == cut, plan
+
+
+# 256 x 256 tiles in a partial wave and in full waves with the last one cut off across columns or rows,
+# over odd (328, 336, 333: 11) and even (360: 12) numbers of k-steps that go round the five-slot rings
+@pytest.mark.parametrize("M,N,K,cut", [(2300, 2040, 328, None), (2300, 2040, 360, None), (4096, 2176, 328, "n"),
+                                       (4350, 2040, 360, "m")])
+def test_large_tiles_forward(M, N, K, cut):
+    A, B = matrix("normal", M, K, seed=M), matrix("normal", K, 2 * N, seed=N, sigma=0.05)
+    bA, bB = Buf(M, K, A), Buf(K, 2 * N, B)
+    GU, C = Buf(M, 2 * N, ld=2 * N + 8), Buf(M, N, ld=N + 16)
+    g.gemm_bf16_swiglu_train(M, N, K, bA.ptr(), K, bB.ptr(), 2 * N, GU.ptr(), GU.ld, C.ptr(), C.ld, g.current_stream_handle())
+    torch.cuda.synchronize()
+    expect_large(g.gemm_last_plan(), cut)
+    r = some_rows(M)
+    a = np.ascontiguousarray(A[r])
+    ref, sabs = oracle.gemm(a, B, M=len(r), N=2 * N, K=K)
+    res = oracle.check(np.ascontiguousarray(GU.bits()[r]), ref, sabs)
+    assert res.ok, res.summary()
+    h, slack = osw.swiglu(a, B, len(r), N, K)
+    res = osw.check(np.ascontiguousarray(C.bits()[r]), h, slack)
+    assert res.ok, res.summary()
+
+
+# rows of the output, its columns, the sum's length
+@pytest.mark.parametrize("R,C,S,cut", [(2300, 4088, 336, None), (2300, 4088, 360, None), (4350, 4088, 360, "m"),
+                                       (4090, 4352, 336, "n")])
+def test_large_tiles_grad_a(R, C, S, cut):
+    D, B = matrix("normal", R, S, seed=R, sigma=0.01), matrix("normal", C, S, seed=C, sigma=0.05)
+    bD, bB, dA = Buf(R, S, D), Buf(C, S, B), Buf(R, C, ld=C + 8)
+    g.gemm_bf16_bwd(R, S, C, bD.ptr(), S, None, C, bB.ptr(), S, dA.ptr(), dA.ld, None, S, g.current_stream_handle())
+    torch.cuda.synchronize()
+    expect_large(g.gemm_last_plan(), cut)
+    r = some_rows(R)
+    ref, sabs = oracle.gemm(np.ascontiguousarray(D[r]), np.ascontiguousarray(B.T), M=len(r), N=C, K=S)
+    res = oracle.check(np.ascontiguousarray(dA.bits()[r]), ref, sabs)
+    assert res.ok, res.summary()
+
+
+@pytest.mark.parametrize("R,C,S,cut", [(2296, 4088, 333, None), (2296, 4088, 360, None), (4352, 4088, 360, "m"),
+                                       (4088, 4352, 333, "n")])
+def test_large_tiles_grad_b(R, C, S, cut):
+    A, D = matrix("normal", S, R, seed=R), matrix("normal", S, C, seed=C, sigma=0.01)
+    bA, bD, dB = Buf(S, R, A), Buf(S, C, D), Buf(R, C, ld=C + 8)
+    g.gemm_bf16_bwd(S, C, R, bD.ptr(), C, bA.ptr(), R, None, C, None, R, dB.ptr(), dB.ld, g.current_stream_handle())
+    torch.cuda.synchronize()
+    expect_large(g.gemm_last_plan(), cut)
+    r = some_rows(R)
+    ref, sabs = oracle.gemm(np.ascontiguousarray(A.T[r]), D, M=len(r), N=C, K=S)
+    res = oracle.check(np.ascontiguousarray(dB.bits()[r]), ref, sabs)
+    assert res.ok, res.summary()
+
+
+@pytest.mark.parametrize("R,C,S,splits", [(1400, 2032, 6440, 2), (1400, 2032, 4512, 1), (1400, 2032, 3872, 1)])
+def test_two_pieces_on_most_cus(R, C, S, splits):
+    """dA, dB and the forward on 176 tiles of 128 x 128, sums of 202, 141 and 121 k-steps: two pieces of dA
+    from 200 and of the others from 120, an even number of k-steps in each."""
+    whole_cus = torch.cuda.get_device_properties(0).multi_processor_count == 256
+
+    def planned(splits, steps):
+        p = g.gemm_last_plan()
+        assert p["bm"] == 128
+        if whole_cus:
+            assert (p["splits"], p["kt_per_split"]) == ((2, (steps + 1) // 2 + (steps + 1) // 2 % 2) if splits == 2 else (1, steps))
+
+    def check(out, X, Y):
+        r = some_rows(len(X), 32)
+        ref, sabs = oracle.gemm(np.ascontiguousarray(X[r]), Y, M=len(r), N=Y.shape[1], K=S)
+        res = oracle.check(np.ascontiguousarray(out[r]), ref, sabs)
+        assert res.ok, res.summary()
+
+    steps, s = -(-S // 32), g.current_stream_handle()
+    X, Y = matrix("normal", R, S, seed=1), matrix("normal", C, S, seed=2, sigma=0.05)
+    bX, bY, out = Buf(R, S, X), Buf(C, S, Y), Buf(R, C)
+    g.gemm_bf16_bwd(R, S, C, bX.ptr(), S, None, C, bY.ptr(), S, out.ptr(), C, None, S, s)
+    torch.cuda.synchronize()
+    planned(splits, steps)
+    check(out.bits(), X, np.ascontiguousarray(Y.T))
+    XT, YT = np.ascontiguousarray(X.T), np.ascontiguousarray(Y.T)
+    bX, bY, out = Buf(S, R, XT), Buf(S, C, YT), Buf(R, C)
+    g.gemm_bf16_bwd(S, C, R, bY.ptr(), C, bX.ptr(), R, None, C, None, R, out.ptr(), C, s)
+    torch.cuda.synchronize()
+    planned(2, steps)
+    check(out.bits(), X, YT)
+    bX, GU, h = Buf(R, S, X), Buf(R, C), Buf(R, C // 2)
+    g.gemm_bf16_swiglu_train(R, C // 2, S, bX.ptr(), S, bY.ptr(), C, GU.ptr(), C, h.ptr(), C // 2, s)
+    torch.cuda.synchronize()
+    planned(2, steps)
+    check(GU.bits(), X, YT)
