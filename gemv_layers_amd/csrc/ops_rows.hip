@@ -3,9 +3,10 @@
 // Quantisation of rows (the arithmetic is in codes.h). A row stays in the registers of its workgroup
 // between the maximum and the codes, so that memory is read once (2 bytes an element) and written
 // once (1 byte). Few rows are bound by latency, a load, a reduction and a store, and take wide
-// workgroups; many rows by memory. 16 rows of 4096 take 4.8 us, 4096 rows 13 us (3.8 TB/s). Rows may start
-// at any element: the 16-byte loads need no alignment, and cost a quarter more without it (4096 x 4095: 15
-// us, where element by element it took 24). Rows of up to 65536 stay in registers (16 x 28672: 5.6 us
+// workgroups; many rows by memory. 16 rows of 4096 take 4.8 us, 4096 rows 12.0 us (4.2 TB/s; a copy
+// reaches 6: each workgroup's load, reduction and store are in series). Rows may start at any element: the
+// 16-byte loads need no alignment, and cost a quarter more without it (4096 x 4095: 15 us, where element
+// by element it took 24). Rows of up to 65536 stay in registers (16 x 28672: 5.6 us
 // against 35 in two passes).
 //
 // The gated block's gradient, element by element: reads dC, g and u, writes dg and du, 10 bytes an

@@ -28,9 +28,10 @@
 // Codes past K in the last 16-byte chunk of a row are whatever the caller's padding holds: they are
 // cleared in the A operand, which is enough, as 0 times any code is 0.
 //
-// Measured, 256 x 256 tiles: 8-bit 4096 x 4096 x 11008 126 us a call, 2.9 POP/s; medians of the kernel, dA
-// = dC B^T 4096 x 4096 x 22016 484 us, 1.53 PFLOP/s; of dB = A^T dC 4096 x 22016 x 4096 the 1280 tiles of
-// its full waves 560-574 us, 1.2, and as many of the forward 552-566 us. What bounds them, from timing-only
+// Measured, 256 x 256 tiles, medians of the kernel once the clock has settled: 8-bit 4096 x 4096 x 11008
+// 127 us, 2.9 POP/s of the 4.0 that the matrix cores reach on random codes in registers; dA = dC B^T 4096
+// x 4096 x 22016 484 us, 1.53 PFLOP/s of 2.0; of dB = A^T dC 4096 x 22016 x 4096 the 1280 tiles of its full
+// waves 558 us, 1.23, and as many of the forward 542 us, 1.27 (after an idle spell 130, 486, 577 and 578). What bounds them, from timing-only
 // copies that leave one part out (us, in that order, the whole 124, 470, 556, and 666 for the forward's
 // 1376 tiles): without the copies 105, 362, 443, 478; without the operand reads 113, 469, 451, 641;
 // without the MFMAs 84, 430, 360, 474; the operand reads alone 59, 187, 280, 273. dA waits
