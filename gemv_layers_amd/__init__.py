@@ -40,6 +40,8 @@ EXPORTS = (
     "gemm_mx_decode_bf16", "gemm_pack_weight_bf16", "gemm_bf16_packed",
     "gemm_i8_quantize", "gemm_i8", "gemm_i8_swiglu", "gemm_i8_work_bytes", "gemm_i8_bf16",
     "gemm_i8_swiglu_bf16", "gemm_bf16_bwd", "gemm_bf16_swiglu_train", "gemm_bf16_swiglu_bwd",
+    "gemm_f8_quantize", "gemm_f8_quantize_weight", "gemm_f8", "gemm_f8_work_bytes", "gemm_f8_bf16",
+    "gemm_bf16_grouped", "gemm_bf16_grouped_bwd", "gemm_f8_grouped", "gemm_f8_grouped_bf16",
 )
 
 
@@ -120,6 +122,18 @@ def lib() -> ctypes.CDLL:
     L.gemm_bf16_swiglu_bwd.argtypes = [i64, i64, i64, p, i64, p, i64, p, i64, p, i64, p, i64, p, i64, p, i64, p]
     for name in ("gemm_i8_quantize", "gemm_i8_work_bytes", "gemm_i8", "gemm_i8_swiglu", "gemm_i8_bf16",
                  "gemm_i8_swiglu_bf16", "gemm_bf16_bwd", "gemm_bf16_swiglu_train", "gemm_bf16_swiglu_bwd"):
+        getattr(L, name).restype = i32
+    L.gemm_f8_quantize.argtypes = [i64, i64, p, i64, p, i64, p, i64, p]
+    L.gemm_f8_quantize_weight.argtypes = [i64, i64, i64, p, i64, i64, p, i64, i64, p, i64, i64, p]
+    L.gemm_f8.argtypes = [i64, i64, i64, p, i64, p, i64, p, i64, p, i64, p, i64, p]
+    L.gemm_f8_work_bytes.argtypes = [i64, i64, ctypes.POINTER(ctypes.c_int64)]
+    L.gemm_f8_bf16.argtypes = [i64, i64, i64, p, i64, p, i64, p, i64, p, i64, p, i64, p]
+    L.gemm_bf16_grouped.argtypes = [i64, i64, i64, i64, p, i64, p, i64, i64, p, p, i64, p]
+    L.gemm_bf16_grouped_bwd.argtypes = [i64, i64, i64, i64, p, i64, p, i64, p, i64, i64, p, p, i64, p, i64, i64, p]
+    L.gemm_f8_grouped.argtypes = [i64, i64, i64, i64, p, i64, p, i64, p, i64, i64, p, i64, i64, p, p, i64, p]
+    L.gemm_f8_grouped_bf16.argtypes = [i64, i64, i64, i64, p, i64, p, i64, i64, p, i64, i64, p, p, i64, p, i64, p]
+    for name in ("gemm_f8_quantize", "gemm_f8_quantize_weight", "gemm_f8", "gemm_f8_work_bytes", "gemm_f8_bf16",
+                 "gemm_bf16_grouped", "gemm_bf16_grouped_bwd", "gemm_f8_grouped", "gemm_f8_grouped_bf16"):
         getattr(L, name).restype = i32
     _lib = L
     return L
@@ -257,6 +271,55 @@ def gemm_bf16_swiglu_bwd(M, N, K, dC, lddc, GU, ldgu, A, lda, B, ldb, dGU, lddgu
                                       stream))
 
 
+def gemm_f8_quantize(R, K, X, ldx, Q, ldq, S, lds, stream=None) -> None:
+    _check("gemm_f8_quantize", lib().gemm_f8_quantize(R, K, X, ldx, Q, ldq, S, lds, stream))
+
+
+def gemm_f8_quantize_weight(E, N, K, W, ldw, stride_w, Q, ldq, stride_q, S, lds, stride_s, stream=None) -> None:
+    _check("gemm_f8_quantize_weight",
+           lib().gemm_f8_quantize_weight(E, N, K, W, ldw, stride_w, Q, ldq, stride_q, S, lds, stride_s, stream))
+
+
+def gemm_f8(M, N, K, Aq, ldaq, Sa, ldsa, Wq, ldwq, Sw, ldsw, C, ldc, stream=None) -> None:
+    _check("gemm_f8", lib().gemm_f8(M, N, K, Aq, ldaq, Sa, ldsa, Wq, ldwq, Sw, ldsw, C, ldc, stream))
+
+
+def gemm_f8_work_bytes(M: int, K: int) -> int:
+    """Bytes of the work buffer of gemm_f8_bf16 and gemm_f8_grouped_bf16."""
+    n = ctypes.c_int64()
+    _check("gemm_f8_work_bytes", lib().gemm_f8_work_bytes(M, K, ctypes.byref(n)))
+    return n.value
+
+
+def gemm_f8_bf16(M, N, K, A, lda, Wq, ldwq, Sw, ldsw, C, ldc, work, work_bytes, stream=None) -> None:
+    _check("gemm_f8_bf16", lib().gemm_f8_bf16(M, N, K, A, lda, Wq, ldwq, Sw, ldsw, C, ldc, work, work_bytes, stream))
+
+
+def gemm_bf16_grouped(M, N, K, E, A, lda, B, ldb, stride_b, offsets, C, ldc, stream=None) -> None:
+    _check("gemm_bf16_grouped", lib().gemm_bf16_grouped(M, N, K, E, A, lda, B, ldb, stride_b, offsets, C, ldc, stream))
+
+
+def gemm_bf16_grouped_bwd(M, N, K, E, dC, lddc, A, lda, B, ldb, stride_b, offsets, dA, ldda, dB, lddb, stride_db,
+                          stream=None) -> None:
+    _check("gemm_bf16_grouped_bwd",
+           lib().gemm_bf16_grouped_bwd(M, N, K, E, dC, lddc, A, lda, B, ldb, stride_b, offsets, dA, ldda, dB, lddb,
+                                       stride_db, stream))
+
+
+def gemm_f8_grouped(M, N, K, E, Aq, ldaq, Sa, ldsa, Wq, ldwq, stride_wq, Sw, ldsw, stride_sw, offsets, C, ldc,
+                    stream=None) -> None:
+    _check("gemm_f8_grouped",
+           lib().gemm_f8_grouped(M, N, K, E, Aq, ldaq, Sa, ldsa, Wq, ldwq, stride_wq, Sw, ldsw, stride_sw, offsets, C,
+                                 ldc, stream))
+
+
+def gemm_f8_grouped_bf16(M, N, K, E, A, lda, Wq, ldwq, stride_wq, Sw, ldsw, stride_sw, offsets, C, ldc, work,
+                         work_bytes, stream=None) -> None:
+    _check("gemm_f8_grouped_bf16",
+           lib().gemm_f8_grouped_bf16(M, N, K, E, A, lda, Wq, ldwq, stride_wq, Sw, ldsw, stride_sw, offsets, C, ldc,
+                                      work, work_bytes, stream))
+
+
 def gemm_wave_efficiency(ctas: int, slots: int):
     eff, waves = ctypes.c_double(), ctypes.c_int64()
     _check("gemm_wave_efficiency", lib().gemm_wave_efficiency(ctas, slots, ctypes.byref(eff),
@@ -363,14 +426,14 @@ def swiglu_matmul(A, B, out=None, stream=None):
     return out
 
 
-# ---- 8-bit products and training: PyTorch marshalling ----------------------------------------
+# ---- 8-bit and grouped products, training: PyTorch marshalling ----------------------------------------
 #
 # A small product takes the GPU a few microseconds, so the tensors are checked, and the outputs made,
 # in a C++ module (_torch_ops). The functions below name its arguments. With `stream`, a handle, a call
 # runs as under torch.cuda.stream of it: its outputs belong to that stream. They record no graph: a
-# tensor that requires grad, with grad mode on, is refused (RuntimeError) by all but i8_quantize, whose
-# codes have no gradient. Wrap swiglu_forward and swiglu_backward in a torch.autograd.Function to train
-# with autograd.
+# tensor that requires grad, with grad mode on, is refused (RuntimeError) by all but i8_quantize and
+# f8_quantize(_weight), whose codes have no gradient. Wrap swiglu_forward and swiglu_backward, or grouped_matmul
+# and grouped_matmul_backward, in a torch.autograd.Function to train with autograd.
 
 _ops = None
 
@@ -390,6 +453,9 @@ def _load_ops():
         m.bind(_check, *(ctypes.cast(getattr(L, f), ctypes.c_void_p).value for f in (
             "gemm_i8_quantize", "gemm_i8", "gemm_i8_swiglu", "gemm_i8_bf16", "gemm_i8_swiglu_bf16", "gemm_bf16_bwd",
             "gemm_bf16_swiglu_train", "gemm_bf16_swiglu_bwd")))
+        m.bind_grouped(*(ctypes.cast(getattr(L, f), ctypes.c_void_p).value for f in (
+            "gemm_f8_quantize", "gemm_f8_quantize_weight", "gemm_f8", "gemm_f8_bf16", "gemm_f8_grouped",
+            "gemm_f8_grouped_bf16", "gemm_bf16_grouped", "gemm_bf16_grouped_bwd")))
         _ops = m
     return _ops
 
@@ -436,3 +502,54 @@ def swiglu_forward(A, B, stream=None):
 def swiglu_backward(dC, GU, A, B, need_dA=True, need_dB=True, inplace=False, stream=None):
     """(dA, dB, dGU): the gradients of swiglu_forward's C. With `inplace`, dGU takes GU's memory."""
     return (_ops or _load_ops()).swiglu_bwd(dC, GU, A, B, need_dA, need_dB, inplace, stream)
+
+
+# 8-bit floating point: codes are torch.float8_e4m3fn, scales float32 over blocks of 128 inputs.
+
+def f8_quantize(X, stream=None):
+    """e4m3 codes and scales of each block of 128 columns of each row of a bf16 matrix: (Q float8_e4m3fn of X's
+    shape, S float32 of ceil(K / 128) x rows, S[b, r] the scale of row r's block b). Q's rows are padded to 16
+    bytes in memory, as the matrix kernels want them."""
+    return (_ops or _load_ops()).f8_quantize(X, stream)
+
+
+def f8_quantize_weight(W, stream=None):
+    """e4m3 codes and scales of each 128 x 128 block of a bf16 weight (N x K, the nn.Linear layout) or of a stack
+    of them (E x N x K): (Q of W's shape, S float32 of [E x] ceil(N / 128) x ceil(K / 128))."""
+    return (_ops or _load_ops()).f8_quantize_weight(W, stream)
+
+
+def f8_matmul(Aq, Sa, Wq, Sw, out=None, stream=None):
+    """The product of e4m3 codes Aq (M x K) and Wq (N x K) with their block scales (f8_quantize's and
+    f8_quantize_weight's): Aq @ Wq.T with every block of 128 inputs scaled, as M x N bf16."""
+    return (_ops or _load_ops()).f8(Aq, Sa, Wq, Sw, None, out, stream)
+
+
+def f8_linear(A, Wq, Sw, out=None, work=None, stream=None):
+    """f8_matmul of bf16 activations A (M x K), quantised in the call. `work`: a uint8 tensor of
+    gemm_f8_work_bytes(M, K) bytes to reuse, else one is allocated."""
+    return (_ops or _load_ops()).f8_dynamic(A, Wq, Sw, None, out, work, stream)
+
+
+# Grouped by expert: rows offsets[e] .. offsets[e + 1] - 1 belong to group e, `offsets` an int32 device tensor of
+# E + 1 values that only the kernels read. Rows of no group come out as zeros.
+
+def grouped_matmul(A, B, offsets, out=None, stream=None):
+    """Each group's rows of A (M x K, bf16) times its own B[e] (E x K x N): M x N bf16."""
+    return (_ops or _load_ops()).grouped(A, B, offsets, out, stream)
+
+
+def grouped_matmul_backward(dC, A, B, offsets, need_dA=True, need_dB=True, stream=None):
+    """(dA, dB): the gradients of grouped_matmul(A, B, offsets); None for one not needed. dB is E x K x N, zero for
+    groups without rows."""
+    return (_ops or _load_ops()).grouped_bwd(dC, A, B, offsets, need_dA, need_dB, stream)
+
+
+def f8_grouped_matmul(Aq, Sa, Wq, Sw, offsets, out=None, stream=None):
+    """f8_matmul with each group's own weight: Wq E x N x K codes, Sw E x ceil(N / 128) x ceil(K / 128) scales."""
+    return (_ops or _load_ops()).f8(Aq, Sa, Wq, Sw, offsets, out, stream)
+
+
+def f8_grouped_linear(A, Wq, Sw, offsets, out=None, work=None, stream=None):
+    """f8_grouped_matmul of bf16 activations A (M x K), quantised in the call."""
+    return (_ops or _load_ops()).f8_dynamic(A, Wq, Sw, offsets, out, work, stream)

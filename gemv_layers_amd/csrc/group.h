@@ -1,0 +1,114 @@
+// Which rows a workgroup of a grouped product takes (device side). The groups' row offsets are data on the
+// device: the host sizes a grid for the most tiles that any offsets could make, and every workgroup finds
+// its tile in them.
+//
+// The rows 0 .. rows - 1 are cut into spans: those before the first offset, each group's, and those after the
+// last offset. An offset counts as the largest of itself, the ones before it and 0, and as `rows` beyond that:
+// the spans are disjoint and in range whatever the offsets hold. A wave reads 64 offsets at a time, and its
+// prefix maximum and the sum of the spans' tiles are scans over the lanes (six data-parallel steps each, no
+// LDS and no barrier): about 0.5 us with the load, against a launch more for a table of tiles.
+#pragma once
+
+#include "common.h"
+#include "ops.h"
+
+namespace glk {
+
+// v with lane i's operand from lane i - SHIFT's scan: the inclusive scan of 64 lanes by `f`, `id` its identity
+template <class F>
+__device__ __forceinline__ int wave_scan(int v, int id, F f) {
+#define GLK_SCAN(ctrl, rows) v = f(v, __builtin_amdgcn_update_dpp(id, v, ctrl, rows, 0xF, false))
+    GLK_SCAN(0x111, 0xF);  // row_shr 1, 2, 4, 8 within rows of 16 lanes
+    GLK_SCAN(0x112, 0xF);
+    GLK_SCAN(0x114, 0xF);
+    GLK_SCAN(0x118, 0xF);
+    GLK_SCAN(0x142, 0xA);  // row_bcast15 into rows 1 and 3, row_bcast31 into rows 2 and 3
+    GLK_SCAN(0x143, 0xC);
+#undef GLK_SCAN
+    return v;
+}
+__device__ __forceinline__ int wave_scan_max(int v) {
+    return wave_scan(v, 0, [](int a, int b) { return max(a, b); });  // (values of 0 and more)
+}
+__device__ __forceinline__ int wave_scan_add(int v) {
+    return wave_scan(v, 0, [](int a, int b) { return a + b; });
+}
+
+struct GroupSpan {
+    int group;        // -1: rows of no group
+    int first, rows;
+    int tiles, tile;  // row tiles of this span, and of all before it
+    int unit;         // the workgroup's unit among the span's tiles * per
+};
+
+// The span and unit of workgroup `block` for row tiles of `bm` rows, each of `per` units, or false where the
+// offsets make fewer tiles. Units in order of rows, each XCD a contiguous share. Every lane of the wave calls it.
+__device__ __forceinline__ bool find_span(const GroupArgs& g, int bm, int per, int nxcd, int block, GroupSpan* out) {
+    auto uni = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
+    if (!g.offsets) {
+        const int tiles = (g.rows - 1) / bm + 1;
+        if (block >= tiles * per) return false;
+        *out = GroupSpan{0, 0, g.rows, uni(tiles), 0, uni(xcd_remap(block, tiles * per, nxcd))};
+        return true;
+    }
+    const int lane = threadIdx.x & 63, spans = g.groups + 2;
+    // of span s0 + lane: its end, its start and the tiles up to its end; the next 64 start at end, tiles
+    struct Part {
+        int start, end, tiles, upto;
+    };
+    auto part = [&](int s0, int& row, int& tiles) {
+        const int s = s0 + lane;
+        int end = s <= g.groups ? g.offsets[s] : g.rows;
+        end = max(wave_scan_max(min(max(end, 0), g.rows)), row);
+        const int before = __builtin_amdgcn_update_dpp(0, end, 0x138, 0xF, 0xF, false);  // wave_shr 1
+        Part p;
+        p.start = lane == 0 ? row : before;
+        p.end = end;
+        p.tiles = (end - p.start + bm - 1) / bm;
+        p.upto = wave_scan_add(p.tiles) + tiles;
+        row = __builtin_amdgcn_readlane(end, 63);
+        tiles = __builtin_amdgcn_readlane(p.upto, 63);
+        return p;
+    };
+    int row = 0, total = 0;
+    Part p = part(0, row, total);
+    for (int s0 = 64; s0 < spans; s0 += 64) part(s0, row, total);
+    if (block >= total * per) return false;
+    const int unit = uni(xcd_remap(block, total * per, nxcd)), tile = uni(unit / per);
+    int s0 = 0, upto = 0;
+    row = 0;
+    if (spans > 64) p = part(0, row, upto);
+    uint64_t hit;
+    while (!(hit = __ballot(tile < p.upto))) {  // (a tile below the total is in one of them)
+        s0 += 64;
+        p = part(s0, row, upto);
+    }
+    const int at = __builtin_ctzll(hit), s = s0 + at;
+    GroupSpan r;
+    r.group = s >= 1 && s <= g.groups ? s - 1 : -1;
+    r.first = __builtin_amdgcn_readlane(p.start, at);
+    r.rows = __builtin_amdgcn_readlane(p.end, at) - r.first;
+    r.tiles = __builtin_amdgcn_readlane(p.tiles, at);
+    r.tile = __builtin_amdgcn_readlane(p.upto, at) - r.tiles;
+    r.unit = unit - r.tile * per;
+    *out = r;
+    return true;
+}
+
+// The rows of group `e` (as find_span cuts them). Every lane of the wave calls it.
+__device__ __forceinline__ void group_rows(const GroupArgs& g, int e, int* first, int* rows) {
+    if (!g.offsets) {
+        *first = 0;
+        *rows = g.rows;
+        return;
+    }
+    const int lane = threadIdx.x & 63;
+    int most = 0;
+    for (int i = lane; i <= e; i += 64) most = max(most, g.offsets[i]);
+    const int end = g.offsets[e + 1];
+    const int start = min(__builtin_amdgcn_readlane(wave_scan_max(most), 63), g.rows);
+    *first = start;
+    *rows = __builtin_amdgcn_readfirstlane(max(min(end, g.rows), start)) - start;
+}
+
+}  // namespace glk

@@ -13,6 +13,8 @@ enum OpMode : int {
     kOpAbt = 1,    // C = A B^T: bf16, both operands contiguous (B is N x K)
     kOpAtb = 2,    // C = A^T B: bf16, both operands strided (A is K x M, B is K x N)
     kOpTrain = 3,  // GU = A B, C = silu(g) u: bf16, A contiguous, B (K x 2N) strided; gated
+    kOpAb = 4,     // C = A B: bf16, A contiguous, B (K x N) strided
+    kOpF8 = 5,     // C = sum over blocks of 128 k of (A W^T) sa sw: e4m3 codes, both contiguous (W is N x K)
 };
 
 // One product: an M x N output summed over K. Sizes and leading dimensions are in elements.
@@ -21,14 +23,36 @@ struct OpArgs {
     const void* B;
     uint16_t* C;
     uint16_t* GU;     // kOpTrain: M x 2N
-    const float* sa;  // kOpI8: M
-    const float* sb;  // kOpI8: N, or 2N gated
+    const float* sa;  // kOpI8: M; kOpF8: ceil(K / 128) x M
+    const float* sb;  // kOpI8: N, or 2N gated; kOpF8: ceil(N / 128) x ceil(K / 128)
     int64_t M, N, K;
     int64_t lda, ldb, ldc, ldgu;
+    int64_t ldsa = 0, ldsb = 0;  // kOpF8
+};
+
+// The groups of a product whose rows belong to groups with a B of their own. Rows are those of A and C, or
+// of A and B (dC) where the rows are summed over (kOpAtb).
+struct GroupArgs {
+    const int32_t* offsets;  // groups + 1 row offsets on the device, or null: one group of all rows
+    int groups;
+    int rows;                // of all groups and of none
+    int64_t stride_b;        // elements from one group's B to the next's (kOpAb, kOpAbt, kOpF8)
+    int64_t stride_c;        // and from one's C (kOpAtb)
+    int64_t stride_sb;       // and from one's scales (kOpF8)
 };
 
 // ---- general kernel (any alignment, leading dimension or size) -------------------------------
 hipError_t launch_op_generic(int mode, bool glu, const OpArgs& a, hipStream_t s);
+
+// The same element by element for products grouped by rows and for kOpF8. a.M is all rows, or A's width
+// (kOpAtb, where a.K is not read).
+hipError_t launch_group_generic(int mode, const OpArgs& a, const GroupArgs& g, hipStream_t s);
+constexpr int kMaxGroups = 65536;
+// most tiles of `bm` rows over `rows` rows in `groups` groups and those of none, wherever they are cut
+inline int64_t most_row_tiles(int64_t rows, int64_t groups, int64_t bm) {
+    const int64_t parts = groups + 2 < rows ? groups + 2 : rows;
+    return (rows + parts * (bm - 1)) / bm;
+}
 
 // ---- MFMA tiles ---------------------------------------------------------------------------------
 // One launch over an M x N output (or a rectangle of it), sizes in elements.
@@ -77,6 +101,17 @@ hipError_t configure_i8_decode();
 // symmetric 8-bit codes of each row: see gemm_i8_quantize
 hipError_t launch_i8_quantize(const uint16_t* X, int64_t R, int64_t K, int64_t ldx, int8_t* Q, int64_t ldq,
                               float* S, hipStream_t s);
+// e4m3 codes and a scale for each block of 128 values of each row, S[block * lds + row]: see gemm_f8_quantize
+hipError_t launch_f8_quantize(const uint16_t* X, int64_t R, int64_t K, int64_t ldx, uint8_t* Q, int64_t ldq,
+                              float* S, int64_t lds, hipStream_t s);
+// the same for each 128 x 128 block of E matrices: see gemm_f8_quantize_weight
+struct F8WeightArgs {
+    const uint16_t* W;
+    uint8_t* Q;
+    float* S;
+    int64_t E, N, K, ldw, stride_w, ldq, stride_q, lds, stride_s;
+};
+hipError_t launch_f8_quantize_weight(const F8WeightArgs& a, hipStream_t s);
 // dGU from dC and GU: see gemm_bf16_swiglu_bwd
 hipError_t launch_swiglu_grad(const uint16_t* dC, int64_t lddc, const uint16_t* GU, int64_t ldgu, uint16_t* dGU,
                               int64_t lddgu, int64_t M, int64_t N, hipStream_t s);

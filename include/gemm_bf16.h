@@ -377,6 +377,130 @@ int gemm_bf16_swiglu_bwd(int64_t M, int64_t N, int64_t K, const void *dC, int64_
                          int64_t ldb, void *dGU, int64_t lddgu, void *dA, int64_t ldda, void *dB,
                          int64_t lddb, gemm_stream_t stream);
 
+/* ------------------------------------------------------------------------------------------
+ * 8-bit floating-point products: e4m3 codes (OCP FP8: 4 exponent and 3 mantissa bits, largest magnitude
+ * 448) with float32 scales over blocks of 128 of the summed index. Activations have a scale for each row
+ * and block, weights (nn.Linear layout, N x K) one for each block of 128 outputs and 128 inputs:
+ *   C[m][n] = bf16( sum_b Sa[b][m] Sw[n / 128][b] sum_{k in block b} a[m][k] w[n][k] ),
+ * block b being k = 128 b .. 128 b + 127 (the last one shorter). Products and sums are float32, the two
+ * scales of a block are multiplied first, and each output is rounded once (to nearest even).
+ * ------------------------------------------------------------------------------------------ */
+
+/*
+ * gemm_f8_quantize: codes and scales of a bf16 matrix X (R x K, ldx >= K) by row and block of 128 columns:
+ *   S[b][r] = max_{k in b} |X[r][k]| / 448 (float32, and at least 2^-126),
+ *   Q[r][k] = e4m3( 448 X[r][k] / max ), to nearest, ties to even (e4m3(2^126 X[r][k]) where S is 2^-126).
+ * Blocks of zeros get S = 0. A block that holds an infinity or a NaN gets S = NaN and codes 0, so that every
+ * output made from it is NaN. Q is R x K bytes (ldq >= K); bytes K .. min(ldq, K rounded up to 16) - 1 of
+ * each row are written as zeros. S is ceil(K / 128) x R float32 values, block by block: S[b][r] at S[b * lds
+ * + r], lds >= R, 4-byte aligned. X needs 2-byte alignment only.
+ * R == 0 or K == 0: nothing. GEMM_ERR_INVALID_ARG for negative sizes, leading dimensions that are too small,
+ * a null pointer with a non-empty extent, or a misaligned X or S; GEMM_ERR_UNSUPPORTED for R >= 2^24 or K >
+ * 2^30. Deterministic, one launch (more from about 2^28 blocks).
+ */
+int gemm_f8_quantize(int64_t R, int64_t K, const void *X, int64_t ldx, void *Q, int64_t ldq,
+                     float *S, int64_t lds, gemm_stream_t stream);
+
+/*
+ * gemm_f8_quantize_weight: the same for E bf16 weights W (N x K each, ldw >= K, one weight stride_w elements
+ * after the other), with a scale for each 128 x 128 block: S[j][b] covers rows 128 j .. 128 j + 127 and columns
+ * 128 b .. 128 b + 127, at S[j * lds + b], lds >= ceil(K / 128). Q and S of the next weight follow after
+ * stride_q bytes and stride_s floats (E > 1: at least N * ldq and ceil(N / 128) * lds, else
+ * GEMM_ERR_INVALID_ARG). Otherwise as gemm_f8_quantize; GEMM_ERR_UNSUPPORTED for N >= 2^24, E > 65536, or a
+ * weight of 2^24 blocks or more.
+ */
+int gemm_f8_quantize_weight(int64_t E, int64_t N, int64_t K, const void *W, int64_t ldw,
+                            int64_t stride_w, void *Q, int64_t ldq, int64_t stride_q, float *S,
+                            int64_t lds, int64_t stride_s, gemm_stream_t stream);
+
+/*
+ * gemm_f8: the product above. Aq is M x K codes (ldaq >= K), Sa ceil(K / 128) x M scales (ldsa >= M), Wq N x K
+ * codes (ldwq >= K), Sw ceil(N / 128) x ceil(K / 128) scales (ldsw >= ceil(K / 128)), C M x N bf16 (ldc >= N,
+ * fully overwritten, no overlap with the inputs). Codes that are NaN make the outputs that use them NaN.
+ * Aq and Wq with 16-byte aligned pointers and leading dimensions (what the quantisers write with ldq a
+ * multiple of 16) run the matrix kernels for any M, N and K; other operands run a general kernel with the
+ * same result contract, tens of times slower. Bytes between K and the leading dimension may hold anything.
+ * M == 0 or N == 0: nothing. K == 0: C = 0. GEMM_ERR_INVALID_ARG for negative sizes, a leading dimension that
+ * is too small, a null pointer with a non-empty extent, a C that is not 2-byte or a scale that is not 4-byte
+ * aligned; GEMM_ERR_UNSUPPORTED for M >= 2^24, K > 2^30, or a general kernel's C of 2^24 or more 64 x 64
+ * tiles. Deterministic, enqueued without synchronising, and using the stream's workspace region like gemm_bf16.
+ */
+int gemm_f8(int64_t M, int64_t N, int64_t K, const void *Aq, int64_t ldaq, const float *Sa,
+            int64_t ldsa, const void *Wq, int64_t ldwq, const float *Sw, int64_t ldsw, void *C,
+            int64_t ldc, gemm_stream_t stream);
+
+/*
+ * gemm_f8_work_bytes: host-only. Bytes of the buffer `work` that gemm_f8_bf16 and gemm_f8_grouped_bf16 need
+ * for M x K activations (codes with rows padded to 16 bytes, then scales). GEMM_ERR_INVALID_ARG for negative
+ * sizes or a null result pointer; GEMM_ERR_UNSUPPORTED when M reaches 2^24 or K exceeds 2^30.
+ */
+int gemm_f8_work_bytes(int64_t M, int64_t K, int64_t *bytes);
+
+/*
+ * gemm_f8_bf16: gemm_f8_quantize of the bf16 activations A (M x K, lda >= K) into `work`, then gemm_f8.
+ * `work` is device memory of at least gemm_f8_work_bytes(M, K) bytes, 16-byte aligned, that the caller owns
+ * and may reuse once the call's work on the stream is done; `work_bytes` is its size (GEMM_ERR_INVALID_ARG
+ * when it is too small or misaligned). Other errors as gemm_f8. A refused call has not written to `work`.
+ */
+int gemm_f8_bf16(int64_t M, int64_t N, int64_t K, const void *A, int64_t lda, const void *Wq,
+                 int64_t ldwq, const float *Sw, int64_t ldsw, void *C, int64_t ldc, void *work,
+                 int64_t work_bytes, gemm_stream_t stream);
+
+/* ------------------------------------------------------------------------------------------
+ * Products grouped by expert: the M rows of A are cut into E groups, each with a weight of its own. Group e
+ * is rows offsets[e] .. offsets[e + 1] - 1, of `offsets`, E + 1 32-bit integers in device memory that are
+ * read by the kernels (a router's counts need not come to the host; the call may be captured, and replayed
+ * with other offsets). Groups may be empty. Rows before offsets[0] and from offsets[E] on belong to no
+ * group: they are not read, and their rows of C (or dA) are written as zeros. No value of the offsets reads
+ * or writes out of range: an offset counts as the largest of itself, 0 and those before it, and as M
+ * beyond M.
+ * One group's weight may be anywhere: B of group e starts stride_b elements after group e - 1's (0: one
+ * weight for all). Otherwise operands, arithmetic and errors are those of the products of one weight, with
+ * GEMM_ERR_INVALID_ARG for negative E or strides and for offsets that are null (M > 0 and E > 0) or not
+ * 4-byte aligned, and GEMM_ERR_UNSUPPORTED for M >= 2^24 or E > 65536. E == 0: C (or dA) is zero.
+ * Deterministic, enqueued without synchronising, using the stream's workspace region like gemm_bf16. A
+ * refused call has written nothing.
+ * ------------------------------------------------------------------------------------------ */
+
+/*
+ * gemm_bf16_grouped: C[r] = A[r] * B[e] for every row r of every group e: A M x K (lda >= K), B E x K x N
+ * (ldb >= N), C M x N (ldc >= N), bf16, float32 accumulation, each output rounded once. Operands whose
+ * pointers are not 16-byte aligned, or whose N, K, strides or leading dimensions are not multiples of 8, run
+ * a general kernel with the same contract, tens of times slower (GEMM_ERR_UNSUPPORTED for a C of about 2^24
+ * or more 64 x 64 tiles there).
+ */
+int gemm_bf16_grouped(int64_t M, int64_t N, int64_t K, int64_t E, const void *A, int64_t lda,
+                      const void *B, int64_t ldb, int64_t stride_b, const int32_t *offsets, void *C,
+                      int64_t ldc, gemm_stream_t stream);
+
+/*
+ * gemm_bf16_grouped_bwd: its gradients from dC (M x N, lddc >= N): for every group e with rows R_e
+ *   dA[R_e] = dC[R_e] * B[e]^T (M x K, ldda >= K),   dB[e] = A[R_e]^T * dC[R_e] (E x K x N, lddb >= N, the
+ * next one after stride_db elements, at least K * lddb where E > 1). An empty group's dB is zero; rows of no
+ * group have zero dA, and neither their A nor their dC is read. A null dA or dB is not computed; then B or A
+ * respectively is not read and may be null. Both are overwritten, not accumulated into. A weight that groups
+ * share (stride_b 0) has the sum of their dB as its gradient.
+ */
+int gemm_bf16_grouped_bwd(int64_t M, int64_t N, int64_t K, int64_t E, const void *dC, int64_t lddc,
+                          const void *A, int64_t lda, const void *B, int64_t ldb, int64_t stride_b,
+                          const int32_t *offsets, void *dA, int64_t ldda, void *dB, int64_t lddb,
+                          int64_t stride_db, gemm_stream_t stream);
+
+/*
+ * gemm_f8_grouped: gemm_f8 with E weights: Wq E x N x K codes (the next weight after stride_wq bytes), Sw their
+ * scales (after stride_sw floats). Rows of no group are written as zeros.
+ */
+int gemm_f8_grouped(int64_t M, int64_t N, int64_t K, int64_t E, const void *Aq, int64_t ldaq,
+                    const float *Sa, int64_t ldsa, const void *Wq, int64_t ldwq, int64_t stride_wq,
+                    const float *Sw, int64_t ldsw, int64_t stride_sw, const int32_t *offsets,
+                    void *C, int64_t ldc, gemm_stream_t stream);
+
+/* gemm_f8_grouped_bf16: gemm_f8_quantize of A into `work`, then gemm_f8_grouped; as gemm_f8_bf16. */
+int gemm_f8_grouped_bf16(int64_t M, int64_t N, int64_t K, int64_t E, const void *A, int64_t lda,
+                         const void *Wq, int64_t ldwq, int64_t stride_wq, const float *Sw,
+                         int64_t ldsw, int64_t stride_sw, const int32_t *offsets, void *C,
+                         int64_t ldc, void *work, int64_t work_bytes, gemm_stream_t stream);
+
 /* Flags of gemm_plan_describe. */
 #define GEMM_PLAN_SKINNY 1 /* the plan of gemm_bf16_skinny */
 #define GEMM_PLAN_SWIGLU 2 /* the plan of gemm_bf16_swiglu (with GEMM_PLAN_SKINNY: its skinny form) */
