@@ -8,6 +8,7 @@
 #include "f8.h"
 #include "group.h"
 #include "ops.h"
+#include "plan.h"
 
 namespace glk {
 

@@ -1,0 +1,126 @@
+// Matrix kernels of the bf16 products grouped by expert for gfx950: the tiles, copies, schedules and epilogue of
+// ops_tile.h, each workgroup finding its group and tile in the row offsets on the device (group.h).
+
+#include "group.h"
+#include "ops_tile.h"
+
+namespace glk {
+
+// Narrows p to the group and tile of workgroup `block`; false where there is none. Rows of no group are a product
+// over nothing, which writes zeros.
+template <int MODE, int BT>
+__device__ __forceinline__ bool group_tile(OpTileArgs& p, const GroupArgs& g, int block, OpPlace* at) {
+    constexpr int ES = MODE == kOpF8 ? 1 : 2;
+    auto uni = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
+    if constexpr (MODE == kOpAtb) {
+        const int tiles = p.tiles_m * p.tiles_n, per = tiles * p.splits;
+        const int unit = xcd_remap(block, g.groups * per, p.nxcd), group = uni(unit / per);
+        int first, rows;
+        group_rows(g, group, &first, &rows);
+        *at = op_place_unit<BT, BT>(p, unit - group * per);
+        at->tile += group * tiles;
+        p.A = static_cast<const char*>(p.A) + (int64_t)first * p.lda * ES;
+        p.B = static_cast<const char*>(p.B) + (int64_t)first * p.ldb * ES;
+        p.C += group * g.stride_c;
+        p.K = rows;
+        const int steps = (rows + 31) / 32;
+        p.kt_per_split = uni((steps + p.splits - 1) / p.splits);
+    } else {
+        GroupSpan s;
+        if (!find_span(g, BT, p.tiles_n * p.splits, p.nxcd, block, &s)) return false;
+        p.tiles_m = s.tiles;
+        *at = op_place_unit<BT, BT>(p, s.unit);
+        at->tile += s.tile * p.tiles_n;
+        p.A = static_cast<const char*>(p.A) + (int64_t)s.first * p.lda * ES;
+        p.C += (int64_t)s.first * p.ldc;
+        p.M = s.rows;
+        if (s.group < 0)
+            p.K = 0;
+        else
+            p.B = static_cast<const char*>(p.B) + s.group * g.stride_b * ES;
+    }
+    return true;
+}
+
+template <int MODE>
+__global__ void __attribute__((amdgpu_flat_work_group_size(512, 512), amdgpu_waves_per_eu(2, 2)))
+group_pp_kernel(OpTileArgs p, GroupArgs g) {
+    extern __shared__ __attribute__((aligned(1024))) char lds[];
+    OpPlace at;
+    if (group_tile<MODE, 256>(p, g, (int)blockIdx.x, &at)) op_pp<MODE, false>(p, at, lds);
+}
+
+template <int BT, int MODE>
+__global__ void __attribute__((amdgpu_flat_work_group_size(256, 256), amdgpu_waves_per_eu(2, BT == 64 ? 4 : 2)))
+group_small_kernel(OpTileArgs p, GroupArgs g) {
+    extern __shared__ __attribute__((aligned(1024))) char lds[];
+    OpPlace at;
+    if (group_tile<MODE, BT>(p, g, (int)blockIdx.x, &at)) op_small<BT, MODE, false>(p, at, lds);
+}
+
+// Both gradients in one launch: dA = dC B^T first, dB = A^T dC after.
+template <int BT>
+__global__ void __attribute__((amdgpu_flat_work_group_size(256, 256), amdgpu_waves_per_eu(2, BT == 64 ? 4 : 2)))
+group_pair_kernel(OpTileArgs pa, GroupArgs ga, int grid_a, OpTileArgs pb, GroupArgs gb) {
+    extern __shared__ __attribute__((aligned(1024))) char lds[];
+    OpPlace at;
+    if ((int)blockIdx.x < grid_a) {
+        if (group_tile<kOpAbt, BT>(pa, ga, (int)blockIdx.x, &at)) op_small<BT, kOpAbt, false>(pa, at, lds);
+    } else {
+        if (group_tile<kOpAtb, BT>(pb, gb, (int)blockIdx.x - grid_a, &at)) op_small<BT, kOpAtb, false>(pb, at, lds);
+    }
+}
+
+template <int MODE>
+static hipError_t launch_mode(int tile, const OpTileArgs& a, const GroupArgs& g, int grid, hipStream_t s) {
+    if (tile == 256) {
+        if (a.splits != 1) return hipErrorInvalidValue;
+        group_pp_kernel<MODE><<<grid, 512, OpTile<256, 256, 2, 4, MODE>::LDS_BYTES, s>>>(a, g);
+    } else if (tile == 128) {
+        group_small_kernel<128, MODE><<<grid, 256, OpTile<128, 128, 2, 2, MODE>::LDS_BYTES, s>>>(a, g);
+    } else {
+        group_small_kernel<64, MODE><<<grid, 256, OpTile<64, 64, 2, 2, MODE>::LDS_BYTES, s>>>(a, g);
+    }
+    return hipGetLastError();
+}
+
+hipError_t launch_group_tile(int mode, int tile, const OpTileArgs& a, const GroupArgs& g, int grid, hipStream_t s) {
+    switch (mode) {
+        case kOpAb: return launch_mode<kOpAb>(tile, a, g, grid, s);
+        case kOpAbt: return launch_mode<kOpAbt>(tile, a, g, grid, s);
+        case kOpAtb: return launch_mode<kOpAtb>(tile, a, g, grid, s);
+        default: return hipErrorInvalidValue;
+    }
+}
+
+hipError_t launch_group_pair(int tile, const OpTileArgs& a, const GroupArgs& ga, int grid_a, const OpTileArgs& b,
+                             const GroupArgs& gb, int grid_b, hipStream_t s) {
+    if (tile == 128)
+        group_pair_kernel<128><<<grid_a + grid_b, 256, OpTile<128, 128, 2, 2, kOpAbt>::LDS_BYTES, s>>>(a, ga, grid_a, b, gb);
+    else
+        group_pair_kernel<64><<<grid_a + grid_b, 256, OpTile<64, 64, 2, 2, kOpAbt>::LDS_BYTES, s>>>(a, ga, grid_a, b, gb);
+    return hipGetLastError();
+}
+
+static hipError_t set_lds(const void* kernel, int bytes) {
+    return hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
+// (the 64 x 64 kernels ask for 40 KB, which needs no setting)
+template <int MODE>
+static hipError_t configure_mode() {
+    hipError_t e = set_lds((const void*)group_pp_kernel<MODE>, OpTile<256, 256, 2, 4, MODE>::LDS_BYTES);
+    if (e == hipSuccess)
+        e = set_lds((const void*)group_small_kernel<128, MODE>, OpTile<128, 128, 2, 2, MODE>::LDS_BYTES);
+    return e;
+}
+
+hipError_t configure_group_kernels() {
+    hipError_t e = configure_mode<kOpAb>();
+    if (e == hipSuccess) e = configure_mode<kOpAbt>();
+    if (e == hipSuccess) e = configure_mode<kOpAtb>();
+    if (e == hipSuccess) e = set_lds((const void*)group_pair_kernel<128>, OpTile<128, 128, 2, 2, kOpAbt>::LDS_BYTES);
+    return e;
+}
+
+}  // namespace glk

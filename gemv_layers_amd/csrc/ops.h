@@ -48,12 +48,6 @@ hipError_t launch_op_generic(int mode, bool glu, const OpArgs& a, hipStream_t s)
 // (kOpAtb, where a.K is not read).
 hipError_t launch_group_generic(int mode, const OpArgs& a, const GroupArgs& g, hipStream_t s);
 constexpr int kMaxGroups = 65536;
-// most tiles of `bm` rows over `rows` rows in `groups` groups and those of none, wherever they are cut
-inline int64_t most_row_tiles(int64_t rows, int64_t groups, int64_t bm) {
-    const int64_t parts = groups + 2 < rows ? groups + 2 : rows;
-    return (rows + parts * (bm - 1)) / bm;
-}
-
 // ---- MFMA tiles ---------------------------------------------------------------------------------
 // One launch over an M x N output (or a rectangle of it), sizes in elements.
 struct OpTileArgs {
@@ -77,6 +71,14 @@ hipError_t launch_op_tile(int mode, bool glu, int tile, const OpTileArgs& a, int
 // kOpAbt on `a` and kOpAtb on `b` in one launch, tiles of 128 or 64
 hipError_t launch_op_pair(int tile, const OpTileArgs& a, const OpTileArgs& b, int grid, hipStream_t s);
 hipError_t configure_op_kernels();
+// the same tiles over grouped rows, their sizes read from the offsets (kOpAb, kOpAbt, kOpAtb). a.M is all rows,
+// a.tiles_m not read; for kOpAtb a.M is A's width, a.K and a.kt_per_split are not read and the tiles are those of
+// one group. `grid`: the most units that any offsets make.
+hipError_t launch_group_tile(int mode, int tile, const OpTileArgs& a, const GroupArgs& g, int grid, hipStream_t s);
+// kOpAbt on `a`, its first `grid_a` workgroups, and kOpAtb on `b` in one launch, tiles of 128 or 64
+hipError_t launch_group_pair(int tile, const OpTileArgs& a, const GroupArgs& ga, int grid_a, const OpTileArgs& b,
+                             const GroupArgs& gb, int grid_b, hipStream_t s);
+hipError_t configure_group_kernels();
 
 // ---- 8-bit product of few tokens -------------------------------------------------------------------
 constexpr int kI8FusedK = 16384;  // the longest row that the fused form quantises

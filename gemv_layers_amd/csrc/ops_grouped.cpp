@@ -35,12 +35,26 @@ const char* op_name(int mode, bool grouped) {
 // A product that is ready to launch: planned, its limits checked, its workspace at hand. A call prepares
 // every product it makes before it launches anything, so that a refused one has written nothing.
 struct Ready {
-    enum Route { kZero, kGeneral } route = kZero;
+    enum Route { kZero, kGeneral, kTiles } route = kZero;
     int mode = 0;
     OpArgs a{};
     GroupArgs g{};
     glk::Plan p;
+    glk::Workspace w;
 };
+
+// Whether the matrix kernels take these operands: 16-byte aligned rows, 32-bit offsets within a tile, and
+// widths of 8 except along the rows of groups.
+bool matrix_ok(int mode, const OpArgs& a, const GroupArgs& g) {
+    const int64_t unit = mode == glk::kOpF8 ? 16 : 8;
+    const int64_t max_ld = int64_t(1) << 20, max_dim = int64_t(1) << 26;
+    if (misaligned(a.A, 16) || misaligned(a.B, 16) || (a.lda % unit) || (a.ldb % unit) || (g.stride_b % unit)) return false;
+    if (a.lda > max_ld || a.ldb > max_ld || a.ldc > max_ld) return false;
+    if (a.M > max_dim || a.N > max_dim || a.K > max_dim) return false;
+    if (mode == glk::kOpF8) return false;
+    if (misaligned(a.C, 16) || (a.ldc % 8) || (g.stride_c % 8) || (a.N % 8)) return false;
+    return mode == glk::kOpAtb ? a.M % 8 == 0 : a.K % 8 == 0;
+}
 
 // One product on the current device with a non-empty C, operands checked. The rows of C (of kOpAtb those of
 // all groups' C together) are written whole.
@@ -56,6 +70,12 @@ int prepare(int mode, const OpArgs& a, const GroupArgs& g, hipStream_t stream, R
         r->p = glk::make_plan(a.M, a.N, 0, *dev, false, 2, false);
         return GEMM_OK;
     }
+    if (matrix_ok(mode, a, g)) {
+        r->route = Ready::kTiles;
+        r->p = glk::make_group_plan(g.rows, a.M, a.N, a.K, g.groups, *dev, mode == glk::kOpAtb);
+        if (r->p.grid > INT32_MAX) return GEMM_ERR_UNSUPPORTED;
+        return r->p.ws_floats > 0 ? glk::stream_workspace(stream, &r->w) : GEMM_OK;
+    }
     // 64 x 64 tiles of 256 threads, 32-bit grids
     const int64_t row_tiles =
         mode == glk::kOpAtb ? ((a.M - 1) / 64 + 1) * g.groups : glk::most_row_tiles(g.rows, g.offsets ? g.groups : 1, 64);
@@ -69,6 +89,33 @@ glk::OpPlan plan_of(const Ready& r) {
     return {op_name(r.mode, r.g.offsets != nullptr), r.p, r.a.M, r.a.N, r.mode == glk::kOpAtb ? r.g.rows : r.a.K};
 }
 
+glk::OpTileArgs tile_args(const Ready& r) {
+    const OpArgs& a = r.a;
+    glk::OpTileArgs t{};
+    t.A = a.A;
+    t.B = a.B;
+    t.C = a.C;
+    t.sa = a.sa;
+    t.sb = a.sb;
+    t.M = (int)a.M;
+    t.N = (int)a.N;
+    t.K = (int)a.K;
+    t.lda = (int)a.lda;
+    t.ldb = (int)a.ldb;
+    t.ldc = (int)a.ldc;
+    t.up = (int)a.N;
+    t.vec = !misaligned(a.C, 16) && a.ldc % 8 == 0 && a.N % 8 == 0;
+    t.tiles_m = (int)r.p.tiles_m;
+    t.tiles_n = (int)r.p.tiles_n;
+    t.group_m = r.p.group_m;
+    t.nxcd = r.p.nxcd;
+    t.splits = r.p.splits;
+    t.kt_per_split = r.p.kt_per_split;
+    t.ws = r.w.ws;
+    t.counters = r.w.counters;
+    return t;
+}
+
 int launch(const Ready& r, hipStream_t stream) {
     const OpArgs& a = r.a;
     hipError_t e = hipSuccess;
@@ -79,9 +126,33 @@ int launch(const Ready& r, hipStream_t stream) {
         case Ready::kGeneral:
             e = glk::launch_group_generic(r.mode, a, r.g, stream);
             break;
+        case Ready::kTiles:
+            e = glk::launch_group_tile(r.mode, r.p.bm, tile_args(r), r.g, (int)r.p.grid, stream);
+            break;
     }
     if (e != hipSuccess) return GEMM_ERR_HIP;
     glk::set_last_plan(plan_of(r));
+    return GEMM_OK;
+}
+
+// Both gradients as one launch where each is a grid of the same small tiles: the second's partials follow the
+// first's.
+int launch_gradients(const Ready& a, Ready b, const glk::DeviceInfo& dev, hipStream_t stream) {
+    const glk::Plan &pa = a.p, &pb = b.p;
+    const bool pair = a.route == Ready::kTiles && b.route == Ready::kTiles && pa.bm == pb.bm && pa.bm < 256 &&
+                      pa.grid + pb.grid <= INT32_MAX && pa.ws_floats + pb.ws_floats <= dev.ws_floats &&
+                      pa.counters + pb.counters <= dev.ws_counters;
+    if (!pair) {
+        const int st = launch(a, stream);
+        return st == GEMM_OK ? launch(b, stream) : st;
+    }
+    if (pa.ws_floats > 0 && pb.ws_floats > 0) {
+        b.w.ws = a.w.ws + pa.ws_floats;
+        b.w.counters = a.w.counters + pa.counters;
+    }
+    if (glk::launch_group_pair(pa.bm, tile_args(a), a.g, (int)pa.grid, tile_args(b), b.g, (int)pb.grid, stream) != hipSuccess)
+        return GEMM_ERR_HIP;
+    glk::set_last_plan(plan_of(b), plan_of(a));
     return GEMM_OK;
 }
 
@@ -282,9 +353,13 @@ int gemm_bf16_grouped_bwd(int64_t M, int64_t N, int64_t K, int64_t E, const void
             const OpArgs b{A, dC, static_cast<uint16_t*>(dB), nullptr, nullptr, nullptr, K, N, 0, lda, lddc, lddb, 0};
             st = prepare(glk::kOpAtb, b, GroupArgs{offsets, (int)E, (int)M, 0, stride_db, 0}, hip_stream(stream), &rb);
         }
-        if (st == GEMM_OK && need_a) st = launch(ra, hip_stream(stream));
-        if (st == GEMM_OK && need_b) st = launch(rb, hip_stream(stream));
-        return st;
+        if (st != GEMM_OK) return st;
+        if (need_a && need_b) {
+            const glk::DeviceInfo* dev = glk::current_device(&st);
+            return dev ? launch_gradients(ra, rb, *dev, hip_stream(stream)) : st;
+        }
+        if (need_a) return launch(ra, hip_stream(stream));
+        return need_b ? launch(rb, hip_stream(stream)) : GEMM_OK;
     });
 }
 

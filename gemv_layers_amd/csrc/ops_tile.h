@@ -191,11 +191,10 @@ __device__ __forceinline__ void op_clear_tail(int left, int lane, u32x4 (&f)[T])
 struct OpPlace {
     int m0, n0, piece, tile;
 };
-// which tile, in grouped order over the XCDs' contiguous shares
+// the tile and piece of unit `unit` of p's tiles times pieces, in grouped order
 template <int BM, int BNO>
-__device__ __forceinline__ OpPlace op_place(const OpTileArgs& p, int block) {
-    const int pieces = p.splits, ntiles = p.tiles_m * p.tiles_n;
-    const int unit = xcd_remap(block, ntiles * pieces, p.nxcd);
+__device__ __forceinline__ OpPlace op_place_unit(const OpTileArgs& p, int unit) {
+    const int pieces = p.splits;
     const int tile = unit / pieces;
     const int per_group = p.group_m * p.tiles_n;
     const int g = tile / per_group, first = g * p.group_m;
@@ -204,6 +203,11 @@ __device__ __forceinline__ OpPlace op_place(const OpTileArgs& p, int block) {
     // (uniform, but the divisions leave them in vector registers)
     auto uni = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
     return OpPlace{uni((first + in % gm) * BM), uni((in / gm) * BNO), uni(unit - tile * pieces), uni(tile)};
+}
+// which tile, in grouped order over the XCDs' contiguous shares
+template <int BM, int BNO>
+__device__ __forceinline__ OpPlace op_place(const OpTileArgs& p, int block) {
+    return op_place_unit<BM, BNO>(p, xcd_remap(block, p.tiles_m * p.tiles_n * p.splits, p.nxcd));
 }
 
 // ---- epilogue ------------------------------------------------------------------------------------

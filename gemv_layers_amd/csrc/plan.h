@@ -89,6 +89,17 @@ Plan make_i8_decode_plan(int64_t M, int64_t N, int64_t K, const DeviceInfo& dev,
 // whether that plan beats the tiles (M may be any)
 bool i8_decode_fits(int64_t M, int64_t K, const Plan& p);
 
+// most tiles of `bm` rows over `rows` rows in `groups` groups and those of none, wherever they are cut
+inline int64_t most_row_tiles(int64_t rows, int64_t groups, int64_t bm) {
+    const int64_t parts = groups + 2 < rows ? groups + 2 : rows;
+    return (rows + parts * (bm - 1)) / bm;
+}
+
+// The products grouped by rows: `rows` rows in `groups` groups whose sizes the host does not know, an output of N
+// columns over K (kOpAb, kOpAbt, kOpF8 in k-steps of 32 bf16 elements); or, `summed`, for each group an M x N
+// output over its own rows. The grid and workspace hold whatever sizes the groups have.
+Plan make_group_plan(int64_t rows, int64_t M, int64_t N, int64_t K, int64_t groups, const DeviceInfo& dev, bool summed);
+
 std::string plan_json(const Plan& p, int64_t M, int64_t N, int64_t K);
 
 }  // namespace glk
