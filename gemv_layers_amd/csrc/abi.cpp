@@ -613,6 +613,7 @@ int gemm_init(int device) {
     if (rc == GEMM_OK && glk::configure_op_kernels() != hipSuccess) rc = GEMM_ERR_HIP;
     if (rc == GEMM_OK && glk::configure_i8_decode() != hipSuccess) rc = GEMM_ERR_HIP;
     if (rc == GEMM_OK && glk::configure_group_kernels() != hipSuccess) rc = GEMM_ERR_HIP;
+    if (rc == GEMM_OK && glk::configure_f8_kernels() != hipSuccess) rc = GEMM_ERR_HIP;
     if (rc == GEMM_OK) {
         ds.ready.store(true, std::memory_order_release);
         ++g_ready_count;

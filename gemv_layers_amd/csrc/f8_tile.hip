@@ -1,0 +1,376 @@
+// Matrix kernels of the 8-bit floating-point products for gfx950: C = sum over blocks b of 128 k of (A W^T)_b
+// sa[b][m] sw[n / 128][b], one weight or one for each group of rows.
+//
+// A block of the summed index is one v_mfma_f32_16x16x128_f8f6f4 for each 16 x 16 output block, started from
+// zero; its four sums a lane are then added to the accumulators times the block's two scales: four float32 FMAs
+// (16 cycles of the SIMD's vector unit) beside 32 cycles of its matrix core. Weights are the first operand, so
+// that a lane's four sums belong to one row of C and take one factor.
+//
+// Copies, LDS rings of 128-byte rows and schedules are those of ops_tile.h for 64-byte steps of two contiguous
+// operands, of which two make a block: a pair of steps reads the block's activations once (both 64-byte halves,
+// the MFMA's 32 bytes a lane: any order of k serves that is the same in both operands), and in each step half of
+// the wave's weights. Activations are read in a pair's first step alone, so their ring needs four slots for the
+// five of the weights, and the scales fit beside them: those of the tile's rows come for each block by a copy of
+// 4 bytes a lane, two blocks in turn, and the weight's, one number for each 128 columns that a wave's columns lie
+// within, wait in two registers of 64 blocks each.
+// Codes past K in the last 16-byte chunk of a row are the caller's padding, which may hold NaN: cleared in both
+// operands.
+
+#include "group_tile.h"
+
+namespace glk {
+
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+
+// WM x WN waves; a wave's columns lie within 128
+template <int BM_, int BN_, int WM, int WN>
+struct F8Tile {
+    static constexpr int BM = BM_, BN = BN_;
+    static constexpr int NW = WM * WN;
+    static constexpr int WTM = BM / WM, WTN = BN / WN;
+    static constexpr int TM = WTM / 16, TN = WTN / 16, HN = TN / 2;  // HN weight tiles a step
+    static constexpr int A_SLOTS = 4, B_SLOTS = 5;
+    static constexpr int A_BYTES = BM * 64, B_BYTES = BN * 64;  // one slot: half of the rows, 128 bytes of each
+    static constexpr int B_RING = A_SLOTS * A_BYTES;
+    static constexpr int S_RING = B_RING + B_SLOTS * B_BYTES;  // scales: 256 bytes a wave and block, two blocks
+    static constexpr int S_BYTES = NW * 256;
+    static constexpr int S_ROWS = BM / NW;                     // rows whose scales a wave copies
+    static constexpr int LDS_BYTES = S_RING + 2 * S_BYTES;
+    static constexpr int A_PW = A_BYTES / 1024 / NW, B_PW = B_BYTES / 1024 / NW;
+    static constexpr int LOADS = A_PW + B_PW;
+    using Acc = f32x4;
+    static_assert(A_PW * NW * 1024 == A_BYTES && B_PW * NW * 1024 == B_BYTES, "copies split evenly");
+    static_assert(WTN <= 128 && S_ROWS <= 64 && LDS_BYTES <= 160 * 1024, "layout");
+};
+
+// T tiles of 16 rows from `w0` (within one half of the R rows) of the block in units `unit` and unit + 1 of a
+// ring of SLOTS: both 64-byte halves of the lane's k
+template <int R, int SLOTS, int T>
+__device__ __forceinline__ void f8_read(const char* ring, int unit_slot, int w0, int lane, u32x4 (&f)[T][2]) {
+    const int j = lane & 15, G = lane >> 4;
+    int at = unit_slot + (w0 >= R / 2 ? 1 : 0);
+    at = at >= SLOTS ? at - SLOTS : at;
+    const char* row = ring + at * (64 * R) + (w0 % (R / 2) + j) * 128;
+#pragma unroll
+    for (int i = 0; i < T; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            f[i][h] = *reinterpret_cast<const u32x4*>(row + i * 2048 + 16 * ((4 * h + G) ^ (j >> 1)));
+}
+
+// clears the codes at `left` and after in a block's fragments
+template <int T>
+__device__ __forceinline__ void f8_clear_tail(int left, int lane, u32x4 (&f)[T][2]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int n = left - 64 * h - 16 * (lane >> 4);  // codes of the lane's 16 that count
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            const int b = n - 4 * w;
+            const uint32_t mask = b >= 4 ? 0xFFFFFFFFu : (b <= 0 ? 0u : (1u << (8 * b)) - 1u);
+#pragma unroll
+            for (int i = 0; i < T; ++i) f[i][h][w] &= mask;
+        }
+    }
+}
+
+__device__ __forceinline__ f32x4 f8_mfma(const u32x4 (&w)[2], const u32x4 (&a)[2]) {
+    const i32x8 x = {(int)w[0][0], (int)w[0][1], (int)w[0][2], (int)w[0][3], (int)w[1][0], (int)w[1][1], (int)w[1][2], (int)w[1][3]};
+    const i32x8 y = {(int)a[0][0], (int)a[0][1], (int)a[0][2], (int)a[0][3], (int)a[1][0], (int)a[1][1], (int)a[1][2], (int)a[1][3]};
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
+}
+
+// Each lane copies 4 bytes from descriptor + voff into LDS at lds_base + 4 * lane (as dma16).
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+__device__ __forceinline__ void dma4(const i32x4& rsrc, uint32_t lds_base, uint32_t voff) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
+                 :
+                 : "s"(lds_base), "v"(voff), "s"(rsrc)
+                 : "memory", "m0");
+}
+#pragma clang diagnostic pop
+
+// The scales of a tile: its rows' copied into LDS block by block, the weight's in registers.
+template <class T>
+struct F8Scales {
+    const float* sa;   // of the wave's rows to copy, block 0
+    const float* sb;   // of the weight's 128 columns, block 0
+    int64_t ldsa;
+    uint32_t off;      // of the lane's row to copy
+    int count;         // blocks
+    float w[2];        // of blocks 128 i + lane and 64 more
+
+    __device__ __forceinline__ void init(const OpTileArgs& p, const OpPlace& at, int first, int blocks, int wave, int wn,
+                                         int lane) {
+        const int row = wave * T::S_ROWS + lane;
+        ldsa = p.ldsa;
+        sa = p.sa + first * ldsa + at.m0;
+        off = sel_off(lane < T::S_ROWS && at.m0 + row < p.M, (uint32_t)row * 4u);
+        // (past N: any block of the weight, whose columns are not stored)
+        const int nb = min((at.n0 + wn * T::WTN) / 128, (p.N - 1) / 128);
+        sb = p.sb + nb * p.ldsb + first;
+        count = blocks;
+        load(0, lane);
+    }
+    __device__ __forceinline__ void load(int b, int lane) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) w[i] = b + 64 * i + lane < count ? sb[b + 64 * i + lane] : 0.f;
+    }
+    __device__ __forceinline__ void issue(int b, uint32_t lds, int wave) const {
+        const int from = b < count ? b : 0;  // (a block past the last: any, not read)
+        dma4(rsrc_words(sa + from * ldsa, kBufRecords), lds + T::S_RING + (b & 1) * T::S_BYTES + wave * 256, off);
+    }
+    // the factors of the wave's rows in block b: row w0 + 16 mi + (lane & 15)
+    __device__ __forceinline__ void read(const char* lds, int b, int w0, int lane, float (&s)[T::TM]) {
+        const int bits = __builtin_bit_cast(int, (b & 64) ? w[1] : w[0]);
+        const float sw = __builtin_bit_cast(float, __builtin_amdgcn_readlane(bits, b & 63));
+#pragma unroll
+        for (int mi = 0; mi < T::TM; ++mi) {
+            const int r = w0 + 16 * mi;
+            s[mi] = *reinterpret_cast<const float*>(lds + T::S_RING + (b & 1) * T::S_BYTES + (r / T::S_ROWS) * 256 +
+                                                    (r % T::S_ROWS + (lane & 15)) * 4) * sw;
+        }
+        if ((b & 127) == 127) load(b + 1, lane);
+    }
+};
+
+// acc += s (W A) for the weight tiles of step parity P. Product j + 2 is issued before product j's sums are added,
+// so that the FMAs read a result that is two MFMAs old and fit between their issues. (The empty statements and
+// scheduling barriers hold that order: left alone, the compiler issues all MFMAs first and runs out of registers.)
+template <class T, int P>
+__device__ __forceinline__ void f8_multiply(const u32x4 (&fb)[T::HN][2], const u32x4 (&fa)[T::TM][2], const float (&s)[T::TM],
+                                            f32x4 (&acc)[T::TN][T::TM]) {
+    constexpr int N = T::HN * T::TM;
+    f32x4 x[3];
+    x[0] = f8_mfma(fb[0], fa[0]);
+    x[1] = f8_mfma(fb[1 / T::TM], fa[1 % T::TM]);
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        if (j + 2 < N) x[(j + 2) % 3] = f8_mfma(fb[(j + 2) / T::TM], fa[(j + 2) % T::TM]);
+        __builtin_amdgcn_sched_barrier(0);
+        const int ni = P * T::HN + j / T::TM, mi = j % T::TM;
+        float c[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) c[r] = __builtin_fmaf(x[j % 3][r], s[mi], acc[ni][mi][r]);
+        asm volatile("" : "+v"(c[0]), "+v"(c[1]), "+v"(c[2]), "+v"(c[3]));
+        acc[ni][mi] = f32x4{c[0], c[1], c[2], c[3]};
+        __builtin_amdgcn_sched_barrier(0);
+    }
+}
+
+// ---- 256 x 256: two wave groups alternating memory and MFMA phases (op_pp's schedule) ------------------
+// Activations' unit u (half of the rows of block u / 2) is read in step u & ~1 alone, at the latest one step
+// before op_pp frees its slot: step t refills the slot of unit t - 1 with unit t + 3. The scales of block b + 1
+// are issued in the first step of block b, before that step's other copies, and awaited in its second.
+__global__ void __attribute__((amdgpu_flat_work_group_size(512, 512), amdgpu_waves_per_eu(2, 2)))
+f8_pp_kernel(OpTileArgs p, GroupArgs g) {
+    using T = F8Tile<256, 256, 4, 2>;
+    extern __shared__ __attribute__((aligned(1024))) char lds[];
+    OpPlace at;
+    if (!group_tile<kOpF8, 256>(p, g, (int)blockIdx.x, &at)) return;
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int grp = wave >> 2, wm = wave & 3, wn = grp;
+    const int blocks = (p.K + 127) / 128;
+
+    OpCopy<256, T::A_PW, true, 1, false, T::WTM> ca;
+    OpCopy<256, T::B_PW, true, 1, false, T::WTN> cb;
+    ca.init(p.A, p.lda, at.m0, p.M, 0, 0, p.K, wave, lane);
+    cb.init(p.B, p.ldb, at.n0, p.N, 0, 0, p.K, wave, lane);
+    F8Scales<T> sc;
+    sc.init(p, at, 0, blocks, wave, wn, lane);
+    const uint32_t ring = lds_addr(lds);
+    auto issue_a = [&](auto h, int u) { ca.template issue<decltype(h)::value>(u, ring + (u & 3) * T::A_BYTES, wave); };
+    auto issue_b = [&](auto h, int u, int slot) {
+        cb.template issue<decltype(h)::value>(u, ring + T::B_RING + slot * T::B_BYTES, wave);
+    };
+    f32x4 acc[T::TN][T::TM];
+#pragma unroll
+    for (int ni = 0; ni < T::TN; ++ni)
+#pragma unroll
+        for (int mi = 0; mi < T::TM; ++mi) acc[ni][mi] = f32x4{};
+    auto phase_barrier = [&]() {
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    const int tail = (p.K & 15) ? blocks - 1 : -1;
+    using P0 = std::integral_constant<int, 0>;
+    using P1 = std::integral_constant<int, 1>;
+
+    sc.issue(0, ring, wave);
+    issue_a(P0{}, 0);
+    issue_b(P0{}, 0, 0);
+    issue_a(P1{}, 1);
+    issue_b(P1{}, 1, 1);
+    issue_a(P0{}, 2);
+    issue_b(P0{}, 2, 2);
+    wait_vmcnt<T::LOADS>();
+    lds_barrier();
+    if (grp == 1) phase_barrier();
+    int slot = 0;  // of the weights' unit 2 b
+    u32x4 fa[T::TM][2];
+    float s[T::TM];
+#pragma clang loop unroll(disable)
+    for (int b = 0; b < blocks; ++b) {
+        {  // first step: all activations, the first weights
+            u32x4 fb[T::HN][2];
+            sc.read(lds, b, wm * T::WTM, lane, s);
+            f8_read<256, 4>(lds, (2 * b) & 3, wm * T::WTM, lane, fa);
+            f8_read<256, 5>(lds + T::B_RING, slot, wn * T::WTN, lane, fb);
+            sc.issue(b + 1, ring, wave);
+            issue_a(P1{}, 2 * b + 3);
+            issue_b(P1{}, 2 * b + 3, op_wrap(slot + 3));
+            if (b == tail) {
+                f8_clear_tail(p.K - 128 * b, lane, fa);
+                f8_clear_tail(p.K - 128 * b, lane, fb);
+            }
+            wait_lgkmcnt0();
+            phase_barrier();
+            f8_multiply<T, 0>(fb, fa, s, acc);
+            phase_barrier();
+        }
+        {  // second step: the other weights
+            u32x4 fb[T::HN][2];
+            f8_read<256, 5>(lds + T::B_RING, slot, wn * T::WTN + T::WTN / 2, lane, fb);
+            issue_a(P0{}, 2 * b + 4);
+            issue_b(P0{}, 2 * b + 4, op_wrap(slot + 4));
+            if (b == tail) f8_clear_tail(p.K - 128 * b, lane, fb);
+            wait_vmcnt<T::LOADS>();
+            wait_lgkmcnt0();
+            phase_barrier();
+            f8_multiply<T, 1>(fb, fa, s, acc);
+            phase_barrier();
+        }
+        slot = op_wrap(slot + 2);
+    }
+    if (grp == 0) phase_barrier();
+    wait_vmcnt<0>();  // the copies past K included
+    lds_barrier();    // the rings are free for the output
+    op_epilogue<T, kOpF8, false>(p, lds, at, wave, wm, wn, lane, acc);
+}
+
+// ---- 128 x 128 and 64 x 64, K split over idle CUs (op_small's schedule) --------------------------------
+// Iteration i reads the operands of step i + 1: a block's activations and first weights in the odd iteration
+// before it, where unit i of the activations, read two iterations before or in the last one, is over at the
+// barrier and takes unit i + 4. The scales of the block after the next are issued in odd iterations, whose
+// copies the next odd one awaits.
+template <int BT>
+__global__ void __attribute__((amdgpu_flat_work_group_size(256, 256), amdgpu_waves_per_eu(2, BT == 64 ? 4 : 2)))
+f8_small_kernel(OpTileArgs p, GroupArgs g) {
+    using T = F8Tile<BT, BT, 2, 2>;
+    extern __shared__ __attribute__((aligned(1024))) char lds[];
+    OpPlace at;
+    if (!group_tile<kOpF8, BT>(p, g, (int)blockIdx.x, &at)) return;
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave >> 1, wn = wave & 1;
+    const int total = (p.K + 127) / 128, per = p.kt_per_split / 2;
+    const int first = at.piece * per;
+    const int blocks = max(min(total - first, per), 0);
+    const int count = max(min(p.K - first * 128, blocks * 128), 0);  // of the summed index
+
+    OpCopy<BT, T::A_PW, true, 1, false, T::WTM> ca;
+    OpCopy<BT, T::B_PW, true, 1, false, T::WTN> cb;
+    ca.init(p.A, p.lda, at.m0, p.M, 0, (int64_t)first * 128, count, wave, lane);
+    cb.init(p.B, p.ldb, at.n0, p.N, 0, (int64_t)first * 128, count, wave, lane);
+    F8Scales<T> sc;
+    sc.init(p, at, first, blocks, wave, wn, lane);
+    const uint32_t ring = lds_addr(lds);
+    auto issue_a = [&](auto h, int u) { ca.template issue<decltype(h)::value>(u, ring + (u & 3) * T::A_BYTES, wave); };
+    auto issue_b = [&](auto h, int u, int slot) {
+        cb.template issue<decltype(h)::value>(u, ring + T::B_RING + slot * T::B_BYTES, wave);
+    };
+    f32x4 acc[T::TN][T::TM];
+#pragma unroll
+    for (int ni = 0; ni < T::TN; ++ni)
+#pragma unroll
+        for (int mi = 0; mi < T::TM; ++mi) acc[ni][mi] = f32x4{};
+    const int tail = (count & 15) ? blocks - 1 : -1;
+    using P0 = std::integral_constant<int, 0>;
+    using P1 = std::integral_constant<int, 1>;
+
+    u32x4 fa[T::TM][2], na[T::TM][2], fb[T::HN][2], nb[T::HN][2];
+    float s[T::TM], ns[T::TM];
+    sc.issue(0, ring, wave);
+    sc.issue(1, ring, wave);
+    issue_a(P0{}, 0);
+    issue_b(P0{}, 0, 0);
+    issue_a(P1{}, 1);
+    issue_b(P1{}, 1, 1);
+    issue_a(P0{}, 2);
+    issue_b(P0{}, 2, 2);
+    issue_a(P1{}, 3);
+    issue_b(P1{}, 3, 3);
+    wait_vmcnt<2 * T::LOADS>();  // units 0 and 1; 2 and 3 may be in flight
+    lds_barrier();
+    auto read_first = [&](int b, int at_slot, u32x4 (&xa)[T::TM][2], u32x4 (&xb)[T::HN][2], float (&xs)[T::TM]) {
+        sc.read(lds, b, wm * T::WTM, lane, xs);
+        f8_read<BT, 4>(lds, (2 * b) & 3, wm * T::WTM, lane, xa);
+        f8_read<BT, 5>(lds + T::B_RING, at_slot, wn * T::WTN, lane, xb);
+        if (b == tail) {
+            f8_clear_tail(count - 128 * b, lane, xa);
+            f8_clear_tail(count - 128 * b, lane, xb);
+        }
+    };
+    auto read_second = [&](int b, int at_slot, u32x4 (&xb)[T::HN][2]) {
+        f8_read<BT, 5>(lds + T::B_RING, at_slot, wn * T::WTN + T::WTN / 2, lane, xb);
+        if (b == tail) f8_clear_tail(count - 128 * b, lane, xb);
+    };
+    read_first(0, 0, fa, fb, s);
+    int slot = 0;  // of the weights' unit 2 b
+#pragma clang loop unroll(disable)
+    for (int b = 0; b < blocks; ++b) {
+        // step 2 b
+        lds_barrier();
+        issue_a(P0{}, 2 * b + 4);
+        issue_b(P0{}, 2 * b + 4, op_wrap(slot + 4));
+        read_second(b, slot, nb);
+        f8_multiply<T, 0>(fb, fa, s, acc);
+        // step 2 b + 1
+        const int next = op_wrap(slot + 2);
+        wait_vmcnt<T::LOADS>();  // this wave's copies of block b + 1 landed
+        lds_barrier();           // every wave's did, and the operands of step 2 b + 1 are in registers
+        sc.issue(b + 2, ring, wave);
+        issue_a(P1{}, 2 * b + 5);
+        issue_b(P1{}, 2 * b + 5, slot);
+        read_first(b + 1, next, na, fb, ns);
+        f8_multiply<T, 1>(nb, fa, s, acc);
+#pragma unroll
+        for (int mi = 0; mi < T::TM; ++mi) {
+            s[mi] = ns[mi];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) fa[mi][h] = na[mi][h];
+        }
+        slot = next;
+    }
+    wait_vmcnt<0>();
+    lds_barrier();
+    if (p.splits > 1 && !op_join<T>(p, at, lds, wave, lane, acc)) return;
+    op_epilogue<T, kOpF8, false>(p, lds, at, wave, wm, wn, lane, acc);
+}
+
+hipError_t launch_f8_tile(int tile, const OpTileArgs& a, const GroupArgs& g, int grid, hipStream_t s) {
+    if (tile == 256) {
+        if (a.splits != 1) return hipErrorInvalidValue;
+        f8_pp_kernel<<<grid, 512, F8Tile<256, 256, 4, 2>::LDS_BYTES, s>>>(a, g);
+    } else if (tile == 128) {
+        f8_small_kernel<128><<<grid, 256, F8Tile<128, 128, 2, 2>::LDS_BYTES, s>>>(a, g);
+    } else {
+        f8_small_kernel<64><<<grid, 256, F8Tile<64, 64, 2, 2>::LDS_BYTES, s>>>(a, g);
+    }
+    return hipGetLastError();
+}
+
+// (the 64 x 64 kernel asks for 38 KB, which needs no setting)
+hipError_t configure_f8_kernels() {
+    hipError_t e = hipFuncSetAttribute((const void*)f8_pp_kernel, hipFuncAttributeMaxDynamicSharedMemorySize,
+                                       F8Tile<256, 256, 4, 2>::LDS_BYTES);
+    if (e == hipSuccess)
+        e = hipFuncSetAttribute((const void*)f8_small_kernel<128>, hipFuncAttributeMaxDynamicSharedMemorySize,
+                                F8Tile<128, 128, 2, 2>::LDS_BYTES);
+    return e;
+}
+
+}  // namespace glk

@@ -1,46 +1,9 @@
 // Matrix kernels of the bf16 products grouped by expert for gfx950: the tiles, copies, schedules and epilogue of
 // ops_tile.h, each workgroup finding its group and tile in the row offsets on the device (group.h).
 
-#include "group.h"
-#include "ops_tile.h"
+#include "group_tile.h"
 
 namespace glk {
-
-// Narrows p to the group and tile of workgroup `block`; false where there is none. Rows of no group are a product
-// over nothing, which writes zeros.
-template <int MODE, int BT>
-__device__ __forceinline__ bool group_tile(OpTileArgs& p, const GroupArgs& g, int block, OpPlace* at) {
-    constexpr int ES = MODE == kOpF8 ? 1 : 2;
-    auto uni = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
-    if constexpr (MODE == kOpAtb) {
-        const int tiles = p.tiles_m * p.tiles_n, per = tiles * p.splits;
-        const int unit = xcd_remap(block, g.groups * per, p.nxcd), group = uni(unit / per);
-        int first, rows;
-        group_rows(g, group, &first, &rows);
-        *at = op_place_unit<BT, BT>(p, unit - group * per);
-        at->tile += group * tiles;
-        p.A = static_cast<const char*>(p.A) + (int64_t)first * p.lda * ES;
-        p.B = static_cast<const char*>(p.B) + (int64_t)first * p.ldb * ES;
-        p.C += group * g.stride_c;
-        p.K = rows;
-        const int steps = (rows + 31) / 32;
-        p.kt_per_split = uni((steps + p.splits - 1) / p.splits);
-    } else {
-        GroupSpan s;
-        if (!find_span(g, BT, p.tiles_n * p.splits, p.nxcd, block, &s)) return false;
-        p.tiles_m = s.tiles;
-        *at = op_place_unit<BT, BT>(p, s.unit);
-        at->tile += s.tile * p.tiles_n;
-        p.A = static_cast<const char*>(p.A) + (int64_t)s.first * p.lda * ES;
-        p.C += (int64_t)s.first * p.ldc;
-        p.M = s.rows;
-        if (s.group < 0)
-            p.K = 0;
-        else
-            p.B = static_cast<const char*>(p.B) + s.group * g.stride_b * ES;
-    }
-    return true;
-}
 
 template <int MODE>
 __global__ void __attribute__((amdgpu_flat_work_group_size(512, 512), amdgpu_waves_per_eu(2, 2)))

@@ -65,6 +65,7 @@ struct OpTileArgs {
     int splits, kt_per_split;  // pieces of K per tile, 64-byte k-steps in each (128 x 128 tiles)
     float* ws;
     uint32_t* counters;
+    int64_t ldsa, ldsb;  // kOpF8
 };
 // tile: 256, 128 or 64 rows and (weight) columns; the gated forms make half as many output columns
 hipError_t launch_op_tile(int mode, bool glu, int tile, const OpTileArgs& a, int grid, hipStream_t s);
@@ -79,6 +80,9 @@ hipError_t launch_group_tile(int mode, int tile, const OpTileArgs& a, const Grou
 hipError_t launch_group_pair(int tile, const OpTileArgs& a, const GroupArgs& ga, int grid_a, const OpTileArgs& b,
                              const GroupArgs& gb, int grid_b, hipStream_t s);
 hipError_t configure_group_kernels();
+// kOpF8: as launch_group_tile; a.kt_per_split is even
+hipError_t launch_f8_tile(int tile, const OpTileArgs& a, const GroupArgs& g, int grid, hipStream_t s);
+hipError_t configure_f8_kernels();
 
 // ---- 8-bit product of few tokens -------------------------------------------------------------------
 constexpr int kI8FusedK = 16384;  // the longest row that the fused form quantises

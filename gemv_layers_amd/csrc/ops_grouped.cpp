@@ -51,7 +51,7 @@ bool matrix_ok(int mode, const OpArgs& a, const GroupArgs& g) {
     if (misaligned(a.A, 16) || misaligned(a.B, 16) || (a.lda % unit) || (a.ldb % unit) || (g.stride_b % unit)) return false;
     if (a.lda > max_ld || a.ldb > max_ld || a.ldc > max_ld) return false;
     if (a.M > max_dim || a.N > max_dim || a.K > max_dim) return false;
-    if (mode == glk::kOpF8) return false;
+    if (mode == glk::kOpF8) return true;  // (any width; C at any element)
     if (misaligned(a.C, 16) || (a.ldc % 8) || (g.stride_c % 8) || (a.N % 8)) return false;
     return mode == glk::kOpAtb ? a.M % 8 == 0 : a.K % 8 == 0;
 }
@@ -72,7 +72,10 @@ int prepare(int mode, const OpArgs& a, const GroupArgs& g, hipStream_t stream, R
     }
     if (matrix_ok(mode, a, g)) {
         r->route = Ready::kTiles;
-        r->p = glk::make_group_plan(g.rows, a.M, a.N, a.K, g.groups, *dev, mode == glk::kOpAtb);
+        // codes: planned as the bf16 product whose k-steps have the same bytes and matrix-core cycles
+        r->p = glk::make_group_plan(g.rows, a.M, a.N, mode == glk::kOpF8 ? (a.K + 1) / 2 : a.K, g.offsets ? g.groups : 1, *dev,
+                                    mode == glk::kOpAtb);
+        if (mode == glk::kOpF8) r->p.kt_per_split += r->p.kt_per_split & 1;  // whole blocks of 128
         if (r->p.grid > INT32_MAX) return GEMM_ERR_UNSUPPORTED;
         return r->p.ws_floats > 0 ? glk::stream_workspace(stream, &r->w) : GEMM_OK;
     }
@@ -113,6 +116,8 @@ glk::OpTileArgs tile_args(const Ready& r) {
     t.kt_per_split = r.p.kt_per_split;
     t.ws = r.w.ws;
     t.counters = r.w.counters;
+    t.ldsa = a.ldsa;
+    t.ldsb = a.ldsb;
     return t;
 }
 
@@ -127,7 +132,8 @@ int launch(const Ready& r, hipStream_t stream) {
             e = glk::launch_group_generic(r.mode, a, r.g, stream);
             break;
         case Ready::kTiles:
-            e = glk::launch_group_tile(r.mode, r.p.bm, tile_args(r), r.g, (int)r.p.grid, stream);
+            e = r.mode == glk::kOpF8 ? glk::launch_f8_tile(r.p.bm, tile_args(r), r.g, (int)r.p.grid, stream)
+                                     : glk::launch_group_tile(r.mode, r.p.bm, tile_args(r), r.g, (int)r.p.grid, stream);
             break;
     }
     if (e != hipSuccess) return GEMM_ERR_HIP;

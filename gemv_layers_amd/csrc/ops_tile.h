@@ -322,7 +322,7 @@ __device__ __forceinline__ void op_epilogue(const OpTileArgs& p, char* lds, cons
                     put(Out{}, mi, ni, acc[ni][mi]);
             }
     }
-    op_store_rows<T::WTM, WTNO>(ob, p.C, p.ldc, mw, p.M, nw, p.N, lane, MODE != kOpI8 || p.vec != 0);
+    op_store_rows<T::WTM, WTNO>(ob, p.C, p.ldc, mw, p.M, nw, p.N, lane, (MODE != kOpI8 && MODE != kOpF8) || p.vec != 0);
 }
 
 // ---- 256 x 256: two wave groups alternating memory and MFMA phases --------------------------------
@@ -412,6 +412,61 @@ __device__ __forceinline__ void op_pp(const OpTileArgs& p, const OpPlace& at, ch
     wait_vmcnt<0>();  // the copies past K included
     lds_barrier();    // the rings are free for the output
     op_epilogue<T, MODE, GLU>(p, lds, at, wave, wm, wn, lane, acc);
+}
+
+// The pieces of a split tile: each stores its partial sums, and the last to arrive adds them in K order into its
+// acc and returns true.
+template <class T>
+__device__ __forceinline__ bool op_join(const OpTileArgs& p, const OpPlace& at, char* lds, int wave, int lane,
+                                        typename T::Acc (&acc)[T::TN][T::TM]) {
+    constexpr int TM = T::TM, TN = T::TN;
+    volatile uint32_t& last_flag = *reinterpret_cast<volatile uint32_t*>(lds);
+    constexpr uint32_t kSlot = T::BM * T::BN * 4;
+    const __amdgpu_buffer_rsrc_t ws = make_rsrc(p.ws + (size_t)at.tile * p.splits * (T::BM * T::BN));
+    auto slot_off = [&](int pc, int ni, int mi) {
+        return (uint32_t)pc * kSlot + (uint32_t)((((wave * TN + ni) * TM + mi) * 64 + lane) * 16);
+    };
+#pragma unroll
+    for (int ni = 0; ni < TN; ++ni)
+#pragma unroll
+        for (int mi = 0; mi < TM; ++mi)
+            buf_store16_dev(ws, slot_off(at.piece, ni, mi), __builtin_bit_cast(u32x4, acc[ni][mi]));
+    wait_all_memory();
+    __syncthreads();
+    if (threadIdx.x == 0)
+        last_flag = (counter_arrive(&p.counters[at.tile]) == (uint32_t)(p.splits - 1)) ? 1u : 0u;
+    __syncthreads();
+    if (!last_flag) return false;
+    if (threadIdx.x == 0) counter_reset(&p.counters[at.tile]);
+    typename T::Acc sum[TN][TM];
+#pragma unroll
+    for (int ni = 0; ni < TN; ++ni)
+#pragma unroll
+        for (int mi = 0; mi < TM; ++mi) sum[ni][mi] = typename T::Acc{};
+    for (int pc = 0; pc < p.splits; ++pc) {  // in K order, its own piece from registers
+        if (pc == at.piece) {
+#pragma unroll
+            for (int ni = 0; ni < TN; ++ni)
+#pragma unroll
+                for (int mi = 0; mi < TM; ++mi) sum[ni][mi] += acc[ni][mi];
+            continue;
+        }
+        u32x4 v[TN][TM];
+#pragma unroll
+        for (int ni = 0; ni < TN; ++ni)
+#pragma unroll
+            for (int mi = 0; mi < TM; ++mi) v[ni][mi] = buf_load16_dev(ws, slot_off(pc, ni, mi));
+#pragma unroll
+        for (int ni = 0; ni < TN; ++ni)
+#pragma unroll
+            for (int mi = 0; mi < TM; ++mi) sum[ni][mi] += __builtin_bit_cast(typename T::Acc, v[ni][mi]);
+    }
+#pragma unroll
+    for (int ni = 0; ni < TN; ++ni)
+#pragma unroll
+        for (int mi = 0; mi < TM; ++mi) acc[ni][mi] = sum[ni][mi];
+    __syncthreads();  // the flag has been read: its place is free for the output
+    return true;
 }
 
 // ---- 128 x 128 and 64 x 64, K split over idle CUs -------------------------------------------------------------
@@ -512,54 +567,7 @@ __device__ __forceinline__ void op_small(const OpTileArgs& p, const OpPlace& at,
     wait_vmcnt<0>();
     lds_barrier();
 
-    if (p.splits > 1) {
-        volatile uint32_t& last_flag = *reinterpret_cast<volatile uint32_t*>(lds);
-        constexpr uint32_t kSlot = BT * BT * 4;
-        const __amdgpu_buffer_rsrc_t ws = make_rsrc(p.ws + (size_t)at.tile * p.splits * (BT * BT));
-        auto slot_off = [&](int pc, int ni, int mi) {
-            return (uint32_t)pc * kSlot + (uint32_t)((((wave * TN + ni) * TM + mi) * 64 + lane) * 16);
-        };
-#pragma unroll
-        for (int ni = 0; ni < TN; ++ni)
-#pragma unroll
-            for (int mi = 0; mi < TM; ++mi)
-                buf_store16_dev(ws, slot_off(at.piece, ni, mi), __builtin_bit_cast(u32x4, acc[ni][mi]));
-        wait_all_memory();
-        __syncthreads();
-        if (threadIdx.x == 0)
-            last_flag = (counter_arrive(&p.counters[at.tile]) == (uint32_t)(p.splits - 1)) ? 1u : 0u;
-        __syncthreads();
-        if (!last_flag) return;
-        if (threadIdx.x == 0) counter_reset(&p.counters[at.tile]);
-        typename T::Acc sum[TN][TM];
-#pragma unroll
-        for (int ni = 0; ni < TN; ++ni)
-#pragma unroll
-            for (int mi = 0; mi < TM; ++mi) sum[ni][mi] = typename T::Acc{};
-        for (int pc = 0; pc < p.splits; ++pc) {  // in K order, its own piece from registers
-            if (pc == at.piece) {
-#pragma unroll
-                for (int ni = 0; ni < TN; ++ni)
-#pragma unroll
-                    for (int mi = 0; mi < TM; ++mi) sum[ni][mi] += acc[ni][mi];
-                continue;
-            }
-            u32x4 v[TN][TM];
-#pragma unroll
-            for (int ni = 0; ni < TN; ++ni)
-#pragma unroll
-                for (int mi = 0; mi < TM; ++mi) v[ni][mi] = buf_load16_dev(ws, slot_off(pc, ni, mi));
-#pragma unroll
-            for (int ni = 0; ni < TN; ++ni)
-#pragma unroll
-                for (int mi = 0; mi < TM; ++mi) sum[ni][mi] += __builtin_bit_cast(typename T::Acc, v[ni][mi]);
-        }
-#pragma unroll
-        for (int ni = 0; ni < TN; ++ni)
-#pragma unroll
-            for (int mi = 0; mi < TM; ++mi) acc[ni][mi] = sum[ni][mi];
-        __syncthreads();  // the flag has been read: its place is free for the output
-    }
+    if (p.splits > 1 && !op_join<T>(p, at, lds, wave, lane, acc)) return;
     op_epilogue<T, MODE, GLU>(p, lds, at, wave, wm, wn, lane, acc);
 }
 

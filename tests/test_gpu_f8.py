@@ -10,7 +10,7 @@ pytestmark = pytest.mark.gpu
 
 torch = pytest.importorskip("torch")
 import gemv_layers_amd as g  # noqa: E402
-from test_gpu_grouped import bf, blocks, close, f8, gen, ints, powers, same, spread, strided4  # noqa: E402
+from test_gpu_grouped import CUT, bf, blocks, close, f8, gen, ints, powers, same, spread, strided4  # noqa: E402
 
 F8 = torch.float8_e4m3fn
 
@@ -148,7 +148,7 @@ def test_linear(M, N, K):
     Aq, Sa = g.f8_quantize(A)
     ref, sabs = reference(Aq.float(), Sa, Wq.float(), Sw)
     C = g.f8_linear(A, Wq, Sw)
-    close(C, ref, sabs, K, "linear")
+    close(C, ref, sabs, K, "linear", CUT)
     assert torch.equal(g.f8_matmul(Aq, Sa, Wq, Sw), C)
     assert torch.equal(g.f8_linear(bf(x, 3, 1), Wq, Sw), C)
     work = torch.full((g.gemm_f8_work_bytes(M, K),), 0xFF, dtype=torch.uint8, device="cuda")
@@ -165,7 +165,7 @@ def test_every_code(M, N, K):
             for t in (pick(1, M, K), pick(2, N, K)))
     Sa, Sw = torch.rand(blocks(K), M, generator=gen(3), device="cuda") + 0.5, torch.rand(blocks(N), blocks(K), generator=gen(4), device="cuda") + 0.5
     ref, sabs = reference(A.float(), Sa, W.float(), Sw)
-    close(g.f8_matmul(A, Sa, W, Sw), ref, sabs, K, "codes")
+    close(g.f8_matmul(A, Sa, W, Sw), ref, sabs, K, "codes", CUT)
     A.view(torch.uint8)[0, 7] = 0x7F
     W.view(torch.uint8)[5, 290] = 0xFF
     C = g.f8_matmul(A, Sa, W, Sw)
@@ -173,6 +173,28 @@ def test_every_code(M, N, K):
     assert bad[0].all() and bad[:, 5].all()
     bad[0], bad[:, 5] = False, False
     assert not bad.any()
+
+
+@pytest.mark.parametrize("M", [1, 40, 300])
+def test_what_the_matrix_instruction_keeps(M):
+    """2^16 at one k, -2^16 at another and a product 2^gap times smaller at a third, of which the first two cancel. Up
+    to gap 13 it is kept wherever the three lie, beyond where it has no large product among its eight; lost, it
+    is off by less than 2^-13 of the largest."""
+    gaps = range(0, 30)
+    N = 4 * len(gaps)
+    places = [(0, 1, 2), (0, 64, 127), (1, 2, 32), (7, 40, 90)]
+    A, W, want = torch.zeros(M, 128, device="cuda"), torch.zeros(N, 128, device="cuda"), torch.zeros(N)
+    for j, (a, b, c) in enumerate(places):
+        for gap in gaps:
+            e = 16 - gap
+            n = len(gaps) * j + gap
+            W[n, a], W[n, b], W[n, c] = 256.0, -256.0, 2.0 ** (e - 8) if e >= -1 else 0.0
+            want[n] = 2.0**e if e >= -1 else 0.0
+    A[:] = 256.0
+    C = g.f8_matmul(A.to(F8), torch.ones(1, M, device="cuda"), W.to(F8), torch.ones(blocks(N), 1, device="cuda")).float().cpu()
+    assert (C == C[0]).all()
+    err = (C[0] - want).abs().view(4, -1)
+    assert not err[:, :14].any() and (err < 2.0**3).all() and not err[1:].any()
 
 
 def test_non_finite_values_spoil_their_rows_alone():
@@ -247,4 +269,4 @@ def test_offsets_past_32_bits():
     C = g.f8_matmul(Aq, Sa, Wq, Sw)
     assert C.numel() * 2 > 1 << 32 and Aq.numel() > 1 << 32
     assert torch.equal(C[-64:], C[:64]) and not C[64:-64].any()
-    close(C[:64], *reference(Aq[:64].float(), Sa[:, :64], Wq.float(), Sw), K, "first rows")
+    close(C[:64], *reference(Aq[:64].float(), Sa[:, :64], Wq.float(), Sw), K, "first rows", CUT)
