@@ -20,7 +20,7 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 
 SOURCES = ["gemm_tile.hip", "gemm_skinny.hip", "gemm_generic.hip", "gemm_mx.hip", "gemm_packed.hip",
-           "ops_tile.hip", "i8_decode.hip", "ops_generic.hip", "ops_rows.hip", "group_tile.hip", "f8_tile.hip", "group_generic.hip", "f8_rows.hip",
+           "ops_tile.hip", "i8_decode.hip", "ops_generic.hip", "ops_rows.hip", "group_tile.hip", "f8_tile.hip", "f8_decode.hip", "group_generic.hip", "f8_rows.hip",
            "peak.hip", "plan.cpp", "abi.cpp", "ops.cpp", "ops_grouped.cpp"]
 
 COMMON = [

@@ -66,6 +66,17 @@ __device__ __forceinline__ u32x2 f8_codes8(const u32x4& v, const F8Scale& c) {
     const u32x2 w = {f8_codes4(q[0], q[1], q[2], q[3]), f8_codes4(q[4], q[5], q[6], q[7])};
     return c.up == 0.f ? u32x2{0, 0} : w;
 }
+// the largest of the 16 lanes of a row of lanes, in all of them
+__device__ __forceinline__ uint32_t row_max(uint32_t v) {
+#define GLK_ROR(n) v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x120 + n, 0xF, 0xF, false))
+    GLK_ROR(8);
+    GLK_ROR(4);
+    GLK_ROR(2);
+    GLK_ROR(1);
+#undef GLK_ROR
+    return v;
+}
+
 // the value of a code
 __device__ __forceinline__ float f8_value(uint8_t code) { return __builtin_amdgcn_cvt_f32_fp8((int)code, 0); }
 

@@ -33,17 +33,6 @@ __device__ __forceinline__ void f8_store(uint8_t* q, int64_t k, int64_t padded, 
 // the bytes of a row that are written: up to a multiple of 16 where the rows have room
 __device__ __forceinline__ int64_t f8_padded(int64_t K, int64_t ldq) { return min(ldq, (K + 15) / 16 * 16); }
 
-// the largest of the 16 lanes of a row of lanes, in all of them
-__device__ __forceinline__ uint32_t row_max(uint32_t v) {
-#define GLK_ROR(n) v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x120 + n, 0xF, 0xF, false))
-    GLK_ROR(8);
-    GLK_ROR(4);
-    GLK_ROR(2);
-    GLK_ROR(1);
-#undef GLK_ROR
-    return v;
-}
-
 // IT: groups of four rows a wave
 template <int IT>
 __global__ void __launch_bounds__(256) f8_quantize_kernel(const uint16_t* __restrict__ X, int64_t R, int64_t K,

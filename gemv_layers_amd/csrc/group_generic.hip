@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(256) group_generic_kernel(OpArgs p, GroupArgs 
 
 hipError_t launch_group_generic(int mode, const OpArgs& a, const GroupArgs& g, hipStream_t s) {
     const int64_t tn = (a.N - 1) / 64 + 1;
-    const int64_t tm = mode == kOpAtb ? ((a.M - 1) / 64 + 1) * g.groups : most_row_tiles(g.rows, g.offsets ? g.groups : 1, 64);
+    const int64_t tm = mode == kOpAtb ? ((a.M - 1) / 64 + 1) * g.groups : most_row_tiles(g.rows, g.offsets ? g.groups : 0, 64);
     if (tm > 0xFFFFFF / tn) return hipErrorInvalidValue;
     const unsigned grid = (unsigned)(tm * tn);
     switch (mode) {

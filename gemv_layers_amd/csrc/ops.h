@@ -103,6 +103,26 @@ struct I8DecodeArgs {
 hipError_t launch_i8_decode(bool glu, int mt, int tn, int nw, const I8DecodeArgs& a, int grid, hipStream_t s);
 hipError_t configure_i8_decode();
 
+// ---- 8-bit floating-point product of few rows ------------------------------------------------------
+constexpr int kF8FusedK = 16384;  // the longest row that the fused form quantises
+struct F8DecodeArgs {
+    const uint8_t* A;     // rows of codes, with scales sa (block by block); or, fused, null and
+    const uint16_t* A16;  // one row of bf16, quantised in the kernel
+    const uint8_t* W;
+    uint16_t* C;
+    const float* sa;
+    const float* sb;
+    int N, K;
+    int lda, ldw, ldc;
+    int strips;           // of tn 16-row weight tiles
+    int pieces;           // of K, one workgroup each
+    float* ws;            // pieces > 1: row tiles * strips * pieces * tn * mt * 256
+    uint32_t* counters;   // one per row tile and strip, zero between launches
+    int64_t ldsa, ldsb;
+};
+// mt: 16-row tiles in a row tile (1, 2 or 4); tn: 16-row weight tiles per workgroup (1, 2 or 4) of four waves
+hipError_t launch_f8_decode(int mt, int tn, const F8DecodeArgs& a, const GroupArgs& g, int grid, hipStream_t s);
+
 // ---- row kernels --------------------------------------------------------------------------------
 // symmetric 8-bit codes of each row: see gemm_i8_quantize
 hipError_t launch_i8_quantize(const uint16_t* X, int64_t R, int64_t K, int64_t ldx, int8_t* Q, int64_t ldq,

@@ -35,7 +35,8 @@ const char* op_name(int mode, bool grouped) {
 // A product that is ready to launch: planned, its limits checked, its workspace at hand. A call prepares
 // every product it makes before it launches anything, so that a refused one has written nothing.
 struct Ready {
-    enum Route { kZero, kGeneral, kTiles } route = kZero;
+    enum Route { kZero, kGeneral, kTiles, kDecode } route = kZero;
+    bool fused = false;  // kDecode: a.A holds one row of bf16
     int mode = 0;
     OpArgs a{};
     GroupArgs g{};
@@ -56,9 +57,10 @@ bool matrix_ok(int mode, const OpArgs& a, const GroupArgs& g) {
     return mode == glk::kOpAtb ? a.M % 8 == 0 : a.K % 8 == 0;
 }
 
-// One product on the current device with a non-empty C, operands checked. The rows of C (of kOpAtb those of
+// One product on the current device with a non-empty C, operands checked. `fused`: one row of bf16 activations
+// and a weight that the weight-streaming kernel takes. The rows of C (of kOpAtb those of
 // all groups' C together) are written whole.
-int prepare(int mode, const OpArgs& a, const GroupArgs& g, hipStream_t stream, Ready* r) {
+int prepare(int mode, const OpArgs& a, const GroupArgs& g, bool fused, hipStream_t stream, Ready* r) {
     int st = GEMM_OK;
     const glk::DeviceInfo* dev = glk::current_device(&st);
     if (!dev) return st;
@@ -70,10 +72,20 @@ int prepare(int mode, const OpArgs& a, const GroupArgs& g, hipStream_t stream, R
         r->p = glk::make_plan(a.M, a.N, 0, *dev, false, 2, false);
         return GEMM_OK;
     }
-    if (matrix_ok(mode, a, g)) {
+    const int64_t groups = g.offsets ? g.groups : 0;
+    const bool matrix = fused || matrix_ok(mode, a, g);
+    r->fused = fused;
+    if (mode == glk::kOpF8 && matrix && glk::f8_decode_fits(g.rows, groups)) {  // the weight-streaming kernel
+        r->p = glk::make_f8_decode_plan(g.rows, a.N, a.K, groups, *dev);
+        if (r->p.grid <= INT32_MAX) {
+            r->route = Ready::kDecode;
+            return r->p.ws_floats > 0 ? glk::stream_workspace(stream, &r->w) : GEMM_OK;
+        }
+    }
+    if (matrix) {
         r->route = Ready::kTiles;
         // codes: planned as the bf16 product whose k-steps have the same bytes and matrix-core cycles
-        r->p = glk::make_group_plan(g.rows, a.M, a.N, mode == glk::kOpF8 ? (a.K + 1) / 2 : a.K, g.offsets ? g.groups : 1, *dev,
+        r->p = glk::make_group_plan(g.rows, a.M, a.N, mode == glk::kOpF8 ? (a.K + 1) / 2 : a.K, mode == glk::kOpAtb ? g.groups : groups, *dev,
                                     mode == glk::kOpAtb);
         if (mode == glk::kOpF8) r->p.kt_per_split += r->p.kt_per_split & 1;  // whole blocks of 128
         if (r->p.grid > INT32_MAX) return GEMM_ERR_UNSUPPORTED;
@@ -81,7 +93,7 @@ int prepare(int mode, const OpArgs& a, const GroupArgs& g, hipStream_t stream, R
     }
     // 64 x 64 tiles of 256 threads, 32-bit grids
     const int64_t row_tiles =
-        mode == glk::kOpAtb ? ((a.M - 1) / 64 + 1) * g.groups : glk::most_row_tiles(g.rows, g.offsets ? g.groups : 1, 64);
+        mode == glk::kOpAtb ? ((a.M - 1) / 64 + 1) * g.groups : glk::most_row_tiles(g.rows, groups, 64);
     if (row_tiles > kMaxRows / ((a.N - 1) / 64 + 1)) return GEMM_ERR_UNSUPPORTED;
     r->route = Ready::kGeneral;
     r->p = glk::make_plan(a.M, a.N, a.K, *dev, false, 2, false);
@@ -131,6 +143,14 @@ int launch(const Ready& r, hipStream_t stream) {
         case Ready::kGeneral:
             e = glk::launch_group_generic(r.mode, a, r.g, stream);
             break;
+        case Ready::kDecode: {
+            const glk::F8DecodeArgs t{r.fused ? nullptr : static_cast<const uint8_t*>(a.A),
+                                      r.fused ? static_cast<const uint16_t*>(a.A) : nullptr,
+                                      static_cast<const uint8_t*>(a.B), a.C, a.sa, a.sb, (int)a.N, (int)a.K, (int)a.lda,
+                                      (int)a.ldb, (int)a.ldc, r.p.strips, r.p.splits, r.w.ws, r.w.counters, a.ldsa, a.ldsb};
+            e = glk::launch_f8_decode(r.p.mtiles, r.p.strip / 16, t, r.g, (int)r.p.grid, stream);
+            break;
+        }
         case Ready::kTiles:
             e = r.mode == glk::kOpF8 ? glk::launch_f8_tile(r.p.bm, tile_args(r), r.g, (int)r.p.grid, stream)
                                      : glk::launch_group_tile(r.mode, r.p.bm, tile_args(r), r.g, (int)r.p.grid, stream);
@@ -218,7 +238,7 @@ int f8_product(int64_t M, int64_t N, int64_t K, const void* Aq, int64_t lda, con
     a.ldsa = ldsa;
     a.ldsb = w.lds;
     Ready r;
-    st = prepare(glk::kOpF8, a, GroupArgs{dense ? nullptr : offsets, (int)E, (int)M, w.stride, 0, w.stride_s}, stream, &r);
+    st = prepare(glk::kOpF8, a, GroupArgs{dense ? nullptr : offsets, (int)E, (int)M, w.stride, 0, w.stride_s}, false, stream, &r);
     return st == GEMM_OK ? launch(r, stream) : st;
 }
 
@@ -234,12 +254,20 @@ int f8_product_bf16(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda,
     if (st != GEMM_OK || M == 0 || N == 0) return st;
     if (K > 0 && (!work || misaligned(work, 16) || work_bytes < work_bytes_of(M, K))) return GEMM_ERR_INVALID_ARG;
     OpArgs a{work, w.q, static_cast<uint16_t*>(C), nullptr, nullptr, w.s, M, N, K, padded_codes(K), w.ld, ldc, 0};
+    const GroupArgs g{dense ? nullptr : offsets, (int)E, (int)M, w.stride, 0, w.stride_s};
+    Ready r;
+    // one row: quantised in the product's kernel (neither its alignment nor its leading dimension matters)
+    if (dense && M == 1 && K > 0 && K <= glk::kF8FusedK && matrix_ok(glk::kOpF8, a, g)) {
+        a.A = A;
+        a.ldsb = w.lds;
+        st = prepare(glk::kOpF8, a, g, true, stream, &r);
+        return st == GEMM_OK ? launch(r, stream) : st;
+    }
     float* sa = reinterpret_cast<float*>(static_cast<char*>(work) + M * a.lda);
     a.sa = sa;
     a.ldsa = M;
     a.ldsb = w.lds;
-    Ready r;
-    st = prepare(glk::kOpF8, a, GroupArgs{dense ? nullptr : offsets, (int)E, (int)M, w.stride, 0, w.stride_s}, stream, &r);
+    st = prepare(glk::kOpF8, a, g, false, stream, &r);
     if (st == GEMM_OK && K > 0 && E > 0) st = quantize(M, K, A, lda, work, a.lda, sa, M, stream);
     return st == GEMM_OK ? launch(r, stream) : st;
 }
@@ -329,7 +357,7 @@ int gemm_bf16_grouped(int64_t M, int64_t N, int64_t K, int64_t E, const void* A,
         if (st != GEMM_OK || M == 0 || N == 0) return st;
         const OpArgs a{A, B, static_cast<uint16_t*>(C), nullptr, nullptr, nullptr, M, N, K, lda, ldb, ldc, 0};
         Ready r;
-        st = prepare(glk::kOpAb, a, GroupArgs{offsets, (int)E, (int)M, stride_b, 0, 0}, hip_stream(stream), &r);
+        st = prepare(glk::kOpAb, a, GroupArgs{offsets, (int)E, (int)M, stride_b, 0, 0}, false, hip_stream(stream), &r);
         return st == GEMM_OK ? launch(r, hip_stream(stream)) : st;
     });
 }
@@ -353,11 +381,11 @@ int gemm_bf16_grouped_bwd(int64_t M, int64_t N, int64_t K, int64_t E, const void
         Ready ra, rb;
         if (need_a) {
             const OpArgs a{dC, B, static_cast<uint16_t*>(dA), nullptr, nullptr, nullptr, M, K, N, lddc, ldb, ldda, 0};
-            st = prepare(glk::kOpAbt, a, GroupArgs{offsets, (int)E, (int)M, stride_b, 0, 0}, hip_stream(stream), &ra);
+            st = prepare(glk::kOpAbt, a, GroupArgs{offsets, (int)E, (int)M, stride_b, 0, 0}, false, hip_stream(stream), &ra);
         }
         if (st == GEMM_OK && need_b) {
             const OpArgs b{A, dC, static_cast<uint16_t*>(dB), nullptr, nullptr, nullptr, K, N, 0, lda, lddc, lddb, 0};
-            st = prepare(glk::kOpAtb, b, GroupArgs{offsets, (int)E, (int)M, 0, stride_db, 0}, hip_stream(stream), &rb);
+            st = prepare(glk::kOpAtb, b, GroupArgs{offsets, (int)E, (int)M, 0, stride_db, 0}, false, hip_stream(stream), &rb);
         }
         if (st != GEMM_OK) return st;
         if (need_a && need_b) {

@@ -535,7 +535,7 @@ Plan make_group_plan(int64_t rows, int64_t M, int64_t N, int64_t K, int64_t grou
     p.tile_cfg = kTileConfigCount;  // none of make_plan's
     p.bk = 32;
     p.nxcd = dev.nxcd;
-    const int64_t parts = std::max<int64_t>(1, std::min(groups, rows));  // groups that can have rows
+    const int64_t parts = std::max<int64_t>(1, std::min(groups, rows));  // that can have rows
     const int64_t each = cdiv(rows, parts);                              // rows of one, in the mean
     // tiles as a router that is even would make them
     auto expect = [&](int64_t b) { return (summed ? groups * cdiv(M, b) : parts * cdiv(each, b)) * cdiv(N, b); };
@@ -573,6 +573,58 @@ Plan make_group_plan(int64_t rows, int64_t M, int64_t N, int64_t K, int64_t grou
     return p;
 }
 
+// The 8-bit floating-point product of few rows streams the weight once for each row tile, and as in the integer
+// form a workgroup's activations cost like as many weight bytes. us a call, weights out of the caches:
+// * tn: one weight tile up to two a CU (8 x 4096 x 4096 7.0, 8.6 with two), then four (16 x 11008 x 4096 14.5 and 15.8
+//   with one); up to 4 rows a group one (1 x 11008 x 4096 12.6, 14.4 with two) until there are eight a CU, then two (41
+//   of 64 groups of 1376 x 4096: 49.4, 52.6 with one, 52.5 with four). Above 16 rows one, two or four as the weight
+//   outgrows the sum of K pieces (64 x 1000 x 2000 8.2 with one, 48 x 2048 x 8192 12.5 with two, 64 x 11008 x 4096 23.0
+//   with four and 28.1 with two).
+// * pieces: as far as the strips leave CUs idle and 10 blocks of 128 remain to each, 4 above 16 rows (16 x 1000 x 4096,
+//   32 blocks: 7.0 in two, 6.5 in three; 4 x 2048 x 2048, 16 blocks: 5.6 whole, 6.2 in two; 64 x 1000 x 2000, 16: 9.7 whole,
+//   8.2 in four).
+// Four waves: eight were 0.4 to 3 us slower, or at best 3% faster (64 x 4096 x 11008 21.6 and 22.3).
+Plan make_f8_decode_plan(int64_t rows, int64_t N, int64_t K, int64_t groups, const DeviceInfo& dev) {
+    Plan p;
+    p.kernel = kKernF8Decode;
+    const int64_t parts = std::max<int64_t>(1, std::min(groups, rows));  // that can have rows
+    const int64_t each = cdiv(rows, parts);
+    p.mtiles = each <= 16 ? 1 : each <= 32 ? 2 : 4;
+    const int64_t row_tiles = parts * cdiv(each, 16 * p.mtiles);  // as an even router would make them
+    const int64_t tiles = cdiv(N, 16) * row_tiles, steps = cdiv(K, 128), cus = dev.cus;
+    const int64_t weight = N * K * parts;
+    int tn;  // 16-row weight tiles per workgroup
+    if (p.mtiles > 1)
+        tn = weight <= (int64_t(8) << 20) ? 1 : (weight <= (int64_t(20) << 20) ? 2 : 4);
+    else if (each <= 4)
+        tn = tiles >= 8 * cus ? 2 : 1;
+    else
+        tn = tiles <= 2 * cus ? 1 : 4;
+    p.strip = 16 * tn;
+    p.strips = (int)cdiv(cdiv(N, 16), tn);
+    p.ks = (int)steps;
+    const int64_t all = p.strips * most_row_tiles(rows, groups, 16 * p.mtiles);
+    const int64_t slot_floats = (int64_t)tn * p.mtiles * 256;
+    int64_t s = std::max<int64_t>(1, std::min<int64_t>(cus / (p.strips * row_tiles), steps / (p.mtiles == 1 ? 10 : 4)));
+    while (s > 1 && all * s * slot_floats > dev.ws_floats) --s;
+    if (s > 1 && all > dev.ws_counters) s = 1;
+    p.splits = (int)s;
+    p.grid = all * s;
+    p.ws_floats = s > 1 ? all * s * slot_floats : 0;
+    p.counters = s > 1 ? all : 0;
+    p.threads = 256;
+    p.slots = 2 * cus;
+    finish_waves(p);
+    p.reason = "8-bit float decode";
+    return p;
+}
+
+// Whether the weight-streaming kernel takes the product: a plain one of at most 64 rows (us, streaming against
+// tiles: 64 x 11008 x 4096 23.0 and 35.3, 64 x 4096 x 11008 22.3 and 28.1, 64 x 512 x 1024 6.5 and 8.6), a grouped one of
+// at most 16 rows a group in the mean (512 rows in 64 groups of 1376 x 4096 79.9 and 101.8; 32 a group: 256 rows in 8
+// groups of 4096 x 4096 48.9 and 49.0, 2000 in 64 of 2048 x 2048 89.1 and 80.8).
+bool f8_decode_fits(int64_t rows, int64_t groups) { return groups == 0 ? rows <= 64 : rows <= 16 * groups; }
+
 static const char* kernel_name(int k) {
     switch (k) {
         case kKernNone: return "none";
@@ -583,6 +635,7 @@ static const char* kernel_name(int k) {
         case kKernMx: return "mx";
         case kKernPacked: return "packed";
         case kKernI8Decode: return "i8_decode";
+        case kKernF8Decode: return "f8_decode";
         default: return "?";
     }
 }
@@ -600,7 +653,7 @@ std::string plan_json(const Plan& p, int64_t M, int64_t N, int64_t K) {
              p.threads, (long long)p.tiles_m, (long long)p.tiles_n, (long long)p.tiles,
              p.kernel == kKernTile ? (p.sched == kSchedSplitK ? "split-k" : "data-parallel")
                                    : (p.kernel == kKernSkinny || p.kernel == kKernMx || p.kernel == kKernPacked ||
-                                           p.kernel == kKernI8Decode
+                                           p.kernel == kKernI8Decode || p.kernel == kKernF8Decode
                                           ? "strips"
                                           : "-"),
              p.splits, p.kt_per_split, p.group_m, p.nxcd, p.mtiles, p.strip, p.strips, p.ks,

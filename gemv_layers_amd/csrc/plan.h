@@ -11,7 +11,7 @@ namespace glk {
 
 enum KernelKind : int {
     kKernNone = 0, kKernZero = 1, kKernGeneric = 2, kKernTile = 3, kKernSkinny = 4, kKernMx = 5,
-    kKernPacked = 6, kKernI8Decode = 7
+    kKernPacked = 6, kKernI8Decode = 7, kKernF8Decode = 8
 };
 
 struct Plan {
@@ -89,16 +89,23 @@ Plan make_i8_decode_plan(int64_t M, int64_t N, int64_t K, const DeviceInfo& dev,
 // whether that plan beats the tiles (M may be any)
 bool i8_decode_fits(int64_t M, int64_t K, const Plan& p);
 
-// most tiles of `bm` rows over `rows` rows in `groups` groups and those of none, wherever they are cut
+// most tiles of `bm` rows over `rows` rows in `groups` groups and those of none, wherever they are cut; no groups: all
+// rows are one's
 inline int64_t most_row_tiles(int64_t rows, int64_t groups, int64_t bm) {
-    const int64_t parts = groups + 2 < rows ? groups + 2 : rows;
+    const int64_t parts = groups == 0 ? 1 : groups + 2 < rows ? groups + 2 : rows;
     return (rows + parts * (bm - 1)) / bm;
 }
 
-// The products grouped by rows: `rows` rows in `groups` groups whose sizes the host does not know, an output of N
+// The products grouped by rows: `rows` rows in `groups` groups whose sizes the host does not know (0: one of all), an output of N
 // columns over K (kOpAb, kOpAbt, kOpF8 in k-steps of 32 bf16 elements); or, `summed`, for each group an M x N
 // output over its own rows. The grid and workspace hold whatever sizes the groups have.
 Plan make_group_plan(int64_t rows, int64_t M, int64_t N, int64_t K, int64_t groups, const DeviceInfo& dev, bool summed);
+
+// The 8-bit floating-point product of few rows (`groups` of them, 0 for a plain product of at most 64): row tiles
+// of mtiles * 16 rows times strips of `strip` weight rows times K pieces (splits), one workgroup of `threads` each.
+Plan make_f8_decode_plan(int64_t rows, int64_t N, int64_t K, int64_t groups, const DeviceInfo& dev);
+// whether that plan beats the tiles (rows may be any number)
+bool f8_decode_fits(int64_t rows, int64_t groups);
 
 std::string plan_json(const Plan& p, int64_t M, int64_t N, int64_t K);
 
