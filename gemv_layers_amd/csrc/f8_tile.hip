@@ -105,6 +105,7 @@ struct F8Scales {
                                          int lane) {
         const int row = wave * T::S_ROWS + lane;
         ldsa = p.ldsa;
+        if (blocks == 0) first = 0;  // (a piece past the last block: block 0 is copied and not read)
         sa = p.sa + first * ldsa + at.m0;
         off = sel_off(lane < T::S_ROWS && at.m0 + row < p.M, (uint32_t)row * 4u);
         // (past N: any block of the weight, whose columns are not stored)

@@ -85,9 +85,8 @@ int prepare(int mode, const OpArgs& a, const GroupArgs& g, bool fused, hipStream
     if (matrix) {
         r->route = Ready::kTiles;
         // codes: planned as the bf16 product whose k-steps have the same bytes and matrix-core cycles
-        r->p = glk::make_group_plan(g.rows, a.M, a.N, mode == glk::kOpF8 ? (a.K + 1) / 2 : a.K, mode == glk::kOpAtb ? g.groups : groups, *dev,
-                                    mode == glk::kOpAtb);
-        if (mode == glk::kOpF8) r->p.kt_per_split += r->p.kt_per_split & 1;  // whole blocks of 128
+        const bool f8 = mode == glk::kOpF8, summed = mode == glk::kOpAtb;
+        r->p = glk::make_group_plan({g.rows, summed ? g.groups : groups, a.M, a.N, f8 ? (a.K + 1) / 2 : a.K, summed, f8}, *dev);
         if (r->p.grid > INT32_MAX) return GEMM_ERR_UNSUPPORTED;
         return r->p.ws_floats > 0 ? glk::stream_workspace(stream, &r->w) : GEMM_OK;
     }

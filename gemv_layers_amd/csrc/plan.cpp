@@ -529,40 +529,43 @@ Plan make_i8_decode_plan(int64_t M, int64_t N, int64_t K, const DeviceInfo& dev,
     return p;
 }
 
-Plan make_group_plan(int64_t rows, int64_t M, int64_t N, int64_t K, int64_t groups, const DeviceInfo& dev, bool summed) {
+Plan make_group_plan(const GroupShape& g, const DeviceInfo& dev) {
     Plan p;
     p.kernel = kKernTile;
     p.tile_cfg = kTileConfigCount;  // none of make_plan's
     p.bk = 32;
     p.nxcd = dev.nxcd;
-    const int64_t parts = std::max<int64_t>(1, std::min(groups, rows));  // that can have rows
-    const int64_t each = cdiv(rows, parts);                              // rows of one, in the mean
+    const int64_t parts = std::max<int64_t>(1, std::min(g.groups, g.rows));  // that can have rows
+    const int64_t each = cdiv(g.rows, parts), cus = dev.cus;                 // rows of one, in the mean
     // tiles as a router that is even would make them
-    auto expect = [&](int64_t b) { return (summed ? groups * cdiv(M, b) : parts * cdiv(each, b)) * cdiv(N, b); };
-    const int64_t high = summed ? M : each;
+    auto expect = [&](int64_t b) {
+        return std::max<int64_t>(1, (g.summed ? g.groups * cdiv(g.M, b) : parts * cdiv(each, b)) * cdiv(g.N, b));
+    };
+    const int64_t high = g.summed ? g.M : each;
     int bm = 64;
-    if (high > 160 && N > 160 && 4 * expect(256) >= 3 * (int64_t)dev.cus)
+    if (high > 160 && g.N > 160 && 4 * expect(256) >= 3 * cus)
         bm = 256;
-    else if (high > 80 && N > 80 && 2 * expect(128) >= (int64_t)dev.cus)
+    else if (high > 80 && g.N > 80 && 2 * expect(128) >= cus)
         bm = 128;
     p.bm = p.bn = bm;
     p.threads = bm == 256 ? 512 : 256;
-    p.tiles_n = cdiv(N, bm);
-    p.tiles_m = summed ? cdiv(M, bm) : most_row_tiles(rows, groups, bm);
-    p.tiles = (summed ? groups : 1) * p.tiles_m * p.tiles_n;
+    p.tiles_n = cdiv(g.N, bm);
+    p.tiles_m = g.summed ? cdiv(g.M, bm) : most_row_tiles(g.rows, g.groups, bm);
+    p.tiles = (g.summed ? g.groups : 1) * p.tiles_m * p.tiles_n;
     p.group_m = (int)std::min<int64_t>(4, p.tiles_m);
-    const int64_t kt = cdiv(summed ? each : K, 32);
+    const int64_t kt = cdiv(g.summed ? each : g.K, 32);
     int64_t s = 1;
     if (bm < 256) {
-        s = std::min<int64_t>({(int64_t)dev.cus / std::max<int64_t>(1, expect(bm)), kt / 16, 16});
-        s = std::max<int64_t>(s, 1);
+        s = std::max<int64_t>(1, std::min<int64_t>({cus / expect(bm), kt / 16, 16}));
         while (s > 1 && p.tiles * s * bm * bm > dev.ws_floats / 2) --s;  // (two products may share a launch)
         if (s > 1 && p.tiles > dev.ws_counters / 2) s = 1;
     }
-    p.kt_per_split = (int)cdiv(kt, s);
-    p.splits = (int)(summed ? s : cdiv(kt, p.kt_per_split));
+    int64_t per = std::max<int64_t>(1, cdiv(kt, s));
+    if (g.pairs) per += per & 1;
+    p.kt_per_split = (int)per;
+    p.splits = (int)(g.summed ? s : std::max<int64_t>(1, cdiv(kt, per)));
     p.sched = p.splits > 1 ? kSchedSplitK : kSchedDataParallel;
-    p.slots = (bm == 256 ? 1 : bm == 128 ? 2 : 4) * (int64_t)dev.cus;
+    p.slots = (bm == 256 ? 1 : bm == 128 ? 2 : 4) * cus;
     p.grid = p.tiles * p.splits;
     if (p.splits > 1) {
         p.ws_floats = p.grid * bm * bm;

@@ -96,10 +96,15 @@ inline int64_t most_row_tiles(int64_t rows, int64_t groups, int64_t bm) {
     return (rows + parts * (bm - 1)) / bm;
 }
 
-// The products grouped by rows: `rows` rows in `groups` groups whose sizes the host does not know (0: one of all), an output of N
-// columns over K (kOpAb, kOpAbt, kOpF8 in k-steps of 32 bf16 elements); or, `summed`, for each group an M x N
-// output over its own rows. The grid and workspace hold whatever sizes the groups have.
-Plan make_group_plan(int64_t rows, int64_t M, int64_t N, int64_t K, int64_t groups, const DeviceInfo& dev, bool summed);
+// The products grouped by rows: `rows` rows in `groups` groups whose sizes the host does not know (0: one of all), an
+// output of N columns over K; or, `summed`, for each group an M x N output over its own rows. `pairs`: pieces of K are
+// whole pairs of k-steps (blocks of 128 codes, K counting two as one).
+struct GroupShape {
+    int64_t rows, groups, M, N, K;
+    bool summed, pairs;
+};
+// The grid and workspace hold whatever sizes the groups have.
+Plan make_group_plan(const GroupShape& g, const DeviceInfo& dev);
 
 // The 8-bit floating-point product of few rows (`groups` of them, 0 for a plain product of at most 64): row tiles
 // of mtiles * 16 rows times strips of `strip` weight rows times K pieces (splits), one workgroup of `threads` each.
