@@ -86,7 +86,8 @@ int prepare(int mode, const OpArgs& a, const GroupArgs& g, bool fused, hipStream
         r->route = Ready::kTiles;
         // codes: planned as the bf16 product whose k-steps have the same bytes and matrix-core cycles
         const bool f8 = mode == glk::kOpF8, summed = mode == glk::kOpAtb;
-        r->p = glk::make_group_plan({g.rows, summed ? g.groups : groups, a.M, a.N, f8 ? (a.K + 1) / 2 : a.K, summed, f8}, *dev);
+        r->p = glk::make_group_plan({g.rows, summed ? g.groups : groups, a.M, a.N, f8 ? (a.K + 1) / 2 : a.K, summed, f8,
+                                     mode == glk::kOpAb}, *dev);
         if (r->p.grid > INT32_MAX) return GEMM_ERR_UNSUPPORTED;
         return r->p.ws_floats > 0 ? glk::stream_workspace(stream, &r->w) : GEMM_OK;
     }

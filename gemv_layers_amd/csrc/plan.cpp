@@ -529,6 +529,19 @@ Plan make_i8_decode_plan(int64_t M, int64_t N, int64_t K, const DeviceInfo& dev,
     return p;
 }
 
+// Tiles. Rounds of the tiles that fill the card (one of 256 x 256, two of 128 x 128 or four of 64 x 64 a CU), each at
+// what it measured to take for a k-step: 256 x 256 takes 1.24 times a round of 128 x 128 for codes and 1.45 times for bf16,
+// 64 x 64 0.92 times. The host knows the number of rows and of groups, and takes a group's last row tile as half full.
+// us, the three sizes in this order: codes 2048 x 4096 x 11008 153, 124, 203; 4096 x 4096 x 11008 153, 243, 379; 1024 x 4096
+// x 4096 -, 47.5, 43.4; 2048 rows in 8 groups, 4096 x 4096 70.6, 107, 122; 8192 in 64, 1376 x 4096 148, 176, 186; 4096 in 64
+// -, 130, 140; bf16 2048 rows in 8 groups, 4096 x 4096 89.5, 113, 159; 8192 in 64, 1376 x 4096 192, 206, 282.
+// Two exceptions: gradients of weights over few rows are a stream of output, which 128 x 128 tiles write faster (16
+// rows, 8 groups, 4096 x 1376 25.6, 21.5, 38); and a strided weight is read in rows of a tile's width, 256 bytes of which
+// suit a stream for few rows better than 128 (256 rows in 8 groups, 4096 x 4096 -, 47, 69; 64 in 64, 1376 x 4096 -, 83, 90).
+// Pieces of K: as many as fill the card where 16 k-steps remain to each, but no more than the square root of a
+// quarter of the steps (a sixth for bf16, and three tiles a CU), as a fixup costs like a few steps for each (codes 256 x
+// 4096 x 4096 34 whole, 21 in four; 128 x 4096 x 4096 20.8 in two, 15.5 in four; 509 x 2501 x 1003 11.0 whole, 11.7 in two; bf16 16
+// rows in 8 groups, 1376 x 4096 31 whole, 22.4 in three, 23.8 in four; 300 in 3, 1000 x 1000 10.1 whole, 9.3 in two).
 Plan make_group_plan(const GroupShape& g, const DeviceInfo& dev) {
     Plan p;
     p.kernel = kKernTile;
@@ -537,16 +550,18 @@ Plan make_group_plan(const GroupShape& g, const DeviceInfo& dev) {
     p.nxcd = dev.nxcd;
     const int64_t parts = std::max<int64_t>(1, std::min(g.groups, g.rows));  // that can have rows
     const int64_t each = cdiv(g.rows, parts), cus = dev.cus;                 // rows of one, in the mean
-    // tiles as a router that is even would make them
     auto expect = [&](int64_t b) {
-        return std::max<int64_t>(1, (g.summed ? g.groups * cdiv(g.M, b) : parts * cdiv(each, b)) * cdiv(g.N, b));
+        const int64_t rows = g.summed        ? g.groups * cdiv(g.M, b)
+                             : g.groups == 0 ? cdiv(g.rows, b)
+                                             : std::max(parts, (2 * g.rows / b + parts) / 2);
+        return std::max<int64_t>(1, rows * cdiv(g.N, b));
     };
     const int64_t high = g.summed ? g.M : each;
-    int bm = 64;
-    if (high > 160 && g.N > 160 && 4 * expect(256) >= 3 * cus)
-        bm = 256;
-    else if (high > 80 && g.N > 80 && 2 * expect(128) >= cus)
-        bm = 128;
+    const int64_t t256 = cdiv(expect(256), cus) * (g.pairs ? 124 : 145), t128 = cdiv(expect(128), 2 * cus) * 100,
+                  t64 = cdiv(expect(64), 4 * cus) * 92;
+    int bm = t128 < t64 && high > 32 && g.N > 64 ? 128 : 64;
+    if (high > 80 && g.N > 80 && 2 * expect(256) >= cus && t256 < std::min(t128, t64) && !(g.summed && each <= 64)) bm = 256;
+    if (g.strided && each <= 32 && 4 * expect(128) >= 3 * cus) bm = 128;
     p.bm = p.bn = bm;
     p.threads = bm == 256 ? 512 : 256;
     p.tiles_n = cdiv(g.N, bm);
@@ -556,8 +571,12 @@ Plan make_group_plan(const GroupShape& g, const DeviceInfo& dev) {
     const int64_t kt = cdiv(g.summed ? each : g.K, 32);
     int64_t s = 1;
     if (bm < 256) {
-        s = std::max<int64_t>(1, std::min<int64_t>({cus / expect(bm), kt / 16, 16}));
-        while (s > 1 && p.tiles * s * bm * bm > dev.ws_floats / 2) --s;  // (two products may share a launch)
+        const int64_t fill = (g.pairs ? 4 : 3) * cus / (bm == 128 ? 2 : 1);
+        int64_t root = 1;
+        while ((root + 1) * (root + 1) * (g.pairs ? 4 : 6) <= kt) ++root;
+        s = std::max<int64_t>(1, std::min<int64_t>({fill / expect(bm), kt / 16, root, 16}));
+        // (both gradients may share a launch)
+        while (s > 1 && p.tiles * s * bm * bm > dev.ws_floats / (g.pairs || g.strided ? 1 : 2)) --s;
         if (s > 1 && p.tiles > dev.ws_counters / 2) s = 1;
     }
     int64_t per = std::max<int64_t>(1, cdiv(kt, s));

@@ -98,10 +98,10 @@ inline int64_t most_row_tiles(int64_t rows, int64_t groups, int64_t bm) {
 
 // The products grouped by rows: `rows` rows in `groups` groups whose sizes the host does not know (0: one of all), an
 // output of N columns over K; or, `summed`, for each group an M x N output over its own rows. `pairs`: pieces of K are
-// whole pairs of k-steps (blocks of 128 codes, K counting two as one).
+// whole pairs of k-steps (blocks of 128 codes, K counting two as one). `strided`: the weight holds K as its row index.
 struct GroupShape {
     int64_t rows, groups, M, N, K;
-    bool summed, pairs;
+    bool summed, pairs, strided;
 };
 // The grid and workspace hold whatever sizes the groups have.
 Plan make_group_plan(const GroupShape& g, const DeviceInfo& dev);

@@ -1,5 +1,5 @@
-// Prints plans of the products grouped by rows: for each line "tile rows groups M N K summed pairs cus" or "decode rows
-// groups 0 N K 0 0 cus" of the input, one JSON line {"plan": ..., "counters": ..., "fits": ...}. Linked to the library.
+// Prints plans of the products grouped by rows: for each line "tile rows groups M N K summed pairs strided cus" or
+// "decode rows groups 0 N K 0 0 0 cus" of the input, one JSON line {"plan": ..., "counters": ..., "fits": ...}. Linked to the library.
 #include <iostream>
 #include <string>
 
@@ -8,8 +8,8 @@
 int main() {
     std::string kind;
     glk::GroupShape g;
-    int cus, summed, pairs;
-    while (std::cin >> kind >> g.rows >> g.groups >> g.M >> g.N >> g.K >> summed >> pairs >> cus) {
+    int cus, summed, pairs, strided;
+    while (std::cin >> kind >> g.rows >> g.groups >> g.M >> g.N >> g.K >> summed >> pairs >> strided >> cus) {
         glk::DeviceInfo dev;
         dev.cus = cus;
         dev.nxcd = cus % 8 == 0 ? 8 : 1;
@@ -17,6 +17,7 @@ int main() {
         dev.ws_counters = int64_t(1) << 16;
         g.summed = summed != 0;
         g.pairs = pairs != 0;
+        g.strided = strided != 0;
         const glk::Plan p = kind == "tile" ? glk::make_group_plan(g, dev) : glk::make_f8_decode_plan(g.rows, g.N, g.K, g.groups, dev);
         std::cout << "{\"plan\": " << glk::plan_json(p, g.M, g.N, g.K) << ", \"counters\": " << p.counters
                   << ", \"fits\": " << (glk::f8_decode_fits(g.rows, g.groups) ? "true" : "false") << "}\n";

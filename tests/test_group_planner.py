@@ -24,7 +24,7 @@ def cdiv(a, b):
 
 @pytest.fixture(scope="module")
 def plans(tmp_path_factory):
-    """plans([(kind, rows, groups, M, N, K, summed, pairs, cus), ...]) -> [{"plan", "counters", "fits"}, ...]"""
+    """plans([(kind, rows, groups, M, N, K, summed, pairs, strided, cus), ...]) -> [{"plan", "counters", "fits"}, ...]"""
     exe = str(tmp_path_factory.mktemp("plan") / "group_plan_check")
     subprocess.run(["g++", "-O1", "-std=c++17", "-Wall", "-Werror", f"-I{os.path.join(PKG, 'csrc')}",
                     os.path.join(HERE, "group_plan_check.cpp"), os.path.join(PKG, "libgemm_bf16.so"), f"-Wl,-rpath,{PKG}",
@@ -59,10 +59,10 @@ def test_tile_plans_hold_whatever_rows_groups_have(plans):
         if not summed and rng.random() < 0.2:
             groups = 0                                     # all rows are one's
         asked.append(("tile", rows, groups, size(rng, 1, 12000), size(rng, 1, 12000), size(rng, 1, 30000), summed,
-                      pairs and not summed, rng.choice(CUS)))
+                      pairs and not summed, not pairs and not summed and rng.random() < 0.5, rng.choice(CUS)))
     seen = set()
     for a, got in zip(asked, plans(asked)):
-        _, rows, groups, M, N, K, summed, pairs, cus = a
+        _, rows, groups, M, N, K, summed, pairs, strided, cus = a
         p, kt = got["plan"], cdiv(K, 32)
         bm, splits, per = p["bm"], p["splits"], p["kt_per_split"]
         assert p["tiles_n"] == cdiv(N, bm), a
@@ -81,7 +81,7 @@ def test_tile_plans_hold_whatever_rows_groups_have(plans):
             assert not pairs or per % 2 == 0, a
         assert p["grid"] == p["tiles"] * splits, a
         if splits > 1:
-            assert bm < 256 and p["ws_floats"] == p["grid"] * bm * bm <= WS_FLOATS and got["counters"] == p["tiles"] <= WS_COUNTERS, (a, p)
+            assert bm < 256 and p["ws_floats"] == p["grid"] * bm * bm <= WS_FLOATS // (1 if pairs or strided else 2) and got["counters"] == p["tiles"] <= WS_COUNTERS, (a, p)
         else:
             assert p["ws_floats"] == got["counters"] == 0, a
         seen.add((bm, splits > 1, summed))
@@ -94,7 +94,7 @@ def test_pieces_of_whole_blocks(plans, kt):
     """Pieces rounded up to whole blocks of 128 codes are counted after the rounding."""
     for M, N in ((1, 64), (64, 64), (65, 129), (300, 520), (200, 1000)):
         for K in (32 * kt, 32 * kt - 1, 32 * kt - 31):
-            p = plans([("tile", M, 0, M, N, K, False, True, 256)])[0]["plan"]
+            p = plans([("tile", M, 0, M, N, K, False, True, False, 256)])[0]["plan"]
             per, splits = p["kt_per_split"], p["splits"]
             assert per % 2 == 0 and per * splits >= kt and per * (splits - 1) < kt
 
@@ -105,10 +105,10 @@ def test_decode_plans_hold_whatever_rows_groups_have(plans):
     for _ in range(3000):
         groups = rng.choice([0, size(rng, 1, 300)])
         asked.append(("decode", size(rng, 1, 64 if groups == 0 else 16 * groups + 1), groups, 0, size(rng, 1, 40000), size(rng, 1, 100000),
-                      False, False, rng.choice(CUS)))
+                      False, False, False, rng.choice(CUS)))
     shapes = set()
     for a, got in zip(asked, plans(asked)):
-        _, rows, groups, _, N, K, _, _, cus = a
+        _, rows, groups, _, N, K, _, _, _, cus = a
         p = got["plan"]
         assert got["fits"] == (rows <= 64 if groups == 0 else rows <= 16 * groups)
         mt, tn, s = p["mtiles"], p["strip"] // 16, p["splits"]
