@@ -118,31 +118,32 @@ struct F8Scales {
 #pragma unroll
         for (int i = 0; i < 2; ++i) w[i] = b + 64 * i + lane < count ? sb[b + 64 * i + lane] : 0.f;
     }
-    __device__ __forceinline__ void issue(int b, uint32_t lds, int wave) const {
+    // block b's into place `slot` of the ring
+    __device__ __forceinline__ void issue(int b, uint32_t lds, int slot, int wave) const {
         const int from = b < count ? b : 0;  // (a block past the last: any, not read)
-        dma4(rsrc_words(sa + from * ldsa, kBufRecords), lds + T::S_RING + (b & 1) * T::S_BYTES + wave * 256, off);
+        dma4(rsrc_words(sa + from * ldsa, kBufRecords), lds + T::S_RING + slot * T::S_BYTES + wave * 256, off);
     }
-    // the factors of the wave's rows in block b: row w0 + 16 mi + (lane & 15)
-    __device__ __forceinline__ void read(const char* lds, int b, int w0, int lane, float (&s)[T::TM]) {
+    // the factors of the wave's rows in block b, in place `slot`: row w0 + 16 mi + (lane & 15)
+    __device__ __forceinline__ void read(const char* lds, int b, int slot, int w0, int lane, float (&s)[T::TM]) {
         const int bits = __builtin_bit_cast(int, (b & 64) ? w[1] : w[0]);
         const float sw = __builtin_bit_cast(float, __builtin_amdgcn_readlane(bits, b & 63));
 #pragma unroll
         for (int mi = 0; mi < T::TM; ++mi) {
             const int r = w0 + 16 * mi;
-            s[mi] = *reinterpret_cast<const float*>(lds + T::S_RING + (b & 1) * T::S_BYTES + (r / T::S_ROWS) * 256 +
+            s[mi] = *reinterpret_cast<const float*>(lds + T::S_RING + slot * T::S_BYTES + (r / T::S_ROWS) * 256 +
                                                     (r % T::S_ROWS + (lane & 15)) * 4) * sw;
         }
         if ((b & 127) == 127) load(b + 1, lane);
     }
 };
 
-// acc += s (W A) for the weight tiles of step parity P. Product j + 2 is issued before product j's sums are added,
+// acc += s (W A) for H weight tiles from tile FROM. Product j + 2 is issued before product j's sums are added,
 // so that the FMAs read a result that is two MFMAs old and fit between their issues. (The empty statements and
 // scheduling barriers hold that order: left alone, the compiler issues all MFMAs first and runs out of registers.)
-template <class T, int P>
-__device__ __forceinline__ void f8_multiply(const u32x4 (&fb)[T::HN][2], const u32x4 (&fa)[T::TM][2], const float (&s)[T::TM],
+template <class T, int FROM, int H>
+__device__ __forceinline__ void f8_multiply(const u32x4 (&fb)[H][2], const u32x4 (&fa)[T::TM][2], const float (&s)[T::TM],
                                             f32x4 (&acc)[T::TN][T::TM]) {
-    constexpr int N = T::HN * T::TM;
+    constexpr int N = H * T::TM;
     f32x4 x[3];
     x[0] = f8_mfma(fb[0], fa[0]);
     x[1] = f8_mfma(fb[1 / T::TM], fa[1 % T::TM]);
@@ -150,7 +151,7 @@ __device__ __forceinline__ void f8_multiply(const u32x4 (&fb)[T::HN][2], const u
     for (int j = 0; j < N; ++j) {
         if (j + 2 < N) x[(j + 2) % 3] = f8_mfma(fb[(j + 2) / T::TM], fa[(j + 2) % T::TM]);
         __builtin_amdgcn_sched_barrier(0);
-        const int ni = P * T::HN + j / T::TM, mi = j % T::TM;
+        const int ni = FROM + j / T::TM, mi = j % T::TM;
         float c[4];
 #pragma unroll
         for (int r = 0; r < 4; ++r) c[r] = __builtin_fmaf(x[j % 3][r], s[mi], acc[ni][mi][r]);
@@ -200,7 +201,7 @@ f8_pp_kernel(OpTileArgs p, GroupArgs g) {
     using P0 = std::integral_constant<int, 0>;
     using P1 = std::integral_constant<int, 1>;
 
-    sc.issue(0, ring, wave);
+    sc.issue(0, ring, 0, wave);
     issue_a(P0{}, 0);
     issue_b(P0{}, 0, 0);
     issue_a(P1{}, 1);
@@ -217,10 +218,10 @@ f8_pp_kernel(OpTileArgs p, GroupArgs g) {
     for (int b = 0; b < blocks; ++b) {
         {  // first step: all activations, the first weights
             u32x4 fb[T::HN][2];
-            sc.read(lds, b, wm * T::WTM, lane, s);
+            sc.read(lds, b, b & 1, wm * T::WTM, lane, s);
             f8_read<256, 4>(lds, (2 * b) & 3, wm * T::WTM, lane, fa);
             f8_read<256, 5>(lds + T::B_RING, slot, wn * T::WTN, lane, fb);
-            sc.issue(b + 1, ring, wave);
+            sc.issue(b + 1, ring, (b + 1) & 1, wave);
             issue_a(P1{}, 2 * b + 3);
             issue_b(P1{}, 2 * b + 3, op_wrap(slot + 3));
             if (b == tail) {
@@ -229,7 +230,7 @@ f8_pp_kernel(OpTileArgs p, GroupArgs g) {
             }
             wait_lgkmcnt0();
             phase_barrier();
-            f8_multiply<T, 0>(fb, fa, s, acc);
+            f8_multiply<T, 0, T::HN>(fb, fa, s, acc);
             phase_barrier();
         }
         {  // second step: the other weights
@@ -241,7 +242,7 @@ f8_pp_kernel(OpTileArgs p, GroupArgs g) {
             wait_vmcnt<T::LOADS>();
             wait_lgkmcnt0();
             phase_barrier();
-            f8_multiply<T, 1>(fb, fa, s, acc);
+            f8_multiply<T, T::HN, T::HN>(fb, fa, s, acc);
             phase_barrier();
         }
         slot = op_wrap(slot + 2);
@@ -252,15 +253,36 @@ f8_pp_kernel(OpTileArgs p, GroupArgs g) {
     op_epilogue<T, kOpF8, false>(p, lds, at, wave, wm, wn, lane, acc);
 }
 
-// ---- 128 x 128 and 64 x 64, K split over idle CUs (op_small's schedule) --------------------------------
-// Iteration i reads the operands of step i + 1: a block's activations and first weights in the odd iteration
-// before it, where unit i of the activations, read two iterations before or in the last one, is over at the
-// barrier and takes unit i + 4. The scales of the block after the next are issued in odd iterations, whose
-// copies the next odd one awaits.
+// ---- 128 x 128 and 64 x 64, K split over idle CUs --------------------------------------------------------
+// Four waves in step, one step a block: iteration b multiplies block b, which is in registers, while block b + 1 comes
+// to registers from LDS and block b + 2 to LDS, into the place of block b, whose reads are over in every wave at the
+// iteration's barrier. Before it each wave waits for its copies of block b + 1. 34 KB for 64 x 64, four workgroups a CU,
+// 66 KB for 128 x 128, two. us, against steps of half a block in op_small's rings: 2048 x 4096 x 11008 91 and 114, 1024 x
+// 4096 x 4096 32.8 and 40.3, 509 x 2501 x 1003 8.3 and 10.5; a third block of 64 x 64, three workgroups a CU: 38.8 and 9.0.
+template <int BT>
+struct F8Small : F8Tile<BT, BT, 2, 2> {
+    using Base = F8Tile<BT, BT, 2, 2>;
+    static constexpr int BLOCK = BT * 128;  // of either operand
+    static constexpr int B_RING = 2 * BLOCK, S_RING = 4 * BLOCK;
+    static constexpr int LDS_BYTES = S_RING + 2 * Base::S_BYTES;
+    static constexpr int LOADS = 2 * Base::LOADS + 1;  // copies of a wave and block
+};
+
+// T tiles of 16 rows from `w0` of a block
+template <int T>
+__device__ __forceinline__ void f8_read_block(const char* block, int w0, int lane, u32x4 (&f)[T][2]) {
+    const int j = lane & 15, G = lane >> 4;
+#pragma unroll
+    for (int i = 0; i < T; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            f[i][h] = *reinterpret_cast<const u32x4*>(block + (w0 + 16 * i + j) * 128 + 16 * ((4 * h + G) ^ (j >> 1)));
+}
+
 template <int BT>
 __global__ void __attribute__((amdgpu_flat_work_group_size(256, 256), amdgpu_waves_per_eu(2, BT == 64 ? 4 : 2)))
 f8_small_kernel(OpTileArgs p, GroupArgs g) {
-    using T = F8Tile<BT, BT, 2, 2>;
+    using T = F8Small<BT>;
     extern __shared__ __attribute__((aligned(1024))) char lds[];
     OpPlace at;
     if (!group_tile<kOpF8, BT>(p, g, (int)blockIdx.x, &at)) return;
@@ -279,9 +301,13 @@ f8_small_kernel(OpTileArgs p, GroupArgs g) {
     F8Scales<T> sc;
     sc.init(p, at, first, blocks, wave, wn, lane);
     const uint32_t ring = lds_addr(lds);
-    auto issue_a = [&](auto h, int u) { ca.template issue<decltype(h)::value>(u, ring + (u & 3) * T::A_BYTES, wave); };
-    auto issue_b = [&](auto h, int u, int slot) {
-        cb.template issue<decltype(h)::value>(u, ring + T::B_RING + slot * T::B_BYTES, wave);
+    auto issue = [&](int b, int slot) {
+        sc.issue(b, ring, slot, wave);
+        const uint32_t a = ring + slot * T::BLOCK, w = ring + T::B_RING + slot * T::BLOCK;
+        ca.template issue<0>(2 * b, a, wave);
+        ca.template issue<1>(2 * b + 1, a + T::BLOCK / 2, wave);
+        cb.template issue<0>(2 * b, w, wave);
+        cb.template issue<1>(2 * b + 1, w + T::BLOCK / 2, wave);
     };
     f32x4 acc[T::TN][T::TM];
 #pragma unroll
@@ -289,63 +315,38 @@ f8_small_kernel(OpTileArgs p, GroupArgs g) {
 #pragma unroll
         for (int mi = 0; mi < T::TM; ++mi) acc[ni][mi] = f32x4{};
     const int tail = (count & 15) ? blocks - 1 : -1;
-    using P0 = std::integral_constant<int, 0>;
-    using P1 = std::integral_constant<int, 1>;
-
-    u32x4 fa[T::TM][2], na[T::TM][2], fb[T::HN][2], nb[T::HN][2];
-    float s[T::TM], ns[T::TM];
-    sc.issue(0, ring, wave);
-    sc.issue(1, ring, wave);
-    issue_a(P0{}, 0);
-    issue_b(P0{}, 0, 0);
-    issue_a(P1{}, 1);
-    issue_b(P1{}, 1, 1);
-    issue_a(P0{}, 2);
-    issue_b(P0{}, 2, 2);
-    issue_a(P1{}, 3);
-    issue_b(P1{}, 3, 3);
-    wait_vmcnt<2 * T::LOADS>();  // units 0 and 1; 2 and 3 may be in flight
-    lds_barrier();
-    auto read_first = [&](int b, int at_slot, u32x4 (&xa)[T::TM][2], u32x4 (&xb)[T::HN][2], float (&xs)[T::TM]) {
-        sc.read(lds, b, wm * T::WTM, lane, xs);
-        f8_read<BT, 4>(lds, (2 * b) & 3, wm * T::WTM, lane, xa);
-        f8_read<BT, 5>(lds + T::B_RING, at_slot, wn * T::WTN, lane, xb);
+    struct Operands {
+        u32x4 a[T::TM][2], b[T::TN][2];
+        float s[T::TM];
+    };
+    auto read = [&](int b, int slot, Operands& x) {
+        sc.read(lds, b, slot, wm * T::WTM, lane, x.s);
+        f8_read_block(lds + slot * T::BLOCK, wm * T::WTM, lane, x.a);
+        f8_read_block(lds + T::B_RING + slot * T::BLOCK, wn * T::WTN, lane, x.b);
         if (b == tail) {
-            f8_clear_tail(count - 128 * b, lane, xa);
-            f8_clear_tail(count - 128 * b, lane, xb);
+            f8_clear_tail(count - 128 * b, lane, x.a);
+            f8_clear_tail(count - 128 * b, lane, x.b);
         }
     };
-    auto read_second = [&](int b, int at_slot, u32x4 (&xb)[T::HN][2]) {
-        f8_read<BT, 5>(lds + T::B_RING, at_slot, wn * T::WTN + T::WTN / 2, lane, xb);
-        if (b == tail) f8_clear_tail(count - 128 * b, lane, xb);
-    };
-    read_first(0, 0, fa, fb, s);
-    int slot = 0;  // of the weights' unit 2 b
-#pragma clang loop unroll(disable)
-    for (int b = 0; b < blocks; ++b) {
-        // step 2 b
+    Operands x0, x1;
+    issue(0, 0);
+    issue(1, 1);
+    wait_vmcnt<T::LOADS>();
+    lds_barrier();
+    read(0, 0, x0);
+    auto step = [&](int b, int slot, Operands& x, Operands& next) {
+        wait_vmcnt<0>();
         lds_barrier();
-        issue_a(P0{}, 2 * b + 4);
-        issue_b(P0{}, 2 * b + 4, op_wrap(slot + 4));
-        read_second(b, slot, nb);
-        f8_multiply<T, 0>(fb, fa, s, acc);
-        // step 2 b + 1
-        const int next = op_wrap(slot + 2);
-        wait_vmcnt<T::LOADS>();  // this wave's copies of block b + 1 landed
-        lds_barrier();           // every wave's did, and the operands of step 2 b + 1 are in registers
-        sc.issue(b + 2, ring, wave);
-        issue_a(P1{}, 2 * b + 5);
-        issue_b(P1{}, 2 * b + 5, slot);
-        read_first(b + 1, next, na, fb, ns);
-        f8_multiply<T, 1>(nb, fa, s, acc);
-#pragma unroll
-        for (int mi = 0; mi < T::TM; ++mi) {
-            s[mi] = ns[mi];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) fa[mi][h] = na[mi][h];
-        }
-        slot = next;
+        issue(b + 2, slot);
+        read(b + 1, slot ^ 1, next);
+        f8_multiply<T, 0, T::TN>(x.b, x.a, x.s, acc);
+    };
+    int b = 0;
+    for (; b + 1 < blocks; b += 2) {
+        step(b, 0, x0, x1);
+        step(b + 1, 1, x1, x0);
     }
+    if (b < blocks) step(b, 0, x0, x1);
     wait_vmcnt<0>();
     lds_barrier();
     if (p.splits > 1 && !op_join<T>(p, at, lds, wave, lane, acc)) return;
@@ -357,20 +358,20 @@ hipError_t launch_f8_tile(int tile, const OpTileArgs& a, const GroupArgs& g, int
         if (a.splits != 1) return hipErrorInvalidValue;
         f8_pp_kernel<<<grid, 512, F8Tile<256, 256, 4, 2>::LDS_BYTES, s>>>(a, g);
     } else if (tile == 128) {
-        f8_small_kernel<128><<<grid, 256, F8Tile<128, 128, 2, 2>::LDS_BYTES, s>>>(a, g);
+        f8_small_kernel<128><<<grid, 256, F8Small<128>::LDS_BYTES, s>>>(a, g);
     } else {
-        f8_small_kernel<64><<<grid, 256, F8Tile<64, 64, 2, 2>::LDS_BYTES, s>>>(a, g);
+        f8_small_kernel<64><<<grid, 256, F8Small<64>::LDS_BYTES, s>>>(a, g);
     }
     return hipGetLastError();
 }
 
-// (the 64 x 64 kernel asks for 38 KB, which needs no setting)
+// (the 64 x 64 kernel asks for 34 KB, which needs no setting)
 hipError_t configure_f8_kernels() {
     hipError_t e = hipFuncSetAttribute((const void*)f8_pp_kernel, hipFuncAttributeMaxDynamicSharedMemorySize,
                                        F8Tile<256, 256, 4, 2>::LDS_BYTES);
     if (e == hipSuccess)
         e = hipFuncSetAttribute((const void*)f8_small_kernel<128>, hipFuncAttributeMaxDynamicSharedMemorySize,
-                                F8Tile<128, 128, 2, 2>::LDS_BYTES);
+                                F8Small<128>::LDS_BYTES);
     return e;
 }
 

@@ -557,8 +557,8 @@ Plan make_group_plan(const GroupShape& g, const DeviceInfo& dev) {
         return std::max<int64_t>(1, rows * cdiv(g.N, b));
     };
     const int64_t high = g.summed ? g.M : each;
-    const int64_t t256 = cdiv(expect(256), cus) * (g.pairs ? 124 : 145), t128 = cdiv(expect(128), 2 * cus) * 100,
-                  t64 = cdiv(expect(64), 4 * cus) * 92;
+    const int64_t t256 = cdiv(expect(256), cus) * (g.pairs ? 168 : 145), t128 = cdiv(expect(128), 2 * cus) * 100,
+                  t64 = cdiv(expect(64), 4 * cus) * (g.pairs ? 96 : 92);
     int bm = t128 < t64 && high > 32 && g.N > 64 ? 128 : 64;
     if (high > 80 && g.N > 80 && 2 * expect(256) >= cus && t256 < std::min(t128, t64) && !(g.summed && each <= 64)) bm = 256;
     if (g.strided && each <= 32 && 4 * expect(128) >= 3 * cus) bm = 128;
