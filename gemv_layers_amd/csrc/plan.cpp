@@ -530,11 +530,13 @@ Plan make_i8_decode_plan(int64_t M, int64_t N, int64_t K, const DeviceInfo& dev,
 }
 
 // Tiles. Rounds of the tiles that fill the card (one of 256 x 256, two of 128 x 128 or four of 64 x 64 a CU), each at
-// what it measured to take for a k-step: 256 x 256 takes 1.24 times a round of 128 x 128 for codes and 1.45 times for bf16,
-// 64 x 64 0.92 times. The host knows the number of rows and of groups, and takes a group's last row tile as half full.
-// us, the three sizes in this order: codes 2048 x 4096 x 11008 153, 124, 203; 4096 x 4096 x 11008 153, 243, 379; 1024 x 4096
-// x 4096 -, 47.5, 43.4; 2048 rows in 8 groups, 4096 x 4096 70.6, 107, 122; 8192 in 64, 1376 x 4096 148, 176, 186; 4096 in 64
-// -, 130, 140; bf16 2048 rows in 8 groups, 4096 x 4096 89.5, 113, 159; 8192 in 64, 1376 x 4096 192, 206, 282.
+// what it measured to take for a k-step: 256 x 256 takes 1.68 times a round of 128 x 128 for codes and 1.45 times for bf16,
+// 64 x 64 1.1 times. The host knows the number of rows and of groups, and takes a group's last row tile as half full. 128
+// x 128 tiles on less than three quarters of the CUs lose to 64 x 64 with more pieces of K, and 256 x 256 ones for
+// groups of 100 rows or less to 128 x 128. us, the three sizes in this order: codes 4096 x 4096 x 11008 152, 192, 300; 2048 x
+// 4096 x 11008 135, 106, 164; 1024 x 4096 x 4096 52, 33, 38; 1018 rows in 8 groups, 1376 x 512 15.8, 11.0, 10.3; 2048 in 8,
+// 4096 x 4096 70.5, 85.7, 102; 2000 in 64, 2048 x 2048 80, 66, 73; bf16 2048 rows in 8 groups, 4096 x 4096 87, 113, 158; 8192 in 64,
+// 1376 x 4096 189, 208, 282; 3000 in 32, 2048 x 2048 77, 67, 83.
 // Two exceptions: gradients of weights over few rows are a stream of output, which 128 x 128 tiles write faster (16
 // rows, 8 groups, 4096 x 1376 25.6, 21.5, 38); and a strided weight is read in rows of a tile's width, 256 bytes of which
 // suit a stream for few rows better than 128 (256 rows in 8 groups, 4096 x 4096 -, 47, 69; 64 in 64, 1376 x 4096 -, 83, 90).
@@ -558,9 +560,9 @@ Plan make_group_plan(const GroupShape& g, const DeviceInfo& dev) {
     };
     const int64_t high = g.summed ? g.M : each;
     const int64_t t256 = cdiv(expect(256), cus) * (g.pairs ? 168 : 145), t128 = cdiv(expect(128), 2 * cus) * 100,
-                  t64 = cdiv(expect(64), 4 * cus) * (g.pairs ? 96 : 92);
-    int bm = t128 < t64 && high > 32 && g.N > 64 ? 128 : 64;
-    if (high > 80 && g.N > 80 && 2 * expect(256) >= cus && t256 < std::min(t128, t64) && !(g.summed && each <= 64)) bm = 256;
+                  t64 = cdiv(expect(64), 4 * cus) * 110;
+    int bm = t128 < t64 && 4 * expect(128) >= 3 * cus && high > 16 && g.N > 64 ? 128 : 64;
+    if (high > 100 && g.N > 100 && 2 * expect(256) >= cus && t256 < std::min(t128, t64) && !(g.summed && each <= 64)) bm = 256;
     if (g.strided && each <= 32 && 4 * expect(128) >= 3 * cus) bm = 128;
     p.bm = p.bn = bm;
     p.threads = bm == 256 ? 512 : 256;
