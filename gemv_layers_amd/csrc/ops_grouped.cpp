@@ -57,6 +57,19 @@ bool matrix_ok(int mode, const OpArgs& a, const GroupArgs& g) {
     return mode == glk::kOpAtb ? a.M % 8 == 0 : a.K % 8 == 0;
 }
 
+// plans r's product on MFMA tiles, of `tile` rows and columns if that is not 0
+int plan_tiles(int tile, const glk::DeviceInfo& dev, hipStream_t stream, Ready* r) {
+    const bool f8 = r->mode == glk::kOpF8, summed = r->mode == glk::kOpAtb;
+    // codes: planned as the bf16 product whose k-steps have the same bytes and matrix-core cycles
+    glk::GroupShape shape{r->g.rows, r->g.offsets || summed ? r->g.groups : 0, r->a.M, r->a.N, f8 ? (r->a.K + 1) / 2 : r->a.K,
+                          summed, f8, r->mode == glk::kOpAb};
+    shape.tile = tile;
+    r->route = Ready::kTiles;
+    r->p = glk::make_group_plan(shape, dev);
+    if (r->p.grid > INT32_MAX) return GEMM_ERR_UNSUPPORTED;
+    return r->p.ws_floats > 0 ? glk::stream_workspace(stream, &r->w) : GEMM_OK;
+}
+
 // One product on the current device with a non-empty C, operands checked. `fused`: one row of bf16 activations
 // and a weight that the weight-streaming kernel takes. The rows of C (of kOpAtb those of
 // all groups' C together) are written whole.
@@ -82,15 +95,7 @@ int prepare(int mode, const OpArgs& a, const GroupArgs& g, bool fused, hipStream
             return r->p.ws_floats > 0 ? glk::stream_workspace(stream, &r->w) : GEMM_OK;
         }
     }
-    if (matrix) {
-        r->route = Ready::kTiles;
-        // codes: planned as the bf16 product whose k-steps have the same bytes and matrix-core cycles
-        const bool f8 = mode == glk::kOpF8, summed = mode == glk::kOpAtb;
-        r->p = glk::make_group_plan({g.rows, summed ? g.groups : groups, a.M, a.N, f8 ? (a.K + 1) / 2 : a.K, summed, f8,
-                                     mode == glk::kOpAb}, *dev);
-        if (r->p.grid > INT32_MAX) return GEMM_ERR_UNSUPPORTED;
-        return r->p.ws_floats > 0 ? glk::stream_workspace(stream, &r->w) : GEMM_OK;
-    }
+    if (matrix) return plan_tiles(0, *dev, stream, r);
     // 64 x 64 tiles of 256 threads, 32-bit grids
     const int64_t row_tiles =
         mode == glk::kOpAtb ? ((a.M - 1) / 64 + 1) * g.groups : glk::most_row_tiles(g.rows, groups, 64);
@@ -162,8 +167,14 @@ int launch(const Ready& r, hipStream_t stream) {
 }
 
 // Both gradients as one launch where each is a grid of the same small tiles: the second's partials follow the
-// first's.
-int launch_gradients(const Ready& a, Ready b, const glk::DeviceInfo& dev, hipStream_t stream) {
+// first's. Small ones whose tiles differ take dB's (1018 rows in 8 groups, 512 to 1376: 9.8 and 7.8 us alone with 64 x 64 and
+// 128 x 128 tiles, 18.0 in two launches, 13.3 in one with 128 x 128, 15.1 with 64 x 64).
+int launch_gradients(Ready a, Ready b, const glk::DeviceInfo& dev, hipStream_t stream) {
+    if (a.route == Ready::kTiles && b.route == Ready::kTiles && a.p.bm < 256 && b.p.bm < 256 && a.p.bm != b.p.bm &&
+        a.p.grid <= 4 * dev.cus && b.p.grid <= 4 * dev.cus) {
+        const int st = plan_tiles(b.p.bm, dev, stream, &a);
+        if (st != GEMM_OK) return st;
+    }
     const glk::Plan &pa = a.p, &pb = b.p;
     const bool pair = a.route == Ready::kTiles && b.route == Ready::kTiles && pa.bm == pb.bm && pa.bm < 256 &&
                       pa.grid + pb.grid <= INT32_MAX && pa.ws_floats + pb.ws_floats <= dev.ws_floats &&

@@ -564,6 +564,7 @@ Plan make_group_plan(const GroupShape& g, const DeviceInfo& dev) {
     int bm = t128 < t64 && 4 * expect(128) >= 3 * cus && high > 16 && g.N > 64 ? 128 : 64;
     if (high > 100 && g.N > 100 && 2 * expect(256) >= cus && t256 < std::min(t128, t64) && !(g.summed && each <= 64)) bm = 256;
     if (g.strided && each <= 32 && 4 * expect(128) >= 3 * cus) bm = 128;
+    if (g.tile) bm = g.tile;
     p.bm = p.bn = bm;
     p.threads = bm == 256 ? 512 : 256;
     p.tiles_n = cdiv(g.N, bm);

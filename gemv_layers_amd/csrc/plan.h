@@ -102,6 +102,7 @@ inline int64_t most_row_tiles(int64_t rows, int64_t groups, int64_t bm) {
 struct GroupShape {
     int64_t rows, groups, M, N, K;
     bool summed, pairs, strided;
+    int tile = 0;  // 128 or 64: tiles of that size
 };
 // The grid and workspace hold whatever sizes the groups have.
 Plan make_group_plan(const GroupShape& g, const DeviceInfo& dev);
