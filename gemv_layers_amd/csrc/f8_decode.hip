@@ -250,39 +250,44 @@ __global__ void __launch_bounds__(64 * NW) f8_decode_kernel(F8DecodeArgs p, Grou
     }
 }
 
-// blocks of 128 k in flight per wave
-static constexpr int depth(int mt, int tn) { return mt * tn >= 8 ? 2 : 3; }
-
 static constexpr int kWaves = 4;
+
+// Blocks of 128 k in flight per wave: two, and three where a wave has 16 or more and its row and weight tiles are few
+// (us with two and three: 41 of 64 groups of 1376 x 4096, 8 blocks a wave, 46.9 and 50.0, 1 x 11008 x 4096 12.0 and 12.6; 16 x
+// 4096 x 11008, 21 blocks, 15.2 and 14.5; four are as three, five slower).
+static bool deep(const F8DecodeArgs& a, int mt, int tn) { return mt * tn < 8 && a.K / 128 >= 16 * kWaves * a.pieces; }
 
 // the kernel of a shape that the planner makes, and its LDS bytes, or null
 struct F8Decode {
     void (*kernel)(F8DecodeArgs, GroupArgs);
     int lds;
 };
-template <int MT, int TN, bool FUSED>
-static F8Decode of() {
-    return {f8_decode_kernel<MT, TN, kWaves, depth(MT, TN), FUSED>, kWaves * TN * MT * 1024};
+template <int MT, int TN, bool FUSED = false>
+static F8Decode of(bool deep) {
+    constexpr int lds = kWaves * TN * MT * 1024;
+    if constexpr (MT * TN < 8)
+        if (deep) return {f8_decode_kernel<MT, TN, kWaves, 3, FUSED>, lds};
+    return {f8_decode_kernel<MT, TN, kWaves, 2, FUSED>, lds};
 }
-static F8Decode find(int mt, int tn, bool fused) {
-    if (fused) return mt != 1 ? F8Decode{} : tn == 1 ? of<1, 1, true>() : tn == 2 ? of<1, 2, true>() : F8Decode{};
+static F8Decode find(int mt, int tn, bool fused, bool deep) {
+    if (fused) return mt != 1 ? F8Decode{} : tn == 1 ? of<1, 1, true>(deep) : tn == 2 ? of<1, 2, true>(deep) : F8Decode{};
     switch (mt * 8 + tn) {
-        case 9: return of<1, 1, false>();
-        case 10: return of<1, 2, false>();
-        case 12: return of<1, 4, false>();
-        case 17: return of<2, 1, false>();
-        case 18: return of<2, 2, false>();
-        case 20: return of<2, 4, false>();
-        case 33: return of<4, 1, false>();
-        case 34: return of<4, 2, false>();
-        case 36: return of<4, 4, false>();
+        case 9: return of<1, 1>(deep);
+        case 10: return of<1, 2>(deep);
+        case 12: return of<1, 4>(deep);
+        case 17: return of<2, 1>(deep);
+        case 18: return of<2, 2>(deep);
+        case 20: return of<2, 4>(deep);
+        case 33: return of<4, 1>(deep);
+        case 34: return of<4, 2>(deep);
+        case 36: return of<4, 4>(deep);
         default: return {};
     }
 }
 
 // (at most 64 KB, which needs no setting: with the codes and scales of a row of kF8FusedK the fused ones 25 KB)
 hipError_t launch_f8_decode(int mt, int tn, const F8DecodeArgs& a, const GroupArgs& g, int grid, hipStream_t s) {
-    const F8Decode k = find(mt, tn, a.A16 != nullptr);
+    const F8Decode k = find(mt, tn, a.A16 != nullptr, deep(a, mt, tn));
     if (!k.kernel) return hipErrorInvalidValue;
     k.kernel<<<grid, 64 * kWaves, k.lds + (a.A16 ? (a.K + 127) / 128 * 132 : 0), s>>>(a, g);
     return hipGetLastError();
