@@ -79,8 +79,9 @@ __device__ __forceinline__ bool find_span(const GroupArgs& g, int bm, int per, i
     row = 0;
     if (spans > 64) p = part(0, row, upto);
     uint64_t hit;
-    while (!(hit = __ballot(tile < p.upto))) {  // (a tile below the total is in one of them)
+    while (!(hit = __ballot(tile < p.upto))) {
         s0 += 64;
+        if (s0 >= spans) return false;  // (offsets that changed since the first pass)
         p = part(s0, row, upto);
     }
     const int at = __builtin_ctzll(hit), s = s0 + at;

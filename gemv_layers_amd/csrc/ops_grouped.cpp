@@ -66,7 +66,7 @@ int plan_tiles(int tile, const glk::DeviceInfo& dev, hipStream_t stream, Ready* 
     shape.tile = tile;
     r->route = Ready::kTiles;
     r->p = glk::make_group_plan(shape, dev);
-    if (r->p.grid > INT32_MAX) return GEMM_ERR_UNSUPPORTED;
+    if (r->p.grid > glk::kMostThreads / r->p.threads) return GEMM_ERR_UNSUPPORTED;
     return r->p.ws_floats > 0 ? glk::stream_workspace(stream, &r->w) : GEMM_OK;
 }
 
@@ -90,7 +90,7 @@ int prepare(int mode, const OpArgs& a, const GroupArgs& g, bool fused, hipStream
     r->fused = fused;
     if (mode == glk::kOpF8 && matrix && glk::f8_decode_fits(g.rows, groups)) {  // the weight-streaming kernel
         r->p = glk::make_f8_decode_plan(g.rows, a.N, a.K, groups, *dev);
-        if (r->p.grid <= INT32_MAX) {
+        if (r->p.grid <= glk::kMostThreads / r->p.threads) {
             r->route = Ready::kDecode;
             return r->p.ws_floats > 0 ? glk::stream_workspace(stream, &r->w) : GEMM_OK;
         }
@@ -177,7 +177,7 @@ int launch_gradients(Ready a, Ready b, const glk::DeviceInfo& dev, hipStream_t s
     }
     const glk::Plan &pa = a.p, &pb = b.p;
     const bool pair = a.route == Ready::kTiles && b.route == Ready::kTiles && pa.bm == pb.bm && pa.bm < 256 &&
-                      pa.grid + pb.grid <= INT32_MAX && pa.ws_floats + pb.ws_floats <= dev.ws_floats &&
+                      pa.grid + pb.grid <= glk::kMostThreads / 256 && pa.ws_floats + pb.ws_floats <= dev.ws_floats &&
                       pa.counters + pb.counters <= dev.ws_counters;
     if (!pair) {
         const int st = launch(a, stream);

@@ -565,6 +565,12 @@ Plan make_group_plan(const GroupShape& g, const DeviceInfo& dev) {
     if (high > 100 && g.N > 100 && 2 * expect(256) >= cus && t256 < std::min(t128, t64) && !(g.summed && each <= 64)) bm = 256;
     if (g.strided && each <= 32 && 4 * expect(128) >= 3 * cus) bm = 128;
     if (g.tile) bm = g.tile;
+    // a launch holds 2^32 - 1 threads
+    auto fits = [&](int64_t b) {
+        const int64_t rows = g.summed ? g.groups * cdiv(g.M, b) : most_row_tiles(g.rows, g.groups, b);
+        return rows <= kMostThreads / (b == 256 ? 512 : 256) / cdiv(g.N, b);
+    };
+    while (bm < 256 && !fits(bm)) bm *= 2;
     p.bm = p.bn = bm;
     p.threads = bm == 256 ? 512 : 256;
     p.tiles_n = cdiv(g.N, bm);

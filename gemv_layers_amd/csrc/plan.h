@@ -89,6 +89,7 @@ Plan make_i8_decode_plan(int64_t M, int64_t N, int64_t K, const DeviceInfo& dev,
 // whether that plan beats the tiles (M may be any)
 bool i8_decode_fits(int64_t M, int64_t K, const Plan& p);
 
+constexpr int64_t kMostThreads = 0xFFFFFFFF;  // of a launch
 // most tiles of `bm` rows over `rows` rows in `groups` groups and those of none, wherever they are cut; no groups: all
 // rows are one's
 inline int64_t most_row_tiles(int64_t rows, int64_t groups, int64_t bm) {
