@@ -124,10 +124,10 @@ def test_decode_plans_hold_whatever_rows_groups_have(plans):
 
 
 def test_large_grids_take_larger_tiles(plans):
-    """A launch holds 2^32 - 1 threads: a million rows of 65536 groups against 70000 columns (16 a group in the mean)
-    would be 88 million 64 x 64 tiles."""
-    for rows, groups, N, pairs in ((1 << 20, 65536, 70000, False), (1 << 20, 65536, 70000, True), ((1 << 24) - 1, 65536, 8192, True)):
-        p = plans([("tile", rows, groups, rows, N, 512, False, pairs, not pairs, 256)])[0]["plan"]
+    """A launch holds 2^32 - 1 threads: 2^18 rows of 16384 groups (16 a group in the mean) against 70000 columns would be
+    22 million 64 x 64 tiles of 256."""
+    for rows, groups, N, pairs in ((1 << 18, 16384, 70000, False), (1 << 18, 16384, 70000, True), ((1 << 24) - 1, 65536, 8192, True)):
+        p = plans([("tile", rows, groups, rows, N, 512, False, pairs, False, 256)])[0]["plan"]
         assert p["bm"] > 64 and p["grid"] * p["threads"] < 1 << 32, p
-    small = plans([("tile", 1 << 20, 65536, 1 << 20, 64, 512, False, False, False, 256)])[0]["plan"]
+    small = plans([("tile", 1 << 18, 16384, 1 << 18, 64, 512, False, False, False, 256)])[0]["plan"]
     assert small["bm"] == 64 and small["grid"] * small["threads"] < 1 << 32
