@@ -250,6 +250,7 @@ f8_pp_kernel(OpTileArgs p, GroupArgs g) {
     if (grp == 0) phase_barrier();
     wait_vmcnt<0>();  // the copies past K included
     lds_barrier();    // the rings are free for the output
+    if (p.splits > 1 && !op_join_tile<T>(p, at, lds, wave, lane, acc)) return;
     op_epilogue<T, kOpF8, false>(p, lds, at, wave, wm, wn, lane, acc);
 }
 

@@ -41,14 +41,26 @@ struct GroupSpan {
     int unit;         // the workgroup's unit among the span's tiles * per
 };
 
-// The span and unit of workgroup `block` for row tiles of `bm` rows, each of `per` units, or false where the
-// offsets make fewer tiles. Units in order of rows, each XCD a contiguous share. Every lane of the wave calls it.
-__device__ __forceinline__ bool find_span(const GroupArgs& g, int bm, int per, int nxcd, int block, GroupSpan* out) {
+// Which unit of `total` workgroup `block` takes, or false for none: each XCD a contiguous share.
+struct EvenUnits {
+    int block, nxcd;
+    __device__ __forceinline__ bool operator()(int total, int* unit) const {
+        if (block >= total) return false;
+        *unit = xcd_remap(block, total, nxcd);
+        return true;
+    }
+};
+
+// The span and unit of a workgroup for row tiles of `bm` rows, each of `per` units, as `which` picks the unit of all in
+// order of rows, or false where it picks none. Every lane of the wave calls it.
+template <class Which>
+__device__ __forceinline__ bool find_span(const GroupArgs& g, int bm, int per, Which&& which, GroupSpan* out) {
     auto uni = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
+    int unit;
     if (!g.offsets) {
         const int tiles = (g.rows - 1) / bm + 1;
-        if (block >= tiles * per) return false;
-        *out = GroupSpan{0, 0, g.rows, uni(tiles), 0, uni(xcd_remap(block, tiles * per, nxcd))};
+        if (!which(tiles * per, &unit)) return false;
+        *out = GroupSpan{0, 0, g.rows, uni(tiles), 0, uni(unit)};
         return true;
     }
     const int lane = threadIdx.x & 63, spans = g.groups + 2;
@@ -73,8 +85,9 @@ __device__ __forceinline__ bool find_span(const GroupArgs& g, int bm, int per, i
     int row = 0, total = 0;
     Part p = part(0, row, total);
     for (int s0 = 64; s0 < spans; s0 += 64) part(s0, row, total);
-    if (block >= total * per) return false;
-    const int unit = uni(xcd_remap(block, total * per, nxcd)), tile = uni(unit / per);
+    if (!which(total * per, &unit)) return false;
+    unit = uni(unit);
+    const int tile = uni(unit / per);
     int s0 = 0, upto = 0;
     row = 0;
     if (spans > 64) p = part(0, row, upto);

@@ -35,7 +35,7 @@ __global__ void __launch_bounds__(256) group_generic_kernel(OpArgs p, GroupArgs 
         n0 = (int64_t)(tile % tiles_n) * T;
     } else {
         GroupSpan s;
-        if (!find_span(g, T, tiles_n, 1, (int)blockIdx.x, &s)) return;
+        if (!find_span(g, T, tiles_n, EvenUnits{(int)blockIdx.x, 1}, &s)) return;
         group = max(s.group, 0);
         first = s.first;
         M = s.rows;

@@ -6,6 +6,34 @@
 
 namespace glk {
 
+// 256 x 256 tiles, one a CU: the tiles of whole rounds, then those of a last round that fills at most half of the
+// CUs, each in up to g.tail pieces of K as far as CUs and slots of the workspace go. The host cannot tell how many tiles
+// the groups make. 8192 rows in 8 groups, 4096 to 11008: 1548 tiles, 12 past six rounds, 666 us whole and 640 in pieces;
+// the gradient of its rows, 576 tiles, 64 past two rounds, 680 and 605.
+struct TailUnits {
+    const GroupArgs& g;
+    int block, nxcd;
+    int tile = 0, piece = 0, pieces = 1;  // of a tile in pieces: which, and of how many
+    __device__ __forceinline__ bool operator()(int total, int* unit) {
+        const int rest = total % g.cus;
+        pieces = rest > 0 ? min(min(g.slots / rest, g.cus / rest), g.tail) : 1;
+        if (pieces < 2) {
+            pieces = 1;
+            return EvenUnits{block, nxcd}(total, unit);
+        }
+        const int whole = total - rest, at = block - whole;
+        if (at < 0) {
+            pieces = 1;
+            return EvenUnits{block, nxcd}(whole, unit);
+        }
+        if (at >= rest * pieces) return false;
+        tile = at / pieces;
+        piece = at - tile * pieces;
+        *unit = whole + tile;
+        return true;
+    }
+};
+
 // Narrows p to the group and tile of workgroup `block`; false where there is none. Rows of no group are a product
 // over nothing, which writes zeros.
 template <int MODE, int BT>
@@ -28,7 +56,12 @@ __device__ __forceinline__ bool group_tile(OpTileArgs& p, const GroupArgs& g, in
         p.kt_per_split = uni((steps + p.splits - 1) / p.splits);
     } else {
         GroupSpan s;
-        if (!find_span(g, BT, p.tiles_n * p.splits, p.nxcd, block, &s)) return false;
+        TailUnits tail{g, block, p.nxcd};
+        if constexpr (BT == 256) {
+            if (!find_span(g, BT, p.tiles_n, tail, &s)) return false;
+        } else {
+            if (!find_span(g, BT, p.tiles_n * p.splits, EvenUnits{block, p.nxcd}, &s)) return false;
+        }
         p.tiles_m = s.tiles;
         *at = op_place_unit<BT, BT>(p, s.unit);
         at->tile += s.tile * p.tiles_n;
@@ -42,6 +75,23 @@ __device__ __forceinline__ bool group_tile(OpTileArgs& p, const GroupArgs& g, in
         if constexpr (MODE == kOpF8) {
             p.sa += s.first;
             p.sb += max(s.group, 0) * g.stride_sb;
+        }
+        if (BT == 256 && tail.pieces > 1) {  // whole 128-byte lines of a contiguous operand, none past the end
+            constexpr int LINE = 128 / ES;
+            const int per = (p.K + LINE - 1) / LINE, share = (per + tail.pieces - 1) / tail.pieces * LINE;
+            const int k0 = uni(min(tail.piece * share, p.K) / LINE * LINE);
+            p.K = uni(max(min(p.K - k0, share), 0));
+            if (p.K > 0) {
+                p.A = static_cast<const char*>(p.A) + (int64_t)k0 * ES;
+                p.B = static_cast<const char*>(p.B) + (MODE == kOpAb ? (int64_t)k0 * p.ldb : (int64_t)k0) * ES;
+                if constexpr (MODE == kOpF8) {
+                    p.sa += k0 / 128 * p.ldsa;
+                    p.sb += k0 / 128;
+                }
+            }
+            p.splits = uni(tail.pieces);
+            at->tile = uni(tail.tile);
+            at->piece = uni(tail.piece);
         }
     }
     return true;

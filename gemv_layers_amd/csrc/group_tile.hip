@@ -10,7 +10,7 @@ __global__ void __attribute__((amdgpu_flat_work_group_size(512, 512), amdgpu_wav
 group_pp_kernel(OpTileArgs p, GroupArgs g) {
     extern __shared__ __attribute__((aligned(1024))) char lds[];
     OpPlace at;
-    if (group_tile<MODE, 256>(p, g, (int)blockIdx.x, &at)) op_pp<MODE, false>(p, at, lds);
+    if (group_tile<MODE, 256>(p, g, (int)blockIdx.x, &at)) op_pp<MODE, false, MODE != kOpAtb>(p, at, lds);
 }
 
 template <int BT, int MODE>

@@ -67,6 +67,9 @@ int plan_tiles(int tile, const glk::DeviceInfo& dev, hipStream_t stream, Ready* 
     r->route = Ready::kTiles;
     r->p = glk::make_group_plan(shape, dev);
     if (r->p.grid > glk::kMostThreads / r->p.threads) return GEMM_ERR_UNSUPPORTED;
+    r->g.cus = dev.cus;
+    r->g.tail = r->p.tail;
+    r->g.slots = (int)r->p.counters;
     return r->p.ws_floats > 0 ? glk::stream_workspace(stream, &r->w) : GEMM_OK;
 }
 

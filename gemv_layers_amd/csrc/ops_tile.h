@@ -325,6 +325,108 @@ __device__ __forceinline__ void op_epilogue(const OpTileArgs& p, char* lds, cons
     op_store_rows<T::WTM, WTNO>(ob, p.C, p.ldc, mw, p.M, nw, p.N, lane, (MODE != kOpI8 && MODE != kOpF8) || p.vec != 0);
 }
 
+// Stores the partial sums of a piece at `slot_off` and counts it in: true for the last of the tile's, which returns the
+// counter to zero.
+template <class T, class Off>
+__device__ __forceinline__ bool op_arrive(const OpTileArgs& p, const OpPlace& at, char* lds,
+                                          typename T::Acc (&acc)[T::TN][T::TM], __amdgpu_buffer_rsrc_t ws, Off&& slot_off) {
+    constexpr int TM = T::TM, TN = T::TN;
+    volatile uint32_t& last_flag = *reinterpret_cast<volatile uint32_t*>(lds);
+#pragma unroll
+    for (int ni = 0; ni < TN; ++ni)
+#pragma unroll
+        for (int mi = 0; mi < TM; ++mi)
+            buf_store16_dev(ws, slot_off(at.piece, ni, mi), __builtin_bit_cast(u32x4, acc[ni][mi]));
+    wait_all_memory();
+    __syncthreads();
+    if (threadIdx.x == 0)
+        last_flag = (counter_arrive(&p.counters[at.tile]) == (uint32_t)(p.splits - 1)) ? 1u : 0u;
+    __syncthreads();
+    if (!last_flag) return false;
+    if (threadIdx.x == 0) counter_reset(&p.counters[at.tile]);
+    return true;
+}
+
+// The pieces of a split tile: each stores its partial sums, and the last to arrive adds them in K order into its
+// acc and returns true.
+template <class T>
+__device__ __forceinline__ bool op_join(const OpTileArgs& p, const OpPlace& at, char* lds, int wave, int lane,
+                                        typename T::Acc (&acc)[T::TN][T::TM]) {
+    constexpr int TM = T::TM, TN = T::TN;
+    constexpr uint32_t kSlot = T::BM * T::BN * 4;
+    const __amdgpu_buffer_rsrc_t ws = make_rsrc(p.ws + (size_t)at.tile * p.splits * (T::BM * T::BN));
+    auto slot_off = [&](int pc, int ni, int mi) {
+        return (uint32_t)pc * kSlot + (uint32_t)((((wave * TN + ni) * TM + mi) * 64 + lane) * 16);
+    };
+    if (!op_arrive<T>(p, at, lds, acc, ws, slot_off)) return false;
+    typename T::Acc sum[TN][TM];
+#pragma unroll
+    for (int ni = 0; ni < TN; ++ni)
+#pragma unroll
+        for (int mi = 0; mi < TM; ++mi) sum[ni][mi] = typename T::Acc{};
+    for (int pc = 0; pc < p.splits; ++pc) {  // in K order, its own piece from registers
+        if (pc == at.piece) {
+#pragma unroll
+            for (int ni = 0; ni < TN; ++ni)
+#pragma unroll
+                for (int mi = 0; mi < TM; ++mi) sum[ni][mi] += acc[ni][mi];
+            continue;
+        }
+        u32x4 v[TN][TM];
+#pragma unroll
+        for (int ni = 0; ni < TN; ++ni)
+#pragma unroll
+            for (int mi = 0; mi < TM; ++mi) v[ni][mi] = buf_load16_dev(ws, slot_off(pc, ni, mi));
+#pragma unroll
+        for (int ni = 0; ni < TN; ++ni)
+#pragma unroll
+            for (int mi = 0; mi < TM; ++mi) sum[ni][mi] += __builtin_bit_cast(typename T::Acc, v[ni][mi]);
+    }
+#pragma unroll
+    for (int ni = 0; ni < TN; ++ni)
+#pragma unroll
+        for (int mi = 0; mi < TM; ++mi) acc[ni][mi] = sum[ni][mi];
+    __syncthreads();  // the flag has been read: its place is free for the output
+    return true;
+}
+
+// op_join for a tile whose accumulators leave no room for two more copies: one row of 16 x 16 blocks at a time, the
+// loads of two pieces (of eight blocks a row) in flight before their adds.
+template <class T>
+__device__ __forceinline__ bool op_join_tile(const OpTileArgs& p, const OpPlace& at, char* lds, int wave, int lane,
+                                             typename T::Acc (&acc)[T::TN][T::TM]) {
+    constexpr int TM = T::TM, TN = T::TN, BATCH = 16 / TM;
+    constexpr uint32_t kSlot = T::BM * T::BN * 4;
+    const __amdgpu_buffer_rsrc_t ws = make_rsrc(p.ws + (size_t)at.tile * p.splits * (T::BM * T::BN));
+    auto slot_off = [&](int pc, int ni, int mi) {
+        return (uint32_t)pc * kSlot + (uint32_t)((((wave * TN + ni) * TM + mi) * 64 + lane) * 16);
+    };
+    if (!op_arrive<T>(p, at, lds, acc, ws, slot_off)) return false;
+#pragma unroll
+    for (int ni = 0; ni < TN; ++ni) {
+        typename T::Acc sum[TM];
+#pragma unroll
+        for (int mi = 0; mi < TM; ++mi) sum[mi] = typename T::Acc{};
+        for (int b0 = 0; b0 < p.splits; b0 += BATCH) {
+            u32x4 v[BATCH][TM];
+#pragma unroll
+            for (int u = 0; u < BATCH; ++u)
+#pragma unroll
+                for (int mi = 0; mi < TM; ++mi)
+                    v[u][mi] = buf_load16_dev(ws, sel_off(b0 + u < p.splits && b0 + u != at.piece, slot_off(b0 + u, ni, mi)));
+#pragma unroll
+            for (int u = 0; u < BATCH; ++u)
+#pragma unroll
+                for (int mi = 0; mi < TM; ++mi)
+                    sum[mi] += b0 + u == at.piece ? acc[ni][mi] : __builtin_bit_cast(typename T::Acc, v[u][mi]);
+        }
+#pragma unroll
+        for (int mi = 0; mi < TM; ++mi) acc[ni][mi] = sum[mi];
+    }
+    __syncthreads();  // the flag has been read: its place is free for the output
+    return true;
+}
+
 // ---- 256 x 256: two wave groups alternating memory and MFMA phases --------------------------------
 // Phases are separated by workgroup barriers b1, b2, ...; group 0 runs the memory phase of step t
 // before b(2 t + 1) and its MFMAs before b(2 t + 2), group 1 one barrier later, so every read of step
@@ -332,7 +434,8 @@ __device__ __forceinline__ void op_epilogue(const OpTileArgs& p, char* lds, cons
 // operand's slot of step t - 1 with step t + 4; a contiguous one's slot of unit t - 2 (of steps t - 2
 // and t - 1 for even t, t - 3 and t - 2 for odd t) with unit t + 3. Each wave ends its memory phase
 // waiting for its own copies that step t + 1 reads, and a barrier follows before any wave reads them.
-template <int MODE, bool GLU>
+// JOIN: p may be a piece of K (p.splits, at.piece, at.tile of the workspace)
+template <int MODE, bool GLU, bool JOIN = false>
 __device__ __forceinline__ void op_pp(const OpTileArgs& p, const OpPlace& at, char* lds) {
     using T = OpTile<256, 256, 2, 4, MODE>;
     constexpr int TM = T::TM, TN = T::TN;
@@ -411,62 +514,9 @@ __device__ __forceinline__ void op_pp(const OpTileArgs& p, const OpPlace& at, ch
     if (grp == 0) phase_barrier();
     wait_vmcnt<0>();  // the copies past K included
     lds_barrier();    // the rings are free for the output
+    if constexpr (JOIN)
+        if (p.splits > 1 && !op_join_tile<T>(p, at, lds, wave, lane, acc)) return;
     op_epilogue<T, MODE, GLU>(p, lds, at, wave, wm, wn, lane, acc);
-}
-
-// The pieces of a split tile: each stores its partial sums, and the last to arrive adds them in K order into its
-// acc and returns true.
-template <class T>
-__device__ __forceinline__ bool op_join(const OpTileArgs& p, const OpPlace& at, char* lds, int wave, int lane,
-                                        typename T::Acc (&acc)[T::TN][T::TM]) {
-    constexpr int TM = T::TM, TN = T::TN;
-    volatile uint32_t& last_flag = *reinterpret_cast<volatile uint32_t*>(lds);
-    constexpr uint32_t kSlot = T::BM * T::BN * 4;
-    const __amdgpu_buffer_rsrc_t ws = make_rsrc(p.ws + (size_t)at.tile * p.splits * (T::BM * T::BN));
-    auto slot_off = [&](int pc, int ni, int mi) {
-        return (uint32_t)pc * kSlot + (uint32_t)((((wave * TN + ni) * TM + mi) * 64 + lane) * 16);
-    };
-#pragma unroll
-    for (int ni = 0; ni < TN; ++ni)
-#pragma unroll
-        for (int mi = 0; mi < TM; ++mi)
-            buf_store16_dev(ws, slot_off(at.piece, ni, mi), __builtin_bit_cast(u32x4, acc[ni][mi]));
-    wait_all_memory();
-    __syncthreads();
-    if (threadIdx.x == 0)
-        last_flag = (counter_arrive(&p.counters[at.tile]) == (uint32_t)(p.splits - 1)) ? 1u : 0u;
-    __syncthreads();
-    if (!last_flag) return false;
-    if (threadIdx.x == 0) counter_reset(&p.counters[at.tile]);
-    typename T::Acc sum[TN][TM];
-#pragma unroll
-    for (int ni = 0; ni < TN; ++ni)
-#pragma unroll
-        for (int mi = 0; mi < TM; ++mi) sum[ni][mi] = typename T::Acc{};
-    for (int pc = 0; pc < p.splits; ++pc) {  // in K order, its own piece from registers
-        if (pc == at.piece) {
-#pragma unroll
-            for (int ni = 0; ni < TN; ++ni)
-#pragma unroll
-                for (int mi = 0; mi < TM; ++mi) sum[ni][mi] += acc[ni][mi];
-            continue;
-        }
-        u32x4 v[TN][TM];
-#pragma unroll
-        for (int ni = 0; ni < TN; ++ni)
-#pragma unroll
-            for (int mi = 0; mi < TM; ++mi) v[ni][mi] = buf_load16_dev(ws, slot_off(pc, ni, mi));
-#pragma unroll
-        for (int ni = 0; ni < TN; ++ni)
-#pragma unroll
-            for (int mi = 0; mi < TM; ++mi) sum[ni][mi] += __builtin_bit_cast(typename T::Acc, v[ni][mi]);
-    }
-#pragma unroll
-    for (int ni = 0; ni < TN; ++ni)
-#pragma unroll
-        for (int mi = 0; mi < TM; ++mi) acc[ni][mi] = sum[ni][mi];
-    __syncthreads();  // the flag has been read: its place is free for the output
-    return true;
 }
 
 // ---- 128 x 128 and 64 x 64, K split over idle CUs -------------------------------------------------------------

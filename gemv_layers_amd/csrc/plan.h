@@ -37,6 +37,7 @@ struct Plan {
     int64_t slots = 0;       // workgroups resident at once
     int64_t waves = 0;       // ceil(grid / slots)
     double wave_eff = 0.0;   // (grid / slots) / waves
+    int tail = 1;            // grouped rows, 256 x 256 tiles: most pieces of a tile of the last round
     int64_t ws_floats = 0;   // workspace floats the launch uses
     int64_t counters = 0;    // workspace counters the launch uses
     // A product whose last wave of 256 x 256 tiles would be at most half full is cut in two: this

@@ -1,5 +1,5 @@
 // Prints plans of the products grouped by rows: for each line "tile rows groups M N K summed pairs strided cus" or
-// "decode rows groups 0 N K 0 0 0 cus" of the input, one JSON line {"plan": ..., "counters": ..., "fits": ...}. Linked to the library.
+// "decode rows groups 0 N K 0 0 0 cus" of the input, one JSON line {"plan": ..., "counters": ..., "tail": ..., "fits": ...}. Linked to the library.
 #include <iostream>
 #include <string>
 
@@ -19,7 +19,7 @@ int main() {
         g.pairs = pairs != 0;
         g.strided = strided != 0;
         const glk::Plan p = kind == "tile" ? glk::make_group_plan(g, dev) : glk::make_f8_decode_plan(g.rows, g.N, g.K, g.groups, dev);
-        std::cout << "{\"plan\": " << glk::plan_json(p, g.M, g.N, g.K) << ", \"counters\": " << p.counters
+        std::cout << "{\"plan\": " << glk::plan_json(p, g.M, g.N, g.K) << ", \"counters\": " << p.counters << ", \"tail\": " << p.tail
                   << ", \"fits\": " << (glk::f8_decode_fits(g.rows, g.groups) ? "true" : "false") << "}\n";
     }
 }

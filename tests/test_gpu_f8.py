@@ -121,7 +121,9 @@ def reference(A, Sa, W, Sw):
 SHAPES = [(1, 1, 1), (1, 11008, 4096), (1, 1000, 11008), (2, 17, 130), (3, 2352, 9118), (8, 4096, 4096), (16, 4096, 11008), (17, 520, 1003),
           (32, 1376, 512), (33, 64, 16), (64, 4096, 11008), (64, 1000, 2000), (65, 300, 129), (100, 129, 128), (257, 256, 512), (300, 520, 328),
           (509, 2501, 1003), (777, 1024, 2049), (1000, 1000, 1000), (2000, 4001, 257), (4096, 4096, 1024), (4097, 2056, 390),
-          (640, 4352, 4096), (2048, 2048, 11008), (100, 72, 16448), (70, 64, 16385), (200, 130, 8300)]
+          (640, 4352, 4096), (2048, 2048, 11008), (100, 72, 16448), (70, 64, 16385), (200, 130, 8300),
+          (4096, 4352, 4096), (4353, 4096, 1104), (2176, 8200, 2064), (6000, 2900, 4100), (4100, 4352, 16500),
+          (8192, 4352, 4736), (4609, 11000, 4130)]
 
 
 @pytest.mark.parametrize("M,N,K", SHAPES)

@@ -153,6 +153,30 @@ def test_backward(M, N, K, offsets):
         assert none is None and torch.equal(oneB, dB)
 
 
+# few tiles of 256 x 256 past whole rounds of the CUs: those are in pieces of K, the last of them short
+@pytest.mark.parametrize("M,N,K,offsets", [(3840, 4400, 1100, even(3840, 3)), (4200, 4100, 4700, [0, 4096]), (4300, 4104, 3600, [7, 4100]),
+                                           (4096, 4352, 2184, even(4096, 4)), (4100, 4352, 16456, [0, 4100]), (4096, 4096, 4800, [0, 4100]),
+                                           (3840, 4400, 1104, even(3840, 3)), (4200, 4104, 4712, [0, 4096])])
+def test_last_round_in_pieces(M, N, K, offsets):
+    E, at = len(offsets) - 1, spans(offsets, M)
+    A, B = ints(M, M, K), ints(N, E, K, N)
+    a, b, off = bf(A, -K % 8), bf(B, -N % 8), offsets_of(offsets)
+    ref = product(A, B, at, M, N)
+    first = g.grouped_matmul(a, b, off)
+    assert g.gemm_last_plan()["bm"] == (256 if K % 8 == N % 8 == 0 else 0)
+    same(first, ref, "C")
+    # the gradient of a product with K outputs is as long
+    bt = bf(B.transpose(1, 2).contiguous(), -K % 8)
+    dA, _ = g.grouped_matmul_backward(a, torch.empty(M, N, dtype=torch.bfloat16, device="cuda"), bt, off, need_dB=False)
+    same(dA, ref, "dA")
+    # the order of the pieces changes no bit
+    x, w = torch.randn(M, K, generator=gen(1), device="cuda").bfloat16(), torch.randn(E, K, N, generator=gen(2), device="cuda").bfloat16()
+    once = g.grouped_matmul(x, w, off)
+    for _ in range(3):
+        assert torch.equal(g.grouped_matmul(x, w, off), once)
+    close(once, product(x, w, at, M, N), product(x.abs(), w.abs(), at, M, N), K, "normal")
+
+
 @pytest.mark.parametrize("pad,offset", LOOSE)
 @pytest.mark.parametrize("M,N,K,offsets", [(5, 3, 7, [0, 2, 5]), (130, 100, 90, ragged(130, 5, 1, 3, 120)),
                                            (300, 131, 70, ragged(300, 70, 2))])

@@ -24,7 +24,7 @@ def cdiv(a, b):
 
 @pytest.fixture(scope="module")
 def plans(tmp_path_factory):
-    """plans([(kind, rows, groups, M, N, K, summed, pairs, strided, cus), ...]) -> [{"plan", "counters", "fits"}, ...]"""
+    """plans([(kind, rows, groups, M, N, K, summed, pairs, strided, cus), ...]) -> [{"plan", "counters", "tail", "fits"}, ...]"""
     exe = str(tmp_path_factory.mktemp("plan") / "group_plan_check")
     subprocess.run(["g++", "-O1", "-std=c++17", "-Wall", "-Werror", f"-I{os.path.join(PKG, 'csrc')}",
                     os.path.join(HERE, "group_plan_check.cpp"), os.path.join(PKG, "libgemm_bf16.so"), f"-Wl,-rpath,{PKG}",
@@ -79,14 +79,19 @@ def test_tile_plans_hold_whatever_rows_groups_have(plans):
                 assert tiles == p["tiles"], a
             assert per * splits >= kt and per * (splits - 1) < max(kt, 1), (a, p)   # all of K, and no empty piece
             assert not pairs or per % 2 == 0, a
-        assert p["grid"] == p["tiles"] * splits, a
-        if splits > 1:
+        slots = WS_FLOATS // 65536
+        tail = got["tail"] > 1                             # 256 x 256: tiles of a last round in pieces
+        assert not tail or (bm == 256 and splits == 1 and not summed and got["tail"] <= 8 and got["tail"] ** 2 <= kt // (4 if pairs else 8)), (a, p)
+        assert p["grid"] == p["tiles"] * splits + (slots if tail else 0), a
+        if tail:
+            assert p["ws_floats"] == slots * 65536 <= WS_FLOATS and got["counters"] == slots, a
+        elif splits > 1:
             assert bm < 256 and p["ws_floats"] == p["grid"] * bm * bm <= WS_FLOATS // (1 if pairs or strided else 2) and got["counters"] == p["tiles"] <= WS_COUNTERS, (a, p)
         else:
             assert p["ws_floats"] == got["counters"] == 0, a
-        seen.add((bm, splits > 1, summed))
-    assert seen >= {(64, True, False), (64, False, False), (128, False, False), (256, False, False), (64, False, True),
-                    (256, False, True)}, seen
+        seen.add((bm, tail or splits > 1, summed))
+    assert seen >= {(64, True, False), (64, False, False), (128, False, False), (256, True, False), (256, False, False),
+                    (64, False, True), (256, False, True)}, seen
 
 
 @pytest.mark.parametrize("kt", [1, 2, 3, 5, 31, 33, 63, 95, 255, 256, 257, 511, 513, 1000])
