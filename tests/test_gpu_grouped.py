@@ -177,6 +177,27 @@ def test_last_round_in_pieces(M, N, K, offsets):
     close(once, product(x, w, at, M, N), product(x.abs(), w.abs(), at, M, N), K, "normal")
 
 
+# groups about the numbers that one pass over the offsets takes, with rows of no group before and behind
+@pytest.mark.parametrize("E", [61, 62, 63, 64, 125, 126, 127, 128, 253, 254, 255, 256, 257, 511, 1500])
+def test_many_groups(E):
+    for M, first, last, empty in ((E + 40, 3, E + 17, 0.2), (777, 0, 777, 0.0), (70, 0, 69, 0.9)):
+        N, K = 72, 40
+        offsets = ragged(M, E, E + M, first, last, empty)
+        A, B, D, at = ints(M, M, K), ints(N, E, K, N), ints(K, M, N), spans(offsets, M)
+        a, b, d, off = bf(A), bf(B), bf(D), offsets_of(offsets)
+        same(g.grouped_matmul(a, b, off), product(A, B, at, M, N), "C")
+        dA, dB = g.grouped_matmul_backward(d, a, b, off)
+        same(dA, product(D, B.transpose(1, 2), at, M, K), "dA")
+        refB = torch.zeros(E, K, N, dtype=torch.float64, device="cuda")
+        for e, r0, r1 in at:
+            if r1 > r0:
+                refB[e] = torch.mm(A[r0:r1].double().t(), D[r0:r1].double())
+        same(dB, refB, "dB")
+        W, Sa, Sw = ints(N, E, N, K), powers(1, blocks(K), M), powers(2, E, blocks(N), blocks(K))
+        ref, _ = f8_reference(A, Sa, W, Sw, at, M)
+        same(g.f8_grouped_matmul(f8(A, -K % 16), Sa, f8(W, -K % 16), Sw, off), ref, "codes")
+
+
 @pytest.mark.parametrize("pad,offset", LOOSE)
 @pytest.mark.parametrize("M,N,K,offsets", [(5, 3, 7, [0, 2, 5]), (130, 100, 90, ragged(130, 5, 1, 3, 120)),
                                            (300, 131, 70, ragged(300, 70, 2))])
