@@ -382,8 +382,10 @@ int gemm_bf16_swiglu_bwd(int64_t M, int64_t N, int64_t K, const void *dC, int64_
  * 448) with float32 scales over blocks of 128 of the summed index. Activations have a scale for each row
  * and block, weights (nn.Linear layout, N x K) one for each block of 128 outputs and 128 inputs:
  *   C[m][n] = bf16( sum_b Sa[b][m] Sw[n / 128][b] sum_{k in block b} a[m][k] w[n][k] ),
- * block b being k = 128 b .. 128 b + 127 (the last one shorter). Products and sums are float32, the two
- * scales of a block are multiplied first, and each output is rounded once (to nearest even).
+ * block b being k = 128 b .. 128 b + 127 (the last one shorter). Sums over blocks are float32, the two scales of a
+ * block are multiplied first, and each output is rounded once (to nearest even). Within a block the matrix
+ * instruction aligns products in eights and cuts what lies below 2^-13 of the largest of eight: the inner sum is
+ * off by at most 7 * 2^-13 of the sum of |a w| (the general kernel's by float32 roundings alone).
  * ------------------------------------------------------------------------------------------ */
 
 /*
@@ -422,8 +424,8 @@ int gemm_f8_quantize_weight(int64_t E, int64_t N, int64_t K, const void *W, int6
  * same result contract, tens of times slower. Bytes between K and the leading dimension may hold anything.
  * M == 0 or N == 0: nothing. K == 0: C = 0. GEMM_ERR_INVALID_ARG for negative sizes, a leading dimension that
  * is too small, a null pointer with a non-empty extent, a C that is not 2-byte or a scale that is not 4-byte
- * aligned; GEMM_ERR_UNSUPPORTED for M >= 2^24, K > 2^30, or a general kernel's C of 2^24 or more 64 x 64
- * tiles. Deterministic, enqueued without synchronising, and using the stream's workspace region like gemm_bf16.
+ * aligned; GEMM_ERR_UNSUPPORTED for M >= 2^24, K > 2^30, a general kernel's C of 2^24 or more 64 x 64 tiles, or
+ * one of more 256 x 256 tiles than a launch of 2^32 threads holds. Deterministic, enqueued without synchronising, and using the stream's workspace region like gemm_bf16.
  */
 int gemm_f8(int64_t M, int64_t N, int64_t K, const void *Aq, int64_t ldaq, const float *Sa,
             int64_t ldsa, const void *Wq, int64_t ldwq, const float *Sw, int64_t ldsw, void *C,
@@ -451,13 +453,15 @@ int gemm_f8_bf16(int64_t M, int64_t N, int64_t K, const void *A, int64_t lda, co
  * is rows offsets[e] .. offsets[e + 1] - 1, of `offsets`, E + 1 32-bit integers in device memory that are
  * read by the kernels (a router's counts need not come to the host; the call may be captured, and replayed
  * with other offsets). Groups may be empty. Rows before offsets[0] and from offsets[E] on belong to no
- * group: they are not read, and their rows of C (or dA) are written as zeros. No value of the offsets reads
+ * group: they are not read (gemm_f8_grouped_bf16 quantises them, and they reach no output), and their rows of C
+ * (or dA) are written as zeros. No value of the offsets reads
  * or writes out of range: an offset counts as the largest of itself, 0 and those before it, and as M
  * beyond M.
  * One group's weight may be anywhere: B of group e starts stride_b elements after group e - 1's (0: one
  * weight for all). Otherwise operands, arithmetic and errors are those of the products of one weight, with
  * GEMM_ERR_INVALID_ARG for negative E or strides and for offsets that are null (M > 0 and E > 0) or not
- * 4-byte aligned, and GEMM_ERR_UNSUPPORTED for M >= 2^24 or E > 65536. E == 0: C (or dA) is zero.
+ * 4-byte aligned, and GEMM_ERR_UNSUPPORTED for M >= 2^24 or E > 65536, or where the tiles that M rows in E groups
+ * may make are more than a launch of 2^32 threads holds. E == 0: C (or dA) is zero.
  * Deterministic, enqueued without synchronising, using the stream's workspace region like gemm_bf16. A
  * refused call has written nothing.
  * ------------------------------------------------------------------------------------------ */
@@ -479,7 +483,8 @@ int gemm_bf16_grouped(int64_t M, int64_t N, int64_t K, int64_t E, const void *A,
  * next one after stride_db elements, at least K * lddb where E > 1). An empty group's dB is zero; rows of no
  * group have zero dA, and neither their A nor their dC is read. A null dA or dB is not computed; then B or A
  * respectively is not read and may be null. Both are overwritten, not accumulated into. A weight that groups
- * share (stride_b 0) has the sum of their dB as its gradient.
+ * share (stride_b 0) has the sum of their dB as its gradient. A gradient alone may be summed in another order than
+ * beside the other.
  */
 int gemm_bf16_grouped_bwd(int64_t M, int64_t N, int64_t K, int64_t E, const void *dC, int64_t lddc,
                           const void *A, int64_t lda, const void *B, int64_t ldb, int64_t stride_b,
