@@ -113,7 +113,7 @@ struct F8Scales {
     int count;         // blocks
     float w[2];        // of blocks 128 i + lane and 64 more
 
-    __device__ __forceinline__ void init(const OpTileArgs& p, const OpPlace& at, int first, int blocks, int wave, int wn,
+    __device__ __forceinline__ void init(const F8TileArgs& p, const OpPlace& at, int first, int blocks, int wave, int wn,
                                          int lane) {
         const int row = wave * T::S_ROWS + lane;
         ldsa = p.ldsa;
@@ -178,7 +178,7 @@ __device__ __forceinline__ void f8_multiply(const u32x4 (&fb)[H][2], const u32x4
 // before op_pp frees its slot: step t refills the slot of unit t - 1 with unit t + 3. The scales of block b + 1
 // are issued in the first step of block b, before that step's other copies, and awaited in its second.
 __global__ void __attribute__((amdgpu_flat_work_group_size(512, 512), amdgpu_waves_per_eu(2, 2)))
-f8_pp_kernel(OpTileArgs p, GroupArgs g) {
+f8_pp_kernel(F8TileArgs p, GroupArgs g) {
     using T = F8Tile<256, 256, 4, 2>;
     extern __shared__ __attribute__((aligned(1024))) char lds[];
     OpPlace at;
@@ -294,7 +294,7 @@ __device__ __forceinline__ void f8_read_block(const char* block, int w0, int lan
 
 template <int BT>
 __global__ void __attribute__((amdgpu_flat_work_group_size(256, 256), amdgpu_waves_per_eu(2, BT == 64 ? 4 : 2)))
-f8_small_kernel(OpTileArgs p, GroupArgs g) {
+f8_small_kernel(F8TileArgs p, GroupArgs g) {
     using T = F8Small<BT>;
     extern __shared__ __attribute__((aligned(1024))) char lds[];
     OpPlace at;
@@ -366,7 +366,7 @@ f8_small_kernel(OpTileArgs p, GroupArgs g) {
     op_epilogue<T, kOpF8, false>(p, lds, at, wave, wm, wn, lane, acc);
 }
 
-hipError_t launch_f8_tile(int tile, const OpTileArgs& a, const GroupArgs& g, int grid, hipStream_t s) {
+hipError_t launch_f8_tile(int tile, const F8TileArgs& a, const GroupArgs& g, int grid, hipStream_t s) {
     if (tile == 256) {
         if (a.splits != 1) return hipErrorInvalidValue;
         f8_pp_kernel<<<grid, 512, F8Tile<256, 256, 4, 2>::LDS_BYTES, s>>>(a, g);

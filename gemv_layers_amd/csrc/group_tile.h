@@ -36,8 +36,8 @@ struct TailUnits {
 
 // Narrows p to the group and tile of workgroup `block`; false where there is none. Rows of no group are a product
 // over nothing, which writes zeros.
-template <int MODE, int BT>
-__device__ __forceinline__ bool group_tile(OpTileArgs& p, const GroupArgs& g, int block, OpPlace* at) {
+template <int MODE, int BT, class Args>
+__device__ __forceinline__ bool group_tile(Args& p, const GroupArgs& g, int block, OpPlace* at) {
     constexpr int ES = MODE == kOpF8 ? 1 : 2;
     auto uni = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
     if constexpr (MODE == kOpAtb) {

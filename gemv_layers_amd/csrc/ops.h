@@ -68,7 +68,9 @@ struct OpTileArgs {
     int splits, kt_per_split;  // pieces of K per tile, 64-byte k-steps in each (128 x 128 tiles)
     float* ws;
     uint32_t* counters;
-    int64_t ldsa, ldsb;  // kOpF8
+};
+struct F8TileArgs : OpTileArgs {
+    int64_t ldsa, ldsb;
 };
 // tile: 256, 128 or 64 rows and (weight) columns; the gated forms make half as many output columns
 hipError_t launch_op_tile(int mode, bool glu, int tile, const OpTileArgs& a, int grid, hipStream_t s);
@@ -84,7 +86,7 @@ hipError_t launch_group_pair(int tile, const OpTileArgs& a, const GroupArgs& ga,
                              const GroupArgs& gb, int grid_b, hipStream_t s);
 hipError_t configure_group_kernels();
 // kOpF8: as launch_group_tile; a.kt_per_split is even
-hipError_t launch_f8_tile(int tile, const OpTileArgs& a, const GroupArgs& g, int grid, hipStream_t s);
+hipError_t launch_f8_tile(int tile, const F8TileArgs& a, const GroupArgs& g, int grid, hipStream_t s);
 hipError_t configure_f8_kernels();
 
 // ---- 8-bit product of few tokens -------------------------------------------------------------------

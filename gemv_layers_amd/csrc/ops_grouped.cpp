@@ -136,10 +136,10 @@ glk::OpTileArgs tile_args(const Ready& r) {
     t.kt_per_split = r.p.kt_per_split;
     t.ws = r.w.ws;
     t.counters = r.w.counters;
-    t.ldsa = a.ldsa;
-    t.ldsb = a.ldsb;
     return t;
 }
+
+glk::F8TileArgs f8_tile_args(const Ready& r) { return {tile_args(r), r.a.ldsa, r.a.ldsb}; }
 
 int launch(const Ready& r, hipStream_t stream) {
     const OpArgs& a = r.a;
@@ -160,7 +160,7 @@ int launch(const Ready& r, hipStream_t stream) {
             break;
         }
         case Ready::kTiles:
-            e = r.mode == glk::kOpF8 ? glk::launch_f8_tile(r.p.bm, tile_args(r), r.g, (int)r.p.grid, stream)
+            e = r.mode == glk::kOpF8 ? glk::launch_f8_tile(r.p.bm, f8_tile_args(r), r.g, (int)r.p.grid, stream)
                                      : glk::launch_group_tile(r.mode, r.p.bm, tile_args(r), r.g, (int)r.p.grid, stream);
             break;
     }
