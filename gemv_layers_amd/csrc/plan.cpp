@@ -560,15 +560,17 @@ Plan make_group_plan(const GroupShape& g, const DeviceInfo& dev) {
     };
     const int64_t high = g.summed ? g.M : each, kt = cdiv(g.summed ? each : g.K, 32);
     // Few 256 x 256 tiles past whole rounds are in pieces of K: up to the square root of an eighth of the k-steps (a quarter
-    // for codes), from 48 steps. The grid has a workgroup for each slot of the workspace. us whole and in 2, 4 and 8
-    // pieces, 16 tiles past a round: codes 4096 x 4352 x 11008 251, 212, 187, 188; x 4096 101, 94, 85, 94; x 2048 58, 60, 56, 67;
+    // for codes), from 48 steps. The grid of a grouped product has a workgroup for each slot of the workspace. us whole
+    // and in 2, 4 and 8 pieces, 16 tiles past a round: codes 4096 x 4352 x 11008 251, 212, 187, 188; x 4096 101, 94, 85, 94; x 2048 58, 60, 56, 67;
     // bf16 436, 354, 314, 303; 169, 145, 132, 135; 91, 83, 79, 87; x 1024 52, 52, 53, 64.
     const int64_t slots = g.summed || kt < 48 ? 0 : dev.ws_floats / (256 * 256);
     while (slots > 1 && p.tail < 8 && (p.tail + 1) * (p.tail + 1) * (g.pairs ? 4 : 8) <= kt) ++p.tail;
-    int64_t rounds256 = cdiv(expect(256), cus) * 100;  // hundredths
-    if (const int64_t rest = expect(256) % cus; g.groups == 0 && rest > 0) {
-        const int64_t pieces = std::min<int64_t>({slots / rest, cus / rest, p.tail});
+    int64_t rounds256 = cdiv(expect(256), cus) * 100, extra = slots;  // hundredths; workgroups
+    if (g.groups == 0 && !g.summed) {  // (the tiles are known)
+        const int64_t rest = expect(256) % cus, pieces = rest ? std::min<int64_t>({slots / rest, cus / rest, p.tail}) : 1;
         if (pieces > 2) rounds256 -= 50 - 100 / pieces;  // (the sum takes about half a round)
+        if (pieces < 2) p.tail = 1;
+        extra = rest * (pieces - 1);
     }
     const int64_t t256 = rounds256 * (g.pairs ? 168 : 145) / 100, t128 = cdiv(expect(128), 2 * cus) * 100,
                   t64 = cdiv(expect(64), 4 * cus) * 110;
@@ -611,7 +613,7 @@ Plan make_group_plan(const GroupShape& g, const DeviceInfo& dev) {
     }
     if (bm != 256) p.tail = 1;
     if (p.tail > 1) {
-        p.grid += slots;
+        p.grid += extra;
         p.ws_floats = slots * 256 * 256;
         p.counters = slots;
     }

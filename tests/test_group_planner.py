@@ -82,7 +82,13 @@ def test_tile_plans_hold_whatever_rows_groups_have(plans):
         slots = WS_FLOATS // 65536
         tail = got["tail"] > 1                             # 256 x 256: tiles of a last round in pieces
         assert not tail or (bm == 256 and splits == 1 and not summed and got["tail"] <= 8 and got["tail"] ** 2 <= kt // (4 if pairs else 8)), (a, p)
-        assert p["grid"] == p["tiles"] * splits + (slots if tail else 0), a
+        extra = slots if tail else 0
+        if tail and groups == 0:                           # the tiles are known: as many as there are
+            rest = p["tiles"] % cus
+            pieces = min(slots // rest, cus // rest, got["tail"])
+            assert pieces > 1, (a, p)
+            extra = rest * (pieces - 1)
+        assert p["grid"] == p["tiles"] * splits + extra, a
         if tail:
             assert p["ws_floats"] == slots * 65536 <= WS_FLOATS and got["counters"] == slots, a
         elif splits > 1:
