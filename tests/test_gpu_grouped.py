@@ -411,6 +411,45 @@ def test_streams_graphs_and_repeats():
                 assert torch.equal(bits(x), bits(y))
 
 
+def test_last_round_on_two_streams_and_in_a_graph():
+    """Products whose last tiles are in pieces share a stream's workspace: two streams at once, and replays whose
+    offsets make other numbers of pieces, or none."""
+    M, N, K, E = 4096, 4352, 2184, 4
+    A, B = torch.randn(M, K, generator=gen(1), device="cuda").bfloat16(), torch.randn(E, K, N, generator=gen(2), device="cuda").bfloat16()
+    D = torch.randn(M, N, generator=gen(3), device="cuda").bfloat16()
+    x, Wq, Sw = D[:, :4096], *g.f8_quantize_weight(torch.randn(N, 4096, generator=gen(4), device="cuda").bfloat16())
+    off = offsets_of(even(M, E))
+
+    def run():
+        return [g.grouped_matmul(A, B, off), g.grouped_matmul_backward(D, A, B, off, need_dB=False)[0], g.f8_linear(x, Wq, Sw)]
+
+    kinds = [even(M, E), [0, M, M, M, M], [0, 1, 2, 3, M], [0, 300, 1500, 2900, 4000], [5, 5, 5, 5, 5], even(M, E)]
+    want = []
+    for k in kinds:
+        off.copy_(offsets_of(k))
+        want.append(run())
+    torch.cuda.synchronize()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    outs = []
+    for _ in range(2):
+        for s in (s1, s2):
+            with torch.cuda.stream(s):
+                outs.append(run())
+    torch.cuda.synchronize()
+    for o in outs:
+        assert all(torch.equal(bits(y), bits(z)) for y, z in zip(o, want[-1]))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = run()
+    for k, w in zip(kinds * 2, want * 2):
+        off.copy_(offsets_of(k))
+        fresh = run()
+        graph.replay()
+        torch.cuda.synchronize()
+        for h, f, y in zip(held, fresh, w):
+            assert torch.equal(bits(h), bits(y)) and torch.equal(bits(f), bits(y)), k
+
+
 def test_memory_belongs_to_the_stream_given():
     import ctypes
 
