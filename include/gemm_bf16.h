@@ -425,7 +425,8 @@ int gemm_f8_quantize_weight(int64_t E, int64_t N, int64_t K, const void *W, int6
  * M == 0 or N == 0: nothing. K == 0: C = 0. GEMM_ERR_INVALID_ARG for negative sizes, a leading dimension that
  * is too small, a null pointer with a non-empty extent, a C that is not 2-byte or a scale that is not 4-byte
  * aligned; GEMM_ERR_UNSUPPORTED for M >= 2^24, K > 2^30, a general kernel's C of 2^24 or more 64 x 64 tiles, or
- * one of more 256 x 256 tiles than a launch of 2^32 threads holds. Deterministic, enqueued without synchronising, and using the stream's workspace region like gemm_bf16.
+ * one of more 256 x 256 tiles than a launch of 2^32 threads holds. Deterministic, enqueued without
+ * synchronising, and using the stream's workspace region like gemm_bf16.
  */
 int gemm_f8(int64_t M, int64_t N, int64_t K, const void *Aq, int64_t ldaq, const float *Sa,
             int64_t ldsa, const void *Wq, int64_t ldwq, const float *Sw, int64_t ldsw, void *C,
