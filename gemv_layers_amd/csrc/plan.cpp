@@ -15,6 +15,7 @@
 #include <stdio.h>
 
 #include <algorithm>
+#include <cmath>
 
 #include "kernels.h"
 
@@ -539,19 +540,26 @@ Plan make_i8_decode_plan(int64_t M, int64_t N, int64_t K, const DeviceInfo& dev,
 // 1376 x 4096 189, 208, 282; 3000 in 32, 2048 x 2048 77, 67, 83.
 // Two exceptions: gradients of weights over few rows are a stream of output, which 128 x 128 tiles write faster (16
 // rows, 8 groups, 4096 x 1376 25.6, 21.5, 38); and a strided weight is read in rows of a tile's width, 256 bytes of which
-// suit a stream for few rows better than 128 (256 rows in 8 groups, 4096 x 4096 -, 47, 69; 64 in 64, 1376 x 4096 -, 83, 90).
+// suit a stream for few rows better than 128 where there is one a CU (256 rows in 8 groups, 4096 x 4096 -, 47, 69; 64 in
+// 64, 1376 x 4096 -, 83, 90; but 224 tiles, 16 in 8, 4096 x 1376 -, 17.2, 15.7).
 // Pieces of K: as many as fill the card where 16 k-steps remain to each, but no more than the square root of a
-// quarter of the steps (a sixth for bf16, and three tiles a CU), as a fixup costs like a few steps for each (codes 256 x
-// 4096 x 4096 34 whole, 21 in four; 128 x 4096 x 4096 20.8 in two, 15.5 in four; 509 x 2501 x 1003 11.0 whole, 11.7 in two; bf16 16
-// rows in 8 groups, 1376 x 4096 31 whole, 22.4 in three, 23.8 in four; 300 in 3, 1000 x 1000 10.1 whole, 9.3 in two).
+// quarter of the steps (a sixth for bf16), as a fixup costs like a few steps for each (codes 256 x 4096 x 4096 34 whole, 21
+// in four; 128 x 4096 x 4096 20.8 in two, 15.5 in four; 509 x 2501 x 1003 11.0 whole, 11.7 in two). bf16 64 x 64 tiles: one
+// workgroup a CU, or two where 20 steps remain (32 where both operands are contiguous); a third on some CUs costs more
+// than shorter pieces save (16 rows in 8 groups, 7 with rows, 1376 x 4096, 154 tiles: 25.8 whole, 21.8, 17.8, 19.8,
+// 21.4, 21.0 in two to six; 32 in 8, 768 x 8192, 96 tiles: 22.7, 20.8, 22.9 in four to six; 300 in 8, 1376 x 1024, 200
+// tiles: 9.0 whole, 10.2 in two; 300 in 3, 1000 x 1000 10.1, 9.3; dA of 128 rows in 4, 1376 x 4096, 256 tiles of 43 steps:
+// 11.8, 13.3; of 24 in 4, 2048 x 4096, 64 steps: 15.3, 14.8).
 Plan make_group_plan(const GroupShape& g, const DeviceInfo& dev) {
     Plan p;
     p.kernel = kKernTile;
     p.tile_cfg = kTileConfigCount;  // none of make_plan's
     p.bk = 32;
     p.nxcd = dev.nxcd;
-    const int64_t parts = std::max<int64_t>(1, std::min(g.groups, g.rows));  // that can have rows
-    const int64_t each = cdiv(g.rows, parts), cus = dev.cus;                 // rows of one, in the mean
+    // groups that have rows where every row falls to any of them alike, and the rows of one
+    const double miss = g.groups > 1 ? std::pow(1.0 - 1.0 / double(g.groups), double(g.rows)) : 0.0;
+    const int64_t parts = std::max<int64_t>(1, std::llround(double(g.groups) * (1.0 - miss)));
+    const int64_t each = cdiv(g.rows, parts), cus = dev.cus;
     auto expect = [&](int64_t b) {
         const int64_t rows = g.summed        ? g.groups * cdiv(g.M, b)
                              : g.groups == 0 ? cdiv(g.rows, b)
@@ -576,7 +584,7 @@ Plan make_group_plan(const GroupShape& g, const DeviceInfo& dev) {
                   t64 = cdiv(expect(64), 4 * cus) * 110;
     int bm = t128 < t64 && 4 * expect(128) >= 3 * cus && high > 16 && g.N > 64 ? 128 : 64;
     if (high > 100 && g.N > 100 && 2 * expect(256) >= cus && t256 < std::min(t128, t64) && !(g.summed && each <= 64)) bm = 256;
-    if (g.strided && each <= 32 && 4 * expect(128) >= 3 * cus) bm = 128;
+    if (g.strided && each <= 32 && expect(128) >= cus) bm = 128;
     if (g.tile) bm = g.tile;
     // a launch holds 2^32 - 1 threads
     auto fits = [&](int64_t b) {
@@ -592,10 +600,15 @@ Plan make_group_plan(const GroupShape& g, const DeviceInfo& dev) {
     p.group_m = (int)std::min<int64_t>(4, p.tiles_m);
     int64_t s = 1;
     if (bm < 256) {
-        const int64_t fill = (g.pairs ? 4 : 3) * cus / (bm == 128 ? 2 : 1);
+        const int64_t tiles = expect(bm);
+        if (bm == 64 && !g.pairs && !g.summed) {
+            s = std::max(std::min(cus / tiles, kt / 16), std::min(2 * cus / tiles, kt / (g.strided ? 20 : 32)));
+        } else {
+            s = std::min((g.pairs ? 4 : 3) * cus / (bm == 128 ? 2 : 1) / tiles, kt / 16);
+        }
         int64_t root = 1;
         while ((root + 1) * (root + 1) * (g.pairs ? 4 : 6) <= kt) ++root;
-        s = std::max<int64_t>(1, std::min<int64_t>({fill / expect(bm), kt / 16, root, 16}));
+        s = std::max<int64_t>(1, std::min<int64_t>({s, root, 16}));
         // (both gradients may share a launch)
         while (s > 1 && p.tiles * s * bm * bm > dev.ws_floats / (g.pairs || g.strided ? 1 : 2)) --s;
         if (s > 1 && p.tiles > dev.ws_counters / 2) s = 1;
