@@ -6,7 +6,7 @@
 // uneven groups leave CUs idle in the last round: 8192 rows, 4096 to 11008, as one product 558 us (1.32 PFLOP/s), dA 477,
 // dB 590; in 8 even groups 605, 524 and 677; as an uneven router left them 635, 600 and 690 (1.16, 1.23, 1.07). Beyond that they
 // are bound as op_pp is: copies, L2 to LDS, and matrix cores alike, at the power limit.
-// Few rows are a stream of weights in 64 x 64 tiles: 16 rows, 7 of 8 groups, 4096 to 1376, 79 MB, 19.7 us (4.0 TB/s).
+// Few rows are a stream of weights in 64 x 64 tiles: 16 rows, 7 of 8 groups, 4096 to 1376, 79 MB, 17.8 us (4.4 TB/s).
 // Small products are one launch and the latency of their k-steps: 600 rows in 8 groups, 328 to 520, 5.6 us; both gradients
 // of 1018 rows, 512 to 1376, 14.2 in one launch and 9.7 + 7.8 in two.
 
