@@ -532,7 +532,8 @@ def f8_linear(A, Wq, Sw, out=None, work=None, stream=None):
 
 
 # Grouped by expert: rows offsets[e] .. offsets[e + 1] - 1 belong to group e, `offsets` an int32 device tensor of
-# E + 1 values that only the kernels read. Rows of no group come out as zeros.
+# E + 1 values that only the kernels read, and that stay as they are until the call's work is done. Rows of no
+# group come out as zeros.
 
 def grouped_matmul(A, B, offsets, out=None, stream=None):
     """Each group's rows of A (M x K, bf16) times its own B[e] (E x K x N): M x N bf16."""

@@ -454,10 +454,10 @@ int gemm_f8_bf16(int64_t M, int64_t N, int64_t K, const void *A, int64_t lda, co
  * is rows offsets[e] .. offsets[e + 1] - 1, of `offsets`, E + 1 32-bit integers in device memory that are
  * read by the kernels (a router's counts need not come to the host; the call may be captured, and replayed
  * with other offsets). Groups may be empty. Rows before offsets[0] and from offsets[E] on belong to no
- * group: they are not read (gemm_f8_grouped_bf16 quantises them, and they reach no output), and their rows of C
- * (or dA) are written as zeros. No value of the offsets reads
- * or writes out of range: an offset counts as the largest of itself, 0 and those before it, and as M
- * beyond M.
+ * group: they are not read (gemm_f8_grouped_bf16 quantises them, and they reach no output), and their rows
+ * of C (or dA) are written as zeros. No value of the offsets reads or writes out of range: an offset counts
+ * as the largest of itself, 0 and those before it, and as M beyond M. They must stay as they are until the
+ * call's work on the stream is done: every workgroup reads them.
  * One group's weight may be anywhere: B of group e starts stride_b elements after group e - 1's (0: one
  * weight for all). Otherwise operands, arithmetic and errors are those of the products of one weight, with
  * GEMM_ERR_INVALID_ARG for negative E or strides and for offsets that are null (M > 0 and E > 0) or not
