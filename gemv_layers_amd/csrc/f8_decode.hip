@@ -4,19 +4,20 @@
 // As in the integer form (i8_decode.hip) the product is a stream of weight codes, from HBM to registers in operand
 // order, with no LDS and no barrier in the loop: a workgroup takes TN tiles of 16 weight rows, all rows of a row tile
 // and one of `pieces` ranges of K; its NW waves take contiguous parts of the range and keep D blocks of 128 k of
-// weights, activations and scales in flight. A block is one v_mfma_f32_16x16x128_f8f6f4 a tile (lane l: row l % 16,
-// codes 16 (l / 16) .. + 15 of each 64), whose sums are added times the two scales. The waves' sums meet in LDS and
-// the pieces' in the workspace, added in order: the same bits on every run. Rows past the group's and columns past N
-// load nothing and store nothing.
+// weights, activations and scales in flight (lane l: row l % 16, codes 16 (l / 16) .. + 15 of each 64). A block's codes are
+// widened to bf16, which holds each of them, for four v_mfma_f32_16x16x32_bf16 a tile: its sum is a float32 one, as the
+// general kernel's is, and is added times the two scales. (The 8-bit instruction, one a tile, cuts small products, as f8_tile.hip
+// says, and has twice the rate, which a stream does not need. us with it and as here, weights out of the caches: 1 x 11008
+// x 4096 12.0 and 12.1, 16 x 4096 x 11008 14.5 and 14.6, 32 x 4096 x 11008 17.2 and 16.7, 64 x 11008 x 4096 23.0 and 24.4; 512 rows in
+// 64 groups, 4096 to 1376, 79 and 82.) The waves' sums meet in LDS and the pieces' in the workspace, added in order: the
+// same bits on every run. Rows past the group's and columns past N load nothing and store nothing.
 //
 // FUSED (one row): the activations come as bf16 and every workgroup quantises the row itself, with its first weight
 // loads already in flight, into LDS, where the loop reads codes and scales.
 //
-// Bound by the weight's stream and the launch. us: 1 x 11008 x 4096 10.3 a call, where a bare read of these 45 MB takes
-// 10.4 and a copy's rate would be 7.5; 16 x 4096 x 11008 13.7 (3.3 TB/s; K is in pieces over 256 workgroups, whose sums
-// meet at the end); 64 rows in 41 of 64 groups, 4096 to 1376, 42.6 (231 MB, 5.4 TB/s).
-// The matrix instruction cuts products below 2^-13 of the largest of eight, as f8_tile.hip says: every form gives sums
-// within the same bound, and none the same bits as another.
+// Bound by the weight's stream and the launch. us: 1 x 11008 x 4096 10.7 a call, where a bare read of these 45 MB takes
+// 10.4 and a copy's rate would be 7.5; 16 x 4096 x 11008 13.1; 64 rows in 41 of 64 groups, 4096 to 1376, 43 (231 MB, 5.4
+// TB/s).
 
 #include "f8.h"
 #include "group.h"
@@ -25,18 +26,27 @@
 
 namespace glk {
 
-typedef int i32x8 __attribute__((ext_vector_type(8)));
-
 template <int MT, int TN>
 struct F8Stage {
     u32x4 w[TN][2], a[MT][2];
     float sa[MT], sw;
 };
 
-__device__ __forceinline__ f32x4 f8_block(const u32x4 (&w)[2], const u32x4 (&a)[2]) {
-    const i32x8 x = {(int)w[0][0], (int)w[0][1], (int)w[0][2], (int)w[0][3], (int)w[1][0], (int)w[1][1], (int)w[1][2], (int)w[1][3]};
-    const i32x8 y = {(int)a[0][0], (int)a[0][1], (int)a[0][2], (int)a[0][3], (int)a[1][0], (int)a[1][1], (int)a[1][2], (int)a[1][3]};
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
+// a block's codes of a lane as bf16, exactly: eight of each half h and quarter q at [2 h + q]
+__device__ __forceinline__ void f8_widen(const u32x4 (&v)[2], bf16x8 (&x)[4]) {
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        u32x4 w;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int c = (int)v[i >> 1][2 * (i & 1) + (j >> 1)];
+            const bf16x2 p = (j & 1) ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, 1.f, true)
+                                     : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, 1.f, false);
+            w[j] = __builtin_bit_cast(uint32_t, p);
+        }
+        x[i] = __builtin_bit_cast(bf16x8, w);
+    }
 }
 
 // Quantises the row p.A16 into `codes` (whole blocks, zeros past K) and `scales`.
@@ -162,15 +172,23 @@ __global__ void __launch_bounds__(64 * NW) f8_decode_kernel(F8DecodeArgs p, Grou
                     for (int mt = 0; mt < MT; ++mt) st.a[mt][h][w] &= mask;
                 }
         }
+        bf16x8 a[MT][4];
 #pragma unroll
-        for (int t = 0; t < TN; ++t)
+        for (int mt = 0; mt < MT; ++mt) f8_widen(st.a[mt], a[mt]);
+#pragma unroll
+        for (int t = 0; t < TN; ++t) {
+            bf16x8 w[4];
+            f8_widen(st.w[t], w);
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
-                const f32x4 x = f8_block(st.w[t], st.a[mt]);
+                f32x4 x = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x = mfma16(w[i], a[mt][i], x);
                 const float s = st.sa[mt] * st.sw;
 #pragma unroll
                 for (int r = 0; r < 4; ++r) acc[t][mt][r] = __builtin_fmaf(x[r], s, acc[t][mt][r]);
             }
+        }
     };
     F8Stage<MT, TN> st[D];
 #pragma unroll

@@ -8,9 +8,12 @@
 //
 // The instruction does not keep every bit of its 128 products: it aligns them in eights and cuts what lies below
 // 2^-13 of the largest of eight (measured; a test pins it), so a block's sum is off by at most 7 * 2^-13 of the sum of
-// magnitudes, and in the mean far less, cuts of either sign falling on random products. That is a choice: the exact form
-// would take the 16-bit instructions at half the rate. Against 64 bits the products' error is 0.0017 of their norm, all of
-// it the bf16 output's.
+// magnitudes, and in the mean far less, cuts of either sign falling on random products: 1.3e-5 of the norm of normal
+// products' sums, 5e-5 where magnitudes spread over 2^6, 2.4e-6 less of sums of one sign (float32 sums 1e-8 to 7e-8).
+// That is a choice: all 8-bit instructions cut alike, and the 16-bit ones, on codes widened to bf16, sum in float32 at half the rate
+// (3.9 and 2.0 PFLOP/s from registers), too little for these tiles, whose matrix cores are busy for three quarters of their time,
+// and enough for the products of few rows, which take them (f8_decode.hip). Against 64 bits the products' error is 0.0017 of
+// their norm, all of it the bf16 output's.
 //
 // 256 x 256 tiles: copies, LDS rings of 128-byte rows and the two alternating wave groups are those of op_pp in
 // ops_tile.h for 64-byte steps of two contiguous operands, of which two make a block: a pair of steps reads the
