@@ -21,15 +21,13 @@
 // in both operands), and in each step half of the wave's weights. Activations are read in a pair's first step alone, so
 // their ring needs four slots for the five of the weights, and the scales fit beside them: those of the tile's rows come
 // for each block by a copy of 4 bytes a lane, two blocks in turn, and the weight's, one number for each 128 columns that a
-// wave's columns lie within, wait in two registers of 64 blocks each. 128 x 128 and 64 x 64 tiles: below.
+// wave's columns lie within, by a scalar load. 128 x 128 and 64 x 64 tiles: below.
 // Codes past K in the last 16-byte chunk of a row are the caller's padding, which may hold NaN: cleared in both
 // operands.
 //
-// us: 4096 x 4096 x 11008 145-152 (2.5 PFLOP/s; the integer form, without FMAs, 127), 8192^3 437-450 (2.5; a library
-// product of one scale for all 2.76). What bounds it, by timing-only copies of 4096 x 4096 x 11008 at 157 that leave one
-// part out: no copies 130, no FMAs 143, no operand reads 150, no MFMAs 137, copies alone 110, MFMAs and barriers alone
-// 110 (101 on zeros: the clock). Copies, L2 to LDS at 13 TB/s on all CUs, and matrix cores take like long and share
-// issue slots; weights read during the MFMAs, in two ways, stayed within 1%.
+// us: 4096 x 4096 x 11008 142 (2.6 PFLOP/s; the integer form, without FMAs, 127), 8192^3 429 (2.56; a library product
+// of one scale for all 2.76). With the weight's scales from vector loads in the loop, and so a wait for all copies in every
+// block, 145 and 436.
 
 #include "group_tile.h"
 
@@ -106,15 +104,18 @@ __device__ __forceinline__ void dma4(const i32x4& rsrc, uint32_t lds_base, uint3
 }
 #pragma clang diagnostic pop
 
-// The scales of a tile: its rows' copied into LDS block by block, the weight's in registers.
+// The scales of a tile: its rows' copied into LDS block by block, the weight's, one for all rows of the wave, by scalar
+// loads a block ahead. (A vector load of it in the loop would be one that the compiler waits for, and as it cannot count the
+// copies, which are inline assembly, it would wait for all of those too, in every block.)
 template <class T>
 struct F8Scales {
+    typedef const __attribute__((address_space(4))) float* ScalarPtr;
     const float* sa;   // of the wave's rows to copy, block 0
-    const float* sb;   // of the weight's 128 columns, block 0
+    ScalarPtr sb;      // of the weight's 128 columns, block 0
     int64_t ldsa;
     uint32_t off;      // of the lane's row to copy
     int count;         // blocks
-    float w[2];        // of blocks 128 i + lane and 64 more
+    float next;        // of the weight, for the block that is read next
 
     __device__ __forceinline__ void init(const F8TileArgs& p, const OpPlace& at, int first, int blocks, int wave, int wn,
                                          int lane) {
@@ -125,30 +126,25 @@ struct F8Scales {
         off = sel_off(lane < T::S_ROWS && at.m0 + row < p.M, (uint32_t)row * 4u);
         // (past N: any block of the weight, whose columns are not stored)
         const int nb = min((at.n0 + wn * T::WTN) / 128, (p.N - 1) / 128);
-        sb = p.sb + nb * p.ldsb + first;
+        sb = (ScalarPtr)(uintptr_t)(p.sb + nb * p.ldsb + first);
         count = blocks;
-        load(0, lane);
-    }
-    __device__ __forceinline__ void load(int b, int lane) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) w[i] = b + 64 * i + lane < count ? sb[b + 64 * i + lane] : 0.f;
+        next = sb[0];
     }
     // block b's into place `slot` of the ring
     __device__ __forceinline__ void issue(int b, uint32_t lds, int slot, int wave) const {
         const int from = b < count ? b : 0;  // (a block past the last: any, not read)
         dma4(rsrc_words(sa + from * ldsa, kBufRecords), lds + T::S_RING + slot * T::S_BYTES + wave * 256, off);
     }
-    // the factors of the wave's rows in block b, in place `slot`: row w0 + 16 mi + (lane & 15)
+    // the factors of the wave's rows in block b, in place `slot`: row w0 + 16 mi + (lane & 15). Blocks are read in order.
     __device__ __forceinline__ void read(const char* lds, int b, int slot, int w0, int lane, float (&s)[T::TM]) {
-        const int bits = __builtin_bit_cast(int, (b & 64) ? w[1] : w[0]);
-        const float sw = __builtin_bit_cast(float, __builtin_amdgcn_readlane(bits, b & 63));
+        const float sw = next;
+        next = sb[max(min(b + 1, count - 1), 0)];
 #pragma unroll
         for (int mi = 0; mi < T::TM; ++mi) {
             const int r = w0 + 16 * mi;
             s[mi] = *reinterpret_cast<const float*>(lds + T::S_RING + slot * T::S_BYTES + (r / T::S_ROWS) * 256 +
                                                     (r % T::S_ROWS + (lane & 15)) * 4) * sw;
         }
-        if ((b & 127) == 127) load(b + 1, lane);
     }
 };
 
