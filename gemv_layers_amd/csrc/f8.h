@@ -77,6 +77,23 @@ __device__ __forceinline__ uint32_t row_max(uint32_t v) {
     return v;
 }
 
+// A scale as m 2^(e - 127), e from 0 to 254: its exponent field, and 1 <= |m| < 2 for a normal one (zeros, infinities and
+// NaN are m themselves). The product of two scales may be outside float32's range, or among its subnormal numbers, where an
+// output is inside: a block's sum is taken times the powers of two first, which is exact, and then times m m', below 4.
+// Where the product of the scales is a normal number the result is the sum times that, bit for bit.
+struct F8Factor {
+    float m;
+    int e;
+};
+__device__ __forceinline__ F8Factor f8_factor(float s) {
+    const int e = min(__builtin_amdgcn_ubfe(__builtin_bit_cast(uint32_t, s), 23, 8), 254u);
+    return {__builtin_ldexpf(s, 127 - e), e};
+}
+// whether `product`, of scales a and w, is zero, subnormal or infinite though neither of them is zero
+__device__ __forceinline__ bool f8_far_product(float a, float w, float product) {
+    return __builtin_amdgcn_classf(product, 0x2F4) && a != 0.f && w != 0.f;
+}
+
 // the value of a code
 __device__ __forceinline__ float f8_value(uint8_t code) { return __builtin_amdgcn_cvt_f32_fp8((int)code, 0); }
 

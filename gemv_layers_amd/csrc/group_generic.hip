@@ -85,12 +85,12 @@ __global__ void __launch_bounds__(256) group_generic_kernel(OpArgs p, GroupArgs 
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int64_t m = m0 + ty * 4 + i;
-                const float s = m < M ? p.sa[kb * p.ldsa + first + m] : 0.f;
+                const F8Factor a = f8_factor(m < M ? p.sa[kb * p.ldsa + first + m] : 0.f);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const int64_t n = n0 + tx * 4 + j;
-                    const float w = n < p.N ? p.sb[group * g.stride_sb + n / 128 * p.ldsb + kb] : 0.f;
-                    sum[i][j] = __builtin_fmaf(acc[i][j], s * w, sum[i][j]);
+                    const F8Factor w = f8_factor(n < p.N ? p.sb[group * g.stride_sb + n / 128 * p.ldsb + kb] : 0.f);
+                    sum[i][j] = __builtin_fmaf(__builtin_ldexpf(acc[i][j], a.e + w.e - 254), a.m * w.m, sum[i][j]);
                     acc[i][j] = 0.f;
                 }
             }
