@@ -2,6 +2,7 @@
 #pragma once
 
 #include "group.h"
+#include "k_piece.h"
 #include "ops_tile.h"
 
 namespace glk {
@@ -76,11 +77,10 @@ __device__ __forceinline__ bool group_tile(Args& p, const GroupArgs& g, int bloc
             p.sa += s.first;
             p.sb += max(s.group, 0) * g.stride_sb;
         }
-        if (BT == 256 && tail.pieces > 1) {  // whole 128-byte lines of a contiguous operand, none past the end
-            constexpr int LINE = 128 / ES;
-            const int per = (p.K + LINE - 1) / LINE, share = (per + tail.pieces - 1) / tail.pieces * LINE;
-            const int k0 = uni(min(tail.piece * share, p.K) / LINE * LINE);
-            p.K = uni(max(min(p.K - k0, share), 0));
+        if (BT == 256 && tail.pieces > 1) {  // whole 128-byte lines of a contiguous operand
+            const KPiece piece = k_piece(p.K, 128 / ES, tail.pieces, tail.piece);
+            const int k0 = uni(piece.first);
+            p.K = uni(piece.count);
             if (p.K > 0) {
                 p.A = static_cast<const char*>(p.A) + (int64_t)k0 * ES;
                 p.B = static_cast<const char*>(p.B) + (MODE == kOpAb ? (int64_t)k0 * p.ldb : (int64_t)k0) * ES;
