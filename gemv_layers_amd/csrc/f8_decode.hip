@@ -82,7 +82,7 @@ __global__ void __launch_bounds__(64 * NW) f8_decode_kernel(F8DecodeArgs p, Grou
     constexpr int NJ = TN * MT;  // 16 x 16 blocks of sums
     extern __shared__ __attribute__((aligned(16))) char lds[];
     GroupSpan span;
-    if (!find_span(g, 16 * MT, p.strips * p.pieces, EvenUnits{(int)blockIdx.x, 1}, &span)) return;
+    if (!find_span(g, 16 * MT, p.strips * p.pieces, EvenUnits{(int)blockIdx.x, p.nxcd}, &span)) return;
     const int tid = threadIdx.x, lane = tid & 63;
     auto uni = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
     const int wave = uni(tid >> 6);

@@ -121,6 +121,7 @@ struct F8DecodeArgs {
     int lda, ldw, ldc;
     int strips;           // of tn 16-row weight tiles
     int pieces;           // of K, one workgroup each
+    int nxcd;             // XCDs the hardware deals workgroups over (1 = no remap)
     float* ws;            // pieces > 1: row tiles * strips * pieces * tn * mt * 256
     uint32_t* counters;   // one per row tile and strip, zero between launches
     int64_t ldsa, ldsb;

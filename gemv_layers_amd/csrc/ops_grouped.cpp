@@ -155,7 +155,7 @@ int launch(const Ready& r, hipStream_t stream) {
             const glk::F8DecodeArgs t{r.fused ? nullptr : static_cast<const uint8_t*>(a.A),
                                       r.fused ? static_cast<const uint16_t*>(a.A) : nullptr,
                                       static_cast<const uint8_t*>(a.B), a.C, a.sa, a.sb, (int)a.N, (int)a.K, (int)a.lda,
-                                      (int)a.ldb, (int)a.ldc, r.p.strips, r.p.splits, r.w.ws, r.w.counters, a.ldsa, a.ldsb};
+                                      (int)a.ldb, (int)a.ldc, r.p.strips, r.p.splits, r.p.nxcd, r.w.ws, r.w.counters, a.ldsa, a.ldsb};
             e = glk::launch_f8_decode(r.p.mtiles, r.p.strip / 16, t, r.g, (int)r.p.grid, stream);
             break;
         }

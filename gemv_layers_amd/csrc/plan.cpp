@@ -649,6 +649,11 @@ Plan make_group_plan(const GroupShape& g, const DeviceInfo& dev) {
 Plan make_f8_decode_plan(int64_t rows, int64_t N, int64_t K, int64_t groups, const DeviceInfo& dev) {
     Plan p;
     p.kernel = kKernF8Decode;
+    // The row tiles of one strip and piece, neighbours in the order of units, go to one XCD and share its L2: a group of more
+    // than 16 rows reads its weight once for each XCD else (us with and without: 128 rows all of one of 8 groups, 4096 x
+    // 4096 25.2 and 27.3, of two 29.8 and 32.2; 64 of two 24.8 and 26.1; 64 in 41 of 64, 1376 x 4096 46.2 and 46.2). A plain
+    // product is one row tile (1 x 11008 x 4096 10.6 and 10.5).
+    p.nxcd = groups > 0 ? dev.nxcd : 1;
     const int64_t parts = std::max<int64_t>(1, std::min(groups, rows));  // that can have rows
     const int64_t each = cdiv(rows, parts);
     p.mtiles = each <= 16 ? 1 : each <= 32 ? 2 : 4;
