@@ -91,7 +91,7 @@ int prepare(int mode, const OpArgs& a, const GroupArgs& g, bool fused, hipStream
     const int64_t groups = g.offsets ? g.groups : 0;
     const bool matrix = fused || matrix_ok(mode, a, g);
     r->fused = fused;
-    if (mode == glk::kOpF8 && matrix && glk::f8_decode_fits(g.rows, groups)) {  // the weight-streaming kernel
+    if (mode == glk::kOpF8 && matrix && glk::f8_decode_pays(g.rows, groups)) {  // the weight-streaming kernel
         r->p = glk::make_f8_decode_plan(g.rows, a.N, a.K, groups, *dev);
         if (r->p.grid <= glk::kMostThreads / r->p.threads) {
             r->route = Ready::kDecode;

@@ -686,11 +686,18 @@ Plan make_f8_decode_plan(int64_t rows, int64_t N, int64_t K, int64_t groups, con
     return p;
 }
 
-// Whether the weight-streaming kernel takes the product: a plain one of at most 64 rows (us, streaming against
+// Whether the weight-streaming kernel is made for the product: a plain one of at most 64 rows (us, streaming against
 // tiles: 64 x 11008 x 4096 23.0 and 35.3, 64 x 4096 x 11008 22.3 and 28.1, 64 x 512 x 1024 6.5 and 8.6), a grouped one of
-// at most 16 rows a group in the mean (512 rows in 64 groups of 1376 x 4096 79.9 and 101.8; 32 a group: 256 rows in 8
-// groups of 4096 x 4096 48.9 and 49.0, 2000 in 64 of 2048 x 2048 89.1 and 80.8).
+// at most 16 rows a group in the mean.
 bool f8_decode_fits(int64_t rows, int64_t groups) { return groups == 0 ? rows <= 64 : rows <= 16 * groups; }
+
+// Whether it takes the product from the tiles. The host knows the rows a group in the mean and not how a router deals them,
+// and the kernel reads the weight of a group once for every 16 of its rows, the tiles once for every 64. us, streaming against tiles,
+// rows over nearly all groups, over a quarter of them and all in one: 64 groups, 4096 to 1376, 1 row a group 46 and 56, 22
+// and 22, 12 and 19; 2 62 and 81, 23 and 22, 18 and 20; 4 64 and 89, 32 and 23, 24 and 21; 8 78 and 85, 46 and 24, 38 and 23; 16 98 and 97, 75
+// and 27, 69 and 26. 8 groups, 4096 x 4096, 4 a group 26 and 25, 15 and 16, 12 and 15; 8 26 and 25, 25 and 16, 16 and 15; 16 34 and 26, 30 and 17, 25
+// and 16.
+bool f8_decode_pays(int64_t rows, int64_t groups) { return f8_decode_fits(rows, groups) && (groups == 0 || rows <= 4 * groups); }
 
 static const char* kernel_name(int k) {
     switch (k) {

@@ -112,8 +112,9 @@ Plan make_group_plan(const GroupShape& g, const DeviceInfo& dev);
 // The 8-bit floating-point product of few rows (`groups` of them, 0 for a plain product of at most 64): row tiles
 // of mtiles * 16 rows times strips of `strip` weight rows times K pieces (splits), one workgroup of `threads` each.
 Plan make_f8_decode_plan(int64_t rows, int64_t N, int64_t K, int64_t groups, const DeviceInfo& dev);
-// whether that plan beats the tiles (rows may be any number)
+// whether that plan is made for the product, and whether it takes it from the tiles (rows may be any number)
 bool f8_decode_fits(int64_t rows, int64_t groups);
+bool f8_decode_pays(int64_t rows, int64_t groups);
 
 std::string plan_json(const Plan& p, int64_t M, int64_t N, int64_t K);
 

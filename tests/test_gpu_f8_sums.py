@@ -29,7 +29,7 @@ def finite(seed, *shape):
 
 # plain products and groups of few rows, in all sizes of row and weight tiles, whole and in pieces of K
 @pytest.mark.parametrize("M,E,N,K", [(1, 0, 120, 128), (1, 0, 5504, 300), (16, 0, 120, 4096), (16, 0, 9000, 128), (17, 0, 120, 128), (33, 0, 120, 1000),
-                                     (33, 0, 4096, 4096), (64, 0, 5504, 4096), (64, 8, 120, 128), (100, 50, 1376, 300), (300, 20, 120, 128)])
+                                     (33, 0, 4096, 4096), (64, 0, 5504, 4096), (32, 8, 120, 128), (100, 50, 1376, 300), (80, 20, 120, 128)])
 def test_few_rows_sum_in_float32(M, E, N, K):
     """2^16 at one k, -2^16 at another and a product down to 2^-17 of them at a third, in one block: the third is the
     output, bit for bit, as float32 holds 2^16 + 2^-1. And random codes within the bound of float32 sums."""
@@ -72,7 +72,7 @@ LARGE, SMALL = [256.0, 288.0, 320.0, 384.0, 448.0], [m * 2.0**-8 for m in (-3, -
 
 # each kernel: one row, few rows, tiles of 64, 128 and 256, the general one; plain and grouped
 @pytest.mark.parametrize("M,E,N,bm", [(1, 0, 300, 0), (40, 0, 300, 0), (70, 0, 300, 64), (1024, 0, 4096, 128), (8192, 0, 2048, 256),
-                                      (30, 4, 300, 0), (300, 3, 264, 64), (7000, 2, 2000, 256)])
+                                      (16, 4, 300, 0), (300, 3, 264, 64), (7000, 2, 2000, 256)])
 @pytest.mark.parametrize("values,sa,sw", [(LARGE, (-126, -125), (-23, -21)),   # products of scales below 2^-126
                                           (LARGE, (-147, -140), (0, 3)),       # subnormal scales
                                           (SMALL, (105, 110), (20, 21)),       # above 2^128
@@ -126,7 +126,7 @@ def test_zeros_beside_scales_of_any_size():
 
 # tiles whose K is in pieces: of 64 and 128 rows, of 256 past whole rounds, of a group's few rows
 @pytest.mark.parametrize("M,E,N,K,bm", [(200, 0, 130, 8300, 64), (1024, 0, 4096, 4130, 128), (4096, 0, 4352, 4130, 256), (300, 3, 264, 4130, 64),
-                                        (3900, 1, 4352, 4130, 256), (40, 0, 300, 4130, 0), (30, 4, 300, 4130, 0)])
+                                        (3900, 1, 4352, 4130, 256), (40, 0, 300, 4130, 0), (16, 4, 300, 4130, 0)])
 @pytest.mark.parametrize("values,sa,sw", [([256.0, 384.0], (-126, -125), (-23, -21)), ([2.0**-9, 2.0**-8], (108, 109), (21, 21))])
 def test_scales_of_any_size_in_pieces(M, E, N, K, bm, values, sa, sw):
     """As above, every third row with scales about 1, and every seventh of zeros with a zero scale. (Products are 2^14 or 2^-18
@@ -153,3 +153,16 @@ def test_scales_of_any_size_in_pieces(M, E, N, K, bm, values, sa, sw):
     again = run()
     torch.cuda.synchronize()
     assert torch.equal(other, C) and torch.equal(again, C)
+
+
+@pytest.mark.parametrize("M,E,kernel", [(32, 8, "f8_decode"), (33, 8, "tile"), (64, 64, "f8_decode"), (512, 32, "tile")])
+@pytest.mark.parametrize("hit", [1, 3])
+def test_routers_of_few_groups(M, E, kernel, hit):
+    """All rows in one group or three of many."""
+    N, K, cuts = 264, 300, sorted([M // 5, M // 3][: hit - 1])
+    offsets = [0] * (E - hit) + [0, *cuts, M]
+    A, W = codes_of([-2.0, -1.0, 0.0, 1.0, 2.0], M, M, K), codes_of([-2.0, -1.0, 0.0, 1.0, 2.0], N, E, N, K)
+    Sa, Sw = torch.ones(blocks(K), M, device="cuda"), torch.ones(E, blocks(N), blocks(K), device="cuda")
+    ref, _ = f8_reference(A, Sa, W, Sw, spans(offsets, M), M)
+    C = g.f8_grouped_matmul(f8(A, -K % 16), Sa, f8(W, -K % 16), Sw, offsets_of(offsets))
+    assert g.gemm_last_plan()["kernel"] == kernel and torch.equal(C, ref.float().bfloat16())
