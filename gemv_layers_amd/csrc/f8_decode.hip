@@ -7,17 +7,20 @@
 // weights, activations and scales in flight (lane l: row l % 16, codes 16 (l / 16) .. + 15 of each 64). A block's codes are
 // widened to bf16, which holds each of them, for four v_mfma_f32_16x16x32_bf16 a tile: its sum is a float32 one, as the
 // general kernel's is, and is added times the two scales. (The 8-bit instruction, one a tile, cuts small products, as f8_tile.hip
-// says, and has twice the rate, which a stream does not need. us with it and as here, weights out of the caches: 1 x 11008
-// x 4096 12.0 and 12.1, 16 x 4096 x 11008 14.5 and 14.6, 32 x 4096 x 11008 17.2 and 16.7, 64 x 11008 x 4096 23.0 and 24.4; 512 rows in
-// 64 groups, 4096 to 1376, 79 and 82.) The waves' sums meet in LDS and the pieces' in the workspace, added in order: the
-// same bits on every run. Rows past the group's and columns past N load nothing and store nothing.
+// says, and has twice the rate, which a stream does not need: us with it and as here, 1 x 11008 x 4096 12.0 and 12.1, 16 x
+// 4096 x 11008 14.5 and 14.6, 32 x 4096 x 11008 17.2 and 16.7, 64 x 11008 x 4096 23.0 and 24.4.) The waves' sums meet in LDS and
+// the pieces' in the workspace, added in order: the same bits on every run. Rows past the group's and columns past N load nothing
+// and store nothing.
 //
 // FUSED (one row): the activations come as bf16 and every workgroup quantises the row itself, with its first weight
 // loads already in flight, into LDS, where the loop reads codes and scales.
 //
-// Bound by the weight's stream and the launch. us: 1 x 11008 x 4096 10.7 a call, where a bare read of these 45 MB takes
-// 10.4 and a copy's rate would be 7.5; 16 x 4096 x 11008 13.1; 64 rows in 41 of 64 groups, 4096 to 1376, 43 (231 MB, 5.4
-// TB/s).
+// Bound by the weight's stream and the launch. Here and below and in the planner, us a call with weights that come from HBM; in
+// brackets with two 45 MB weights in turn, which the 256 MB cache behind the L2s holds: 1 x 11008 x 4096 11.9 (10.5, as a
+// bare read of them), 16 x 4096 x 11008 14.4 (13.1), where 256 workgroups, one a CU, of 16 columns over all of K read as many
+// bytes of activations through the caches as of weights; 64 x 11008 x 4096 24.6 (21.4) and 64 x 4096 x 11008 24.0 (21.0), 16 products
+// of 16 x 16 for each 8 KB of weights and 8 of activations in 172 and 256 workgroups; 64 rows in 41 of 64 groups, 4096 to
+// 1376, 42.6 (231 MB, 5.4 TB/s). At a copy's 6.0 TB/s 45 MB take 7.5.
 
 #include "f8.h"
 #include "group.h"
@@ -297,8 +300,8 @@ __global__ void __launch_bounds__(64 * NW) f8_decode_kernel(F8DecodeArgs p, Grou
 static constexpr int kWaves = 4;
 
 // Blocks of 128 k in flight per wave: two, and three where a wave has 16 or more and its row and weight tiles are few
-// (us with two and three: 41 of 64 groups of 1376 x 4096, 8 blocks a wave, 46.9 and 50.0, 1 x 11008 x 4096 12.0 and 12.6; 16 x
-// 4096 x 11008, 21 blocks, 15.2 and 14.5; four are as three, five slower).
+// (us with two and three: 41 of 64 groups of 1376 x 4096, 8 blocks a wave, 46.4 and 49.4, 1 x 11008 x 4096, 8 blocks, 11.9 and 12.6; 16 x
+// 4096 x 11008, 21 blocks, 15.8 and 14.5, 1 x 4096 x 11008 15.0 and 12.8; four were as three, five slower).
 static bool deep(const F8DecodeArgs& a, int mt, int tn) { return mt * tn < 8 && a.K / 128 >= 16 * kWaves * a.pieces; }
 
 // the kernel of a shape that the planner makes, and its LDS bytes, or null

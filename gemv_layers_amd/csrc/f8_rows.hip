@@ -7,8 +7,9 @@
 // block by block, as the products read them (16 rows are 64 neighbouring bytes).
 // Weights: a workgroup takes a 128 x 128 block, which stays in its registers between the maximum and the codes.
 //
-// Bound by HBM from a few MB on: 8192 x 4096 20.3 us (5.0 TB/s), 4096 x 11008 24.8 (5.5), 4096 x 4096 11.2-11.6 (4.4), where
-// a copy of 1 GiB reaches 5.1 to 6.1; 16 x 11008 2.4 to 3.0, the launch.
+// Bound by HBM from a few MB on, where a copy of 1 GiB reaches 5.1 to 6.1 TB/s: activations 8192 x 4096 19.2 us (5.3 TB/s),
+// 4096 x 11008 25-29 (4.6-5.5), 4096 x 4096 11.6 (4.4); weights 4096 x 11008 25.1 (5.4), 11008 x 4096 26.6 (5.1), 4096 x 4096
+// 11.9 (4.2), 8 of 11008 x 4096 205 (5.3). 16 x 11008 activations 2.4 to 3.0, the launch.
 
 #include "common.h"
 #include "f8.h"

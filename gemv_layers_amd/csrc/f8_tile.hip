@@ -10,10 +10,10 @@
 // 2^-13 of the largest of eight (measured; a test pins it), so a block's sum is off by at most 7 * 2^-13 of the sum of
 // magnitudes, and in the mean far less, cuts of either sign falling on random products: 1.3e-5 of the norm of normal
 // products' sums, 5e-5 where magnitudes spread over 2^6, 2.4e-6 less of sums of one sign (float32 sums 1e-8 to 7e-8).
-// That is a choice: all 8-bit instructions cut alike, and the 16-bit ones, on codes widened to bf16, sum in float32 at half the rate
-// (3.9 and 2.0 PFLOP/s from registers), too little for these tiles, whose matrix cores are busy for three quarters of their time,
-// and enough for the products of few rows, which take them (f8_decode.hip). Against 64 bits the products' error is 0.0017 of
-// their norm, all of it the bf16 output's.
+// That is a choice: all 8-bit instructions cut alike, and the 16-bit ones, on codes widened to bf16, sum in float32 at half
+// the rate (3.9 and 2.0 PFLOP/s from registers): 4096 x 4096 x 11008 would take 184 us for its MFMAs alone, and takes 147 so.
+// Products of few rows, which wait for their weights, have them (f8_decode.hip). Against 64 bits the products' error is
+// 0.0017 of their norm, all of it the bf16 output's.
 //
 // 256 x 256 tiles: copies, LDS rings of 128-byte rows and the two alternating wave groups are those of op_pp in
 // ops_tile.h for 64-byte steps of two contiguous operands, of which two make a block: a pair of steps reads the
@@ -25,9 +25,11 @@
 // Codes past K in the last 16-byte chunk of a row are the caller's padding, which may hold NaN: cleared in both
 // operands.
 //
-// us: 4096 x 4096 x 11008 142 (2.6 PFLOP/s; the integer form, without FMAs, 127), 8192^3 429 (2.56; a library product
-// of one scale for all 2.76). With the weight's scales from vector loads in the loop, and so a wait for all copies in every
-// block, 145 and 436.
+// us: 4096 x 4096 x 11008 146-150 (2.5 PFLOP/s; the integer form, without FMAs, 127), 8192^3 442 (2.5; a library product
+// of one scale for all 2.76). What bounds it, by timing-only copies of the first at 147 that leave one part out: no copies 99,
+// no MFMAs 96, no FMAs 123; copies alone 105, MFMAs and FMAs 113, MFMAs and barriers 84. Copies, L2 to LDS at 13 TB/s on
+// all CUs, and products with their FMAs take like long and share issue slots: MFMAs are busy 0.60 of the time. (With the
+// weight's scales from vector loads in the loop, and so a wait for all copies in every block, 3 us more.)
 
 #include "f8.h"
 #include "group_tile.h"

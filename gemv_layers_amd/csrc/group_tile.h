@@ -7,8 +7,9 @@
 
 namespace glk {
 
-// 256 x 256 tiles, one a CU: the tiles of whole rounds, then those of a last round that fills at most half of the
-// CUs, each in up to g.tail pieces of K as far as CUs and slots of the workspace go. The host cannot tell how many tiles
+// 256 x 256 tiles, one a CU: the tiles of whole rounds, then those of a last round, where there are at least two slots of the
+// workspace and two CUs for each, in up to g.tail pieces of K as far as both go. 32 MiB are 128 slots of 256 KB: of 256 CUs a
+// last round of at most 64 tiles, a quarter, is cut, and fills at most half of them. The host cannot tell how many tiles
 // the groups make. 8192 rows in 8 groups, 4096 to 11008: 1548 tiles, 12 past six rounds, 666 us whole and 640 in pieces;
 // the gradient of its rows, 576 tiles, 64 past two rounds, 680 and 605.
 struct TailUnits {

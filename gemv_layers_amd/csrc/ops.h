@@ -39,8 +39,8 @@ struct GroupArgs {
     int64_t stride_b;        // elements from one group's B to the next's (kOpAb, kOpAbt, kOpF8)
     int64_t stride_c;        // and from one's C (kOpAtb)
     int64_t stride_sb;       // and from one's scales (kOpF8)
-    // 256 x 256 tiles: the CUs, and the most pieces of K and slots of the workspace for the tiles of a last round that
-    // leaves half of them idle
+    // 256 x 256 tiles: the CUs, and the most pieces of K and slots of the workspace for the tiles of a last round, which are
+    // cut where both have two for each
     int cus = 1, tail = 1, slots = 0;
 };
 

@@ -636,16 +636,17 @@ Plan make_group_plan(const GroupShape& g, const DeviceInfo& dev) {
 }
 
 // The 8-bit floating-point product of few rows streams the weight once for each row tile, and as in the integer
-// form a workgroup's activations cost like as many weight bytes. us a call, weights out of the caches:
-// * tn: one weight tile up to two a CU (8 x 4096 x 4096 7.0, 8.6 with two), then four (16 x 11008 x 4096 14.5 and 15.8
-//   with one); up to 4 rows a group one (1 x 11008 x 4096 12.6, 14.4 with two) until there are eight a CU, then two (41
-//   of 64 groups of 1376 x 4096: 49.4, 52.6 with one, 52.5 with four). Above 16 rows one, two or four as the weight
-//   outgrows the sum of K pieces (64 x 1000 x 2000 8.2 with one, 48 x 2048 x 8192 12.5 with two, 64 x 11008 x 4096 23.0
-//   with four and 28.1 with two).
+// form a workgroup's activations cost like as many weight bytes. us a call, weights from HBM:
+// * tn: one weight tile up to two a CU (8 x 4096 x 4096 7.6, 8.7 with two), then four (16 x 11008 x 4096 14.7 and 15.4
+//   with one); up to 4 rows a group one (1 x 11008 x 4096 11.9, 13.3 with two) until there are eight a CU, then two (41
+//   of 64 groups of 1376 x 4096: 46.4, 48.6 with one, 50.8 with four). Above 16 rows one, two or four as the weight
+//   outgrows the sum of K pieces (64 x 1000 x 2000 7.6, 8.5 with two, 11.2 with four; 48 x 2048 x 8192 12.7 with two, 14.2 with
+//   one, 17.4 with four; 64 x 11008 x 4096 24.6 with four and 29.7 with two).
 // * pieces: as far as the strips leave CUs idle and 10 blocks of 128 remain to each, 4 above 16 rows (16 x 1000 x 4096,
-//   32 blocks: 7.0 in two, 6.5 in three; 4 x 2048 x 2048, 16 blocks: 5.6 whole, 6.2 in two; 64 x 1000 x 2000, 16: 9.7 whole,
-//   8.2 in four).
-// Four waves: eight were 0.4 to 3 us slower, or at best 3% faster (64 x 4096 x 11008 21.6 and 22.3).
+//   32 blocks: 6.5 in two, 6.3 in three; 4 x 2048 x 2048, 16 blocks: 4.7 whole, 5.5 in two; 64 x 1000 x 2000, 16: 8.2 whole,
+//   7.6 in four). More than one workgroup a CU costs more than the CUs that it fills (172 strips: 64 x 11008 x 4096 24.6 whole,
+//   34.5 in two, 38.3 in three; 32 x 11008 x 4096 17.1, 20.0, 21.3; 16 x 11008 x 4096 14.7, 17.3, 18.4).
+// Four waves: eight were 0.4 to 3 us slower, or at best 3% faster.
 Plan make_f8_decode_plan(int64_t rows, int64_t N, int64_t K, int64_t groups, const DeviceInfo& dev) {
     Plan p;
     p.kernel = kKernF8Decode;
@@ -687,7 +688,7 @@ Plan make_f8_decode_plan(int64_t rows, int64_t N, int64_t K, int64_t groups, con
 }
 
 // Whether the weight-streaming kernel is made for the product: a plain one of at most 64 rows (us, streaming against
-// tiles: 64 x 11008 x 4096 23.0 and 35.3, 64 x 4096 x 11008 22.3 and 28.1, 64 x 512 x 1024 6.5 and 8.6), a grouped one of
+// tiles: 64 x 11008 x 4096 24.6 and 35.3, 64 x 4096 x 11008 24.0 and 28.1, 64 x 512 x 1024 6.5 and 8.6), a grouped one of
 // at most 16 rows a group in the mean.
 bool f8_decode_fits(int64_t rows, int64_t groups) { return groups == 0 ? rows <= 64 : rows <= 16 * groups; }
 
