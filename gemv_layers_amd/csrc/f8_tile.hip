@@ -182,10 +182,12 @@ struct F8Scales {
 // Products of two scales that are no normal numbers, though neither scale is zero, spoil the sums of the tile that has them.
 // It is multiplied again, FAR, with the scales' powers of two applied to the sums first, by the matrix instruction. That
 // is found from the sums: terms of a product below 2^-126 are below 2^-100 a block, so that sums of 2^-60 and more are right; and
-// a product that is infinite makes all sums of its row infinite or NaN. Only where a sum is neither are the tile's scales
-// looked through, in a few us. us as here, without, and with the powers of two in every block: 4096 x 4096 x 11008 147, 145, 158,
-// 8192^3 442, 435, 478, 509 x 2501 x 1003 7.7, 7.4, 7.8 (the second run's code costs that, not the look at the sums);
-// with a test of every block's products and branches 4096 x 4096 x 11008 180.
+// a product that is infinite makes all sums of its row infinite or NaN. Only where a sum is neither, as in a row of zeros,
+// are the tile's scales looked through, all of them in flight by eights (us without and with such a row in every tile: 4096
+// x 4096 x 11008 152 and 154, 8192^3 428 and 442, 509 x 2501 x 1003 7.7 and 9.3). us as here, without a second run, and with the
+// powers of two in every block: 4096 x 4096 x 11008 147, 145, 158, 8192^3 442, 435, 478, 509 x 2501 x 1003 7.7, 7.4, 7.8 (the
+// second run's code costs that, not the look at the sums); with a test of every block's products and branches 4096 x 4096 x
+// 11008 180.
 // Whether the sums of a wave say so. Rows past M do not count, and columns past N, which nobody stores, are set to NaN.
 template <class T>
 __device__ __forceinline__ bool f8_suspect(const F8TileArgs& p, const OpPlace& at, int wm, int wn, int lane,
@@ -234,14 +236,28 @@ __device__ __forceinline__ bool f8_any(bool yes, char* lds, int wave, int lane, 
 template <class T>
 __device__ __forceinline__ bool f8_far_scales(const F8TileArgs& p, const OpPlace& at, int first, int blocks, char* lds,
                                               int wave, int lane) {
+    constexpr int PARTS = 64 * T::NW / T::BM, U = 8;  // a thread takes one row and every PARTS-th block, U loads in flight
+    constexpr int NB = (T::BN + 127) / 128;
+    const int row = (int)threadIdx.x % T::BM, part = (int)threadIdx.x / T::BM, nb = at.n0 / 128;
     bool far = false;
-    const int rows = min(p.M - at.m0, T::BM), n = rows * blocks;
-    for (int nb = at.n0 / 128; nb <= (min(at.n0 + T::BN, p.N) - 1) / 128; ++nb)
-        for (int i = threadIdx.x; i < n; i += 64 * T::NW) {
-            const int b = first + i / rows;
-            const float a = p.sa[b * p.ldsa + at.m0 + i % rows], w = p.sb[nb * p.ldsb + b];
-            far |= f8_far_product(a, w, a * w);
+    if (at.m0 + row < p.M) {
+        const float* sa = p.sa + first * p.ldsa + at.m0 + row;
+        for (int b0 = part; b0 < blocks; b0 += U * PARTS) {
+            float a[U], w[NB][U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int b = b0 + u * PARTS;
+                a[u] = b < blocks ? sa[b * p.ldsa] : 0.f;
+#pragma unroll
+                for (int j = 0; j < NB; ++j)  // (past N: the last block of columns)
+                    w[j][u] = b < blocks ? p.sb[min(nb + j, (p.N - 1) / 128) * p.ldsb + first + b] : 0.f;
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int j = 0; j < NB; ++j) far |= f8_far_product(a[u], w[j][u], a[u] * w[j][u]);
         }
+    }
     return f8_any<T>(__ballot(far) != 0, lds, wave, lane, 1);
 }
 
@@ -261,9 +277,8 @@ struct F8Again {
         F8Again k;
         uint32_t* to = reinterpret_cast<uint32_t*>(&k);
 #pragma unroll
-        for (unsigned i = 0; i < sizeof(F8Again) / 4; ++i)
-            to[i] = __builtin_amdgcn_readfirstlane(((const __attribute__((address_space(3))) uint32_t*)from)[i]);
-        return k;
+        for (unsigned i = 0; i < sizeof(F8Again) / 4; ++i) to[i] = ((const __attribute__((address_space(3))) uint32_t*)from)[i];
+        return k.uniform();
     }
     // (p and g are the kernel's arguments, in this order)
     template <int BT>
@@ -280,6 +295,16 @@ struct F8Again {
 #pragma unroll
         for (unsigned i = 0; i < G; ++i) groups[i] = from[N + i];
         group_tile<kOpF8, BT>(k.p, g, (int)blockIdx.x, &k.at);
+        return k.uniform();
+    }
+
+private:
+    // (the copies' descriptors are to be in scalar registers)
+    __device__ __forceinline__ F8Again uniform() const {
+        F8Again k = *this;
+        uint32_t* to = reinterpret_cast<uint32_t*>(&k);
+#pragma unroll
+        for (unsigned i = 0; i < sizeof(F8Again) / 4; ++i) to[i] = __builtin_amdgcn_readfirstlane(to[i]);
         return k;
     }
 };
