@@ -459,8 +459,9 @@ f8_pp_kernel(F8TileArgs p, GroupArgs g) {
 // Four waves in step, one step a block: iteration b multiplies block b, which is in registers, while block b + 1 comes
 // to registers from LDS and block b + 2 to LDS, into the place of block b, whose reads are over in every wave at the
 // iteration's barrier. Before it each wave waits for its copies of block b + 1. 34 KB for 64 x 64, four workgroups a CU,
-// 66 KB for 128 x 128, two. us, against steps of half a block in op_small's rings: 2048 x 4096 x 11008 91 and 114, 1024 x
-// 4096 x 4096 32.8 and 40.3, 509 x 2501 x 1003 8.3 and 10.5; a third block of 64 x 64, three workgroups a CU: 38.8 and 9.0.
+// 66 KB for 128 x 128, two. us: 2048 x 4096 x 11008 91 (2.0 PFLOP/s), 1024 x 4096 x 4096 in two pieces 28, 509 x 2501 x 1003
+// 7.7. As first made, against steps of half a block in op_small's rings: 91 and 114, 32.8 and 40.3 whole, 8.3 and 10.5; a third
+// block of 64 x 64, three workgroups a CU: 38.8 and 9.0.
 template <int BT>
 struct F8Small : F8Tile<BT, BT, 2, 2> {
     using Base = F8Tile<BT, BT, 2, 2>;

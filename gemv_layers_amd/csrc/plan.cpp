@@ -530,6 +530,7 @@ Plan make_i8_decode_plan(int64_t M, int64_t N, int64_t K, const DeviceInfo& dev,
     return p;
 }
 
+// (us of the kernels as they were when a rule was made: both sides of it, on one card.)
 // Tiles. Rounds of the tiles that fill the card (one of 256 x 256, two of 128 x 128 or four of 64 x 64 a CU), each at
 // what it measured to take for a k-step: 256 x 256 takes 1.68 times a round of 128 x 128 for codes and 1.45 times for bf16,
 // 64 x 64 1.1 times. The host knows the number of rows and of groups, and takes a group's last row tile as half full. 128
