@@ -166,3 +166,46 @@ def test_routers_of_few_groups(M, E, kernel, hit):
     ref, _ = f8_reference(A, Sa, W, Sw, spans(offsets, M), M)
     C = g.f8_grouped_matmul(f8(A, -K % 16), Sa, f8(W, -K % 16), Sw, offsets_of(offsets))
     assert g.gemm_last_plan()["kernel"] == kernel and torch.equal(C, ref.float().bfloat16())
+
+
+def test_scales_of_any_size_in_a_graph():
+    """A captured product replayed with scales that ask for a second run of every tile, of some and of none, and with rows of
+    zeros and NaN, between eager calls: the bits of those."""
+    cases = []
+    for M, N, K in ((40, 300, 1000), (200, 130, 8300), (1024, 4096, 520), (4096, 4352, 4130)):
+        A, W = (f8(codes_of([-2.0, -1.0, 1.0, 1.5], i, *s), -K % 16) for i, s in enumerate(((M, K), (N, K))))
+        cases.append((A, torch.ones(blocks(K), M, device="cuda"), W, torch.ones(blocks(N), blocks(K), device="cuda")))
+
+    def fill(turn):
+        for A, Sa, W, Sw in cases:
+            Sa.copy_(torch.rand(Sa.shape, generator=gen(turn), device="cuda") + 0.5)
+            Sw.copy_(torch.rand(Sw.shape, generator=gen(10 + turn), device="cuda") + 0.5)
+            if turn % 4 == 1:                               # sums of magnitudes from 2^-118 on, whose bound is 2^-128 at least,
+                Sa.mul_(2.0**-126)                          # beside outputs' roundings of 2^-134 at most below 2^-126
+                Sw.mul_(0.25)
+            if turn % 4 == 2:
+                Sa[:, 3::50] *= 2.0**-126
+                Sw[-1] *= 0.25
+                Sa[:, 5::70] = 0.0
+            if turn % 4 == 3:
+                Sa[-1, 7] = float("nan")
+                Sa[:, ::9] = 0.0
+
+    fill(0)
+    run = lambda: [g.f8_matmul(*c) for c in cases]  # noqa: E731
+    run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = run()
+    for turn in range(8):
+        fill(turn)
+        fresh = run()
+        graph.replay()
+        torch.cuda.synchronize()
+        for h, f, (A, Sa, W, Sw) in zip(held, fresh, cases):
+            assert torch.equal(h.view(torch.int16), f.view(torch.int16)), turn
+            ref, sabs = f8_reference(A.float(), Sa, W.float()[None], Sw[None], [(0, 0, A.shape[0])], A.shape[0])
+            fine = ~torch.isnan(ref).any(1)
+            assert torch.isnan(f[~fine]).all() and int((~fine).sum()) == (1 if turn % 4 == 3 and A.shape[0] > 7 else 0)
+            close(f[fine], ref[fine], sabs[fine], A.shape[1], f"turn {turn}", CUT)
